@@ -21,6 +21,13 @@ Operations (page "增强 vLLM 对 GPTQv2 格式的支持：分析与实现", sec
   gemm_grouped(A, offsets, qweight[E], qzeros[E], scales[E], bits, group, max_m)
                                                              -> rows of expert e times W_e
   device_status(stream)                                      -> GPTQ_DEV_* bits
+
+Beside the GEMMs, the rest of a decode step (include/gptq_serving.h):
+
+  paged_attention(q, k_cache, v_cache, block_table, seq_lens) -> attention of one new token per sequence
+                                                             (with k_new, v_new: appended first)
+  moe_layer(x, router, up, down, topk, bits, group)          -> router, experts on packed weights and sum
+  sample(logits, uniform, temperature, top_k, top_p, min_p)  -> (token, log probability) of each row
 """
 import ctypes
 import os
@@ -31,10 +38,12 @@ import numpy as np
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "_lib", "libgptq_gb300.so")
 HEADER = os.path.join(os.path.dirname(HERE), "include", "gptq.h")
+SERVING_HEADER = os.path.join(os.path.dirname(HERE), "include", "gptq_serving.h")
 
-F16, BF16 = 0, 1
+F16, BF16, F32 = 0, 1, 2
 V1, V2 = 1, 2
 DEV_TIMEOUT, DEV_GIDX_RANGE, DEV_SCALE_OVERFLOW, DEV_EXPERT_ROWS, DEV_GIDX_GROUPS = 0x1, 0x2, 0x4, 0x8, 0x10
+DEV_PAGE_RANGE, DEV_SEQ_LEN, DEV_NO_TOKEN = 0x20, 0x40, 0x80
 DECODE_MAX_M = 32
 
 _STATUS = {0: "GPTQ_OK", -1: "GPTQ_ERR_ARG", -2: "GPTQ_ERR_SHAPE", -3: "GPTQ_ERR_ALIGN",
@@ -55,7 +64,8 @@ class GPTQError(RuntimeError):
 
 _lib = None
 
-_P, _I, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+_P, _I, _SZ, _F, _LL = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float, ctypes.c_longlong
+_Strides = _LL * 9
 _SIGNATURES = {
     "gptq_dequant": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P]),
     "gptq_gemm": (_I, [_P, _I, _I, _I, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _SZ, _P]),
@@ -80,6 +90,12 @@ _SIGNATURES = {
     "gptq_gemm_grouped": (_I, [_P, _I, _I, _I, _P, _I, _I, _P, _P, _P, _I, _I, _I, _I, _P, _P]),
     "gptq_prepack_interleave": (_I, [_P, _I, _I, _I, _P]),
     "gptq_gemm_interleaved": (_I, [_P, _I, _I, _I, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _SZ, _P]),
+    "gptq_paged_attention_workspace_size": (_SZ, [_I, _I, _I]),
+    "gptq_paged_attention": (_I, [_P, _I, _I, _I, _P, _P, _I, _I, _I, _I, ctypes.POINTER(_LL), _P, _I, _P, _P, _P, _F, _I,
+                                  _P, _P, _P, _SZ, _P]),
+    "gptq_moe_workspace_size": (_SZ, [_I, _I, _I, _I, _I]),
+    "gptq_moe": (_I, [_P, _I, _I, _I, _I, _P, _I, _I, _I, _P, _P, _P, _P, _P, _P, _I, _I, _I, _P, _P, _P, _P, _SZ, _P]),
+    "gptq_sample": (_I, [_P, _I, _I, _LL, _I, _P, _P, _P, _P, _P, _P, _P, _P]),
 }
 
 
@@ -99,9 +115,9 @@ def lib():
     return _lib
 
 
-def header_functions():
-    """Names of the functions include/gptq.h declares."""
-    with open(HEADER) as f:
+def header_functions(header=HEADER):
+    """Names of the functions include/gptq.h (or another header) declares."""
+    with open(header) as f:
         text = f.read()
     return sorted(set(re.findall(r"^\s*(?:int|size_t|const char\s*\*)\s+(gptq_\w+)\s*\(", text, re.M)))
 
@@ -446,3 +462,180 @@ def device_status(stream=None):
 
 def strerror(code):
     return lib().gptq_strerror(code).decode()
+
+
+# ------------------------------------------------------------------ the rest of a decode step
+def _cuda(t, dtype, shape, name):
+    """The address of a contiguous CUDA tensor of this type and shape."""
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.shape != shape:
+        raise ValueError("%s must have the shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t.data_ptr()
+
+
+def _zeroed(nbytes, what):
+    if nbytes == 0:
+        raise GPTQError(-2, what)
+    return _torch().zeros(nbytes, dtype=_torch().uint8, device="cuda")
+
+
+def paged_attention_workspace_size(heads, kv_heads, head_dim):
+    return int(lib().gptq_paged_attention_workspace_size(heads, kv_heads, head_dim))
+
+
+def paged_attention_workspace(heads, kv_heads, head_dim):
+    """A workspace for paged_attention with these heads (zeroed, as its first use needs): kept by the
+    caller and given to one call after the other on one stream, whatever their batch and lengths."""
+    return _zeroed(paged_attention_workspace_size(heads, kv_heads, head_dim), "gptq_paged_attention_workspace_size")
+
+
+def _token_rows(t, dtype, shape, name):
+    """(address, stride between sequences) of [batch, heads, dim] rows that are contiguous within a sequence."""
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.shape != shape:
+        raise ValueError("%s must have the shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    stride = t.stride()
+    if stride[2] != 1 or (shape[1] > 1 and stride[1] != shape[2]):
+        raise ValueError("%s: the heads of a sequence must be contiguous" % name)
+    return t.data_ptr(), stride[0] if shape[0] > 1 else 0
+
+
+def paged_attention(q, k_cache, v_cache, block_table, seq_lens, *, scale=None, window=0, k_new=None, v_new=None,
+                    out=None, lse=None, workspace=None, stream=None):
+    """Attention of one new token of each sequence over a paged cache: q [batch, heads, dim],
+    k_cache / v_cache [pages, page_size, kv_heads, dim] (views in any order of the first three, the
+    last contiguous), block_table [batch, width] int32, seq_lens [batch] int32 -> out [batch, heads,
+    dim].  k_new / v_new [batch, kv_heads, dim] are written to slot seq_lens - 1 first.  window > 0:
+    only the last `window` keys.  scale: dim ** -0.5 where not given.  lse [batch, heads] fp32 takes
+    the log of each row's exponential sum.  A workspace (paged_attention_workspace) is made here
+    when none is given."""
+    torch = _torch()
+    batch, heads, dim = q.shape
+    pages, page_size, kv_heads, _ = k_cache.shape
+    dtype, code = q.dtype, _dtype_code(q)
+    q_ptr, q_stride = _token_rows(q, dtype, q.shape, "q")
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        if not t.is_cuda:
+            raise ValueError("%s must be a CUDA tensor" % name)
+        if t.dtype != dtype:
+            raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+        if t.shape != (pages, page_size, kv_heads, dim) or t.stride(3) != 1:
+            raise ValueError("%s must be [pages, page_size, kv_heads, dim] with contiguous rows" % name)
+    if (k_new is None) != (v_new is None):
+        raise ValueError("k_new and v_new go together")
+    kn = vn = None
+    kn_stride = vn_stride = 0
+    if k_new is not None:
+        kn, kn_stride = _token_rows(k_new, dtype, (batch, kv_heads, dim), "k_new")
+        vn, vn_stride = _token_rows(v_new, dtype, (batch, kv_heads, dim), "v_new")
+    if block_table.dim() != 2 or block_table.shape[0] != batch:
+        raise ValueError("block_table must be [batch, width]")
+    table_ptr = _cuda(block_table, torch.int32, block_table.shape, "block_table")
+    lens_ptr = _cuda(seq_lens, torch.int32, (batch,), "seq_lens")
+    if out is None:
+        out = torch.empty((batch, heads, dim), dtype=dtype, device=q.device)
+        out_ptr = out.data_ptr()
+    else:
+        out_ptr = _cuda(out, dtype, (batch, heads, dim), "out")
+    lse_ptr = None if lse is None else _cuda(lse, torch.float32, (batch, heads), "lse")
+    if workspace is None:
+        workspace = paged_attention_workspace(heads, kv_heads, dim)
+    k_stride, v_stride = k_cache.stride(), v_cache.stride()
+    strides = _Strides(q_stride, kn_stride, vn_stride, k_stride[0], k_stride[1], k_stride[2], v_stride[0], v_stride[1],
+                       v_stride[2])
+    rc = lib().gptq_paged_attention(q_ptr, batch, heads, code, k_cache.data_ptr(), v_cache.data_ptr(), pages, page_size,
+                                    kv_heads, dim, strides, table_ptr, block_table.shape[1], lens_ptr, kn, vn,
+                                    dim ** -0.5 if scale is None else scale, window, out_ptr, lse_ptr,
+                                    _ptr(workspace, name="workspace"), workspace.numel() * workspace.element_size(),
+                                    _stream(stream))
+    _check(rc, "gptq_paged_attention")
+    return out
+
+
+def moe_workspace_size(tokens, hidden, inter, experts, topk):
+    return int(lib().gptq_moe_workspace_size(tokens, hidden, inter, experts, topk))
+
+
+def moe_workspace(tokens, hidden, inter, experts, topk):
+    """A workspace for moe_layer of this shape or any smaller one (zeroed, as its first use needs):
+    kept by the caller and given to one call after the other on one stream."""
+    return _zeroed(moe_workspace_size(tokens, hidden, inter, experts, topk), "gptq_moe_workspace_size")
+
+
+def moe_layer(x, router, up, down, *, topk, bits, group, fmt=V2, renormalize=True, out=None, workspace=None,
+              return_routing=False, stream=None):
+    """The mixture-of-experts layer for up to 32 tokens x [tokens, hidden]: the `topk` experts of the
+    largest softmax(router x) (router [experts, hidden], equal ones by index), their weights
+    renormalised over the chosen (renormalize), and the weighted sum of down(silu(gate x) * up x)
+    over them.  up = (qweight [E, hidden*bits/32, 2*inter], qzeros, scales) holds the gate in its
+    first `inter` columns, down = (qweight [E, inter*bits/32, hidden], qzeros, scales); layouts as
+    for gemm_grouped.  Returns out [tokens, hidden], or (out, ids, weights) with return_routing.  A
+    workspace (moe_workspace) is made here when none is given."""
+    torch = _torch()
+    tokens, hidden = x.shape
+    experts = router.shape[0]
+    inter = up[0].shape[2] // 2
+    dtype, code = x.dtype, _dtype_code(x)
+    x_ptr = _cuda(x, dtype, (tokens, hidden), "x")
+    router_ptr = _cuda(router, dtype, (experts, hidden), "router")
+    ptrs = []
+    for weight, K, N, name in ((up, hidden, 2 * inter, "up"), (down, inter, hidden, "down")):
+        G = 1 if group == -1 else K // max(1, group)
+        ptrs.append(_cuda(weight[0], torch.int32, (experts, K * bits // 32, N), name + " qweight"))
+        ptrs.append(_cuda(weight[1], torch.int32, (experts, G, N * bits // 32), name + " qzeros"))
+        ptrs.append(_cuda(weight[2], torch.float16, (experts, G, N), name + " scales"))
+    if out is None:
+        out = torch.empty((tokens, hidden), dtype=dtype, device=x.device)
+        out_ptr = out.data_ptr()
+    else:
+        out_ptr = _cuda(out, dtype, (tokens, hidden), "out")
+    ids = weights = None
+    if return_routing:
+        ids = torch.empty((tokens, topk), dtype=torch.int32, device=x.device)
+        weights = torch.empty((tokens, topk), dtype=torch.float32, device=x.device)
+    if workspace is None and tokens > 0:
+        workspace = moe_workspace(tokens, hidden, inter, experts, topk)
+    rc = lib().gptq_moe(x_ptr, tokens, hidden, inter, code, router_ptr, experts, topk, int(bool(renormalize)), *ptrs,
+                        bits, group, fmt, out_ptr, None if ids is None else ids.data_ptr(),
+                        None if weights is None else weights.data_ptr(),
+                        None if workspace is None else _ptr(workspace, name="workspace"),
+                        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream))
+    _check(rc, "gptq_moe")
+    return (out, ids, weights) if return_routing else out
+
+
+def sample(logits, uniform, *, temperature=None, top_k=None, top_p=None, min_p=None, out=None, stream=None):
+    """One token for each row of logits [batch, vocab] (float16, bfloat16 or float32; rows may be
+    strided) from uniform [batch] fp32 in [0, 1), with [batch] settings (temperature, top_p, min_p
+    fp32; top_k int32; None: off) -> (token [batch] int32, logprob [batch] fp32), written into `out` =
+    (token, logprob) when given.  Among the kept tokens the first, in index order, whose cumulated
+    probability exceeds the uniform number."""
+    torch = _torch()
+    batch, vocab = logits.shape
+    code = F32 if logits.dtype == torch.float32 else _dtype_code(logits)
+    if not logits.is_cuda:
+        raise ValueError("logits must be a CUDA tensor")
+    if vocab > 1 and logits.stride(1) != 1:
+        raise ValueError("logits: a row must be contiguous")
+    row = logits.stride(0) if batch > 1 else vocab
+    ptrs = [_cuda(uniform, torch.float32, (batch,), "uniform")]
+    for t, dtype, name in ((temperature, torch.float32, "temperature"), (top_k, torch.int32, "top_k"),
+                           (top_p, torch.float32, "top_p"), (min_p, torch.float32, "min_p")):
+        ptrs.append(None if t is None else _cuda(t, dtype, (batch,), name))
+    if out is None:
+        token = torch.empty(batch, dtype=torch.int32, device=logits.device)
+        logprob = torch.empty(batch, dtype=torch.float32, device=logits.device)
+    else:
+        token, logprob = out
+    rc = lib().gptq_sample(logits.data_ptr(), batch, vocab, row, code, *ptrs, _cuda(token, torch.int32, (batch,), "token"),
+                           _cuda(logprob, torch.float32, (batch,), "logprob"), _stream(stream))
+    _check(rc, "gptq_sample")
+    return token, logprob

@@ -9,6 +9,7 @@
 
 #include "../../include/gptq.h"
 #include "gptq_internal.h"
+#include "serving_internal.h"
 
 namespace gptq {
 
@@ -156,6 +157,13 @@ const DeviceInfo& device_info() {
   DeviceState* st = current_state(&err);
   static DeviceInfo fallback{0, 1, 0, 0, 48 * 1024};
   return st ? st->info : fallback;
+}
+
+int device_status_word(unsigned** status) {
+  Problem p = {};
+  const int rc = device_ready(&p);
+  *status = p.status;
+  return rc;
 }
 
 }  // namespace gptq
