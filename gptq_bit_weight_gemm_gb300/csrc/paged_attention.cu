@@ -17,14 +17,18 @@
 // who is last).  A run has at most two partials, so the workspace does not grow with the problem.
 //
 // Inside a CTA each of 4 warps takes 16 of a tile's 64 keys and streams them through a ring of its
-// own: every lane copies (cp.async, 16 bytes) exactly the pieces of k and v that it will feed to the
-// tensor cores, so the ring needs no barrier, only the lane's own wait.  The k dimension of an MMA
-// may be permuted as long as both operands agree: lane (g, t) = (lane / 4, lane % 4) reads 8
-// consecutive dimensions of key g as the B fragments of two k-steps of q k^T (the query fragments are
-// loaded in the same order), and 8 consecutive dimensions 8 g .. 8 g + 7 of keys 2t, 2t+1, 2t+8, 2t+9
-// as the B fragments of eight column tiles of p v, tile j taking column 8 g + j.  The scores' C
-// fragment is the A fragment of p v as it stands.
+// own (cp.async, 16 bytes a lane, whole rows of consecutive bytes an instruction), so the main loop
+// has no CTA barrier.  Measured on the same 512 MB: cp.async moves 6.9 TB/s with 96 KB in flight per
+// SM, while one bulk copy per 256-byte row moves 1.4 to 2.7 TB/s (about 50 ns of issue each), so rows
+// scattered over pages go through cp.async.  The 16-byte pieces of row r sit at piece ^ swizzle(r), with
+// which the three ways a warp touches a stage are free of bank conflicts: whole rows written, k
+// fragments read with 16-byte loads, v fragments with ldmatrix.  The k dimension of an MMA may be
+// permuted as long as both operands agree: lane (g, t) = (lane / 4, lane % 4) reads 8 consecutive
+// dimensions of key g as the B fragments of two k-steps of q k^T, and the query fragments are loaded in
+// the same order.  The scores' C fragment is the A fragment of p v as it stands.
 #include <math_constants.h>
+
+#include <atomic>
 
 #include "decode.cuh"
 #include "gptq_device.cuh"
@@ -44,15 +48,20 @@ constexpr size_t kControlBytes = 4096;   // arrival counters, one per run
 template <int DP, int R>
 struct Shape {
   static constexpr int kBlocks = DP / 32;                  // 32-dimension blocks of k
-  static constexpr int kHalves = DP / 64;                  // 64-dimension blocks of v
-  static constexpr int kPieces = 2 * kBlocks + 4 * kHalves;   // 16-byte pieces per lane and stage
+  static constexpr int kCols = DP / 8;                     // column tiles of v, 16-byte pieces of a row
+  static constexpr int kRowBytes = DP * 2;
+  static constexpr int kLaneRows = DP / 16;                // rows one lane copies: 16 rows, 32 / kCols lanes each
+  static constexpr int kStageBytes = 2 * kWarpKeys * kRowBytes;   // k rows, then v rows
   static constexpr int kStages = DP == 64 ? 4 : 3;
   static constexpr int kCtas = DP == 256 ? 1 : (DP == 128 ? 2 : 3);   // per SM
-  static constexpr int kAcc = kHalves * 8 * 2 * R;         // live accumulators per thread
-  static constexpr size_t kRing = static_cast<size_t>(kStages) * kWarps * kPieces * 512;
-  static constexpr size_t kMerge = 2 * static_cast<size_t>(kAcc) * 128;
+  static constexpr size_t kRing = static_cast<size_t>(kStages) * kWarps * kStageBytes;
+  static constexpr size_t kMerge = static_cast<size_t>(kWarps - 1) * kCols * 2 * 128;   // one block of 8 rows
   static constexpr size_t kSmem = kRing + kMerge;
 };
+
+__host__ __device__ constexpr int swizzle(int row) {
+  return ((row >> 1 & 1) * 5) ^ ((row >> 2 & 1) * 2) ^ ((row & 1) * 4);
+}
 
 // floats of one partial: accumulators, then m and l per row
 constexpr size_t partial_floats(int dp) { return static_cast<size_t>(kMaxRows) * dp + 2 * kMaxRows; }
@@ -69,6 +78,16 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
   return v;
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void ldsm4_trans(uint32_t (&v)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+               : "r"(a)
+               : "memory");
 }
 
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -92,6 +111,10 @@ struct Args {
   int row_blocks;     // items per (sequence, kv head): 16 query heads each
   int items;          // items per sequence
   float scale_log2;   // scale * log2(e)
+  // key / page_size = key * page_mul >> page_shift for keys below 2^30
+  unsigned page_mul, page_shift;
+  // cache strides in 16-byte units
+  unsigned k_page16, k_slot16, k_head16, v_page16, v_slot16, v_head16;
   unsigned* counters;
   float* partials;
 };
@@ -111,12 +134,13 @@ __device__ __forceinline__ int tile_count(const AttentionProblem& p, int n) {
   return nt > 0 ? nt : 1;
 }
 
-// A place on the line of tiles.
+// A place on the line of tiles: tile t of nt of item h of sequence b, whose live keys are [lo, n).
 struct Cursor {
-  int b, h, t, nt, n, n_next;
+  int b, h, t, nt, n, lo, n_next;
   __device__ __forceinline__ void set(const AttentionProblem& p, int seq, int raw) {
     b = seq;
     n = clamp_len(p, raw);
+    lo = first_key(p, n);
     nt = tile_count(p, n);
     n_next = seq + 1 < p.batch ? p.lens[seq + 1] : 0;      // fetched a sequence ahead
   }
@@ -144,6 +168,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, R>::kCtas)) k_attention(c
   const AttentionProblem& p = a.p;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ float sm_m[kWarps][kMaxRows], sm_l[kWarps][kMaxRows];
+  __shared__ __align__(16) unsigned sm_rows[kWarps][2][kWarpKeys];
   __shared__ long long sm_sum[kWarps];
   __shared__ long long sm_at;
   __shared__ int sm_seq, sm_last;
@@ -211,88 +236,91 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, R>::kCtas)) k_attention(c
   }
   get = put;
 
-  // ---- the ring: stage s of this warp, piece i of this lane
-  const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + warp * S::kPieces * 512 + lane * 16;
-  auto stage_at = [&](int s) { return ring + s * (kWarps * S::kPieces * 512); };
+  // ---- the ring of this warp.  The offsets of a stage's 16 rows (in 16-byte units, 32 bits: the host
+  // refuses caches past 2^32 of them) go through shared memory from the lanes that look them up.
+  const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + warp * (S::kStages * S::kStageBytes);
   unsigned long long live = 0;                             // 16 key bits per stage in flight, oldest first
-  int page = -1;                                           // lanes 0..15: the page of this lane's next key
-  // lane l < 16 looks up key `key0 + l` of the producer's place
-  auto place = [&](int& key, int& kb) {
-    kb = (first_key(p, put.n) & ~(kWarpKeys - 1)) + put.t * kTileKeys + warp * kWarpKeys;
-    key = kb + (lane & 15);
-  };
+  const int piece = lane % S::kCols, row0 = lane / S::kCols * S::kLaneRows;
+  const bool in_dim = piece * 8 < p.head_dim;
+  // lane l < 16 looks up key l of the producer's place: its page (fetched a tile ahead) and slot
+  int page = -1, slot = 0, kb = 0, put_hk = put.h / a.row_blocks;
+  bool want = false;
   auto fetch_page = [&]() {
-    int key, kb;
-    place(key, kb);
-    page = -1;
-    if (lane < kWarpKeys && key >= first_key(p, put.n) && key < put.n)
-      page = __ldg(p.table + static_cast<long long>(put.b) * p.table_width + key / p.page_size);
+    kb = (put.lo & ~(kWarpKeys - 1)) + put.t * kTileKeys + warp * kWarpKeys;
+    const int key = kb + lane;
+    want = lane < kWarpKeys && key >= put.lo && key < put.n;
+    const int entry = static_cast<int>(static_cast<unsigned long long>(static_cast<unsigned>(key)) * a.page_mul >> a.page_shift);
+    slot = key - entry * p.page_size;
+    page = want ? __ldg(p.table + static_cast<long long>(put.b) * p.table_width + entry) : -1;
   };
   auto issue = [&](int s, int pos) {
-    int key, kb;
-    place(key, kb);
-    const bool wanted = lane < kWarpKeys && key >= first_key(p, put.n) && key < put.n;
-    const bool ok = wanted && page >= 0 && page < p.pages;
-    if (wanted && !ok) atomicOr(p.status, kStatusPageRange);
+    const bool ok = want && page >= 0 && page < p.pages;
+    if (want && !ok) atomicOr(p.status, kStatusPageRange);
     const unsigned mask = __ballot_sync(0xFFFFFFFFu, ok);
     live |= static_cast<unsigned long long>(mask) << (16 * pos);
     if (mask == 0) return;
-    const int hk = put.h / a.row_blocks;
-    // addresses of this lane's key's rows; the new token's rows come from k_new and v_new
-    const T* krow = static_cast<const T*>(p.k_cache);
-    const T* vrow = static_cast<const T*>(p.v_cache);
-    if (ok) {
-      const int slot = key % p.page_size;
-      krow += page * p.k_page + slot * p.k_slot + hk * p.k_head;
-      vrow += page * p.v_page + slot * p.v_slot + hk * p.v_head;
+    if (lane < kWarpKeys) {
+      sm_rows[warp][0][lane] = ok ? page * a.k_page16 + slot * a.k_slot16 + put_hk * a.k_head16 : 0u;
+      sm_rows[warp][1][lane] = ok ? page * a.v_page16 + slot * a.v_slot16 + put_hk * a.v_head16 : 0u;
     }
-    if (p.k_new) {
-      const int last = put.n - 1 - kb;                     // the new token's place among the 16 keys
-      if (last >= 0 && last < kWarpKeys && (mask >> last & 1)) {
-        const T* kn = static_cast<const T*>(p.k_new) + put.b * p.kn_batch + hk * p.head_dim;
-        const T* vn = static_cast<const T*>(p.v_new) + put.b * p.vn_batch + hk * p.head_dim;
-        T* kd = const_cast<T*>(reinterpret_cast<const T*>(__shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(krow), last)));
-        T* vd = const_cast<T*>(reinterpret_cast<const T*>(__shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(vrow), last)));
-        if (put.h % a.row_blocks == 0) {                   // one item of the kv head appends
-          const int pieces = p.head_dim / 8;
-          for (int i = lane; i < 2 * pieces; i += 32) {
-            if (i < pieces) reinterpret_cast<uint4*>(kd)[i] = reinterpret_cast<const uint4*>(kn)[i];
-            else reinterpret_cast<uint4*>(vd)[i - pieces] = reinterpret_cast<const uint4*>(vn)[i - pieces];
+    __syncwarp();
+    // the new token's row is taken from k_new and v_new, and one item of its kv head writes it to
+    // its slot
+    const int last = p.k_new ? put.n - 1 - kb : -1;
+    const bool append = last >= 0 && last < kWarpKeys && (mask >> last & 1);
+    const uint4* fresh[2] = {nullptr, nullptr};
+    if (append) {
+      const int pieces = p.head_dim / 8;
+      fresh[0] = reinterpret_cast<const uint4*>(static_cast<const T*>(p.k_new) + put.b * p.kn_batch) + put_hk * pieces;
+      fresh[1] = reinterpret_cast<const uint4*>(static_cast<const T*>(p.v_new) + put.b * p.vn_batch) + put_hk * pieces;
+      if (put.h % a.row_blocks == 0) {
+        uint4* kd = static_cast<uint4*>(p.k_cache) + sm_rows[warp][0][last];
+        uint4* vd = static_cast<uint4*>(p.v_cache) + sm_rows[warp][1][last];
+        for (int i = lane; i < 2 * pieces; i += 32) {
+          if (i < pieces) kd[i] = fresh[0][i];
+          else vd[i - pieces] = fresh[1][i - pieces];
+        }
+      }
+    }
+    // row row0 + j lands at piece ^ swizzle(row0 + j); the swizzle is linear, and rows start at
+    // multiples of 128 bytes, so it is an exclusive or on the lane's own address
+    const uint32_t dst = ring + s * S::kStageBytes + row0 * S::kRowBytes + ((piece ^ swizzle(row0)) << 4);
+    if (mask == 0xFFFFu && !append) {
+      if (in_dim) {
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          const uint4* base = static_cast<const uint4*>(kv ? p.v_cache : p.k_cache) + piece;
+#pragma unroll
+          for (int j4 = 0; j4 < S::kLaneRows; j4 += 4) {
+            const uint4 off = *reinterpret_cast<const uint4*>(&sm_rows[warp][kv][row0 + j4]);
+#pragma unroll
+            for (int j = j4; j < j4 + 4; ++j)
+              cp_async16((dst ^ (swizzle(j) << 4)) + (kv * kWarpKeys + j) * S::kRowBytes, base + (&off.x)[j - j4]);
           }
         }
-        if (lane == last) {
-          krow = kn;
-          vrow = vn;
+      }
+    } else {
+      // rows without a live key are filled with zeros: what the cache holds there may be NaN
+#pragma unroll 1
+      for (int kv = 0; kv < 2; ++kv) {
+        const uint4* base = static_cast<const uint4*>(kv ? p.v_cache : p.k_cache);
+#pragma unroll 1
+        for (int j = 0; j < S::kLaneRows; ++j) {
+          const bool on = in_dim && (mask >> (row0 + j) & 1);
+          const uint4* from = append && row0 + j == last ? fresh[kv] : base + sm_rows[warp][kv][row0 + j];
+          cp_async16((dst ^ (swizzle(j) << 4)) + (kv * kWarpKeys + j) * S::kRowBytes, on ? from + piece : base, on ? 16u : 0u);
         }
       }
     }
-    const unsigned long long ka = reinterpret_cast<unsigned long long>(krow), va = reinterpret_cast<unsigned long long>(vrow);
-    const uint32_t dst = stage_at(s);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {                          // keys g and g + 8
-      const int k = g + 8 * i;
-      const T* src = reinterpret_cast<const T*>(__shfl_sync(0xFFFFFFFFu, ka, k));
-      const bool on = mask >> k & 1;
-#pragma unroll
-      for (int blk = 0; blk < S::kBlocks; ++blk) {
-        const int d = 32 * blk + 8 * t;
-        const bool in = on && d < p.head_dim;
-        cp_async16(dst + (i * S::kBlocks + blk) * 512, in ? src + d : src, in ? 16u : 0u);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {                          // keys 2t, 2t + 1, 2t + 8, 2t + 9
-      const int k = 2 * t + (i & 1) + 8 * (i >> 1);
-      const T* src = reinterpret_cast<const T*>(__shfl_sync(0xFFFFFFFFu, va, k));
-      const bool on = mask >> k & 1;
-#pragma unroll
-      for (int hb = 0; hb < S::kHalves; ++hb) {
-        const int d = 64 * hb + 8 * g;
-        const bool in = on && d < p.head_dim;
-        cp_async16(dst + (2 * S::kBlocks + i * S::kHalves + hb) * 512, in ? src + d : src, in ? 16u : 0u);
-      }
-    }
+    __syncwarp();                                          // sm_rows is free again
   };
+  if (!in_dim) {                                           // columns past head_dim stay zero
+    for (int s = 0; s < S::kStages; ++s)
+      for (int j = 0; j < 2 * kWarpKeys; ++j)
+        if (j % kWarpKeys / S::kLaneRows == row0 / S::kLaneRows)
+          *reinterpret_cast<uint4*>(smem + warp * (S::kStages * S::kStageBytes) + s * S::kStageBytes + j * S::kRowBytes +
+                                    ((piece ^ swizzle(j)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+  }
   const int ntiles = static_cast<int>(end - begin < 0x7FFFFFFF ? end - begin : 0x7FFFFFFF);
   int put_left = ntiles;
   fetch_page();
@@ -300,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, R>::kCtas)) k_attention(c
     if (put_left > 0) {
       issue(s, pos);
       if (--put_left > 0) {
-        put.advance(a);
+        if (put.advance(a)) put_hk = put.h / a.row_blocks;
         fetch_page();
       }
     }
@@ -311,19 +339,17 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, R>::kCtas)) k_attention(c
 
   // ---- the consumer: queries, running maximum and sum (log2 units) of rows g and g + 8, accumulator
   uint32_t q[R][S::kBlocks * 4];
-  float m[R], l[R], o[S::kHalves * 8][4];
+  float m[R], l[R], o[S::kCols][4];
   auto rows_of = [&](int h) {                              // live query rows of item h
     const int r = a.group - (h % a.row_blocks) * kMaxRows;
     return r < kMaxRows ? r : kMaxRows;
   };
   auto q_head = [&](int h) { return (h / a.row_blocks) * a.group + (h % a.row_blocks) * kMaxRows; };
-  auto open_item = [&]() {
+  auto load_q = [&]() {
     const T* qp = static_cast<const T*>(p.q) + get.b * p.q_batch + static_cast<long long>(q_head(get.h)) * p.head_dim;
     const int rows = rows_of(get.h);
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      m[r] = -CUDART_INF_F;
-      l[r] = 0.f;
+    for (int r = 0; r < R; ++r)
 #pragma unroll
       for (int blk = 0; blk < S::kBlocks; ++blk) {
         const int row = g + 8 * r, d = 32 * blk + 8 * t;
@@ -331,21 +357,32 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, R>::kCtas)) k_attention(c
         if (row < rows && d < p.head_dim) v = __ldg(reinterpret_cast<const uint4*>(qp + row * p.head_dim + d));
         q[r][4 * blk] = v.x; q[r][4 * blk + 1] = v.y; q[r][4 * blk + 2] = v.z; q[r][4 * blk + 3] = v.w;
       }
-    }
+  };
+  auto clear = [&]() {
 #pragma unroll
-    for (int i = 0; i < S::kHalves * 8; ++i)
+    for (int r = 0; r < R; ++r) m[r] = -CUDART_INF_F, l[r] = 0.f;
+#pragma unroll
+    for (int i = 0; i < S::kCols; ++i)
 #pragma unroll
       for (int c = 0; c < 4; ++c) o[i][c] = 0.f;
   };
+  // this lane's k piece of key g: blocks 2 i and 2 i + 1 at k_at[0] and k_at[1] + 128 i; its ldmatrix
+  // row: v tiles 8 i + 2 x and 8 i + 2 x + 1 at v_at[x] + 128 i
+  uint32_t k_at[2], v_at[4];
+#pragma unroll
+  for (int x = 0; x < 2; ++x) k_at[x] = ring + g * S::kRowBytes + ((t ^ swizzle(g) ^ (4 * x)) << 4);
+#pragma unroll
+  for (int x = 0; x < 4; ++x)
+    v_at[x] = ring + (kWarpKeys + (lane & 15)) * S::kRowBytes + (((lane >> 4) ^ swizzle(lane & 7) ^ (2 * x)) << 4);
 
   auto compute = [&](int s, unsigned mask) {
-    const uint32_t src = stage_at(s);
+    const uint32_t at = s * S::kStageBytes;
     float sc[2][4] = {};
 #pragma unroll
     for (int blk = 0; blk < S::kBlocks; ++blk) {
 #pragma unroll
       for (int nt = 0; nt < 2; ++nt) {
-        const uint4 v = lds128(src + (nt * S::kBlocks + blk) * 512);
+        const uint4 v = lds128(k_at[blk & 1] + at + (blk >> 1) * 128 + nt * 8 * S::kRowBytes);
         mma(sc[nt], q[0][4 * blk], R == 2 ? q[R - 1][4 * blk] : 0u, q[0][4 * blk + 1], R == 2 ? q[R - 1][4 * blk + 1] : 0u,
             v.x, v.y, T());
         mma(sc[nt], q[0][4 * blk + 2], R == 2 ? q[R - 1][4 * blk + 2] : 0u, q[0][4 * blk + 3],
@@ -361,7 +398,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, R>::kCtas)) k_attention(c
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int key = 8 * (i >> 1) + 2 * t + (i & 1);
-        x[i] = mask >> key & 1 ? sc[i >> 1][2 * r + (i & 1)] * a.scale_log2 : -CUDART_INF_F;
+        x[i] = sc[i >> 1][2 * r + (i & 1)] * a.scale_log2;
+        if (mask != 0xFFFFu && !(mask >> key & 1)) x[i] = -CUDART_INF_F;
       }
       float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
       top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
@@ -381,52 +419,25 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, R>::kCtas)) k_attention(c
     if (R == 1) pa[1][0] = pa[1][1] = 0u;
     if (__any_sync(0xFFFFFFFFu, moved)) {
 #pragma unroll
-      for (int i = 0; i < S::kHalves * 8; ++i)
+      for (int i = 0; i < S::kCols; ++i)
 #pragma unroll
         for (int c = 0; c < 2 * R; ++c) o[i][c] *= alpha[c >> 1];
     }
 #pragma unroll
-    for (int hb = 0; hb < S::kHalves; ++hb) {
-      uint4 v[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = lds128(src + (2 * S::kBlocks + i * S::kHalves + hb) * 512);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t sel = j & 1 ? 0x7632u : 0x5410u;
-        const uint32_t b0 = __byte_perm((&v[0].x)[j >> 1], (&v[1].x)[j >> 1], sel);
-        const uint32_t b1 = __byte_perm((&v[2].x)[j >> 1], (&v[3].x)[j >> 1], sel);
-        mma(o[hb * 8 + j], pa[0][0], pa[1][0], pa[0][1], pa[1][1], b0, b1, T());
-      }
+    for (int i = 0; i < S::kCols; i += 2) {                // keys 0..7 and 8..15 of two column tiles
+      uint32_t v[4];
+      ldsm4_trans(v, v_at[(i >> 1) & 3] + at + (i >> 3) * 128);
+      mma(o[i], pa[0][0], pa[1][0], pa[0][1], pa[1][1], v[0], v[1], T());
+      mma(o[i + 1], pa[0][0], pa[1][0], pa[0][1], pa[1][1], v[2], v[3], T());
     }
   };
 
-  // One row of an item: the running sum's factor and the place of its values.  Warp 0's lane (g, t)
-  // holds, of row g + 8 r and half hb, dimensions 64 hb + 16 t .. + 15.
-  auto write_row = [&](int b, int h, int r, float mr, float lr) {
-    const int row = g + 8 * r;
-    if (row >= rows_of(h)) return;
-    const long long at = static_cast<long long>(b) * p.heads + q_head(h) + row;
-    const float inv = lr > 0.f || isnan(lr) ? 1.f / lr : 0.f;
-    T* out = static_cast<T*>(p.out) + at * p.head_dim;
-#pragma unroll
-    for (int hb = 0; hb < S::kHalves; ++hb)
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int d = 64 * hb + 16 * t + 8 * c;
-        if (d < p.head_dim) {
-          uint32_t w[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) w[j] = pack2(o[hb * 8 + 2 * j][2 * r + c] * inv, o[hb * 8 + 2 * j + 1][2 * r + c] * inv, T());
-          *reinterpret_cast<uint4*>(out + d) = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-      }
-    if (p.lse && t == 0) p.lse[at] = mr * 0.693147180559945f + logf(lr);
-  };
+  // The item's keys of this run are done: the 4 warps join, and the result or a partial is written.
+  // (b, h): the item; the cursor may already be at the next one.  Thread (warp w, lane (g, t)) sums,
+  // for row g of a block of 8, column tiles w kMine .. of the 4 warps' accumulators.
+  constexpr int kMine = S::kCols / kWarps;
   float* const merge = reinterpret_cast<float*>(smem + S::kRing);
-  auto acc = [&](int i) -> float& { return o[i / (2 * R)][i % (2 * R)]; };
-
-  // The item's keys of this run are done: the 4 warps join, and warp 0 writes the result or a partial.
-  auto close_item = [&](long long item_begin, long long item_end) {
+  auto close_item = [&](int b, int h, long long item_begin, long long item_end) {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], 1);
@@ -437,114 +448,129 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, R>::kCtas)) k_attention(c
       }
     }
     __syncthreads();
+    const bool whole = item_begin >= begin && item_end <= end;
+    // part of an item: runs first .. last hold it; the first leaves its part in its slot 1, the
+    // others in slot 0
+    const int first = whole ? run : static_cast<int>(((item_begin + 1) * runs - 1) / total);
+    const int last = whole ? run : static_cast<int>((item_end * runs - 1) / total);
+    auto slot_of = [&](int r) { return a.partials + (static_cast<size_t>(r) * 2 + (r == first ? 1 : 0)) * partial_floats(DP); };
+    const int rows = rows_of(h);
+    auto write = [&](int r, float M, float L, const float (&sum)[kMine][2]) {
+      const int row = g + 8 * r;
+      if (row >= rows) return;
+      const long long at = static_cast<long long>(b) * p.heads + q_head(h) + row;
+      const float inv = L > 0.f || isnan(L) ? 1.f / L : 0.f;
+      T* out = static_cast<T*>(p.out) + at * p.head_dim;
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        const int d = (warp * kMine + i) * 8 + 2 * t;
+        if (d < p.head_dim) *reinterpret_cast<uint32_t*>(out + d) = pack2(sum[i][0] * inv, sum[i][1] * inv, T());
+      }
+      if (p.lse && warp == 0 && t == 0) p.lse[at] = M * 0.693147180559945f + logf(L);
+    };
     float M[R], L[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       M[r] = -CUDART_INF_F;
+#pragma unroll
       for (int w = 0; w < kWarps; ++w) M[r] = fmaxf(M[r], sm_m[w][g + 8 * r]);
       const float base = M[r] == -CUDART_INF_F ? 0.f : M[r];
       L[r] = 0.f;
+#pragma unroll
       for (int w = 0; w < kWarps; ++w) L[r] += sm_l[w][g + 8 * r] * exp2f(sm_m[w][g + 8 * r] - base);
       const float f = exp2f(m[r] - base);
+      if (r) __syncthreads();                              // the block before has been read
+      // every warp hands the column tiles that others sum to them, and keeps its own
+      float sum[kMine][2];
 #pragma unroll
-      for (int i = 0; i < S::kHalves * 8; ++i) {
-        o[i][2 * r] *= f;
-        o[i][2 * r + 1] *= f;
+      for (int i = 0; i < S::kCols; ++i) {
+        const float2 v = make_float2(o[i][2 * r] * f, o[i][2 * r + 1] * f);
+        const int owner = i / kMine, from = (warp - owner + kWarps - 1) % kWarps;   // 0 .. 2, 3 for the owner
+        if (warp == owner) {
+          sum[i % kMine][0] = v.x;
+          sum[i % kMine][1] = v.y;
+        } else {
+          *reinterpret_cast<float2*>(merge + ((i * (kWarps - 1) + from) * 32 + lane) * 2) = v;
+        }
       }
-    }
-#pragma unroll
-    for (int step = 2; step >= 1; step >>= 1) {
-      if (warp >= step && warp < 2 * step)
-#pragma unroll
-        for (int i = 0; i < S::kAcc; ++i) merge[((warp - step) * S::kAcc + i) * 32 + lane] = acc(i);
       __syncthreads();
-      if (warp < step)
 #pragma unroll
-        for (int i = 0; i < S::kAcc; ++i) acc(i) += merge[(warp * S::kAcc + i) * 32 + lane];
-      __syncthreads();
-    }
-    const bool whole = item_begin >= begin && item_end <= end;
-    if (whole) {
-      if (warp == 0)
+      for (int i = 0; i < kMine; ++i)
 #pragma unroll
-        for (int r = 0; r < R; ++r) write_row(get.b, get.h, r, M[r], L[r]);
-      return;
-    }
-    // ---- part of an item: runs first .. last hold it; the first leaves its part in its slot 1,
-    // the others in slot 0
-    const int first = static_cast<int>(((item_begin + 1) * runs - 1) / total);
-    const int last = static_cast<int>((item_end * runs - 1) / total);
-    auto slot = [&](int r) { return a.partials + (static_cast<size_t>(r) * 2 + (r == first ? 1 : 0)) * partial_floats(DP); };
-    if (warp == 0) {
-      float* to = slot(run);
+        for (int w = 0; w < kWarps - 1; ++w) {
+          const float2 x = *reinterpret_cast<const float2*>(merge + (((warp * kMine + i) * (kWarps - 1) + w) * 32 + lane) * 2);
+          sum[i][0] += x.x;
+          sum[i][1] += x.y;
+        }
+      if (whole) {
+        write(r, M[r], L[r], sum);
+      } else {
+        float* to = slot_of(run);
 #pragma unroll
-      for (int i = 0; i < S::kAcc; ++i) __stcg(to + i * 32 + lane, acc(i));
-#pragma unroll
-      for (int r = 0; r < R; ++r)
-        if (t == 0) {
+        for (int i = 0; i < kMine; ++i)
+          __stcg(reinterpret_cast<float2*>(to + r * 8 * DP) + (warp * kMine + i) * 32 + lane, make_float2(sum[i][0], sum[i][1]));
+        if (warp == 0 && t == 0) {
           __stcg(to + kMaxRows * DP + g + 8 * r, M[r]);
           __stcg(to + kMaxRows * DP + kMaxRows + g + 8 * r, L[r]);
         }
-      __threadfence();
-      __syncwarp();
-      // the counter wraps to zero at the last arrival, ready for the next call
-      if (lane == 0) sm_last = atomicInc(a.counters + first, static_cast<unsigned>(last - first)) == static_cast<unsigned>(last - first);
+      }
     }
+    if (whole) return;
+    __threadfence();
+    __syncthreads();
+    // the counter wraps to zero at the last arrival, ready for the next call
+    if (threadIdx.x == 0)
+      sm_last = atomicInc(a.counters + first, static_cast<unsigned>(last - first)) == static_cast<unsigned>(last - first);
     __syncthreads();
     if (!sm_last) return;
     __threadfence();
-    // the last arrival joins the parts in run order; warp w takes a quarter of the accumulators
-    constexpr int kMine = (S::kAcc + kWarps - 1) / kWarps;
-    float sum[kMine] = {};
+    // the last arrival joins the parts in run order
 #pragma unroll
-    for (int r = 0; r < R; ++r) M[r] = -CUDART_INF_F, L[r] = 0.f;
-    for (int c = first; c <= last; ++c)
-#pragma unroll
-      for (int r = 0; r < R; ++r) M[r] = fmaxf(M[r], __ldcg(slot(c) + kMaxRows * DP + g + 8 * r));
+    for (int r = 0; r < R; ++r) {
+      float top = -CUDART_INF_F, l_all = 0.f, sum[kMine][2] = {};
+#pragma unroll 8
+      for (int c = first; c <= last; ++c) top = fmaxf(top, __ldcg(slot_of(c) + kMaxRows * DP + g + 8 * r));
+      const float base = top == -CUDART_INF_F ? 0.f : top;
 #pragma unroll 4
-    for (int c = first; c <= last; ++c) {
-      const float* from = slot(c);
-      float f[R];
+      for (int c = first; c <= last; ++c) {
+        const float* from = slot_of(c);
+        const float f = exp2f(__ldcg(from + kMaxRows * DP + g + 8 * r) - base);
+        l_all += __ldcg(from + kMaxRows * DP + kMaxRows + g + 8 * r) * f;
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        f[r] = exp2f(__ldcg(from + kMaxRows * DP + g + 8 * r) - (M[r] == -CUDART_INF_F ? 0.f : M[r]));
-        L[r] += __ldcg(from + kMaxRows * DP + kMaxRows + g + 8 * r) * f[r];
+        for (int i = 0; i < kMine; ++i) {
+          const float2 x = __ldcg(reinterpret_cast<const float2*>(from + r * 8 * DP) + (warp * kMine + i) * 32 + lane);
+          sum[i][0] += x.x * f;
+          sum[i][1] += x.y * f;
+        }
       }
-#pragma unroll
-      for (int i = 0; i < kMine; ++i) {
-        const int e = warp * kMine + i;
-        sum[i] += __ldcg(from + e * 32 + lane) * f[R == 2 ? (i % 4) >> 1 : 0];
-      }
+      write(r, top, l_all, sum);
     }
-    // back through shared memory, so that warp 0's lanes hold whole rows
-    static_assert(S::kAcc % kWarps == 0 && (R == 1 || kMine % 4 == 0), "quarters of whole fragments");
-#pragma unroll
-    for (int i = 0; i < kMine; ++i) merge[(warp * kMine + i) * 32 + lane] = sum[i];
-    __syncthreads();
-    if (warp == 0) {
-#pragma unroll
-      for (int i = 0; i < S::kAcc; ++i) acc(i) = merge[i * 32 + lane];
-#pragma unroll
-      for (int r = 0; r < R; ++r) write_row(get.b, get.h, r, M[r], L[r]);
-    }
-    __syncthreads();
   };
 
-  open_item();
+  load_q();
+  clear();
   long long item_begin = begin - get.t;
   int stage = 0;
   for (int i = 0; i < ntiles; ++i) {
     cp_wait<S::kStages - 1>();
+    __syncwarp();                                          // every lane's copies of the stage have landed
     const unsigned mask = static_cast<unsigned>(live & 0xFFFFu);
     if (mask) compute(stage, mask);
     live >>= 16;
+    __syncwarp();                                          // every lane has read the stage
     produce(stage, S::kStages - 1);
     stage = stage + 1 == S::kStages ? 0 : stage + 1;
-    const bool item_done = get.t + 1 == get.nt;
-    if (item_done || i + 1 == ntiles) close_item(item_begin, item_begin + get.nt);
-    if (i + 1 == ntiles) break;
-    item_begin += item_done ? get.nt : 0;
-    if (get.advance(a)) open_item();
+    const int b = get.b, h = get.h;
+    const long long item_end = item_begin + get.nt;
+    const bool last = i + 1 == ntiles;
+    if (last) {
+      close_item(b, h, item_begin, item_end);
+    } else if (get.advance(a)) {
+      load_q();                                            // on its way while the warps join
+      close_item(b, h, item_begin, item_end);
+      clear();
+      item_begin = item_end;
+    }
   }
   cp_wait<0>();
 }
@@ -553,10 +579,15 @@ template <typename T, int DP, int R>
 cudaError_t launch(const Args& a, cudaStream_t stream) {
   using S = Shape<DP, R>;
   auto kern = k_attention<T, DP, R>;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(S::kSmem));
-  if (e != cudaSuccess) return e;
-  int grid = device_info().sm_count * S::kCtas;
+  const DeviceInfo& dev = device_info();
+  static std::atomic<unsigned long long> opted_in{0};       // per device
+  if (dev.device >= 64 || !(opted_in.load(std::memory_order_relaxed) & (1ull << dev.device))) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(S::kSmem));
+    if (e != cudaSuccess) return e;
+    if (dev.device < 64) opted_in.fetch_or(1ull << dev.device, std::memory_order_relaxed);
+  }
+  int grid = dev.sm_count * S::kCtas;
   if (grid > kMaxCtas) grid = kMaxCtas;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
@@ -597,6 +628,17 @@ cudaError_t launch_paged_attention(const AttentionProblem& p, cudaStream_t strea
   a.row_blocks = (a.group + attention::kMaxRows - 1) / attention::kMaxRows;
   a.items = p.kv_heads * a.row_blocks;
   a.scale_log2 = p.scale * 1.44269504088896341f;
+  // m = ceil(2^(30 + L) / d) with 2^L >= d: n m / 2^(30 + L) is off by less than 1 / d for n < 2^30
+  unsigned log = 0;
+  while ((1ull << log) < static_cast<unsigned>(p.page_size)) ++log;
+  a.page_shift = 30 + log;
+  a.page_mul = static_cast<unsigned>(((1ull << a.page_shift) + p.page_size - 1) / p.page_size);
+  a.k_page16 = static_cast<unsigned>(p.k_page / 8);
+  a.k_slot16 = static_cast<unsigned>(p.k_slot / 8);
+  a.k_head16 = static_cast<unsigned>(p.k_head / 8);
+  a.v_page16 = static_cast<unsigned>(p.v_page / 8);
+  a.v_slot16 = static_cast<unsigned>(p.v_slot / 8);
+  a.v_head16 = static_cast<unsigned>(p.v_head / 8);
   a.counters = static_cast<unsigned*>(p.workspace);
   a.partials = reinterpret_cast<float*>(static_cast<char*>(p.workspace) + attention::kControlBytes);
   return p.dtype == 0 ? attention::launch_dim<__half>(a, stream) : attention::launch_dim<__nv_bfloat16>(a, stream);

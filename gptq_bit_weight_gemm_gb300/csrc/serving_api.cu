@@ -48,6 +48,13 @@ extern "C" int gptq_paged_attention(const void* q, int batch, int heads, int dty
   if (!q || !k_cache || !v_cache || !block_table || !seq_lens || !out || !workspace) return GPTQ_ERR_ARG;
   for (int i = 0; i < 9; ++i)
     if (strides[i] < 0 || strides[i] % 8) return GPTQ_ERR_ALIGN;
+  // rows of a cache are found by 32-bit offsets in 16-byte units
+  for (int i = 3; i < 9; i += 3) {
+    if (strides[i] > (1ll << 40) || strides[i + 1] > (1ll << 40) || strides[i + 2] > (1ll << 40)) return GPTQ_ERR_SHAPE;
+    const __int128 last = static_cast<__int128>(pages - 1) * strides[i] + static_cast<__int128>(page_size - 1) * strides[i + 1] +
+                          static_cast<__int128>(kv_heads - 1) * strides[i + 2] + head_dim;
+    if (last > (static_cast<__int128>(1) << 35)) return GPTQ_ERR_SHAPE;
+  }
   if (!aligned_to(q, 16) || !aligned_to(k_cache, 16) || !aligned_to(v_cache, 16) || !aligned_to(k_new, 16) ||
       !aligned_to(v_new, 16) || !aligned_to(out, 16) || !aligned_to(workspace, 16) || !aligned_to(block_table, 4) ||
       !aligned_to(seq_lens, 4) || !aligned_to(lse, 4))

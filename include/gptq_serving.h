@@ -57,7 +57,7 @@ extern "C" {
  *   out          [batch, heads, head_dim] contiguous
  *   lse          nullable [batch, heads] fp32: log sum_j exp(scale * q . k_j), -inf for length 0
  * Everything 16-bit is of `dtype` and 16-byte aligned.  head_dim: a multiple of 8 up to 256; heads a
- * multiple of kv_heads.  workspace: gptq_paged_attention_workspace_size() bytes, 16-byte aligned,
+ * multiple of kv_heads; a cache spans at most 2^35 elements (64 GiB; GPTQ_ERR_SHAPE).  workspace: gptq_paged_attention_workspace_size() bytes, 16-byte aligned,
  * control block zero (above).  batch == 0 is a no-op.
  */
 size_t gptq_paged_attention_workspace_size(int heads, int kv_heads, int head_dim);
