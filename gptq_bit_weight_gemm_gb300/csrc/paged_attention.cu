@@ -74,6 +74,18 @@ template <int N>
 __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
+// 16 bytes from L2 (a partial another SM has written); volatile, so that a batch of them is issued
+// before the first is used
+__device__ __forceinline__ float4 ldcg4(const float* p) {
+  float4 v;
+  asm volatile("ld.global.cg.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ float2 ldcg2(const float* p) {
+  float2 v;
+  asm volatile("ld.global.cg.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "l"(p) : "memory");
+  return v;
+}
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
@@ -134,19 +146,30 @@ __device__ __forceinline__ int tile_count(const AttentionProblem& p, int n) {
   return nt > 0 ? nt : 1;
 }
 
-// A place on the line of tiles: tile t of nt of item h of sequence b, whose live keys are [lo, n).
+// An item counts as its tiles and kItemUnits more on the line that is cut into runs: what opening,
+// joining and writing it takes, in tiles.  Without it a run of many short items ends last (16
+// sequences of 40 to 2048 keys, 32 kv heads: the last run at 39 us, the median at 30 us).
+constexpr int kItemUnits = 2;
+
+// A place on the line: u units after the run's begin, tile t of nt of item h of sequence b, whose live
+// keys are [lo, n).
 struct Cursor {
-  int b, h, t, nt, n, lo, n_next;
-  __device__ __forceinline__ void set(const AttentionProblem& p, int seq, int raw) {
-    b = seq;
+  int u, b, h, t, nt, n, lo, n_next;
+  __device__ __forceinline__ void set_len(const AttentionProblem& p, int raw) {
     n = clamp_len(p, raw);
     lo = first_key(p, n);
     nt = tile_count(p, n);
+  }
+  __device__ __forceinline__ void set(const AttentionProblem& p, int seq, int raw) {
+    b = seq;
+    set_len(p, raw);
     n_next = seq + 1 < p.batch ? p.lens[seq + 1] : 0;      // fetched a sequence ahead
   }
   __device__ __forceinline__ bool advance(const Args& a) {   // true: a new item begins
+    ++u;
     if (++t < nt) return false;
     t = 0;
+    u += kItemUnits;
     if (++h == a.items) {
       h = 0;
       if (b + 1 < a.p.batch) set(a.p, b + 1, n_next);
@@ -155,10 +178,11 @@ struct Cursor {
   }
 };
 
-__device__ __forceinline__ long long warp_sum(long long v) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-  return v;
+// x / y of nonnegative numbers: a 64-bit division costs a few hundred cycles, and tile counts mostly
+// fit 32 bits
+__device__ __forceinline__ long long divide(long long x, long long y) {
+  if (((x | y) >> 32) == 0) return static_cast<unsigned>(x) / static_cast<unsigned>(y);
+  return x / y;
 }
 
 template <typename T, int DP, int R>
@@ -171,69 +195,83 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, R>::kCtas)) k_attention(c
   __shared__ __align__(16) unsigned sm_rows[kWarps][2][kWarpKeys];
   __shared__ long long sm_sum[kWarps];
   __shared__ long long sm_at;
-  __shared__ int sm_seq, sm_last;
+  __shared__ int sm_seq, sm_last, sm_lens[kThreads];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 
   decode::pdl_launch_dependents();
   decode::pdl_wait();
 
-  // ---- this CTA's run: the tiles of all sequences, then the sequence its first tile falls into
-  long long total = 0;
-  {
-    long long mine = 0;
-    for (int b = threadIdx.x; b < p.batch; b += kThreads) {
-      const int raw = p.lens[b], n = clamp_len(p, raw);
-      if (n != raw && blockIdx.x == 0) atomicOr(p.status, kStatusSeqLen);
-      mine += tile_count(p, n);
+  // ---- this CTA's run: a scan of the sequences' tiles, a chunk of kThreads at a time, gives the total
+  // and then the sequence its first tile falls into (a batch of one chunk is read and scanned once)
+  long long before = 0, upto = 0;                          // tiles before and with this thread's sequence
+  int raw = 0;
+  auto scan_chunk = [&](int b0, long long base) {          // returns the tiles up to the chunk's end
+    const int b = b0 + static_cast<int>(threadIdx.x);
+    raw = b < p.batch ? p.lens[b] : 0;
+    const int n = clamp_len(p, raw);
+    if (n != raw && blockIdx.x == 0) atomicOr(p.status, kStatusSeqLen);
+    const long long w = b < p.batch ? static_cast<long long>(tile_count(p, n) + kItemUnits) * a.items : 0;
+    long long c = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xFFFFFFFFu, c, o);
+      if (lane >= o) c += v;
     }
-    mine = warp_sum(mine);
-    if (lane == 0) sm_sum[warp] = mine;
+    __syncthreads();                                       // sm_sum, sm_lens and sm_seq of the chunk before are read
+    if (lane == 31) sm_sum[warp] = c;
+    if (threadIdx.x == 0) sm_seq = -1;
+    sm_lens[threadIdx.x] = raw;
     __syncthreads();
-    for (int w = 0; w < kWarps; ++w) total += sm_sum[w];
-    total *= a.items;
-  }
+    long long all = base;
+    for (int x = 0; x < kWarps; ++x) {
+      if (x < warp) c += sm_sum[x];
+      all += sm_sum[x];
+    }
+    upto = base + c;
+    before = upto - w;
+    return all;
+  };
+  long long total = 0;
+  for (int b0 = 0; b0 < p.batch; b0 += kThreads) total = scan_chunk(b0, total);
   const int runs = total < static_cast<long long>(gridDim.x) ? static_cast<int>(total) : static_cast<int>(gridDim.x);
   const int run = blockIdx.x;
   if (run >= runs) return;
-  const long long begin = total * run / runs, end = total * (run + 1) / runs;
+  // runs of `share` tiles, the first `extra` of them one longer
+  const long long share = divide(total, runs), extra = total - share * runs;
+  const long long begin = share * run + (run < extra ? run : extra), end = begin + share + (run < extra ? 1 : 0);
+  auto run_of = [&](long long tile) {
+    const long long cut = extra * (share + 1);
+    return static_cast<int>(tile < cut ? divide(tile, share + 1) : extra + divide(tile - cut, share));
+  };
   {
-    long long before = 0;                                  // tiles of the sequences before this chunk
+    long long at = 0;
     for (int b0 = 0; b0 < p.batch; b0 += kThreads) {
-      const int b = b0 + static_cast<int>(threadIdx.x);
-      const long long w = b < p.batch ? static_cast<long long>(tile_count(p, clamp_len(p, p.lens[b]))) * a.items : 0;
-      long long c = w;                                     // inclusive scan over the CTA
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long v = __shfl_up_sync(0xFFFFFFFFu, c, o);
-        if (lane >= o) c += v;
-      }
-      __syncthreads();
-      if (lane == 31) sm_sum[warp] = c;
-      if (threadIdx.x == 0) sm_seq = -1;
-      __syncthreads();
-      long long all = 0;
-      for (int x = 0; x < kWarps; ++x) {
-        if (x < warp) c += sm_sum[x];
-        all += sm_sum[x];
-      }
-      const long long lo = before + c - w;
-      if (lo <= begin && begin < lo + w) {
-        sm_seq = b;
-        sm_at = lo;
+      if (p.batch > kThreads) at = scan_chunk(b0, at);
+      if (before <= begin && begin < upto) {
+        sm_seq = b0 + static_cast<int>(threadIdx.x);
+        sm_at = before;
       }
       __syncthreads();
       if (sm_seq >= 0) break;
-      before += all;
     }
   }
   if (sm_seq < 0) return;                                  // lengths written while this ran
   Cursor put, get;
-  put.set(p, sm_seq, p.lens[sm_seq]);
+  put.b = sm_seq;
+  put.set_len(p, sm_lens[sm_seq % kThreads]);
+  put.n_next = sm_seq + 1 < p.batch ? ((sm_seq + 1) % kThreads ? sm_lens[(sm_seq + 1) % kThreads] : p.lens[sm_seq + 1]) : 0;
+  const int limit = static_cast<int>(end - begin);
+  long long tiles_begin;                                   // the consumer's item: its first tile on the line
   {
     const long long rel = begin - sm_at;
-    put.h = static_cast<int>(rel / put.nt);
-    put.t = static_cast<int>(rel - static_cast<long long>(put.h) * put.nt);
+    const int units = put.nt + kItemUnits;
+    put.h = static_cast<int>(divide(rel, units));
+    const int at = static_cast<int>(rel - static_cast<long long>(put.h) * units);
+    put.t = at > kItemUnits ? at - kItemUnits : 0;
+    put.u = at > kItemUnits ? 0 : kItemUnits - at;
+    tiles_begin = begin - at + kItemUnits;
   }
+  if (put.u >= limit) return;                              // no tile of an item, only its extra units
   get = put;
 
   // ---- the ring of this warp.  The offsets of a stage's 16 rows (in 16-byte units, 32 bits: the host
@@ -245,6 +283,9 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, R>::kCtas)) k_attention(c
   // lane l < 16 looks up key l of the producer's place: its page (fetched a tile ahead) and slot
   int page = -1, slot = 0, kb = 0, put_hk = put.h / a.row_blocks;
   bool want = false;
+  constexpr int kFresh = (2 * S::kCols + 31) / 32;         // 16-byte pieces of the new token's k and v per lane
+  uint4 fresh[kFresh];
+  int fresh_row = -1;                                      // its place among the 16 keys
   auto fetch_page = [&]() {
     kb = (put.lo & ~(kWarpKeys - 1)) + put.t * kTileKeys + warp * kWarpKeys;
     const int key = kb + lane;
@@ -252,6 +293,17 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, R>::kCtas)) k_attention(c
     const int entry = static_cast<int>(static_cast<unsigned long long>(static_cast<unsigned>(key)) * a.page_mul >> a.page_shift);
     slot = key - entry * p.page_size;
     page = want ? __ldg(p.table + static_cast<long long>(put.b) * p.table_width + entry) : -1;
+    // the new token's own row comes from k_new and v_new: fetched here, a tile ahead
+    fresh_row = p.k_new && put.n > kb && put.n <= kb + kWarpKeys ? put.n - 1 - kb : -1;
+    if (fresh_row >= 0) {
+#pragma unroll
+      for (int i = 0; i < kFresh; ++i) {
+        const int kv = (lane + 32 * i) / S::kCols, d = (lane + 32 * i) % S::kCols * 8;
+        const T* from = kv ? static_cast<const T*>(p.v_new) + put.b * p.vn_batch : static_cast<const T*>(p.k_new) + put.b * p.kn_batch;
+        fresh[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (kv < 2 && d < p.head_dim) fresh[i] = __ldg(reinterpret_cast<const uint4*>(from + put_hk * p.head_dim + d));
+      }
+    }
   };
   auto issue = [&](int s, int pos) {
     const bool ok = want && page >= 0 && page < p.pages;
@@ -264,28 +316,11 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, R>::kCtas)) k_attention(c
       sm_rows[warp][1][lane] = ok ? page * a.v_page16 + slot * a.v_slot16 + put_hk * a.v_head16 : 0u;
     }
     __syncwarp();
-    // the new token's row is taken from k_new and v_new, and one item of its kv head writes it to
-    // its slot
-    const int last = p.k_new ? put.n - 1 - kb : -1;
-    const bool append = last >= 0 && last < kWarpKeys && (mask >> last & 1);
-    const uint4* fresh[2] = {nullptr, nullptr};
-    if (append) {
-      const int pieces = p.head_dim / 8;
-      fresh[0] = reinterpret_cast<const uint4*>(static_cast<const T*>(p.k_new) + put.b * p.kn_batch) + put_hk * pieces;
-      fresh[1] = reinterpret_cast<const uint4*>(static_cast<const T*>(p.v_new) + put.b * p.vn_batch) + put_hk * pieces;
-      if (put.h % a.row_blocks == 0) {
-        uint4* kd = static_cast<uint4*>(p.k_cache) + sm_rows[warp][0][last];
-        uint4* vd = static_cast<uint4*>(p.v_cache) + sm_rows[warp][1][last];
-        for (int i = lane; i < 2 * pieces; i += 32) {
-          if (i < pieces) kd[i] = fresh[0][i];
-          else vd[i - pieces] = fresh[1][i - pieces];
-        }
-      }
-    }
     // row row0 + j lands at piece ^ swizzle(row0 + j); the swizzle is linear, and rows start at
     // multiples of 128 bytes, so it is an exclusive or on the lane's own address
     const uint32_t dst = ring + s * S::kStageBytes + row0 * S::kRowBytes + ((piece ^ swizzle(row0)) << 4);
-    if (mask == 0xFFFFu && !append) {
+    const int skip = fresh_row >= 0 && (mask >> fresh_row & 1) ? fresh_row : -1;
+    if (mask == 0xFFFFu && skip < 0) {
       if (in_dim) {
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
@@ -301,14 +336,31 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, R>::kCtas)) k_attention(c
       }
     } else {
       // rows without a live key are filled with zeros: what the cache holds there may be NaN
-#pragma unroll 1
+#pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
         const uint4* base = static_cast<const uint4*>(kv ? p.v_cache : p.k_cache);
-#pragma unroll 1
-        for (int j = 0; j < S::kLaneRows; ++j) {
-          const bool on = in_dim && (mask >> (row0 + j) & 1);
-          const uint4* from = append && row0 + j == last ? fresh[kv] : base + sm_rows[warp][kv][row0 + j];
-          cp_async16((dst ^ (swizzle(j) << 4)) + (kv * kWarpKeys + j) * S::kRowBytes, on ? from + piece : base, on ? 16u : 0u);
+#pragma unroll
+        for (int j4 = 0; j4 < S::kLaneRows; j4 += 4) {
+          const uint4 off = *reinterpret_cast<const uint4*>(&sm_rows[warp][kv][row0 + j4]);
+#pragma unroll
+          for (int j = j4; j < j4 + 4; ++j) {
+            const bool on = in_dim && (mask >> (row0 + j) & 1);
+            if (row0 + j != skip)
+              cp_async16((dst ^ (swizzle(j) << 4)) + (kv * kWarpKeys + j) * S::kRowBytes,
+                         on ? base + (&off.x)[j - j4] + piece : base, on ? 16u : 0u);
+          }
+        }
+      }
+      if (skip >= 0) {                                     // into the stage, and once into the cache's slot
+#pragma unroll
+        for (int i = 0; i < kFresh; ++i) {
+          const int kv = (lane + 32 * i) / S::kCols, c = (lane + 32 * i) % S::kCols;
+          if (kv < 2) {
+            *reinterpret_cast<uint4*>(smem + warp * (S::kStages * S::kStageBytes) + s * S::kStageBytes +
+                                      (kv * kWarpKeys + skip) * S::kRowBytes + ((c ^ swizzle(skip)) << 4)) = fresh[i];
+            if (c * 8 < p.head_dim && put.h % a.row_blocks == 0)
+              static_cast<uint4*>(kv ? p.v_cache : p.k_cache)[sm_rows[warp][kv][skip] + c] = fresh[i];
+          }
         }
       }
     }
@@ -321,16 +373,12 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, R>::kCtas)) k_attention(c
           *reinterpret_cast<uint4*>(smem + warp * (S::kStages * S::kStageBytes) + s * S::kStageBytes + j * S::kRowBytes +
                                     ((piece ^ swizzle(j)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
   }
-  const int ntiles = static_cast<int>(end - begin < 0x7FFFFFFF ? end - begin : 0x7FFFFFFF);
-  int put_left = ntiles;
   fetch_page();
   auto produce = [&](int s, int pos) {                     // one tile into stage s, the fifo's place pos
-    if (put_left > 0) {
+    if (put.u < limit) {
       issue(s, pos);
-      if (--put_left > 0) {
-        if (put.advance(a)) put_hk = put.h / a.row_blocks;
-        fetch_page();
-      }
+      if (put.advance(a)) put_hk = put.h / a.row_blocks;
+      if (put.u < limit) fetch_page();
     }
     cp_commit();
   };
@@ -437,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, R>::kCtas)) k_attention(c
   // for row g of a block of 8, column tiles w kMine .. of the 4 warps' accumulators.
   constexpr int kMine = S::kCols / kWarps;
   float* const merge = reinterpret_cast<float*>(smem + S::kRing);
-  auto close_item = [&](int b, int h, long long item_begin, long long item_end) {
+  auto close_item = [&](int b, int h, long long tiles_begin, long long tiles_end) {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], 1);
@@ -448,11 +496,10 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, R>::kCtas)) k_attention(c
       }
     }
     __syncthreads();
-    const bool whole = item_begin >= begin && item_end <= end;
+    const bool whole = tiles_begin >= begin && tiles_end <= end;
     // part of an item: runs first .. last hold it; the first leaves its part in its slot 1, the
     // others in slot 0
-    const int first = whole ? run : static_cast<int>(((item_begin + 1) * runs - 1) / total);
-    const int last = whole ? run : static_cast<int>((item_end * runs - 1) / total);
+    const int first = whole ? run : run_of(tiles_begin), last = whole ? run : run_of(tiles_end - 1);
     auto slot_of = [&](int r) { return a.partials + (static_cast<size_t>(r) * 2 + (r == first ? 1 : 0)) * partial_floats(DP); };
     const int rows = rows_of(h);
     auto write = [&](int r, float M, float L, const float (&sum)[kMine][2]) {
@@ -505,42 +552,68 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, R>::kCtas)) k_attention(c
       if (whole) {
         write(r, M[r], L[r], sum);
       } else {
+        // [row block][pair of column tiles][lane]: 4 floats; then (m, l) of each row
         float* to = slot_of(run);
+        if (g + 8 * r < rows) {
 #pragma unroll
-        for (int i = 0; i < kMine; ++i)
-          __stcg(reinterpret_cast<float2*>(to + r * 8 * DP) + (warp * kMine + i) * 32 + lane, make_float2(sum[i][0], sum[i][1]));
-        if (warp == 0 && t == 0) {
-          __stcg(to + kMaxRows * DP + g + 8 * r, M[r]);
-          __stcg(to + kMaxRows * DP + kMaxRows + g + 8 * r, L[r]);
+          for (int i = 0; i < kMine; i += 2)
+            __stcg(reinterpret_cast<float4*>(to + r * 8 * DP) + (warp * kMine + i) / 2 * 32 + lane,
+                   make_float4(sum[i][0], sum[i][1], sum[i + 1][0], sum[i + 1][1]));
+          if (warp == 0 && t == 0) __stcg(reinterpret_cast<float2*>(to + kMaxRows * DP) + g + 8 * r, make_float2(M[r], L[r]));
         }
       }
     }
     if (whole) return;
-    __threadfence();
     __syncthreads();
-    // the counter wraps to zero at the last arrival, ready for the next call
-    if (threadIdx.x == 0)
+    // the counter wraps to zero at the last arrival, ready for the next call; thread 0's fences stand
+    // for the CTA (ordered with the other threads' accesses by the barriers)
+    if (threadIdx.x == 0) {
+      __threadfence();
       sm_last = atomicInc(a.counters + first, static_cast<unsigned>(last - first)) == static_cast<unsigned>(last - first);
+      __threadfence();
+    }
     __syncthreads();
     if (!sm_last) return;
-    __threadfence();
-    // the last arrival joins the parts in run order
+    // the last arrival joins the parts in run order, a batch of them in flight at a time
+    constexpr int kBatch = DP == 256 ? 3 : 8;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
+      if (g + 8 * r >= rows) continue;
       float top = -CUDART_INF_F, l_all = 0.f, sum[kMine][2] = {};
-#pragma unroll 8
-      for (int c = first; c <= last; ++c) top = fmaxf(top, __ldcg(slot_of(c) + kMaxRows * DP + g + 8 * r));
-      const float base = top == -CUDART_INF_F ? 0.f : top;
-#pragma unroll 4
-      for (int c = first; c <= last; ++c) {
-        const float* from = slot_of(c);
-        const float f = exp2f(__ldcg(from + kMaxRows * DP + g + 8 * r) - base);
-        l_all += __ldcg(from + kMaxRows * DP + kMaxRows + g + 8 * r) * f;
+      for (int c0 = first; c0 <= last; c0 += kBatch) {
+        float2 ml[kBatch];
+        float4 x[kBatch][kMine / 2];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+          const float* from = slot_of(c0 + j <= last ? c0 + j : last);
+          ml[j] = ldcg2(from + kMaxRows * DP + 2 * (g + 8 * r));
+#pragma unroll
+          for (int i = 0; i < kMine / 2; ++i) x[j][i] = ldcg4(from + r * 8 * DP + ((warp * kMine / 2 + i) * 32 + lane) * 4);
+        }
+        float mn = top;
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) mn = fmaxf(mn, ml[j].x);   // (a repeated last part changes nothing)
+        const float base = mn == -CUDART_INF_F ? 0.f : mn, keep = exp2f(top - base);
+        top = mn;
+        l_all *= keep;
 #pragma unroll
         for (int i = 0; i < kMine; ++i) {
-          const float2 x = __ldcg(reinterpret_cast<const float2*>(from + r * 8 * DP) + (warp * kMine + i) * 32 + lane);
-          sum[i][0] += x.x * f;
-          sum[i][1] += x.y * f;
+          sum[i][0] *= keep;
+          sum[i][1] *= keep;
+        }
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+          if (c0 + j <= last) {
+            const float f = exp2f(ml[j].x - base);
+            l_all += ml[j].y * f;
+#pragma unroll
+            for (int i = 0; i < kMine / 2; ++i) {
+              sum[2 * i][0] += x[j][i].x * f;
+              sum[2 * i][1] += x[j][i].y * f;
+              sum[2 * i + 1][0] += x[j][i].z * f;
+              sum[2 * i + 1][1] += x[j][i].w * f;
+            }
+          }
         }
       }
       write(r, top, l_all, sum);
@@ -549,9 +622,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, R>::kCtas)) k_attention(c
 
   load_q();
   clear();
-  long long item_begin = begin - get.t;
   int stage = 0;
-  for (int i = 0; i < ntiles; ++i) {
+  while (get.u < limit) {
     cp_wait<S::kStages - 1>();
     __syncwarp();                                          // every lane's copies of the stage have landed
     const unsigned mask = static_cast<unsigned>(live & 0xFFFFu);
@@ -561,15 +633,13 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, R>::kCtas)) k_attention(c
     produce(stage, S::kStages - 1);
     stage = stage + 1 == S::kStages ? 0 : stage + 1;
     const int b = get.b, h = get.h;
-    const long long item_end = item_begin + get.nt;
-    const bool last = i + 1 == ntiles;
-    if (last) {
-      close_item(b, h, item_begin, item_end);
-    } else if (get.advance(a)) {
-      load_q();                                            // on its way while the warps join
-      close_item(b, h, item_begin, item_end);
-      clear();
-      item_begin = item_end;
+    const long long tiles_end = tiles_begin + get.nt;
+    const bool next = get.advance(a), more = get.u < limit;
+    if (next || !more) {
+      if (more) load_q();                                  // on its way while the warps join
+      close_item(b, h, tiles_begin, tiles_end);
+      if (more) clear();
+      tiles_begin = tiles_end + kItemUnits;
     }
   }
   cp_wait<0>();
