@@ -478,10 +478,11 @@ def _cuda(t, dtype, shape, name):
     return t.data_ptr()
 
 
-def _zeroed(nbytes, what):
+def _buffer(nbytes, zeroed, what):
     if nbytes == 0:
         raise GPTQError(-2, what)
-    return _torch().zeros(nbytes, dtype=_torch().uint8, device="cuda")
+    make = _torch().zeros if zeroed else _torch().empty
+    return make(nbytes, dtype=_torch().uint8, device="cuda")
 
 
 def paged_attention_workspace_size(heads, kv_heads, head_dim):
@@ -491,7 +492,7 @@ def paged_attention_workspace_size(heads, kv_heads, head_dim):
 def paged_attention_workspace(heads, kv_heads, head_dim):
     """A workspace for paged_attention with these heads (zeroed, as its first use needs): kept by the
     caller and given to one call after the other on one stream, whatever their batch and lengths."""
-    return _zeroed(paged_attention_workspace_size(heads, kv_heads, head_dim), "gptq_paged_attention_workspace_size")
+    return _buffer(paged_attention_workspace_size(heads, kv_heads, head_dim), True, "gptq_paged_attention_workspace_size")
 
 
 def _token_rows(t, dtype, shape, name):
@@ -565,9 +566,9 @@ def moe_workspace_size(tokens, hidden, inter, experts, topk):
 
 
 def moe_workspace(tokens, hidden, inter, experts, topk):
-    """A workspace for moe_layer of this shape or any smaller one (zeroed, as its first use needs):
-    kept by the caller and given to one call after the other on one stream."""
-    return _zeroed(moe_workspace_size(tokens, hidden, inter, experts, topk), "gptq_moe_workspace_size")
+    """A workspace for moe_layer of this shape or any smaller one: kept by the caller and given to one
+    call after the other on one stream."""
+    return _buffer(moe_workspace_size(tokens, hidden, inter, experts, topk), False, "gptq_moe_workspace_size")
 
 
 def moe_layer(x, router, up, down, *, topk, bits, group, fmt=V2, renormalize=True, out=None, workspace=None,

@@ -1,152 +1,201 @@
-// moe.cu -- the mixture-of-experts layer for a few tokens on packed expert weights.
-#include <math_constants.h>
-
+// moe.cu -- the mixture-of-experts layer for a few tokens (gptq_moe): the router's kernel, the
+// workspace and the launches of the expert products (moe.cuh).
+//
+// The router's kernel: every warp takes one expert and four tokens, sums their products in fp32 and
+// writes the logits; the activations are rewritten on the side as the expert products read them
+// (fp16 pairs times a power of two per 128), and the arrival counters of the expert products are zeroed.
 #include "gptq_device.cuh"
 #include "gptq_internal.h"
+#include "moe.cuh"
 #include "serving_internal.h"
 
 namespace gptq {
+
+cudaError_t launch_moe_b2(const moe::Args&, const int32_t*, const moe::Args&, const int32_t*, int, cudaStream_t);
+cudaError_t launch_moe_b3(const moe::Args&, const int32_t*, const moe::Args&, const int32_t*, int, cudaStream_t);
+cudaError_t launch_moe_b4(const moe::Args&, const int32_t*, const moe::Args&, const int32_t*, int, cudaStream_t);
+cudaError_t launch_moe_b8(const moe::Args&, const int32_t*, const moe::Args&, const int32_t*, int, cudaStream_t);
+
+namespace moe {
 namespace {
 
-struct Layout {
-  size_t ids, weights, logits, h, total;
+constexpr int kRouteWarps = 8, kRouteTokens = 4;
+constexpr size_t kCounterBytes = 4096;   // UP's and DOWN's runs
+static_assert(2 * kMaxRuns * 4 <= kCounterBytes, "counters");
+
+struct Space {
+  size_t logits, act, act_scale, h, h_scale, partials, total;
 };
-Layout layout(int tokens, int inter, int experts, int topk) {
+Space space(int tokens, int hidden, int inter, int experts, int topk) {
   auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
-  Layout l;
-  l.ids = 4096;
-  l.weights = l.ids + up(static_cast<size_t>(tokens) * topk * 4);
-  l.logits = l.weights + up(static_cast<size_t>(tokens) * topk * 4);
-  l.h = l.logits + up(static_cast<size_t>(tokens) * experts * 4);
-  l.total = l.h + static_cast<size_t>(tokens) * topk * inter * 4;
-  return l;
+  const size_t rows = static_cast<size_t>(tokens) * topk;
+  Space s;
+  s.logits = kCounterBytes;
+  s.act = s.logits + up(static_cast<size_t>(tokens) * experts * 4);
+  s.act_scale = s.act + up(static_cast<size_t>(tokens) * hidden * 2);
+  s.h = s.act_scale + up(static_cast<size_t>(tokens) * ((hidden + kRun - 1) / kRun) * 4);
+  s.h_scale = s.h + up(rows * inter * 2);
+  s.partials = s.h_scale + up(rows * ((inter + kRun - 1) / kRun) * 4);
+  s.total = s.partials + static_cast<size_t>(kMaxRuns) * 2 * tokens * kCols * 4;
+  return s;
 }
 
-template <typename T>
-__device__ __forceinline__ float act(const void* p, long long i) {
-  return F16Traits<T>::to_f32(static_cast<const T*>(p)[i]);
-}
+struct RouteArgs {
+  const void* x;
+  const void* router;
+  int tokens, hidden, experts;
+  float* logits;
+  __half* act;
+  float* act_scale;
+  unsigned* counters;
+};
 
-template <typename T>
-__global__ void __launch_bounds__(1024) k_route(const MoeProblem p, float* logits, int* ids, float* weights) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
-  for (int i = warp; i < p.tokens * p.experts; i += nw) {
-    const int t = i / p.experts, e = i % p.experts;
-    float s = 0.f;
-    for (int k = lane; k < p.hidden; k += 32)
-      s = fmaf(act<T>(p.x, static_cast<long long>(t) * p.hidden + k), act<T>(p.router, static_cast<long long>(e) * p.hidden + k), s);
-    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-    if (lane == 0) logits[i] = s;
+template <typename T, int BITS>
+__device__ void pack_run(const RouteArgs& a, int item, int lane) {
+  const int runs = (a.hidden + kRun - 1) / kRun, t = item / runs, j0 = item % runs * kRun, j = j0 + 4 * lane;
+  const bool in = j < a.hidden;
+  float v[4] = {};
+  if (in) {
+    const uint2 w = __ldg(reinterpret_cast<const uint2*>(static_cast<const T*>(a.x) + static_cast<long long>(t) * a.hidden + j));
+    v[0] = F16Traits<T>::to_f32(F16Traits<T>::from_bits(lo16(w.x)));
+    v[1] = F16Traits<T>::to_f32(F16Traits<T>::from_bits(hi16(w.x)));
+    v[2] = F16Traits<T>::to_f32(F16Traits<T>::from_bits(lo16(w.y)));
+    v[3] = F16Traits<T>::to_f32(F16Traits<T>::from_bits(hi16(w.y)));
   }
-  __syncthreads();
-  for (int t = warp; t < p.tokens; t += nw) {
-    const float* row = logits + t * p.experts;
-    float m = -CUDART_INF_F, sum = 0.f, kept = 0.f;
-    for (int e = lane; e < p.experts; e += 32) m = fmaxf(m, row[e]);
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-    for (int e = lane; e < p.experts; e += 32) sum += expf(row[e] - m);
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    float last_v = CUDART_INF_F;
-    int last_e = -1;
-    for (int j = 0; j < p.topk; ++j) {            // the best expert after the last one in (value, index) order
-      float bv = -CUDART_INF_F;
-      int be = 0x7FFFFFFF;
-      for (int e = lane; e < p.experts; e += 32) {
-        const float v = isnan(row[e]) ? -CUDART_INF_F : row[e];
-        const bool after = v < last_v || (v == last_v && e > last_e);
-        if (after && (be == 0x7FFFFFFF || v > bv)) { bv = v; be = e; }
+  float top = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
+#pragma unroll
+  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+  const int e = run_exponent(top);
+  const float inv = pow2(-e);
+  __half* to = a.act + static_cast<long long>(t) * a.hidden;
+  constexpr int per = Pack<BITS>::kPerUnit;
+  if (in)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) to[(j + i) / per * per + pair_pos<BITS>((j + i) % per)] = __float2half_rn(v[i] * inv);
+  if (lane == 0) a.act_scale[static_cast<long long>(t) * runs + j0 / kRun] = pow2(e);
+}
+
+template <typename T, int BITS>
+__global__ void __launch_bounds__(kRouteWarps * 32) k_route(const RouteArgs a) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int gw = blockIdx.x * kRouteWarps + warp, nw = gridDim.x * kRouteWarps;
+  decode::pdl_wait();
+  decode::pdl_launch_dependents();
+
+  for (int i = blockIdx.x * kRouteWarps * 32 + threadIdx.x; i < 2 * kMaxRuns; i += gridDim.x * kRouteWarps * 32) a.counters[i] = 0u;
+  const int tblocks = (a.tokens + kRouteTokens - 1) / kRouteTokens;
+  for (int i = gw; i < a.experts * tblocks; i += nw) {
+    const int e = i / tblocks, t0 = i % tblocks * kRouteTokens;
+    const T* r = static_cast<const T*>(a.router) + static_cast<long long>(e) * a.hidden;
+    float s[kRouteTokens] = {};
+#pragma unroll 2
+    for (int k = lane * 8; k < a.hidden; k += 256) {
+      const uint4 rv = __ldg(reinterpret_cast<const uint4*>(r + k));
+#pragma unroll
+      for (int j = 0; j < kRouteTokens; ++j) {
+        const int t = t0 + j < a.tokens ? t0 + j : a.tokens - 1;
+        const uint4 xv = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(a.x) + static_cast<long long>(t) * a.hidden + k));
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const uint32_t p = (&xv.x)[w], q = (&rv.x)[w];
+          s[j] = fmaf(F16Traits<T>::to_f32(F16Traits<T>::from_bits(lo16(p))), F16Traits<T>::to_f32(F16Traits<T>::from_bits(lo16(q))), s[j]);
+          s[j] = fmaf(F16Traits<T>::to_f32(F16Traits<T>::from_bits(hi16(p))), F16Traits<T>::to_f32(F16Traits<T>::from_bits(hi16(q))), s[j]);
+        }
       }
-      for (int o = 16; o; o >>= 1) {
-        const float ov = __shfl_xor_sync(0xFFFFFFFFu, bv, o);
-        const int oe = __shfl_xor_sync(0xFFFFFFFFu, be, o);
-        if (oe != 0x7FFFFFFF && (be == 0x7FFFFFFF || ov > bv || (ov == bv && oe < be))) { bv = ov; be = oe; }
-      }
-      const float pr = expf(bv - m) / sum;
-      kept += pr;
-      if (lane == 0) {
-        ids[t * p.topk + j] = be;
-        weights[t * p.topk + j] = pr;
-      }
-      last_v = bv;
-      last_e = be;
     }
-    __syncwarp();
-    if (p.renormalize)
-      for (int j = lane; j < p.topk; j += 32) weights[t * p.topk + j] /= kept;
-    __syncwarp();
-    for (int j = lane; j < p.topk; j += 32) {
-      if (p.ids) p.ids[t * p.topk + j] = ids[t * p.topk + j];
-      if (p.weights) p.weights[t * p.topk + j] = weights[t * p.topk + j];
+#pragma unroll
+    for (int j = 0; j < kRouteTokens; ++j) {
+#pragma unroll
+      for (int o = 16; o; o >>= 1) s[j] += __shfl_xor_sync(0xFFFFFFFFu, s[j], o);
+      if (lane == 0 && t0 + j < a.tokens) a.logits[(t0 + j) * a.experts + e] = s[j];
     }
   }
-}
+  const int runs = (a.hidden + kRun - 1) / kRun;
+  for (int i = nw - 1 - gw; i < a.tokens * runs; i += nw) pack_run<T, BITS>(a, i, lane);
 
-// fp32 weight (k, n) of expert e
-__device__ __forceinline__ float weight_at(const PackedExperts& w, int e, int k, int n, int K, int N, int bits, int group,
-                                           int zero_offset) {
-  const int G = K / group;
-  auto field = [&](uint32_t lo, uint32_t hi, int sh) { return __funnelshift_r(lo, hi, sh) & ((1u << bits) - 1u); };
-  const int rows = K / 32 * bits, bit = k * bits, words = N / 32 * bits, zbit = n * bits;
-  const int32_t* qw = w.qweight + (static_cast<long long>(e) * rows + (bit >> 5)) * N + n;
-  const uint32_t lo = qw[0], hi = (bit & 31) + bits > 32 ? qw[N] : 0;
-  const long long gz = static_cast<long long>(e) * G + k / group;
-  const int32_t* qz = w.qzeros + gz * words + (zbit >> 5);
-  const uint32_t zlo = qz[0], zhi = (zbit & 31) + bits > 32 ? qz[1] : 0;
-  const int q = static_cast<int>(field(lo, hi, bit & 31)), z = static_cast<int>(field(zlo, zhi, zbit & 31)) + zero_offset;
-  return static_cast<float>(q - z) * __half2float(static_cast<const __half*>(w.scales)[gz * N + n]);
 }
 
 template <typename T>
-__global__ void k_up(const MoeProblem p, const int* ids, float* h) {
-  const int i = blockIdx.x * blockDim.x + threadIdx.x, pair = blockIdx.y, t = pair / p.topk, e = ids[pair];
-  if (i >= p.inter) return;
-  float g = 0.f, u = 0.f;
-  for (int k = 0; k < p.hidden; ++k) {
-    const float x = act<T>(p.x, static_cast<long long>(t) * p.hidden + k);
-    g = fmaf(x, weight_at(p.up, e, k, i, p.hidden, 2 * p.inter, p.bits, p.group_up, p.zero_offset), g);
-    u = fmaf(x, weight_at(p.up, e, k, p.inter + i, p.hidden, 2 * p.inter, p.bits, p.group_up, p.zero_offset), u);
+cudaError_t launch_route(const RouteArgs& a, int bits, int grid, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kRouteWarps * 32);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  switch (bits) {
+    case 2: return cudaLaunchKernelEx(&cfg, k_route<T, 2>, a);
+    case 3: return cudaLaunchKernelEx(&cfg, k_route<T, 3>, a);
+    case 4: return cudaLaunchKernelEx(&cfg, k_route<T, 4>, a);
+    default: return cudaLaunchKernelEx(&cfg, k_route<T, 8>, a);
   }
-  h[static_cast<long long>(pair) * p.inter + i] = g / (1.f + expf(-g)) * u;
-}
-
-template <typename T>
-__global__ void k_down(const MoeProblem p, const int* ids, const float* weights, const float* h) {
-  const int n = blockIdx.x * blockDim.x + threadIdx.x, t = blockIdx.y;
-  if (n >= p.hidden) return;
-  float out = 0.f;
-  for (int j = 0; j < p.topk; ++j) {
-    const int pair = t * p.topk + j;
-    float y = 0.f;
-    for (int k = 0; k < p.inter; ++k)
-      y = fmaf(h[static_cast<long long>(pair) * p.inter + k],
-               weight_at(p.down, ids[pair], k, n, p.inter, p.hidden, p.bits, p.group_down, p.zero_offset), y);
-    out = fmaf(weights[pair], y, out);
-  }
-  static_cast<T*>(p.out)[static_cast<long long>(t) * p.hidden + n] = F16Traits<T>::from_f32(out);
-}
-
-template <typename T>
-void launch(const MoeProblem& p, const Layout& l, cudaStream_t s) {
-  char* ws = static_cast<char*>(p.workspace);
-  int* ids = reinterpret_cast<int*>(ws + l.ids);
-  float* weights = reinterpret_cast<float*>(ws + l.weights);
-  float* h = reinterpret_cast<float*>(ws + l.h);
-  k_route<T><<<1, 1024, 0, s>>>(p, reinterpret_cast<float*>(ws + l.logits), ids, weights);
-  k_up<T><<<dim3((p.inter + 127) / 128, p.tokens * p.topk), 128, 0, s>>>(p, ids, h);
-  k_down<T><<<dim3((p.hidden + 127) / 128, p.tokens), 128, 0, s>>>(p, ids, weights, h);
 }
 
 }  // namespace
+}  // namespace moe
 
-size_t moe_workspace_bytes(int tokens, int, int inter, int experts, int topk) {
-  return layout(tokens, inter, experts, topk).total;
+size_t moe_workspace_bytes(int tokens, int hidden, int inter, int experts, int topk) {
+  return moe::space(tokens, hidden, inter, experts, topk).total;
 }
 
 cudaError_t launch_moe(const MoeProblem& p, cudaStream_t stream) {
-  const Layout l = layout(p.tokens, p.inter, p.experts, p.topk);
-  if (p.dtype == 0) launch<__half>(p, l, stream);
-  else launch<__nv_bfloat16>(p, l, stream);
-  return cudaGetLastError();
+  using moe::kRun;
+  const moe::Space s = moe::space(p.tokens, p.hidden, p.inter, p.experts, p.topk);
+  char* ws = static_cast<char*>(p.workspace);
+  unsigned* counters = static_cast<unsigned*>(p.workspace);
+
+  moe::RouteArgs ra;
+  ra.x = p.x; ra.router = p.router;
+  ra.tokens = p.tokens; ra.hidden = p.hidden; ra.experts = p.experts;
+  ra.logits = reinterpret_cast<float*>(ws + s.logits);
+  ra.act = reinterpret_cast<__half*>(ws + s.act);
+  ra.act_scale = reinterpret_cast<float*>(ws + s.act_scale);
+  ra.counters = counters;
+  const int tblocks = (p.tokens + moe::kRouteTokens - 1) / moe::kRouteTokens;
+  const int runs = (p.hidden + kRun - 1) / kRun;
+  int work = p.experts * tblocks;
+  if (p.tokens * runs / 2 > work) work = p.tokens * runs / 2;
+  int grid = (work + moe::kRouteWarps - 1) / moe::kRouteWarps;
+  if (grid > device_info().sm_count) grid = device_info().sm_count;
+  cudaError_t e = p.dtype == 0 ? moe::launch_route<__half>(ra, p.bits, grid, stream)
+                               : moe::launch_route<__nv_bfloat16>(ra, p.bits, grid, stream);
+  if (e != cudaSuccess) return e;
+
+  moe::Args up = {};
+  up.K = p.hidden; up.N = 2 * p.inter; up.group = p.group_up; up.G = p.hidden / p.group_up; up.zero_offset = p.zero_offset;
+  up.qzeros = p.up.qzeros;
+  up.scales = static_cast<const __half*>(p.up.scales);
+  up.tokens = p.tokens;
+  up.experts = p.experts; up.topk = p.topk; up.renormalize = p.renormalize;
+  up.logits = ra.logits;
+  up.ids = p.ids; up.weights = p.weights;
+  up.act = ra.act; up.act_scale = ra.act_scale; up.act_runs = runs;
+  up.jblocks = (p.inter + moe::kCols / 2 - 1) / (moe::kCols / 2);
+  up.inter = p.inter;
+  up.h = reinterpret_cast<__half*>(ws + s.h);
+  up.h_scale = reinterpret_cast<float*>(ws + s.h_scale);
+  up.h_runs = (p.inter + kRun - 1) / kRun;
+  up.counters = counters;
+  up.partials = reinterpret_cast<float*>(ws + s.partials);
+  up.status = p.status;
+  moe::Args down = up;
+  down.K = p.inter; down.N = p.hidden; down.group = p.group_down; down.G = p.inter / p.group_down;
+  down.qzeros = p.down.qzeros;
+  down.scales = static_cast<const __half*>(p.down.scales);
+  down.act = up.h; down.act_scale = up.h_scale; down.act_runs = up.h_runs;
+  down.jblocks = (p.hidden + moe::kCols - 1) / moe::kCols;
+  down.out = p.out;
+  down.dtype = p.dtype;
+  down.counters = counters + moe::kMaxRuns;
+  switch (p.bits) {
+    case 2: return launch_moe_b2(up, p.up.qweight, down, p.down.qweight, p.experts, stream);
+    case 3: return launch_moe_b3(up, p.up.qweight, down, p.down.qweight, p.experts, stream);
+    case 4: return launch_moe_b4(up, p.up.qweight, down, p.down.qweight, p.experts, stream);
+    default: return launch_moe_b8(up, p.up.qweight, down, p.down.qweight, p.experts, stream);
+  }
 }
 
 }  // namespace gptq

@@ -1,0 +1,785 @@
+// moe.cuh -- the expert products of the mixture-of-experts layer (gptq_moe) for up to 32 tokens.
+//
+// Two launches after the router's (moe.cu, which leaves the logits): UP writes h = silu(x Wg) * (x Wu) for every (expert,
+// token) row, DOWN writes out[t] = sum over t's experts of w * (h Wd).  Both are a stream of packed
+// weights -- those of the chosen experts, each read once -- against a few activations, bound by HBM or,
+// with more than a few rows an expert, by unpacking.  One kernel template runs both.
+//
+// Split: a call's work is a line of chunks (32 columns x 8 warps wide, kRows packed rows deep).  UP's
+// items are (expert, 128 gate and the same 128 up columns), DOWN's are 256 output columns, whose line
+// runs through all experts one after the other, so that the sum over experts stays in the CTA and needs
+// neither atomics nor a pass of its own.  The line is cut into equal runs, one per resident CTA,
+// whatever the experts the tokens chose; an item that spans runs leaves one partial tile per run in the
+// workspace, and the last CTA to arrive adds them in run order.
+//
+// A CTA is one producer warp and 8 consumer warps around a ring of chunks.  The producer copies a
+// chunk's weights (TMA boxes of 32 columns with the 128-byte swizzle, as the decode GEMM reads them), its
+// rows of activations (bulk copies), and its groups' scales and zeros (cp.async), all arriving on one
+// mbarrier.  A consumer warp owns 32 columns: it unpacks codes to exact q - zero pairs in fp16 and
+// multiplies on the tensor cores (m16n8k16, weights as the A operand), a fresh fp32 accumulator per
+// group folded in as acc += scale * act_scale * c.
+//
+// Activations are fp16 in both stages: every row's run of 128 values is stored as fp16 times a power
+// of two chosen for the run (exact for fp16 input; bf16 input and h keep 11 bits relative to the run's
+// largest value), already in the pair order of the codes.  So h may exceed fp16's range, and bf16
+// models lose nothing to the multiply.
+#pragma once
+
+#include <cuda.h>
+
+#include <atomic>
+
+#include "decode_mma.cuh"
+#include "serving_internal.h"
+
+namespace gptq {
+namespace moe {
+
+constexpr int kWarps = 8, kConsumers = kWarps * 32, kThreads = kConsumers + 32;
+constexpr int kCols = kWarps * 32;       // columns of a CTA's tile
+constexpr int kRun = 128;                // activations that share a power of two
+constexpr int kMaxRuns = 480;            // CTAs, at most
+constexpr int kItemUnits = 2;            // what opening and writing an item takes, in chunks
+constexpr int kMinShare = 4;             // chunks of a run, at least: a join of more parts costs more than it saves
+constexpr int kMaxStages = 8;
+
+template <int BITS>
+struct Chunk {
+  static constexpr int kTiles = BITS == 3 ? 1 : 4;                        // k-tiles
+  static constexpr int kTileK = 4 * Pack<BITS>::kPerUnit;                 // k values of a k-tile
+  static constexpr int kK = kTiles * kTileK;
+  static constexpr int kRows = kTiles * 4 * Pack<BITS>::kRowsPerUnit;     // packed rows
+  static constexpr int kSlot = (kRows * 128 + 1023) & ~1023;              // one warp's box
+  static constexpr int kRunsOf = (kK + kRun - 1) / kRun;                  // activation runs of a chunk
+  // bytes of an activation row in the ring: padded so that the B fragments of 4 units and 8 rows
+  // fall into distinct banks
+  static constexpr int kActRow = kK * 2 + (BITS == 4 ? 64 : BITS == 8 ? 32 : 16);
+  static constexpr int kZeroWords = kWarps * BITS;                        // zeros of 256 columns
+};
+
+// The routing of a call in shared memory: every CTA derives it from the logits (identical in all of
+// them), so that no index ever comes from memory another CTA had to write first.
+struct Routing {
+  int* id;               // [pairs] expert of (token, choice)
+  float* w;              // [pairs] its weight
+  int* count;            // [experts] rows, then first row
+  int* slot_expert;      // [slots] chosen experts in order
+  int* slot_off;         // [slots + 1] their rows: [slot_off[s], slot_off[s + 1])
+  int* row_token;        // [pairs] rows by expert, an expert's by token
+  float* row_weight;
+  __host__ __device__ static int bytes(int pairs, int experts) {
+    return (16 * pairs + 4 * experts + 8 * (pairs < experts ? pairs : experts) + 4 + 15) & ~15;
+  }
+};
+
+struct Args {
+  int K, N, group, G, zero_offset, zwords, units;
+  const int32_t* qzeros;
+  const __half* scales;
+  int tokens;            // rows of the ring's activation part
+  int experts, topk, renormalize;
+  const float* logits;   // [tokens][experts]
+  int32_t* ids;          // UP, nullable: the caller's copies
+  float* weights;
+  const __half* act;     // UP: [tokens][K] in pair order; DOWN: [rows][K]
+  const float* act_scale;   // [row][act_runs]
+  int act_runs;
+  int jblocks;           // column blocks: UP ceil(inter / 128), DOWN ceil(hidden / 256)
+  int inter;
+  __half* h;             // UP
+  float* h_scale;
+  int h_runs;
+  void* out;             // DOWN
+  int dtype;
+  unsigned* counters;
+  float* partials;
+  unsigned* status;
+  int stages, gmax, stage_bytes;
+};
+
+// Position of value k of a unit among its halfwords.
+template <int BITS>
+__device__ __forceinline__ int pair_pos(int k) {
+  if constexpr (BITS == 3) {
+    int at = 0;
+#pragma unroll
+    for (int p = 0; p < 16; ++p) {
+      if (code3_pair(p, 0) == k) at = 2 * p;
+      if (code3_pair(p, 1) == k) at = 2 * p + 1;
+    }
+    return at;
+  } else {
+    constexpr int half = Pack<BITS>::kPerUnit / 2;
+    return k < half ? 2 * k : 2 * (k - half) + 1;
+  }
+}
+
+// The power of two (as its exponent) that takes a run's largest magnitude to [2^13, 2^14).
+__device__ __forceinline__ int run_exponent(float largest) {
+  int e = largest > 0.f ? static_cast<int>(__float_as_uint(largest) >> 23) - 127 - 13 : 0;
+  return e < -126 ? -126 : (e > 126 ? 126 : e);
+}
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<unsigned>(e + 127) << 23); }
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory"); }
+
+// Shared memory: [stages][weights | activations | activation scales | group scales | group zeros], the
+// output tile [tokens][kCols] floats, 2 mbarriers per stage, the routing.
+template <int BITS>
+struct Layout {
+  using C = Chunk<BITS>;
+  __host__ __device__ static constexpr int act() { return kWarps * C::kSlot; }
+  __host__ __device__ static int act_scale(int tokens) { return act() + tokens * C::kActRow; }
+  __host__ __device__ static int scales(int tokens) { return (act_scale(tokens) + tokens * C::kRunsOf * 4 + 15) & ~15; }
+  __host__ __device__ static int zeros(int tokens, int gmax) { return scales(tokens) + gmax * kCols * 2; }
+  __host__ __device__ static int stage(int tokens, int gmax) {
+    return (zeros(tokens, gmax) + gmax * C::kZeroWords * 4 + 1023) & ~1023;
+  }
+  __host__ __device__ static int tile_bytes(int tokens) { return tokens * kCols * 4; }
+  // less the stages and their mbarriers
+  __host__ __device__ static int fixed(int tokens, int pairs, int experts) {
+    return 1024 + tile_bytes(tokens) + Routing::bytes(pairs, experts);
+  }
+};
+
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned* status) {
+  if (ptx::mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = ptx::globaltimer();
+  while (true) {
+    if (ptx::mbar_try_wait_hint(bar, parity, 100000u)) return true;
+    if (*abort_flag) return false;
+    if (ptx::globaltimer() - t0 > 2000000000ull) {
+      *abort_flag = 1;
+      atomicOr(status, kStatusTimeout);
+      return false;
+    }
+  }
+}
+
+// Softmax, top-k (equal logits: the lower index; a NaN ranks as -inf) and grouping by expert, by the
+// whole CTA; returns the number of chosen experts.  scratch: kThreads / 32 rows of `experts` floats.
+__device__ __forceinline__ int route(const Args& a, const Routing& r, float* scratch, int (*scan)[2], bool publish) {
+  constexpr int kAll = kThreads / 32;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const float inf = __int_as_float(0x7F800000);
+  for (int e = threadIdx.x; e < a.experts; e += kThreads) r.count[e] = 0;
+  for (int t = warp; t < a.tokens; t += kAll) {
+    float* row = scratch + warp * a.experts;
+    float m = -inf, sum = 0.f, kept = 0.f;
+    for (int e = lane; e < a.experts; e += 32) {
+      const float v = __ldcg(a.logits + t * a.experts + e);
+      row[e] = v;
+      m = fmaxf(m, v);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    for (int e = lane; e < a.experts; e += 32) sum += expf(row[e] - m);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    // the best expert after the last one in (value, index) order; there are experts >= topk of them
+    float last_v = inf, mine = 0.f;
+    int last_e = -1;
+    for (int j = 0; j < a.topk; ++j) {
+      float bv = -inf;
+      int be = 0x7FFFFFFF;
+      for (int e = lane; e < a.experts; e += 32) {
+        const float v = isnan(row[e]) ? -inf : row[e];
+        const bool after = v < last_v || (v == last_v && e > last_e);
+        if (after && (be == 0x7FFFFFFF || v > bv)) {
+          bv = v;
+          be = e;
+        }
+      }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) {
+        const float ov = __shfl_xor_sync(0xFFFFFFFFu, bv, o);
+        const int oe = __shfl_xor_sync(0xFFFFFFFFu, be, o);
+        if (oe != 0x7FFFFFFF && (be == 0x7FFFFFFF || ov > bv || (ov == bv && oe < be))) {
+          bv = ov;
+          be = oe;
+        }
+      }
+      const float pr = expf(bv - m) / sum;
+      kept += pr;
+      if (lane == j) mine = pr;
+      if (lane == 0) r.id[t * a.topk + j] = be;
+      last_v = bv;
+      last_e = be;
+    }
+    if (a.renormalize) mine /= kept;
+    if (lane < a.topk) r.w[t * a.topk + lane] = mine;
+    __syncwarp();
+  }
+  __syncthreads();
+  const int pairs = a.tokens * a.topk;
+  for (int p = threadIdx.x; p < pairs; p += kThreads) {
+    atomicAdd(&r.count[r.id[p]], 1);
+    if (publish && a.ids) a.ids[p] = r.id[p];
+    if (publish && a.weights) a.weights[p] = r.w[p];
+  }
+  __syncthreads();
+  // experts with rows, in order: a scan of (chosen, rows), a CTA's threads at a time
+  int slots = 0, rows = 0;
+  for (int e0 = 0; e0 < a.experts; e0 += kThreads) {
+    const int e = e0 + static_cast<int>(threadIdx.x), n = e < a.experts ? r.count[e] : 0;
+    const unsigned chosen = __ballot_sync(0xFFFFFFFFu, n > 0);
+    int c = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xFFFFFFFFu, c, o);
+      if (lane >= o) c += v;
+    }
+    if (lane == 31) {
+      scan[warp][0] = __popc(chosen);
+      scan[warp][1] = c;
+    }
+    __syncthreads();
+    int s = slots + __popc(chosen & ((1u << lane) - 1u)), off = rows + c - n;
+    for (int w = 0; w < kAll; ++w) {
+      if (w < warp) {
+        s += scan[w][0];
+        off += scan[w][1];
+      }
+      slots += scan[w][0];
+      rows += scan[w][1];
+    }
+    if (n > 0) {
+      r.slot_expert[s] = e;
+      r.slot_off[s] = off;
+      r.count[e] = off;
+    }
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) r.slot_off[slots] = rows;
+  // a pair's place among its expert's rows: the pairs before it with the same expert
+  for (int p = threadIdx.x; p < pairs; p += kThreads) {
+    const int e = r.id[p];
+    int rank = 0;
+    for (int q = 0; q < p; ++q) rank += r.id[q] == e;
+    r.row_token[r.count[e] + rank] = p / a.topk;
+    r.row_weight[r.count[e] + rank] = r.w[p];
+  }
+  ptx::fence_proxy_async_smem();                           // the scratch lies where the ring's copies will land
+  __syncthreads();
+  return slots;
+}
+
+// A place on the line: u units after the run's begin, chunk c of the item, which is chunk kc of slot s.
+struct Cursor {
+  int u, item, c, s, kc;
+};
+
+template <int BITS, int NB, bool DOWN>
+__global__ void __launch_bounds__(kThreads, (NB == 4 ? 1 : 2)) k_experts(const __grid_constant__ CUtensorMap tmW, const Args a) {
+  using P = Pack<BITS>;
+  using C = Chunk<BITS>;
+  using L = Layout<BITS>;
+  using DP = DiffPairs<__half, BITS>;
+  constexpr int NP = DP::kPairs, ROWS = P::kRowsPerUnit;
+  extern __shared__ __align__(128) unsigned char smem_raw[];
+  __shared__ int sm_abort, sm_last, sm_scan[kThreads / 32][2];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  uint8_t* smem = smem_raw + ((1024u - (ptx::smem_addr(smem_raw) & 1023u)) & 1023u);
+  const uint32_t smem_a = ptx::smem_addr(smem);
+  const int stage_bytes = a.stage_bytes;
+  float* tile = reinterpret_cast<float*>(smem + a.stages * stage_bytes);
+  const uint32_t bars = ptx::smem_addr(tile) + L::tile_bytes(a.tokens);
+  auto full = [&](int s) { return bars + 16u * s; };
+  auto empty = [&](int s) { return bars + 16u * s + 8u; };
+  Routing rt;
+  {
+    const int pairs = a.tokens * a.topk, most = pairs < a.experts ? pairs : a.experts;
+    rt.id = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(tile) + L::tile_bytes(a.tokens) + 16 * a.stages);
+    rt.w = reinterpret_cast<float*>(rt.id + pairs);
+    rt.row_token = reinterpret_cast<int*>(rt.w + pairs);
+    rt.row_weight = reinterpret_cast<float*>(rt.row_token + pairs);
+    rt.count = reinterpret_cast<int*>(rt.row_weight + pairs);
+    rt.slot_expert = rt.count + a.experts;
+    rt.slot_off = rt.slot_expert + most;
+  }
+  // UP waits for the router's kernel and only then lets DOWN start; so the logits are final for DOWN from
+  // its first instruction, and it streams its first weights while UP still runs.
+  if (!DOWN) decode::pdl_wait();
+  decode::pdl_launch_dependents();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < a.stages; ++s) {
+      ptx::mbar_init(full(s), 33);                         // the byte count's arrival and 32 lanes' cp.async
+      ptx::mbar_init(empty(s), kWarps);
+    }
+    sm_abort = 0;
+    ptx::fence_mbar_init();
+  }
+  // ---- this CTA's run.  All items of a call are equally long.
+  const int slots = route(a, rt, reinterpret_cast<float*>(smem), sm_scan, !DOWN && blockIdx.x == 0);
+  const int nk = (a.K + C::kK - 1) / C::kK;                // chunks of one expert's K
+  const int per = DOWN ? slots * nk : nk;                  // chunks of an item
+  const int items = DOWN ? a.jblocks : slots * a.jblocks;
+  const long long total = static_cast<long long>(items) * (per + kItemUnits);
+  const long long want = total / kMinShare;
+  const int runs = want < 1 ? 1 : (want < gridDim.x ? static_cast<int>(want) : static_cast<int>(gridDim.x));
+  const int run = blockIdx.x;
+  if (run >= runs) return;
+  const int share = static_cast<int>(total / runs), extra = static_cast<int>(total - static_cast<long long>(share) * runs);
+  const long long begin = static_cast<long long>(share) * run + (run < extra ? run : extra);
+  const int limit = share + (run < extra ? 1 : 0);
+  auto run_of = [&](long long u) {
+    const long long cut = static_cast<long long>(extra) * (share + 1);
+    return static_cast<int>(u < cut ? u / (share + 1) : extra + (u - cut) / share);
+  };
+  Cursor start;
+  {
+    start.item = static_cast<int>(begin / (per + kItemUnits));
+    const int at = static_cast<int>(begin - static_cast<long long>(start.item) * (per + kItemUnits));
+    start.c = at > kItemUnits ? at - kItemUnits : 0;
+    start.u = at > kItemUnits ? 0 : kItemUnits - at;
+    start.s = DOWN ? start.c / nk : start.item / a.jblocks;
+    start.kc = DOWN ? start.c - start.s * nk : start.c;
+  }
+  if (start.u >= limit) return;                            // no chunk, only an item's extra units
+  auto advance = [&](Cursor& x) {                          // true: a new item begins
+    ++x.u;
+    if (++x.c == per) {
+      x.u += kItemUnits;
+      ++x.item;
+      x.c = x.kc = 0;
+      x.s = DOWN ? 0 : x.item / a.jblocks;
+      return true;
+    }
+    if (++x.kc == nk) {                                    // DOWN: the next expert
+      x.kc = 0;
+      ++x.s;
+    }
+    return false;
+  };
+  // first column (of the packed weight) of warp w's 32, or -1 past the end
+  auto col_of = [&](int item, int w) {
+    if (DOWN) {
+      const int n = item * kCols + 32 * w;
+      return n < a.N ? n : -1;
+    }
+    const int j = (item % a.jblocks) * (kCols / 2) + 32 * (w & 3);
+    return j < a.inter ? (w < 4 ? j : a.inter + j) : -1;
+  };
+
+  if (warp == kWarps) {
+    // ---------------------------------------------------------------- producer
+    const uint64_t policy = ptx::policy_evict_first();     // weights are read once
+    // a chunk's weights, scales and zeros; then its activations
+    auto put_weights = [&](const Cursor& x, int st) {
+      const int expert = rt.slot_expert[x.s], rows = rt.slot_off[x.s + 1] - rt.slot_off[x.s];
+      const uint32_t to = smem_a + st * stage_bytes;
+      const int k0 = x.kc * C::kK, ck = a.K - k0 < C::kK ? a.K - k0 : C::kK;
+      const int col = lane < kWarps ? col_of(x.item, lane) : -1;
+      const unsigned boxes = __popc(__ballot_sync(0xFFFFFFFFu, col >= 0));
+      if (lane == 0) ptx::mbar_arrive_expect_tx(full(st), boxes * (C::kRows * 128) + rows * ck * 2);
+      __syncwarp();
+      if (col >= 0)
+        ptx::tma_load_2d_hint(to + lane * C::kSlot, &tmW, col, expert * (a.units * ROWS) + x.kc * C::kRows, full(st), policy);
+      const int g0 = k0 / a.group, g1 = (k0 + ck - 1) / a.group;
+      const int sc_col = col_of(x.item, lane >> 2);
+      for (int g = g0; g <= g1; ++g) {
+        const long long grow = static_cast<long long>(expert) * a.G + g;
+        if (sc_col >= 0)
+          cp_async16(to + L::scales(a.tokens) + (g - g0) * kCols * 2 + lane * 16, a.scales + grow * a.N + sc_col + 8 * (lane & 3));
+#pragma unroll
+        for (int i = 0; i < (C::kZeroWords + 31) / 32; ++i) {
+          const int w = lane + 32 * i, zc = w < C::kZeroWords ? col_of(x.item, w / BITS) : -1;
+          if (zc >= 0)
+            cp_async4(to + L::zeros(a.tokens, a.gmax) + ((g - g0) * C::kZeroWords + w) * 4,
+                      a.qzeros + grow * a.zwords + zc / 32 * BITS + w % BITS);
+        }
+      }
+    };
+    auto put_acts = [&](const Cursor& x, int st) {
+      const int off = rt.slot_off[x.s], rows = rt.slot_off[x.s + 1] - off;
+      const uint32_t to = smem_a + st * stage_bytes;
+      const int k0 = x.kc * C::kK, ck = a.K - k0 < C::kK ? a.K - k0 : C::kK;
+      if (lane < rows) {
+        const int row = DOWN ? off + lane : rt.row_token[off + lane];
+        bulk_load(to + L::act() + lane * C::kActRow, a.act + static_cast<long long>(row) * a.K + k0, ck * 2, full(st));
+        const float* from = a.act_scale + static_cast<long long>(row) * a.act_runs + k0 / kRun;
+        for (int i = 0; i < C::kRunsOf && k0 + i * kRun < a.K; ++i)
+          cp_async4(to + L::act_scale(a.tokens) + (i * a.tokens + lane) * 4, from + i);
+      }
+      cp_async_arrive(full(st));
+    };
+    Cursor x = start;
+    int issued = 0;
+    // the first chunks; DOWN's weights go out before UP has finished
+    {
+      Cursor y = start;
+      for (; issued < a.stages && x.u < limit; ++issued) {
+        put_weights(x, issued);
+        advance(x);
+      }
+      if (DOWN) decode::pdl_wait();
+      for (int i = 0; i < issued; ++i) {
+        put_acts(y, i);
+        advance(y);
+      }
+    }
+    for (; x.u < limit; ++issued) {
+      const int st = issued % a.stages;
+      if (!wait(empty(st), ((issued / a.stages) & 1) ^ 1, &sm_abort, a.status)) break;
+      put_weights(x, st);
+      put_acts(x, st);
+      advance(x);
+    }
+    // let every copy land before shared memory is released (after a timeout no consumer waits for them)
+    if (sm_abort) {
+      const uint64_t t0 = ptx::globaltimer();
+      for (int i = issued > a.stages ? issued - a.stages : 0; i < issued; ++i)
+        while (!ptx::mbar_try_wait(full(i % a.stages), (i / a.stages) & 1) && ptx::globaltimer() - t0 < 2000000000ull) {}
+    }
+    return;
+  }
+
+  // ------------------------------------------------------------------ consumers
+  const int gq = lane >> 2, tq = lane & 3;
+  const int quad = decode::col_quad(gq), col0 = warp * 32 + quad * 4;   // this thread's 4 columns of the tile
+  float acc[2][NB][4], cg[2][NB][4];
+  auto clear = [](float (&x)[2][NB][4]) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[t][nb][i] = 0.f;
+  };
+  Cursor x = start;
+  int cur = -1, rows = 0, off = 0;
+  int tok[NB][2];
+  float wt[NB][2];
+  auto open_slot = [&]() {
+    cur = x.s;
+    off = rt.slot_off[cur];
+    rows = rt.slot_off[cur + 1] - off;
+    if constexpr (DOWN) {
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int m = 8 * nb + 2 * tq + i;
+          tok[nb][i] = m < rows ? rt.row_token[off + m] : 0;
+          wt[nb][i] = m < rows ? rt.row_weight[off + m] : 0.f;
+        }
+    }
+    clear(acc);
+  };
+  // the finished rows of a slot into the tile: UP stores [row][column], DOWN adds w * y to [token]
+  auto close_slot = [&]() {
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int m = 8 * nb + 2 * tq + (i & 1), c = col0 + 2 * t + (i >> 1);
+          if (m < rows) {
+            if constexpr (DOWN) tile[tok[nb][i & 1] * kCols + c] += wt[nb][i & 1] * acc[t][nb][i];
+            else tile[m * kCols + c] = acc[t][nb][i];
+          }
+        }
+  };
+  auto open_item = [&]() {
+    if constexpr (DOWN) {                                  // this warp's own columns
+      for (int t = 0; t < a.tokens; ++t) tile[t * kCols + warp * 32 + lane] = 0.f;
+      __syncwarp();
+    }
+  };
+
+  // the tile is complete: the layer's output
+  auto finish = [&](int item) {
+    if constexpr (DOWN) {
+      const int n = item * kCols + static_cast<int>(threadIdx.x);
+      if (n < a.N)
+        for (int t = 0; t < a.tokens; ++t) {
+          const float v = tile[t * kCols + threadIdx.x];
+          const long long at = static_cast<long long>(t) * a.N + n;
+          if (a.dtype == 0) static_cast<__half*>(a.out)[at] = __float2half_rn(v);
+          else static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(v);
+        }
+    } else {
+      // one warp per row: 4 of the run's 128 columns per lane
+      const int j0 = (item % a.jblocks) * kRun, j = j0 + 4 * lane;
+      for (int m = warp; m < rows; m += kWarps) {
+        const float4 g = *reinterpret_cast<const float4*>(tile + m * kCols + 4 * lane);
+        const float4 u = *reinterpret_cast<const float4*>(tile + m * kCols + kCols / 2 + 4 * lane);
+        float h[4], top = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float gi = (&g.x)[i];
+          h[i] = j < a.inter ? gi / (1.f + expf(-gi)) * (&u.x)[i] : 0.f;
+          top = fmaxf(top, fabsf(h[i]));
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+        const int e = run_exponent(top);
+        const float inv = pow2(-e);
+        __half* to = a.h + static_cast<long long>(off + m) * a.inter;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (j < a.inter) {
+            const int k = j + i;
+            to[k / P::kPerUnit * P::kPerUnit + pair_pos<BITS>(k % P::kPerUnit)] = __float2half_rn(h[i] * inv);
+          }
+        if (lane == 0) a.h_scale[static_cast<long long>(off + m) * a.h_runs + j0 / kRun] = pow2(e);
+      }
+    }
+  };
+  auto close_item = [&](int item, long long first_chunk) {
+    close_slot();
+    const bool whole = first_chunk >= begin && first_chunk + per <= begin + limit;
+    consumer_sync();
+    if (whole) {
+      finish(item);
+      consumer_sync();                                     // the tile is free again
+      return;
+    }
+    // runs first .. last hold the item; the first leaves its part in its slot 1, the others in slot 0
+    const int first = run_of(first_chunk), last = run_of(first_chunk + per - 1);
+    const int live = DOWN ? a.tokens : rows;
+    const size_t part = static_cast<size_t>(a.tokens) * kCols;
+    auto slot_of = [&](int r) { return a.partials + (static_cast<size_t>(r) * 2 + (r == first ? 1 : 0)) * part; };
+    float* to = slot_of(run);
+    for (int m = 0; m < live; ++m) __stcg(to + m * kCols + threadIdx.x, tile[m * kCols + threadIdx.x]);
+    consumer_sync();
+    if (threadIdx.x == 0) {
+      __threadfence();
+      // wraps to zero at the last arrival, ready for the next call
+      sm_last = atomicInc(a.counters + first, static_cast<unsigned>(last - first)) == static_cast<unsigned>(last - first);
+      __threadfence();
+    }
+    consumer_sync();
+    if (sm_last) {
+      for (int m = 0; m < live; ++m) {
+        float v = 0.f;
+        constexpr int kBatch = 8;
+        for (int c0 = first; c0 <= last; c0 += kBatch) {
+          float p[kBatch];
+#pragma unroll
+          for (int j = 0; j < kBatch; ++j) p[j] = c0 + j <= last ? __ldcg(slot_of(c0 + j) + m * kCols + threadIdx.x) : 0.f;
+#pragma unroll
+          for (int j = 0; j < kBatch; ++j) v += p[j];
+        }
+        tile[m * kCols + threadIdx.x] = v;
+      }
+      consumer_sync();
+      finish(item);
+    }
+    consumer_sync();
+  };
+
+  long long first_chunk = begin + start.u - start.c;       // of the current item, on the line
+  open_item();
+  for (int n = 0; x.u < limit; ++n) {
+    const int st = n % a.stages;
+    if (x.s != cur) open_slot();
+    const bool ok = __all_sync(0xFFFFFFFFu, wait(full(st), (n / a.stages) & 1, &sm_abort, a.status));
+    if (ok) {
+      const uint8_t* base = smem + st * stage_bytes;
+      const uint8_t* slot = base + warp * C::kSlot;
+      const uint8_t* acts = base + L::act();
+      const float* act_scale = reinterpret_cast<const float*>(base + L::act_scale(a.tokens));
+      const __half* scales = reinterpret_cast<const __half*>(base + L::scales(a.tokens));
+      const uint32_t* zeros = reinterpret_cast<const uint32_t*>(base + L::zeros(a.tokens, a.gmax));
+      const int k0 = x.kc * C::kK;
+      const int tiles = (a.K - k0 < C::kK ? a.K - k0 : C::kK) / C::kTileK;
+      int g = k0 / a.group;
+      const int g0 = g;
+      int g_end = (g + 1) * a.group;
+      uint32_t zk[4][DP::kConsts];
+      float gs[4];
+      auto load_group = [&]() {
+        const uint2 s = *reinterpret_cast<const uint2*>(scales + (g - g0) * kCols + col0);
+        gs[0] = __half2float(__ushort_as_half(lo16(s.x)));
+        gs[1] = __half2float(__ushort_as_half(hi16(s.x)));
+        gs[2] = __half2float(__ushort_as_half(lo16(s.y)));
+        gs[3] = __half2float(__ushort_as_half(hi16(s.y)));
+        const uint32_t* zw = zeros + (g - g0) * C::kZeroWords + warp * BITS;
+        const int bit = BITS * quad * 4;
+        uint32_t zf = zw[bit >> 5] >> (bit & 31);
+        if (BITS == 3 && (bit & 31) + 12 > 32) zf = __funnelshift_r(zw[bit >> 5], zw[(bit >> 5) + 1], bit & 31);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          DP::consts(static_cast<int>((zf >> (BITS * c)) & P::kMask) + a.zero_offset, zk[c]);
+      };
+      auto fold = [&](int run_i) {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          if (8 * nb < rows) {
+            float s[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int m = 8 * nb + 2 * tq + i;
+              s[i] = act_scale[run_i * a.tokens + (m < rows ? m : rows - 1)];
+            }
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) acc[t][nb][i] = fmaf(gs[2 * t + (i >> 1)], s[i & 1] * cg[t][nb][i], acc[t][nb][i]);
+          }
+        }
+        clear(cg);
+      };
+      int aoff[NB];
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        const int m = 8 * nb + gq;
+        aoff[nb] = (m < rows ? m : rows - 1) * C::kActRow + tq * (NP * 4);
+      }
+      clear(cg);
+      load_group();
+#pragma unroll
+      for (int l = 0; l < C::kTiles; ++l) {
+        if (l < tiles) {
+          uint4 w[ROWS];
+#pragma unroll
+          for (int r = 0; r < ROWS; ++r) {
+            const int row = (l * 4 + tq) * ROWS + r;
+            w[r] = *reinterpret_cast<const uint4*>(slot + row * 128 + ((quad ^ (row & 7)) << 4));
+          }
+          uint32_t d[4][NP];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            if constexpr (BITS == 3) DP::run3((&w[0].x)[c], (&w[1].x)[c], (&w[2].x)[c], zk[c], d[c]);
+            else DP::run((&w[0].x)[c], zk[c], d[c]);
+          }
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            if (8 * nb < rows) {
+              uint32_t b[NP];
+              const uint8_t* src = acts + aoff[nb] + l * (NP * 16);
+              if constexpr (NP % 4 == 0) {
+#pragma unroll
+                for (int i = 0; i < NP / 4; ++i) {
+                  const uint4 v = reinterpret_cast<const uint4*>(src)[i];
+                  b[4 * i] = v.x; b[4 * i + 1] = v.y; b[4 * i + 2] = v.z; b[4 * i + 3] = v.w;
+                }
+              } else {
+                const uint2 v = *reinterpret_cast<const uint2*>(src);
+                b[0] = v.x; b[1] = v.y;
+              }
+#pragma unroll
+              for (int j = 0; j < NP / 2; ++j)
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+                  decode::mma16816(cg[t][nb], d[2 * t][2 * j], d[2 * t + 1][2 * j], d[2 * t][2 * j + 1], d[2 * t + 1][2 * j + 1],
+                                   b[2 * j], b[2 * j + 1], __half());
+            }
+          }
+          // a group, a run of activations or the chunk ends here
+          const int k = k0 + (l + 1) * C::kTileK;
+          const bool group_end = k == g_end, run_end = k % kRun == 0;
+          if (group_end || run_end || l + 1 == tiles) {
+            fold(l * C::kTileK / kRun);
+            if (group_end && l + 1 < tiles) {
+              ++g;
+              g_end += a.group;
+              load_group();
+            }
+          }
+        }
+      }
+    }
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(empty(st));
+    // to the next chunk
+    const int item = x.item;
+    const bool next = advance(x);
+    if (next || x.u >= limit) {
+      close_item(item, first_chunk);
+      first_chunk += per + kItemUnits;
+      cur = -1;
+      if (x.u < limit) open_item();
+    } else if (x.s != cur) {
+      close_slot();
+    }
+  }
+}
+
+template <int BITS, int NB, bool DOWN>
+cudaError_t launch_experts(Args a, const int32_t* qweight, int experts, cudaStream_t stream) {
+  using C = Chunk<BITS>;
+  using L = Layout<BITS>;
+  auto kern = k_experts<BITS, NB, DOWN>;
+  const DeviceInfo& dev = device_info();
+  a.units = a.K / Pack<BITS>::kPerUnit;
+  a.zwords = a.N / 32 * BITS;
+  a.gmax = (C::kK - 1) / a.group + 2;
+  if (a.group % C::kK == 0) a.gmax = 1;
+  else if (C::kK % a.group == 0) a.gmax = C::kK / a.group;
+  a.stage_bytes = L::stage(a.tokens, a.gmax);
+  const int pairs = a.tokens * a.topk;
+  // two CTAs on an SM where their rings hold three chunks each, else one
+  int per_sm = NB == 4 ? 1 : 2;
+  auto fit = [&](int ctas) {
+    const int budget = ctas == 2 ? 233472 / 2 - 1024 - 256 : 227 * 1024 - 256;   // less the static part
+    return (budget - L::fixed(a.tokens, pairs, experts)) / (a.stage_bytes + 16);
+  };
+  a.stages = fit(per_sm);
+  if (per_sm == 2 && a.stages < 3) a.stages = fit(per_sm = 1);
+  if (a.stages > kMaxStages) a.stages = kMaxStages;
+  // the router's scratch lies over the ring
+  if (a.stages < 2 || a.stages * a.stage_bytes < kThreads / 32 * experts * 4) return cudaErrorInvalidConfiguration;
+  const int smem = L::fixed(a.tokens, pairs, experts) + a.stages * (a.stage_bytes + 16);
+  static std::atomic<unsigned long long> opted_in{0};       // per device
+  if (dev.device >= 64 || !(opted_in.load(std::memory_order_relaxed) & (1ull << dev.device))) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024 - 256);
+    if (e != cudaSuccess) return e;
+    if (dev.device < 64) opted_in.fetch_or(1ull << dev.device, std::memory_order_relaxed);
+  }
+  CUtensorMap tmW = {};
+  const uint64_t dims[2] = {static_cast<uint64_t>(a.N), static_cast<uint64_t>(a.units) * Pack<BITS>::kRowsPerUnit * experts};
+  const uint64_t strides[1] = {static_cast<uint64_t>(a.N) * 4};
+  const uint32_t box[2] = {32, static_cast<uint32_t>(C::kRows)};
+  const uint32_t estr[2] = {1, 1};
+  if (!encode_tensor_map(&tmW, CU_TENSOR_MAP_DATA_TYPE_INT32, const_cast<int32_t*>(qweight), dims, strides, box, estr,
+                         CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
+  int grid = dev.sm_count * per_sm;
+  if (grid > kMaxRuns) grid = kMaxRuns;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, tmW, a);
+}
+
+template <int BITS, bool DOWN>
+cudaError_t launch_blocks(const Args& a, const int32_t* qweight, int experts, cudaStream_t stream) {
+  if (a.tokens <= 8) return launch_experts<BITS, 1, DOWN>(a, qweight, experts, stream);
+  if (a.tokens <= 16) return launch_experts<BITS, 2, DOWN>(a, qweight, experts, stream);
+  return launch_experts<BITS, 4, DOWN>(a, qweight, experts, stream);
+}
+
+template <int BITS>
+cudaError_t launch_bits(const Args& up, const int32_t* up_qweight, const Args& down, const int32_t* down_qweight, int experts,
+                        cudaStream_t stream) {
+  const cudaError_t e = launch_blocks<BITS, false>(up, up_qweight, experts, stream);
+  return e != cudaSuccess ? e : launch_blocks<BITS, true>(down, down_qweight, experts, stream);
+}
+
+}  // namespace moe
+}  // namespace gptq

@@ -1,0 +1,10 @@
+// moe_b4.cu -- 4-bit instantiations of the expert products, in their own translation unit so that
+// they compile in parallel with the rest.
+#include "moe.cuh"
+
+namespace gptq {
+cudaError_t launch_moe_b4(const moe::Args& up, const int32_t* up_qweight, const moe::Args& down,
+                          const int32_t* down_qweight, int experts, cudaStream_t stream) {
+  return moe::launch_bits<4>(up, up_qweight, down, down_qweight, experts, stream);
+}
+}  // namespace gptq

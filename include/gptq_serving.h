@@ -10,10 +10,10 @@
  * sets a bit in the status word read by gptq_get_device_status().  Every input is read only after
  * the kernels issued before the call on `stream` have completed.
  *
- * Workspaces of this header start with a control block that has to be zero before the workspace's
- * first use (cudaMemset once, or a zeroed allocation); every call that runs leaves it zero again, so
- * one workspace serves any number of calls of any shape that it is large enough for, one after the
- * other on one stream.  Calls that overlap on the GPU need workspaces of their own.
+ * Workspaces: one serves any number of calls of any shape that it is large enough for, one after the
+ * other on one stream; calls that overlap on the GPU need workspaces of their own.  The workspace of
+ * gptq_paged_attention starts with a control block that has to be zero before its first use
+ * (cudaMemset once, or a zeroed allocation); every call that runs leaves it zero again.
  */
 #ifndef GPTQ_SERVING_H
 #define GPTQ_SERVING_H
@@ -85,7 +85,7 @@ int gptq_paged_attention(const void* q, int batch, int heads, int dtype, void* k
  * multiple of 128 / bits, 128 for 3-bit; with -1 so are hidden and inter), topk <= experts <= 1024,
  * topk <= 16, tokens <= 32; otherwise GPTQ_ERR_SHAPE.  A token whose router logits hold a NaN gets
  * NaN.  workspace: gptq_moe_workspace_size() bytes (0 for a shape outside the limits), 16-byte
- * aligned, control block zero (above).  tokens == 0 is a no-op.
+ * aligned, holding anything.  tokens == 0 is a no-op.
  */
 size_t gptq_moe_workspace_size(int tokens, int hidden, int inter, int experts, int topk);
 int gptq_moe(const void* x, int tokens, int hidden, int inter, int dtype, const void* router, int experts,
