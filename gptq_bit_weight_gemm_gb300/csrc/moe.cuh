@@ -379,66 +379,134 @@ __global__ void __launch_bounds__(kThreads, (NB == 4 ? 1 : 2)) k_experts(const _
   if (warp == kWarps) {
     // ---------------------------------------------------------------- producer
     const uint64_t policy = ptx::policy_evict_first();     // weights are read once
-    // a chunk's weights, scales and zeros; then its activations
-    auto put_weights = [&](const Cursor& x, int st) {
-      const int expert = rt.slot_expert[x.s], rows = rt.slot_off[x.s + 1] - rt.slot_off[x.s];
-      const uint32_t to = smem_a + st * stage_bytes;
-      const int k0 = x.kc * C::kK, ck = a.K - k0 < C::kK ? a.K - k0 : C::kK;
-      const int col = lane < kWarps ? col_of(x.item, lane) : -1;
-      const unsigned boxes = __popc(__ballot_sync(0xFFFFFFFFu, col >= 0));
-      if (lane == 0) ptx::mbar_arrive_expect_tx(full(st), boxes * (C::kRows * 128) + rows * ck * 2);
-      __syncwarp();
-      if (col >= 0)
-        ptx::tma_load_2d_hint(to + lane * C::kSlot, &tmW, col, expert * (a.units * ROWS) + x.kc * C::kRows, full(st), policy);
-      const int g0 = k0 / a.group, g1 = (k0 + ck - 1) / a.group;
-      const int sc_col = col_of(x.item, lane >> 2);
-      for (int g = g0; g <= g1; ++g) {
-        const long long grow = static_cast<long long>(expert) * a.G + g;
-        if (sc_col >= 0)
-          cp_async16(to + L::scales(a.tokens) + (g - g0) * kCols * 2 + lane * 16, a.scales + grow * a.N + sc_col + 8 * (lane & 3));
+    // Everything that changes with the item or the expert only is kept, and a chunk moves it on: with
+    // the divisions in here the one producer warp took longer over a chunk than the consumers did
+    // (one token, 4096 x 14336: 85 us).
+    struct Put {
+      Cursor x;
+      int item, slot, rows, w_row, act_row, g, g_at;       // g: the chunk's first group, g_at: k of the chunk in it
+      int col, sc_col, zc[2];
+      unsigned box_bytes;
+      const __half* sc;
+      const int32_t* zr[2];
+      const __half* act;
+      const float* act_sc;
+    };
+    auto place = [&](Put& p) {                             // after a new item or expert
+      if (p.item != p.x.item) {
+        p.item = p.x.item;
+        p.col = lane < kWarps ? col_of(p.item, lane) : -1;
+        p.sc_col = col_of(p.item, lane >> 2);
 #pragma unroll
-        for (int i = 0; i < (C::kZeroWords + 31) / 32; ++i) {
-          const int w = lane + 32 * i, zc = w < C::kZeroWords ? col_of(x.item, w / BITS) : -1;
-          if (zc >= 0)
-            cp_async4(to + L::zeros(a.tokens, a.gmax) + ((g - g0) * C::kZeroWords + w) * 4,
-                      a.qzeros + grow * a.zwords + zc / 32 * BITS + w % BITS);
+        for (int i = 0; i < 2; ++i) {
+          const int w = lane + 32 * i;
+          p.zc[i] = w < C::kZeroWords ? col_of(p.item, w / BITS) : -1;
         }
+        p.box_bytes = __popc(__ballot_sync(0xFFFFFFFFu, p.col >= 0)) * (C::kRows * 128);
+      }
+      p.slot = p.x.s;
+      const int expert = rt.slot_expert[p.slot], off = rt.slot_off[p.slot];
+      p.rows = rt.slot_off[p.slot + 1] - off;
+      const int k0 = p.x.kc * C::kK;
+      p.g = k0 / a.group;
+      p.g_at = k0 - p.g * a.group;
+      p.w_row = expert * (a.units * ROWS) + p.x.kc * C::kRows;
+      const long long grow = static_cast<long long>(expert) * a.G + p.g;
+      p.sc = a.scales + grow * a.N + p.sc_col + 8 * (lane & 3);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) p.zr[i] = a.qzeros + grow * a.zwords + p.zc[i] / 32 * BITS + (lane + 32 * i) % BITS;
+      const int row = lane < p.rows ? (DOWN ? off + lane : rt.row_token[off + lane]) : 0;
+      p.act = a.act + static_cast<long long>(row) * a.K + k0;
+      p.act_sc = a.act_scale + static_cast<long long>(row) * a.act_runs + k0 / kRun;
+    };
+    auto step = [&](Put& p) {                              // to the next chunk
+      const int item = p.x.item, slot = p.x.s;
+      advance(p.x);
+      if (p.x.item != item || p.x.s != slot) {
+        if (p.x.u < limit) place(p);
+        return;
+      }
+      p.w_row += C::kRows;
+      p.act += C::kK;
+      p.act_sc += C::kK >= kRun ? C::kRunsOf : 1 - (p.x.kc & 1);
+      p.g_at += C::kK;
+      while (p.g_at >= a.group) {
+        p.g_at -= a.group;
+        ++p.g;
+        p.sc += a.N;
+        p.zr[0] += a.zwords;
+        p.zr[1] += a.zwords;
       }
     };
-    auto put_acts = [&](const Cursor& x, int st) {
-      const int off = rt.slot_off[x.s], rows = rt.slot_off[x.s + 1] - off;
+    static_assert(C::kK % kRun == 0 || 2 * C::kK == kRun, "a chunk is whole runs or half of one");
+    // a chunk's weights, scales and zeros; then its activations
+    auto put_weights = [&](const Put& p, int st) {
       const uint32_t to = smem_a + st * stage_bytes;
-      const int k0 = x.kc * C::kK, ck = a.K - k0 < C::kK ? a.K - k0 : C::kK;
-      if (lane < rows) {
-        const int row = DOWN ? off + lane : rt.row_token[off + lane];
-        bulk_load(to + L::act() + lane * C::kActRow, a.act + static_cast<long long>(row) * a.K + k0, ck * 2, full(st));
-        const float* from = a.act_scale + static_cast<long long>(row) * a.act_runs + k0 / kRun;
-        for (int i = 0; i < C::kRunsOf && k0 + i * kRun < a.K; ++i)
-          cp_async4(to + L::act_scale(a.tokens) + (i * a.tokens + lane) * 4, from + i);
+      const int left = a.K - p.x.kc * C::kK, ck = left < C::kK ? left : C::kK;
+      if (lane == 0) ptx::mbar_arrive_expect_tx(full(st), p.box_bytes + p.rows * ck * 2);
+      __syncwarp();
+      if (p.col >= 0) ptx::tma_load_2d_hint(to + lane * C::kSlot, &tmW, p.col, p.w_row, full(st), policy);
+      const __half* sc = p.sc;
+      const int32_t* z0 = p.zr[0];
+      const int32_t* z1 = p.zr[1];
+      uint32_t sc_to = to + L::scales(a.tokens) + lane * 16, z_to = to + L::zeros(a.tokens, a.gmax) + lane * 4;
+      for (int at = -p.g_at; at < ck; at += a.group) {      // the groups that the chunk touches
+        if (p.sc_col >= 0) cp_async16(sc_to, sc);
+        if (p.zc[0] >= 0) cp_async4(z_to, z0);
+        if (C::kZeroWords > 32 && p.zc[1] >= 0) cp_async4(z_to + 128, z1);
+        sc += a.N;
+        z0 += a.zwords;
+        z1 += a.zwords;
+        sc_to += kCols * 2;
+        z_to += C::kZeroWords * 4;
+      }
+    };
+    auto put_acts = [&](const Put& p, int st) {
+      const uint32_t to = smem_a + st * stage_bytes;
+      const int left = a.K - p.x.kc * C::kK, ck = left < C::kK ? left : C::kK;
+      if (lane < p.rows) {
+        bulk_load(to + L::act() + lane * C::kActRow, p.act, ck * 2, full(st));
+#pragma unroll
+        for (int i = 0; i < C::kRunsOf; ++i)
+          if (i * kRun < ck) cp_async4(to + L::act_scale(a.tokens) + (i * a.tokens + lane) * 4, p.act_sc + i);
       }
       cp_async_arrive(full(st));
     };
-    Cursor x = start;
+    Put p = {};
+    p.x = start;
+    p.item = -1;
+    place(p);
     int issued = 0;
     // the first chunks; DOWN's weights go out before UP has finished
-    {
-      Cursor y = start;
-      for (; issued < a.stages && x.u < limit; ++issued) {
-        put_weights(x, issued);
-        advance(x);
+    if (DOWN) {
+      Put y = p;
+      for (; issued < a.stages && p.x.u < limit; ++issued) {
+        put_weights(p, issued);
+        step(p);
       }
-      if (DOWN) decode::pdl_wait();
+      decode::pdl_wait();
       for (int i = 0; i < issued; ++i) {
         put_acts(y, i);
-        advance(y);
+        step(y);
+      }
+    } else {
+      for (; issued < a.stages && p.x.u < limit; ++issued) {
+        put_weights(p, issued);
+        put_acts(p, issued);
+        step(p);
       }
     }
-    for (; x.u < limit; ++issued) {
-      const int st = issued % a.stages;
-      if (!wait(empty(st), ((issued / a.stages) & 1) ^ 1, &sm_abort, a.status)) break;
-      put_weights(x, st);
-      put_acts(x, st);
-      advance(x);
+    int st = 0;
+    unsigned round = 0;                                    // parity of the stage's last emptying
+    for (; p.x.u < limit; ++issued) {
+      if (!wait(empty(st), round, &sm_abort, a.status)) break;
+      put_weights(p, st);
+      put_acts(p, st);
+      step(p);
+      if (++st == a.stages) {
+        st = 0;
+        round ^= 1;
+      }
     }
     // let every copy land before shared memory is released (after a timeout no consumer waits for them)
     if (sm_abort) {
@@ -587,10 +655,14 @@ __global__ void __launch_bounds__(kThreads, (NB == 4 ? 1 : 2)) k_experts(const _
 
   long long first_chunk = begin + start.u - start.c;       // of the current item, on the line
   open_item();
-  for (int n = 0; x.u < limit; ++n) {
-    const int st = n % a.stages;
-    if (x.s != cur) open_slot();
-    const bool ok = __all_sync(0xFFFFFFFFu, wait(full(st), (n / a.stages) & 1, &sm_abort, a.status));
+  int st = 0, g_at = 0;                                    // g_at: k of the chunk within its first group
+  unsigned round = 0;
+  while (x.u < limit) {
+    if (x.s != cur) {
+      open_slot();
+      g_at = x.kc * C::kK % a.group;
+    }
+    const bool ok = __all_sync(0xFFFFFFFFu, wait(full(st), round, &sm_abort, a.status));
     if (ok) {
       const uint8_t* base = smem + st * stage_bytes;
       const uint8_t* slot = base + warp * C::kSlot;
@@ -600,18 +672,17 @@ __global__ void __launch_bounds__(kThreads, (NB == 4 ? 1 : 2)) k_experts(const _
       const uint32_t* zeros = reinterpret_cast<const uint32_t*>(base + L::zeros(a.tokens, a.gmax));
       const int k0 = x.kc * C::kK;
       const int tiles = (a.K - k0 < C::kK ? a.K - k0 : C::kK) / C::kTileK;
-      int g = k0 / a.group;
-      const int g0 = g;
-      int g_end = (g + 1) * a.group;
+      int g = 0;                                           // of the chunk's groups
+      int g_end = k0 - g_at + a.group;
       uint32_t zk[4][DP::kConsts];
       float gs[4];
       auto load_group = [&]() {
-        const uint2 s = *reinterpret_cast<const uint2*>(scales + (g - g0) * kCols + col0);
+        const uint2 s = *reinterpret_cast<const uint2*>(scales + g * kCols + col0);
         gs[0] = __half2float(__ushort_as_half(lo16(s.x)));
         gs[1] = __half2float(__ushort_as_half(hi16(s.x)));
         gs[2] = __half2float(__ushort_as_half(lo16(s.y)));
         gs[3] = __half2float(__ushort_as_half(hi16(s.y)));
-        const uint32_t* zw = zeros + (g - g0) * C::kZeroWords + warp * BITS;
+        const uint32_t* zw = zeros + g * C::kZeroWords + warp * BITS;
         const int bit = BITS * quad * 4;
         uint32_t zf = zw[bit >> 5] >> (bit & 31);
         if (BITS == 3 && (bit & 31) + 12 > 32) zf = __funnelshift_r(zw[bit >> 5], zw[(bit >> 5) + 1], bit & 31);
@@ -699,6 +770,12 @@ __global__ void __launch_bounds__(kThreads, (NB == 4 ? 1 : 2)) k_experts(const _
     }
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(empty(st));
+    if (++st == a.stages) {
+      st = 0;
+      round ^= 1;
+    }
+    g_at += C::kK;
+    while (g_at >= a.group) g_at -= a.group;
     // to the next chunk
     const int item = x.item;
     const bool next = advance(x);
