@@ -1,9 +1,10 @@
 // moe.cu -- the mixture-of-experts layer for a few tokens (gptq_moe): the router's kernel, the
 // workspace and the launches of the expert products (moe.cuh).
 //
-// The router's kernel: every warp takes one expert and four tokens, sums their products in fp32 and
-// writes the logits; the activations are rewritten on the side as the expert products read them
-// (fp16 pairs times a power of two per 128), and the arrival counters of the expert products are zeroed.
+// The router's kernel: a CTA takes one expert and four tokens, its warps a share of hidden each, and
+// writes their logits, summed in fp32 (a warp alone for all of hidden took 13 us at one token); further
+// CTAs rewrite the activations as the expert products read them (store_run) and zero the arrival
+// counters of the expert products.
 #include "gptq_device.cuh"
 #include "gptq_internal.h"
 #include "moe.cuh"
@@ -11,31 +12,35 @@
 
 namespace gptq {
 
-cudaError_t launch_moe_b2(const moe::Args&, const int32_t*, const moe::Args&, const int32_t*, int, cudaStream_t);
-cudaError_t launch_moe_b3(const moe::Args&, const int32_t*, const moe::Args&, const int32_t*, int, cudaStream_t);
-cudaError_t launch_moe_b4(const moe::Args&, const int32_t*, const moe::Args&, const int32_t*, int, cudaStream_t);
-cudaError_t launch_moe_b8(const moe::Args&, const int32_t*, const moe::Args&, const int32_t*, int, cudaStream_t);
+cudaError_t launch_moe_b2(const moe::Args&, const int32_t*, const moe::Args&, const int32_t*, int, int*, cudaStream_t);
+cudaError_t launch_moe_b3(const moe::Args&, const int32_t*, const moe::Args&, const int32_t*, int, int*, cudaStream_t);
+cudaError_t launch_moe_b4(const moe::Args&, const int32_t*, const moe::Args&, const int32_t*, int, int*, cudaStream_t);
+cudaError_t launch_moe_b8(const moe::Args&, const int32_t*, const moe::Args&, const int32_t*, int, int*, cudaStream_t);
 
 namespace moe {
 namespace {
 
 constexpr int kRouteWarps = 8, kRouteTokens = 4;
-constexpr size_t kCounterBytes = 4096;   // UP's and DOWN's runs
-static_assert(2 * kMaxRuns * 4 <= kCounterBytes, "counters");
+constexpr size_t kCounterBytes = 4096;   // UP's runs
+static_assert(kMaxRuns * 4 <= kCounterBytes, "counters");
 
 struct Space {
-  size_t logits, act, act_scale, h, h_scale, partials, total;
+  size_t slots, logits, act, act_scale, act_sum, h, h_scale, h_sum, partials, total;
 };
 Space space(int tokens, int hidden, int inter, int experts, int topk) {
   auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
   const size_t rows = static_cast<size_t>(tokens) * topk;
   Space s;
-  s.logits = kCounterBytes;
+  s.slots = kCounterBytes;
+  s.logits = s.slots + 256;
   s.act = s.logits + up(static_cast<size_t>(tokens) * experts * 4);
   s.act_scale = s.act + up(static_cast<size_t>(tokens) * hidden * 2);
-  s.h = s.act_scale + up(static_cast<size_t>(tokens) * ((hidden + kRun - 1) / kRun) * 4);
+  // sums per k-tile: 16 k values at least
+  s.act_sum = s.act_scale + up(static_cast<size_t>(tokens) * ((hidden + kRun - 1) / kRun) * 4);
+  s.h = s.act_sum + up(static_cast<size_t>(tokens) * (hidden / 16) * 4);
   s.h_scale = s.h + up(rows * inter * 2);
-  s.partials = s.h_scale + up(rows * ((inter + kRun - 1) / kRun) * 4);
+  s.h_sum = s.h_scale + up(rows * ((inter + kRun - 1) / kRun) * 4);
+  s.partials = s.h_sum + up(rows * (inter / 16) * 4);
   s.total = s.partials + static_cast<size_t>(kMaxRuns) * 2 * tokens * kCols * 4;
   return s;
 }
@@ -47,72 +52,77 @@ struct RouteArgs {
   float* logits;
   __half* act;
   float* act_scale;
+  float* act_sum;
   unsigned* counters;
 };
 
-template <typename T, int BITS>
-__device__ void pack_run(const RouteArgs& a, int item, int lane) {
-  const int runs = (a.hidden + kRun - 1) / kRun, t = item / runs, j0 = item % runs * kRun, j = j0 + 4 * lane;
-  const bool in = j < a.hidden;
-  float v[4] = {};
-  if (in) {
-    const uint2 w = __ldg(reinterpret_cast<const uint2*>(static_cast<const T*>(a.x) + static_cast<long long>(t) * a.hidden + j));
-    v[0] = F16Traits<T>::to_f32(F16Traits<T>::from_bits(lo16(w.x)));
-    v[1] = F16Traits<T>::to_f32(F16Traits<T>::from_bits(hi16(w.x)));
-    v[2] = F16Traits<T>::to_f32(F16Traits<T>::from_bits(lo16(w.y)));
-    v[3] = F16Traits<T>::to_f32(F16Traits<T>::from_bits(hi16(w.y)));
+template <typename T>
+__device__ __forceinline__ void unpack8(const uint4& w, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = F16Traits<T>::to_f32(F16Traits<T>::from_bits(lo16((&w.x)[i])));
+    v[2 * i + 1] = F16Traits<T>::to_f32(F16Traits<T>::from_bits(hi16((&w.x)[i])));
   }
-  float top = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
-#pragma unroll
-  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-  const int e = run_exponent(top);
-  const float inv = pow2(-e);
-  __half* to = a.act + static_cast<long long>(t) * a.hidden;
-  constexpr int per = Pack<BITS>::kPerUnit;
-  if (in)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) to[(j + i) / per * per + pair_pos<BITS>((j + i) % per)] = __float2half_rn(v[i] * inv);
-  if (lane == 0) a.act_scale[static_cast<long long>(t) * runs + j0 / kRun] = pow2(e);
 }
 
 template <typename T, int BITS>
 __global__ void __launch_bounds__(kRouteWarps * 32) k_route(const RouteArgs a) {
+  __shared__ float sm[kRouteWarps][kRouteTokens];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int gw = blockIdx.x * kRouteWarps + warp, nw = gridDim.x * kRouteWarps;
   decode::pdl_wait();
   decode::pdl_launch_dependents();
-
-  for (int i = blockIdx.x * kRouteWarps * 32 + threadIdx.x; i < 2 * kMaxRuns; i += gridDim.x * kRouteWarps * 32) a.counters[i] = 0u;
-  const int tblocks = (a.tokens + kRouteTokens - 1) / kRouteTokens;
-  for (int i = gw; i < a.experts * tblocks; i += nw) {
-    const int e = i / tblocks, t0 = i % tblocks * kRouteTokens;
+  const int tblocks = (a.tokens + kRouteTokens - 1) / kRouteTokens, units = a.experts * tblocks;
+  if (static_cast<int>(blockIdx.x) < units) {
+    const int e = blockIdx.x / tblocks, t0 = blockIdx.x % tblocks * kRouteTokens;
     const T* r = static_cast<const T*>(a.router) + static_cast<long long>(e) * a.hidden;
     float s[kRouteTokens] = {};
-#pragma unroll 2
-    for (int k = lane * 8; k < a.hidden; k += 256) {
-      const uint4 rv = __ldg(reinterpret_cast<const uint4*>(r + k));
+    for (int k = threadIdx.x * 8; k < a.hidden; k += kRouteWarps * 256) {
+      float rv[8], xv[8];
+      unpack8<T>(__ldg(reinterpret_cast<const uint4*>(r + k)), rv);
+      uint4 x[kRouteTokens];
 #pragma unroll
       for (int j = 0; j < kRouteTokens; ++j) {
         const int t = t0 + j < a.tokens ? t0 + j : a.tokens - 1;
-        const uint4 xv = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(a.x) + static_cast<long long>(t) * a.hidden + k));
+        x[j] = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(a.x) + static_cast<long long>(t) * a.hidden + k));
+      }
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const uint32_t p = (&xv.x)[w], q = (&rv.x)[w];
-          s[j] = fmaf(F16Traits<T>::to_f32(F16Traits<T>::from_bits(lo16(p))), F16Traits<T>::to_f32(F16Traits<T>::from_bits(lo16(q))), s[j]);
-          s[j] = fmaf(F16Traits<T>::to_f32(F16Traits<T>::from_bits(hi16(p))), F16Traits<T>::to_f32(F16Traits<T>::from_bits(hi16(q))), s[j]);
-        }
+      for (int j = 0; j < kRouteTokens; ++j) {
+        unpack8<T>(x[j], xv);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[j] = fmaf(xv[i], rv[i], s[j]);
       }
     }
 #pragma unroll
     for (int j = 0; j < kRouteTokens; ++j) {
 #pragma unroll
       for (int o = 16; o; o >>= 1) s[j] += __shfl_xor_sync(0xFFFFFFFFu, s[j], o);
-      if (lane == 0 && t0 + j < a.tokens) a.logits[(t0 + j) * a.experts + e] = s[j];
+      if (lane == 0) sm[warp][j] = s[j];
     }
+    __syncthreads();
+    if (threadIdx.x < kRouteTokens && t0 + static_cast<int>(threadIdx.x) < a.tokens) {
+      float v = 0.f;
+#pragma unroll
+      for (int w = 0; w < kRouteWarps; ++w) v += sm[w][threadIdx.x];
+      a.logits[(t0 + threadIdx.x) * a.experts + e] = v;
+    }
+    return;
   }
-  const int runs = (a.hidden + kRun - 1) / kRun;
-  for (int i = nw - 1 - gw; i < a.tokens * runs; i += nw) pack_run<T, BITS>(a, i, lane);
-
+  const int runs = (a.hidden + kRun - 1) / kRun, item = (static_cast<int>(blockIdx.x) - units) * kRouteWarps + warp;
+  for (int i = (static_cast<int>(blockIdx.x) - units) * kRouteWarps * 32 + threadIdx.x; i < kMaxRuns; i += (gridDim.x - units) * kRouteWarps * 32)
+    a.counters[i] = 0u;
+  if (item >= a.tokens * runs) return;
+  const int t = item / runs, j0 = item % runs * kRun, j = j0 + 4 * lane;
+  float v[4] = {};
+  if (j < a.hidden) {
+    const uint2 w = __ldg(reinterpret_cast<const uint2*>(static_cast<const T*>(a.x) + static_cast<long long>(t) * a.hidden + j));
+    v[0] = F16Traits<T>::to_f32(F16Traits<T>::from_bits(lo16(w.x)));
+    v[1] = F16Traits<T>::to_f32(F16Traits<T>::from_bits(hi16(w.x)));
+    v[2] = F16Traits<T>::to_f32(F16Traits<T>::from_bits(lo16(w.y)));
+    v[3] = F16Traits<T>::to_f32(F16Traits<T>::from_bits(hi16(w.y)));
+  }
+  constexpr int tile = 4 * Pack<BITS>::kPerUnit;
+  store_run<BITS>(v, j0, a.hidden, a.act + static_cast<long long>(t) * a.hidden, a.act_scale + static_cast<long long>(t) * runs + j0 / kRun,
+                  a.act_sum + static_cast<long long>(t) * (a.hidden / tile) + j0 / tile);
 }
 
 template <typename T>
@@ -154,12 +164,10 @@ cudaError_t launch_moe(const MoeProblem& p, cudaStream_t stream) {
   ra.act = reinterpret_cast<__half*>(ws + s.act);
   ra.act_scale = reinterpret_cast<float*>(ws + s.act_scale);
   ra.counters = counters;
+  ra.act_sum = reinterpret_cast<float*>(ws + s.act_sum);
   const int tblocks = (p.tokens + moe::kRouteTokens - 1) / moe::kRouteTokens;
   const int runs = (p.hidden + kRun - 1) / kRun;
-  int work = p.experts * tblocks;
-  if (p.tokens * runs / 2 > work) work = p.tokens * runs / 2;
-  int grid = (work + moe::kRouteWarps - 1) / moe::kRouteWarps;
-  if (grid > device_info().sm_count) grid = device_info().sm_count;
+  const int grid = p.experts * tblocks + (p.tokens * runs + moe::kRouteWarps - 1) / moe::kRouteWarps;
   cudaError_t e = p.dtype == 0 ? moe::launch_route<__half>(ra, p.bits, grid, stream)
                                : moe::launch_route<__nv_bfloat16>(ra, p.bits, grid, stream);
   if (e != cudaSuccess) return e;
@@ -172,11 +180,12 @@ cudaError_t launch_moe(const MoeProblem& p, cudaStream_t stream) {
   up.experts = p.experts; up.topk = p.topk; up.renormalize = p.renormalize;
   up.logits = ra.logits;
   up.ids = p.ids; up.weights = p.weights;
-  up.act = ra.act; up.act_scale = ra.act_scale; up.act_runs = runs;
+  up.act = ra.act; up.act_scale = ra.act_scale; up.act_sum = ra.act_sum; up.act_runs = runs;
   up.jblocks = (p.inter + moe::kCols / 2 - 1) / (moe::kCols / 2);
   up.inter = p.inter;
   up.h = reinterpret_cast<__half*>(ws + s.h);
   up.h_scale = reinterpret_cast<float*>(ws + s.h_scale);
+  up.h_sum = reinterpret_cast<float*>(ws + s.h_sum);
   up.h_runs = (p.inter + kRun - 1) / kRun;
   up.counters = counters;
   up.partials = reinterpret_cast<float*>(ws + s.partials);
@@ -185,17 +194,37 @@ cudaError_t launch_moe(const MoeProblem& p, cudaStream_t stream) {
   down.K = p.inter; down.N = p.hidden; down.group = p.group_down; down.G = p.inter / p.group_down;
   down.qzeros = p.down.qzeros;
   down.scales = static_cast<const __half*>(p.down.scales);
-  down.act = up.h; down.act_scale = up.h_scale; down.act_runs = up.h_runs;
+  down.act = up.h; down.act_scale = up.h_scale; down.act_sum = up.h_sum; down.act_runs = up.h_runs;
   down.jblocks = (p.hidden + moe::kCols - 1) / moe::kCols;
   down.out = p.out;
   down.dtype = p.dtype;
-  down.counters = counters + moe::kMaxRuns;
+  down.slots = reinterpret_cast<int*>(ws + s.slots);
+  int down_grid = 0;
   switch (p.bits) {
-    case 2: return launch_moe_b2(up, p.up.qweight, down, p.down.qweight, p.experts, stream);
-    case 3: return launch_moe_b3(up, p.up.qweight, down, p.down.qweight, p.experts, stream);
-    case 4: return launch_moe_b4(up, p.up.qweight, down, p.down.qweight, p.experts, stream);
-    default: return launch_moe_b8(up, p.up.qweight, down, p.down.qweight, p.experts, stream);
+    case 2: e = launch_moe_b2(up, p.up.qweight, down, p.down.qweight, p.experts, &down_grid, stream); break;
+    case 3: e = launch_moe_b3(up, p.up.qweight, down, p.down.qweight, p.experts, &down_grid, stream); break;
+    case 4: e = launch_moe_b4(up, p.up.qweight, down, p.down.qweight, p.experts, &down_grid, stream); break;
+    default: e = launch_moe_b8(up, p.up.qweight, down, p.down.qweight, p.experts, &down_grid, stream);
   }
+  if (e != cudaSuccess) return e;
+  const int chunk = p.bits == 2 ? moe::Chunk<2>::kK : p.bits == 3 ? moe::Chunk<3>::kK : p.bits == 4 ? moe::Chunk<4>::kK : moe::Chunk<8>::kK;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(down.jblocks, (p.tokens + 3) / 4);
+  cfg.blockDim = dim3(moe::kCols);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const int nk = (p.inter + chunk - 1) / chunk;
+  const float* parts = down.partials;
+  const int* slots = down.slots;
+  if (p.dtype == 0)
+    return cudaLaunchKernelEx(&cfg, moe::k_sum_parts<__half>, parts, slots, nk, down.jblocks, down_grid, p.tokens, p.hidden,
+                              static_cast<__half*>(p.out));
+  return cudaLaunchKernelEx(&cfg, moe::k_sum_parts<__nv_bfloat16>, parts, slots, nk, down.jblocks, down_grid, p.tokens, p.hidden,
+                            static_cast<__nv_bfloat16*>(p.out));
 }
 
 }  // namespace gptq

@@ -15,14 +15,18 @@
 // A CTA is one producer warp and 8 consumer warps around a ring of chunks.  The producer copies a
 // chunk's weights (TMA boxes of 32 columns with the 128-byte swizzle, as the decode GEMM reads them), its
 // rows of activations (bulk copies), and its groups' scales and zeros (cp.async), all arriving on one
-// mbarrier.  A consumer warp owns 32 columns: it unpacks codes to exact q - zero pairs in fp16 and
-// multiplies on the tensor cores (m16n8k16, weights as the A operand), a fresh fp32 accumulator per
-// group folded in as acc += scale * act_scale * c.
+// mbarrier.  A consumer warp owns 32 columns and multiplies on the tensor cores (m16n8k16, weights as
+// the A operand).  Unpacking is what the SM runs out of first (with exact q - zero pairs, 9 operations
+// per word of 8 codes, eight tokens took 227 us at 61 % of the issue slots), so a code is only masked:
+// in the low mantissa bits of a half, s bits up, it reads as the subnormal q 2^(s - 24), which the MMA
+// multiplies exactly.  The activations of the codes s bits up are stored times 2^-s, and the zero comes
+// off per group:  sum (q - z) a = 2^24 c - z sum a,  with the rows' sums of a stored beside them.  The
+// difference costs the accuracy of fp32 sums of 15 |a| in place of |q - z| |a|.
 //
 // Activations are fp16 in both stages: every row's run of 128 values is stored as fp16 times a power
-// of two chosen for the run (exact for fp16 input; bf16 input and h keep 11 bits relative to the run's
-// largest value), already in the pair order of the codes.  So h may exceed fp16's range, and bf16
-// models lose nothing to the multiply.
+// of two chosen for the run (11 bits relative to the run's largest value for values above 2^-20 of it;
+// exact for fp16 input in that range), already in the pair order of the codes.  So h may exceed fp16's
+// range, and bf16 models lose nothing to the multiply.
 #pragma once
 
 #include <cuda.h>
@@ -55,6 +59,10 @@ struct Chunk {
   // fall into distinct banks
   static constexpr int kActRow = kK * 2 + (BITS == 4 ? 64 : BITS == 8 ? 32 : 16);
   static constexpr int kZeroWords = kWarps * BITS;                        // zeros of 256 columns
+  static constexpr int kInfo = kTiles + kRunsOf > 4 ? 8 : 4;              // floats per row: k-tile sums, run scales
+  // tiles that share a run of activations (and a group, where groups are multiples of their length)
+  static constexpr int kSegTiles = kTileK * kTiles < kRun ? kTiles : kRun / kTileK;
+  static constexpr int kSegK = kSegTiles * kTileK;
 };
 
 // The routing of a call in shared memory: every CTA derives it from the logits (identical in all of
@@ -83,15 +91,18 @@ struct Args {
   float* weights;
   const __half* act;     // UP: [tokens][K] in pair order; DOWN: [rows][K]
   const float* act_scale;   // [row][act_runs]
+  const float* act_sum;     // [row][K / k-tile]
   int act_runs;
   int jblocks;           // column blocks: UP ceil(inter / 128), DOWN ceil(hidden / 256)
   int inter;
   __half* h;             // UP
   float* h_scale;
+  float* h_sum;
   int h_runs;
   void* out;             // DOWN
   int dtype;
-  unsigned* counters;
+  int* slots;            // DOWN: the number of chosen experts, for the sum of the parts
+  unsigned* counters;    // UP
   float* partials;
   unsigned* status;
   int stages, gmax, stage_bytes;
@@ -114,9 +125,47 @@ __device__ __forceinline__ int pair_pos(int k) {
   }
 }
 
-// The power of two (as its exponent) that takes a run's largest magnitude to [2^13, 2^14).
+// How far up (bits) the code at halfword `pos` of a unit sits in its half after RawPairs.
+template <int BITS>
+__host__ __device__ constexpr int pair_shift(int pos) {
+  const int p = pos >> 1;
+  if (BITS == 2) return 2 * (p & 3);
+  if (BITS == 4) return 4 * (p & 1);
+  if (BITS == 3) return pos & 1 ? CodePairs<__half, 3>::shift_hi(p) : CodePairs<__half, 3>::shift_lo(p);
+  return 0;
+}
+
+// The codes of a unit as pairs of fp16 subnormals q 2^(shift - 24), in DiffPairs' order.
+template <int BITS>
+struct RawPairs {
+  static constexpr int kPairs = 16 / BITS;
+  __device__ static __forceinline__ void run(uint32_t w, uint32_t (&d)[kPairs]) {
+    constexpr uint32_t mask = Pack<BITS>::kMask * 0x00010001u;
+    constexpr int low = 8 / BITS;                          // pairs below bit 8
+#pragma unroll
+    for (int p = 0; p < low; ++p) {
+      d[p] = w & (mask << (BITS * p));
+      d[low + p] = (w >> 8) & (mask << (BITS * p));
+    }
+  }
+};
+template <>
+struct RawPairs<3> {
+  static constexpr int kPairs = 16;
+  __device__ static __forceinline__ void run3(uint32_t w0, uint32_t w1, uint32_t w2, uint32_t (&d)[kPairs]) {
+    const uint32_t x[9] = {w0, w0 >> 4, __funnelshift_r(w0, w1, 10), w1, w1 >> 3, w1 >> 6, __funnelshift_r(w1, w2, 26), w2, w2 >> 6};
+#pragma unroll
+    for (int p = 0; p < kPairs; ++p) {
+      const int s = code3_pair(p, 2);
+      const int xi = s == 0 ? 0 : s == 4 ? 1 : s == 10 ? 2 : s == 32 ? 3 : s == 35 ? 4 : s == 38 ? 5 : s == 58 ? 6 : s == 64 ? 7 : 8;
+      d[p] = x[xi] & ((7u << CodePairs<__half, 3>::shift_lo(p)) | (7u << (16 + CodePairs<__half, 3>::shift_hi(p))));
+    }
+  }
+};
+
+// The power of two (as its exponent) that takes a run's largest magnitude to [2^14, 2^15).
 __device__ __forceinline__ int run_exponent(float largest) {
-  int e = largest > 0.f ? static_cast<int>(__float_as_uint(largest) >> 23) - 127 - 13 : 0;
+  int e = largest > 0.f ? static_cast<int>(__float_as_uint(largest) >> 23) - 127 - 14 : 0;
   return e < -126 ? -126 : (e > 126 ? 126 : e);
 }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<unsigned>(e + 127) << 23); }
@@ -137,14 +186,40 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 }
 __device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory"); }
 
-// Shared memory: [stages][weights | activations | activation scales | group scales | group zeros], the
+// One warp stores a run of a row: lane l holds values 4 l .. 4 l + 3 (zeros past K).  act: the row; the
+// run's power of two goes to *scale, and the sums of the stored values over each k-tile, times it, to
+// sums[0 ..].
+template <int BITS>
+__device__ __forceinline__ void store_run(const float (&v)[4], int j0, int K, __half* act, float* scale, float* sums) {
+  constexpr int per = Pack<BITS>::kPerUnit, tile = 4 * per;
+  const int lane = threadIdx.x & 31, j = j0 + 4 * lane;
+  float top = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
+#pragma unroll
+  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+  const int e = run_exponent(top);
+  const float inv = pow2(-e);
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int pos = pair_pos<BITS>((j + i) % per);
+    const __half x = __float2half_rn(v[i] * inv);
+    sum += __half2float(x);
+    if (j < K) act[(j + i) / per * per + pos] = __float2half_rn(__half2float(x) * pow2(-pair_shift<BITS>(pos)));
+  }
+#pragma unroll
+  for (int o = 1; o < tile / 4; o <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+  if (lane == 0) *scale = pow2(e);
+  if (lane % (tile / 4) == 0 && j < K) sums[4 * lane / tile] = sum * pow2(e);
+}
+
+// Shared memory: [stages][weights | activations | their sums and scales | group scales | group zeros], the
 // output tile [tokens][kCols] floats, 2 mbarriers per stage, the routing.
 template <int BITS>
 struct Layout {
   using C = Chunk<BITS>;
   __host__ __device__ static constexpr int act() { return kWarps * C::kSlot; }
-  __host__ __device__ static int act_scale(int tokens) { return act() + tokens * C::kActRow; }
-  __host__ __device__ static int scales(int tokens) { return (act_scale(tokens) + tokens * C::kRunsOf * 4 + 15) & ~15; }
+  __host__ __device__ static int info(int tokens) { return act() + tokens * C::kActRow; }
+  __host__ __device__ static int scales(int tokens) { return info(tokens) + tokens * C::kInfo * 4; }
   __host__ __device__ static int zeros(int tokens, int gmax) { return scales(tokens) + gmax * kCols * 2; }
   __host__ __device__ static int stage(int tokens, int gmax) {
     return (zeros(tokens, gmax) + gmax * C::kZeroWords * 4 + 1023) & ~1023;
@@ -278,6 +353,23 @@ __device__ __forceinline__ int route(const Args& a, const Routing& r, float* scr
   return slots;
 }
 
+// A line of `total` units cut into runs of `share`, the first `extra` of them one longer.
+struct Line {
+  int runs, share, extra;
+  __device__ __forceinline__ Line(long long total, int grid) {
+    const long long want = total / kMinShare;
+    runs = want < 1 ? 1 : (want < grid ? static_cast<int>(want) : grid);
+    share = static_cast<int>(total / runs);
+    extra = static_cast<int>(total - static_cast<long long>(share) * runs);
+  }
+  __device__ __forceinline__ long long begin(int run) const { return static_cast<long long>(share) * run + (run < extra ? run : extra); }
+  __device__ __forceinline__ int length(int run) const { return share + (run < extra ? 1 : 0); }
+  __device__ __forceinline__ int run_of(long long u) const {
+    const long long cut = static_cast<long long>(extra) * (share + 1);
+    return static_cast<int>(u < cut ? u / (share + 1) : extra + (u - cut) / share);
+  }
+};
+
 // A place on the line: u units after the run's begin, chunk c of the item, which is chunk kc of slot s.
 struct Cursor {
   int u, item, c, s, kc;
@@ -288,8 +380,8 @@ __global__ void __launch_bounds__(kThreads, (NB == 4 ? 1 : 2)) k_experts(const _
   using P = Pack<BITS>;
   using C = Chunk<BITS>;
   using L = Layout<BITS>;
-  using DP = DiffPairs<__half, BITS>;
-  constexpr int NP = DP::kPairs, ROWS = P::kRowsPerUnit;
+  using RP = RawPairs<BITS>;
+  constexpr int NP = RP::kPairs, ROWS = P::kRowsPerUnit;
   extern __shared__ __align__(128) unsigned char smem_raw[];
   __shared__ int sm_abort, sm_last, sm_scan[kThreads / 32][2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -329,18 +421,12 @@ __global__ void __launch_bounds__(kThreads, (NB == 4 ? 1 : 2)) k_experts(const _
   const int nk = (a.K + C::kK - 1) / C::kK;                // chunks of one expert's K
   const int per = DOWN ? slots * nk : nk;                  // chunks of an item
   const int items = DOWN ? a.jblocks : slots * a.jblocks;
-  const long long total = static_cast<long long>(items) * (per + kItemUnits);
-  const long long want = total / kMinShare;
-  const int runs = want < 1 ? 1 : (want < gridDim.x ? static_cast<int>(want) : static_cast<int>(gridDim.x));
+  const Line line(static_cast<long long>(items) * (per + kItemUnits), gridDim.x);
   const int run = blockIdx.x;
-  if (run >= runs) return;
-  const int share = static_cast<int>(total / runs), extra = static_cast<int>(total - static_cast<long long>(share) * runs);
-  const long long begin = static_cast<long long>(share) * run + (run < extra ? run : extra);
-  const int limit = share + (run < extra ? 1 : 0);
-  auto run_of = [&](long long u) {
-    const long long cut = static_cast<long long>(extra) * (share + 1);
-    return static_cast<int>(u < cut ? u / (share + 1) : extra + (u - cut) / share);
-  };
+  if (run >= line.runs) return;
+  const long long begin = line.begin(run);
+  const int limit = line.length(run);
+  auto run_of = [&](long long u) { return line.run_of(u); };
   Cursor start;
   {
     start.item = static_cast<int>(begin / (per + kItemUnits));
@@ -391,6 +477,7 @@ __global__ void __launch_bounds__(kThreads, (NB == 4 ? 1 : 2)) k_experts(const _
       const int32_t* zr[2];
       const __half* act;
       const float* act_sc;
+      const float* act_sum;
     };
     auto place = [&](Put& p) {                             // after a new item or expert
       if (p.item != p.x.item) {
@@ -418,6 +505,7 @@ __global__ void __launch_bounds__(kThreads, (NB == 4 ? 1 : 2)) k_experts(const _
       const int row = lane < p.rows ? (DOWN ? off + lane : rt.row_token[off + lane]) : 0;
       p.act = a.act + static_cast<long long>(row) * a.K + k0;
       p.act_sc = a.act_scale + static_cast<long long>(row) * a.act_runs + k0 / kRun;
+      p.act_sum = a.act_sum + static_cast<long long>(row) * (a.K / C::kTileK) + k0 / C::kTileK;
     };
     auto step = [&](Put& p) {                              // to the next chunk
       const int item = p.x.item, slot = p.x.s;
@@ -428,6 +516,7 @@ __global__ void __launch_bounds__(kThreads, (NB == 4 ? 1 : 2)) k_experts(const _
       }
       p.w_row += C::kRows;
       p.act += C::kK;
+      p.act_sum += C::kTiles;
       p.act_sc += C::kK >= kRun ? C::kRunsOf : 1 - (p.x.kc & 1);
       p.g_at += C::kK;
       while (p.g_at >= a.group) {
@@ -466,9 +555,13 @@ __global__ void __launch_bounds__(kThreads, (NB == 4 ? 1 : 2)) k_experts(const _
       const int left = a.K - p.x.kc * C::kK, ck = left < C::kK ? left : C::kK;
       if (lane < p.rows) {
         bulk_load(to + L::act() + lane * C::kActRow, p.act, ck * 2, full(st));
+        const uint32_t info = to + L::info(a.tokens) + lane * C::kInfo * 4;
+#pragma unroll
+        for (int i = 0; i < C::kTiles; ++i)
+          if (i * C::kTileK < ck) cp_async4(info + 4 * i, p.act_sum + i);
 #pragma unroll
         for (int i = 0; i < C::kRunsOf; ++i)
-          if (i * kRun < ck) cp_async4(to + L::act_scale(a.tokens) + (i * a.tokens + lane) * 4, p.act_sc + i);
+          if (i * kRun < ck) cp_async4(info + 4 * (C::kTiles + i), p.act_sc + i);
       }
       cp_async_arrive(full(st));
     };
@@ -571,7 +664,8 @@ __global__ void __launch_bounds__(kThreads, (NB == 4 ? 1 : 2)) k_experts(const _
     }
   };
 
-  // the tile is complete: the layer's output
+  // the tile is complete.  DOWN: the layer's output; UP: one warp per row, 4 of the run's 128 columns
+  // per lane
   auto finish = [&](int item) {
     if constexpr (DOWN) {
       const int n = item * kCols + static_cast<int>(threadIdx.x);
@@ -582,76 +676,81 @@ __global__ void __launch_bounds__(kThreads, (NB == 4 ? 1 : 2)) k_experts(const _
           if (a.dtype == 0) static_cast<__half*>(a.out)[at] = __float2half_rn(v);
           else static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(v);
         }
-    } else {
-      // one warp per row: 4 of the run's 128 columns per lane
-      const int j0 = (item % a.jblocks) * kRun, j = j0 + 4 * lane;
-      for (int m = warp; m < rows; m += kWarps) {
-        const float4 g = *reinterpret_cast<const float4*>(tile + m * kCols + 4 * lane);
-        const float4 u = *reinterpret_cast<const float4*>(tile + m * kCols + kCols / 2 + 4 * lane);
-        float h[4], top = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float gi = (&g.x)[i];
-          h[i] = j < a.inter ? gi / (1.f + expf(-gi)) * (&u.x)[i] : 0.f;
-          top = fmaxf(top, fabsf(h[i]));
-        }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-        const int e = run_exponent(top);
-        const float inv = pow2(-e);
-        __half* to = a.h + static_cast<long long>(off + m) * a.inter;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (j < a.inter) {
-            const int k = j + i;
-            to[k / P::kPerUnit * P::kPerUnit + pair_pos<BITS>(k % P::kPerUnit)] = __float2half_rn(h[i] * inv);
-          }
-        if (lane == 0) a.h_scale[static_cast<long long>(off + m) * a.h_runs + j0 / kRun] = pow2(e);
-      }
+      return;
     }
+    const int j0 = (item % a.jblocks) * kRun, j = j0 + 4 * lane;
+    for (int m = warp; m < rows; m += kWarps) {
+      const float4 g = *reinterpret_cast<const float4*>(tile + m * kCols + 4 * lane);
+      const float4 u = *reinterpret_cast<const float4*>(tile + m * kCols + kCols / 2 + 4 * lane);
+      float h[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float gi = (&g.x)[i];
+        h[i] = j < a.inter ? gi / (1.f + expf(-gi)) * (&u.x)[i] : 0.f;
+      }
+      const long long row = off + m;
+      store_run<BITS>(h, j0, a.inter, a.h + row * a.inter, a.h_scale + row * a.h_runs + j0 / kRun,
+                      a.h_sum + row * (a.inter / C::kTileK) + j0 / C::kTileK);
+    }
+  };
+  // runs first .. last hold an item; the first leaves its part in its slot 1, the others in slot 0
+  auto slot_of = [&](int r, int first) {
+    return a.partials + (static_cast<size_t>(r) * 2 + (r == first ? 1 : 0)) * (static_cast<size_t>(a.tokens) * kCols);
   };
   auto close_item = [&](int item, long long first_chunk) {
     close_slot();
-    const bool whole = first_chunk >= begin && first_chunk + per <= begin + limit;
     consumer_sync();
+    const int live = DOWN ? a.tokens : rows;
+    const bool whole = first_chunk >= begin && first_chunk + per <= begin + limit;
     if (whole) {
       finish(item);
       consumer_sync();                                     // the tile is free again
       return;
     }
-    // runs first .. last hold the item; the first leaves its part in its slot 1, the others in slot 0
-    const int first = run_of(first_chunk), last = run_of(first_chunk + per - 1);
-    const int live = DOWN ? a.tokens : rows;
-    const size_t part = static_cast<size_t>(a.tokens) * kCols;
-    auto slot_of = [&](int r) { return a.partials + (static_cast<size_t>(r) * 2 + (r == first ? 1 : 0)) * part; };
-    float* to = slot_of(run);
-    for (int m = 0; m < live; ++m) __stcg(to + m * kCols + threadIdx.x, tile[m * kCols + threadIdx.x]);
+    // the part goes to the workspace; threads take (row, 4 columns)
+    const int first = run_of(first_chunk);
+    const int c4 = 4 * (threadIdx.x % (kCols / 4)), m0 = threadIdx.x / (kCols / 4);
+    float* to = slot_of(run, first);
+    for (int m = m0; m < live; m += kConsumers / (kCols / 4))
+      __stcg(reinterpret_cast<float4*>(to + m * kCols + c4), *reinterpret_cast<const float4*>(tile + m * kCols + c4));
+    if (DOWN) {                                            // summed by a kernel of its own
+      consumer_sync();
+      return;
+    }
+    const int last = run_of(first_chunk + per - 1);
     consumer_sync();
     if (threadIdx.x == 0) {
       __threadfence();
-      // wraps to zero at the last arrival, ready for the next call
       sm_last = atomicInc(a.counters + first, static_cast<unsigned>(last - first)) == static_cast<unsigned>(last - first);
       __threadfence();
     }
     consumer_sync();
-    if (sm_last) {
-      for (int m = 0; m < live; ++m) {
-        float v = 0.f;
-        constexpr int kBatch = 8;
+    if (sm_last) {                                         // the last to arrive adds the parts in run order
+      constexpr int kBatch = 8;
+      for (int m = m0; m < live; m += kConsumers / (kCols / 4)) {
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int c0 = first; c0 <= last; c0 += kBatch) {
-          float p[kBatch];
+          float4 p[kBatch];
 #pragma unroll
-          for (int j = 0; j < kBatch; ++j) p[j] = c0 + j <= last ? __ldcg(slot_of(c0 + j) + m * kCols + threadIdx.x) : 0.f;
+          for (int j = 0; j < kBatch; ++j)
+            p[j] = __ldcg(reinterpret_cast<const float4*>(slot_of(c0 + j <= last ? c0 + j : last, first) + m * kCols + c4));
 #pragma unroll
-          for (int j = 0; j < kBatch; ++j) v += p[j];
+          for (int j = 0; j < kBatch; ++j)
+            if (c0 + j <= last) {
+              v.x += p[j].x;
+              v.y += p[j].y;
+              v.z += p[j].z;
+              v.w += p[j].w;
+            }
         }
-        tile[m * kCols + threadIdx.x] = v;
+        *reinterpret_cast<float4*>(tile + m * kCols + c4) = v;
       }
       consumer_sync();
       finish(item);
     }
     consumer_sync();
   };
+  if (DOWN && run == 0 && threadIdx.x == 0) *a.slots = slots;
 
   long long first_chunk = begin + start.u - start.c;       // of the current item, on the line
   open_item();
@@ -666,103 +765,119 @@ __global__ void __launch_bounds__(kThreads, (NB == 4 ? 1 : 2)) k_experts(const _
     if (ok) {
       const uint8_t* base = smem + st * stage_bytes;
       const uint8_t* slot = base + warp * C::kSlot;
-      const uint8_t* acts = base + L::act();
-      const float* act_scale = reinterpret_cast<const float*>(base + L::act_scale(a.tokens));
-      const __half* scales = reinterpret_cast<const __half*>(base + L::scales(a.tokens));
-      const uint32_t* zeros = reinterpret_cast<const uint32_t*>(base + L::zeros(a.tokens, a.gmax));
+      const float* info = reinterpret_cast<const float*>(base + L::info(a.tokens));
+      const __half* scales = reinterpret_cast<const __half*>(base + L::scales(a.tokens)) + col0;
+      const uint32_t* zeros = reinterpret_cast<const uint32_t*>(base + L::zeros(a.tokens, a.gmax)) + warp * BITS;
       const int k0 = x.kc * C::kK;
-      const int tiles = (a.K - k0 < C::kK ? a.K - k0 : C::kK) / C::kTileK;
-      int g = 0;                                           // of the chunk's groups
-      int g_end = k0 - g_at + a.group;
-      uint32_t zk[4][DP::kConsts];
-      float gs[4];
-      auto load_group = [&]() {
-        const uint2 s = *reinterpret_cast<const uint2*>(scales + g * kCols + col0);
-        gs[0] = __half2float(__ushort_as_half(lo16(s.x)));
-        gs[1] = __half2float(__ushort_as_half(hi16(s.x)));
-        gs[2] = __half2float(__ushort_as_half(lo16(s.y)));
-        gs[3] = __half2float(__ushort_as_half(hi16(s.y)));
-        const uint32_t* zw = zeros + g * C::kZeroWords + warp * BITS;
+      const int tiles = a.K - k0 < C::kK ? (a.K - k0) / C::kTileK : C::kTiles;
+      float gs[4], gz[4];                                  // scales and zeros of this thread's 4 columns
+      auto load_group = [&](int g) {
+        const uint2 s = *reinterpret_cast<const uint2*>(scales + g * kCols);
+        constexpr float up = 16777216.f;                   // the codes' 2^-24
+        gs[0] = __half2float(__ushort_as_half(lo16(s.x))) * up;
+        gs[1] = __half2float(__ushort_as_half(hi16(s.x))) * up;
+        gs[2] = __half2float(__ushort_as_half(lo16(s.y))) * up;
+        gs[3] = __half2float(__ushort_as_half(hi16(s.y))) * up;
+        const uint32_t* zw = zeros + g * C::kZeroWords;
         const int bit = BITS * quad * 4;
         uint32_t zf = zw[bit >> 5] >> (bit & 31);
         if (BITS == 3 && (bit & 31) + 12 > 32) zf = __funnelshift_r(zw[bit >> 5], zw[(bit >> 5) + 1], bit & 31);
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          DP::consts(static_cast<int>((zf >> (BITS * c)) & P::kMask) + a.zero_offset, zk[c]);
+        for (int c = 0; c < 4; ++c) gz[c] = static_cast<float>(static_cast<int>((zf >> (BITS * c)) & P::kMask) + a.zero_offset);
       };
-      auto fold = [&](int run_i) {
+      const uint8_t* act[NB];
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        const int m = 8 * nb + gq;
+        act[nb] = base + L::act() + (m < rows ? m : rows - 1) * C::kActRow + tq * (NP * 4);
+      }
+      auto tile_mma = [&](int l) {
+        uint4 w[ROWS];
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) {
+          const int row = (l * 4 + tq) * ROWS + r;
+          w[r] = *reinterpret_cast<const uint4*>(slot + row * 128 + ((quad ^ (row & 7)) << 4));
+        }
+        uint32_t d[4][NP];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if constexpr (BITS == 3) RP::run3((&w[0].x)[c], (&w[1].x)[c], (&w[2].x)[c], d[c]);
+          else RP::run((&w[0].x)[c], d[c]);
+        }
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-          if (8 * nb < rows) {
-            float s[2];
+          if (nb == 0 || 8 * nb < rows) {
+            uint32_t b[NP];
+            const uint8_t* src = act[nb] + l * (NP * 16);
+            if constexpr (NP % 4 == 0) {
+#pragma unroll
+              for (int i = 0; i < NP / 4; ++i) {
+                const uint4 v = reinterpret_cast<const uint4*>(src)[i];
+                b[4 * i] = v.x; b[4 * i + 1] = v.y; b[4 * i + 2] = v.z; b[4 * i + 3] = v.w;
+              }
+            } else {
+              const uint2 v = *reinterpret_cast<const uint2*>(src);
+              b[0] = v.x; b[1] = v.y;
+            }
+#pragma unroll
+            for (int j = 0; j < NP / 2; ++j)
+#pragma unroll
+              for (int t = 0; t < 2; ++t)
+                decode::mma16816(cg[t][nb], d[2 * t][2 * j], d[2 * t + 1][2 * j], d[2 * t][2 * j + 1], d[2 * t + 1][2 * j + 1],
+                                 b[2 * j], b[2 * j + 1], __half());
+          }
+        }
+      };
+      // tiles l0 .. l1 are done: acc += scale 2^24 (act_scale c - zero 2^-24 sum a)
+      auto fold = [&](int l0, int l1) {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          if (nb == 0 || 8 * nb < rows) {
+            float s[2], sum[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               const int m = 8 * nb + 2 * tq + i;
-              s[i] = act_scale[run_i * a.tokens + (m < rows ? m : rows - 1)];
+              const float* row = info + (m < rows ? m : rows - 1) * C::kInfo;
+              s[i] = row[C::kTiles + l0 * C::kTileK / kRun];
+              sum[i] = row[l0];
+              for (int l = l0 + 1; l <= l1; ++l) sum[i] += row[l];
+              sum[i] *= 1.f / 16777216.f;
             }
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
-              for (int i = 0; i < 4; ++i) acc[t][nb][i] = fmaf(gs[2 * t + (i >> 1)], s[i & 1] * cg[t][nb][i], acc[t][nb][i]);
+              for (int i = 0; i < 4; ++i)
+                acc[t][nb][i] = fmaf(gs[2 * t + (i >> 1)], fmaf(-gz[2 * t + (i >> 1)], sum[i & 1], s[i & 1] * cg[t][nb][i]), acc[t][nb][i]);
           }
         }
-        clear(cg);
       };
-      int aoff[NB];
+      if (a.group % C::kSegK == 0 && tiles == C::kTiles) {
+        // every segment of kSegTiles tiles lies in one group and one run
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        const int m = 8 * nb + gq;
-        aoff[nb] = (m < rows ? m : rows - 1) * C::kActRow + tq * (NP * 4);
-      }
-      clear(cg);
-      load_group();
+        for (int l0 = 0; l0 < C::kTiles; l0 += C::kSegTiles) {
+          load_group(l0 == 0 || g_at + l0 * C::kTileK < a.group ? 0 : (g_at + l0 * C::kTileK) / a.group);
+          clear(cg);
 #pragma unroll
-      for (int l = 0; l < C::kTiles; ++l) {
-        if (l < tiles) {
-          uint4 w[ROWS];
+          for (int l = l0; l < l0 + C::kSegTiles; ++l) tile_mma(l);
+          fold(l0, l0 + C::kSegTiles - 1);
+        }
+      } else {
+        int g = 0, l0 = 0, g_end = k0 - g_at + a.group;
+        clear(cg);
+        load_group(0);
 #pragma unroll
-          for (int r = 0; r < ROWS; ++r) {
-            const int row = (l * 4 + tq) * ROWS + r;
-            w[r] = *reinterpret_cast<const uint4*>(slot + row * 128 + ((quad ^ (row & 7)) << 4));
-          }
-          uint32_t d[4][NP];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            if constexpr (BITS == 3) DP::run3((&w[0].x)[c], (&w[1].x)[c], (&w[2].x)[c], zk[c], d[c]);
-            else DP::run((&w[0].x)[c], zk[c], d[c]);
-          }
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb) {
-            if (8 * nb < rows) {
-              uint32_t b[NP];
-              const uint8_t* src = acts + aoff[nb] + l * (NP * 16);
-              if constexpr (NP % 4 == 0) {
-#pragma unroll
-                for (int i = 0; i < NP / 4; ++i) {
-                  const uint4 v = reinterpret_cast<const uint4*>(src)[i];
-                  b[4 * i] = v.x; b[4 * i + 1] = v.y; b[4 * i + 2] = v.z; b[4 * i + 3] = v.w;
-                }
-              } else {
-                const uint2 v = *reinterpret_cast<const uint2*>(src);
-                b[0] = v.x; b[1] = v.y;
+        for (int l = 0; l < C::kTiles; ++l) {
+          if (l < tiles) {
+            tile_mma(l);
+            const int k = k0 + (l + 1) * C::kTileK;
+            if (k == g_end || k % kRun == 0 || l + 1 == tiles) {   // a group, a run or the chunk ends
+              fold(l0, l);
+              clear(cg);
+              l0 = l + 1;
+              if (k == g_end && l + 1 < tiles) {
+                load_group(++g);
+                g_end += a.group;
               }
-#pragma unroll
-              for (int j = 0; j < NP / 2; ++j)
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-                  decode::mma16816(cg[t][nb], d[2 * t][2 * j], d[2 * t + 1][2 * j], d[2 * t][2 * j + 1], d[2 * t + 1][2 * j + 1],
-                                   b[2 * j], b[2 * j + 1], __half());
-            }
-          }
-          // a group, a run of activations or the chunk ends here
-          const int k = k0 + (l + 1) * C::kTileK;
-          const bool group_end = k == g_end, run_end = k % kRun == 0;
-          if (group_end || run_end || l + 1 == tiles) {
-            fold(l * C::kTileK / kRun);
-            if (group_end && l + 1 < tiles) {
-              ++g;
-              g_end += a.group;
-              load_group();
             }
           }
         }
@@ -790,8 +905,44 @@ __global__ void __launch_bounds__(kThreads, (NB == 4 ? 1 : 2)) k_experts(const _
   }
 }
 
+// out = the parts of each 256 columns in run order, rounded once.  A CTA takes 4 tokens of an item, a
+// thread 4 columns of one.  (In DOWN itself the last CTA to arrive would add up to 40 parts of tokens x
+// 256 values alone: 16 tokens of 2048 columns took 60 us that way.)
+template <typename T>
+__global__ void __launch_bounds__(kCols) k_sum_parts(const float* partials, const int* slots, int nk, int items, int grid,
+                                                     int tokens, int hidden, T* out) {
+  decode::pdl_wait();
+  decode::pdl_launch_dependents();
+  const int per = *slots * nk, item = blockIdx.x;
+  const Line line(static_cast<long long>(items) * (per + kItemUnits), grid);
+  const long long first_chunk = static_cast<long long>(item) * (per + kItemUnits) + kItemUnits;
+  const int first = line.run_of(first_chunk), last = line.run_of(first_chunk + per - 1);
+  const int c4 = 4 * (threadIdx.x % (kCols / 4)), m = blockIdx.y * 4 + threadIdx.x / (kCols / 4), n = item * kCols + c4;
+  if (m >= tokens || n >= hidden || first == last) return;   // (DOWN wrote an item inside one run itself)
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  constexpr int kBatch = 16;
+  for (int c0 = first; c0 <= last; c0 += kBatch) {
+    float4 p[kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int r = c0 + j <= last ? c0 + j : last;
+      p[j] = __ldcg(reinterpret_cast<const float4*>(
+          partials + ((static_cast<size_t>(r) * 2 + (r == first ? 1 : 0)) * tokens + m) * kCols + c4));
+    }
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j)
+      if (c0 + j <= last) {
+        v.x += p[j].x;
+        v.y += p[j].y;
+        v.z += p[j].z;
+        v.w += p[j].w;
+      }
+  }
+  *reinterpret_cast<uint2*>(out + static_cast<long long>(m) * hidden + n) = make_uint2(pack2(v.x, v.y, T()), pack2(v.z, v.w, T()));
+}
+
 template <int BITS, int NB, bool DOWN>
-cudaError_t launch_experts(Args a, const int32_t* qweight, int experts, cudaStream_t stream) {
+cudaError_t launch_experts(Args a, const int32_t* qweight, int experts, int* runs, cudaStream_t stream) {
   using C = Chunk<BITS>;
   using L = Layout<BITS>;
   auto kern = k_experts<BITS, NB, DOWN>;
@@ -831,6 +982,7 @@ cudaError_t launch_experts(Args a, const int32_t* qweight, int experts, cudaStre
     return cudaErrorInvalidValue;
   int grid = dev.sm_count * per_sm;
   if (grid > kMaxRuns) grid = kMaxRuns;
+  *runs = grid;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kThreads);
@@ -845,17 +997,18 @@ cudaError_t launch_experts(Args a, const int32_t* qweight, int experts, cudaStre
 }
 
 template <int BITS, bool DOWN>
-cudaError_t launch_blocks(const Args& a, const int32_t* qweight, int experts, cudaStream_t stream) {
-  if (a.tokens <= 8) return launch_experts<BITS, 1, DOWN>(a, qweight, experts, stream);
-  if (a.tokens <= 16) return launch_experts<BITS, 2, DOWN>(a, qweight, experts, stream);
-  return launch_experts<BITS, 4, DOWN>(a, qweight, experts, stream);
+cudaError_t launch_blocks(const Args& a, const int32_t* qweight, int experts, int* runs, cudaStream_t stream) {
+  if (a.tokens <= 8) return launch_experts<BITS, 1, DOWN>(a, qweight, experts, runs, stream);
+  if (a.tokens <= 16) return launch_experts<BITS, 2, DOWN>(a, qweight, experts, runs, stream);
+  return launch_experts<BITS, 4, DOWN>(a, qweight, experts, runs, stream);
 }
 
 template <int BITS>
 cudaError_t launch_bits(const Args& up, const int32_t* up_qweight, const Args& down, const int32_t* down_qweight, int experts,
-                        cudaStream_t stream) {
-  const cudaError_t e = launch_blocks<BITS, false>(up, up_qweight, experts, stream);
-  return e != cudaSuccess ? e : launch_blocks<BITS, true>(down, down_qweight, experts, stream);
+                        int* down_grid, cudaStream_t stream) {
+  int up_grid = 0;
+  const cudaError_t e = launch_blocks<BITS, false>(up, up_qweight, experts, &up_grid, stream);
+  return e != cudaSuccess ? e : launch_blocks<BITS, true>(down, down_qweight, experts, down_grid, stream);
 }
 
 }  // namespace moe
