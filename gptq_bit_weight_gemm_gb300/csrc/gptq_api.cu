@@ -132,9 +132,8 @@ int from_decode(cudaError_t e) { return e == cudaErrorInvalidConfiguration ? GPT
 
 }  // namespace
 
-bool encode_tensor_map(void* tmap, int dtype, void* base, const uint64_t* dims,
-                       const uint64_t* strides, const uint32_t* box, const uint32_t* estr,
-                       int swizzle) {
+bool encode_tensor_map_nd(void* tmap, int dtype, int rank, void* base, const uint64_t* dims, const uint64_t* strides,
+                          const uint32_t* box, const uint32_t* estr, int swizzle) {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   static std::once_flag once;
   std::call_once(once, []() {
@@ -146,10 +145,16 @@ bool encode_tensor_map(void* tmap, int dtype, void* base, const uint64_t* dims,
       fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
   });
   if (!fn) return false;
-  return fn(static_cast<CUtensorMap*>(tmap), static_cast<CUtensorMapDataType>(dtype), 2, base,
+  return fn(static_cast<CUtensorMap*>(tmap), static_cast<CUtensorMapDataType>(dtype), rank, base,
             reinterpret_cast<const cuuint64_t*>(dims), reinterpret_cast<const cuuint64_t*>(strides),
             box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, static_cast<CUtensorMapSwizzle>(swizzle),
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool encode_tensor_map(void* tmap, int dtype, void* base, const uint64_t* dims,
+                       const uint64_t* strides, const uint32_t* box, const uint32_t* estr,
+                       int swizzle) {
+  return encode_tensor_map_nd(tmap, dtype, 2, base, dims, strides, box, estr, swizzle);
 }
 
 const DeviceInfo& device_info() {

@@ -99,6 +99,9 @@ cudaError_t launch_writer_fence(cudaStream_t stream);
 bool encode_tensor_map(void* tmap, int dtype, void* base, const uint64_t* dims,
                        const uint64_t* strides, const uint32_t* box, const uint32_t* estr,
                        int swizzle);
+// The same for `rank` dimensions (rank - 1 strides).
+bool encode_tensor_map_nd(void* tmap, int dtype, int rank, void* base, const uint64_t* dims, const uint64_t* strides,
+                          const uint32_t* box, const uint32_t* estr, int swizzle);
 
 // Largest M handled by the decode (split-K, weight-streaming) kernels; larger M goes to the
 // tensor-core tile kernel.

@@ -12,10 +12,13 @@
 // whatever the experts the tokens chose; an item that spans runs leaves one partial tile per run in the
 // workspace, and the last CTA to arrive adds them in run order.
 //
-// A CTA is one producer warp and 8 consumer warps around a ring of chunks.  The producer copies a
-// chunk's weights (TMA boxes of 32 columns with the 128-byte swizzle, as the decode GEMM reads them), its
-// rows of activations (bulk copies), and its groups' scales and zeros (cp.async), all arriving on one
-// mbarrier.  A consumer warp owns 32 columns and multiplies on the tensor cores (m16n8k16, weights as
+// A CTA is one producer warp and 8 consumer warps around a ring of chunks.  Two CTAs share an SM, so that
+// one computes while the other writes an item: one CTA of 16 or 24 consumer warps took 75 and 83 us for
+// one token against 62, three CTAs 67.  The producer copies a
+// chunk's weights (one or two TMA boxes of slots of 32 columns with the 128-byte swizzle), its rows of
+// activations and its groups' scales and zeros (cp.async), all arriving on one mbarrier.  (A box for
+// each 32 columns and a bulk copy for each row cost the producer about 100 cycles each, which bounded
+// everything: one token 83 us.)  A consumer warp owns 32 columns and multiplies on the tensor cores (m16n8k16, weights as
 // the A operand).  Unpacking is what the SM runs out of first (with exact q - zero pairs, 9 operations
 // per word of 8 codes, eight tokens took 227 us at 61 % of the issue slots), so a code is only masked:
 // in the low mantissa bits of a half, s bits up, it reads as the subnormal q 2^(s - 24), which the MMA
@@ -45,7 +48,10 @@ constexpr int kRun = 128;                // activations that share a power of tw
 constexpr int kMaxRuns = 480;            // CTAs, at most
 constexpr int kItemUnits = 2;            // what opening and writing an item takes, in chunks
 constexpr int kMinShare = 4;             // chunks of a run, at least: a join of more parts costs more than it saves
-constexpr int kMaxStages = 8;
+constexpr int kMaxStages = 12;
+
+// CTAs on an SM, by what the registers allow
+__host__ __device__ constexpr int ctas_of(int nb) { return nb == 4 ? 1 : 2; }
 
 template <int BITS>
 struct Chunk {
@@ -53,7 +59,7 @@ struct Chunk {
   static constexpr int kTileK = 4 * Pack<BITS>::kPerUnit;                 // k values of a k-tile
   static constexpr int kK = kTiles * kTileK;
   static constexpr int kRows = kTiles * 4 * Pack<BITS>::kRowsPerUnit;     // packed rows
-  static constexpr int kSlot = (kRows * 128 + 1023) & ~1023;              // one warp's box
+  static constexpr int kSlot = kRows * 128;                               // one warp's 32 columns
   static constexpr int kRunsOf = (kK + kRun - 1) / kRun;                  // activation runs of a chunk
   // bytes of an activation row in the ring: padded so that the B fragments of 4 units and 8 rows
   // fall into distinct banks
@@ -179,16 +185,18 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
 __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
-               : "memory");
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int x, int y, int z, uint32_t bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
+      "[%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(bar), "l"(policy)
+      : "memory");
 }
 __device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory"); }
 
 // One warp stores a run of a row: lane l holds values 4 l .. 4 l + 3 (zeros past K).  act: the row; the
-// run's power of two goes to *scale, and the sums of the stored values over each k-tile, times it, to
-// sums[0 ..].
+// run's power of two goes to *scale, and 2^-24 of the sums of the stored values over each k-tile, times
+// it, to sums[0 ..].
 template <int BITS>
 __device__ __forceinline__ void store_run(const float (&v)[4], int j0, int K, __half* act, float* scale, float* sums) {
   constexpr int per = Pack<BITS>::kPerUnit, tile = 4 * per;
@@ -209,7 +217,7 @@ __device__ __forceinline__ void store_run(const float (&v)[4], int j0, int K, __
 #pragma unroll
   for (int o = 1; o < tile / 4; o <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
   if (lane == 0) *scale = pow2(e);
-  if (lane % (tile / 4) == 0 && j < K) sums[4 * lane / tile] = sum * pow2(e);
+  if (lane % (tile / 4) == 0 && j < K) sums[4 * lane / tile] = sum * (1.f / 16777216.f) * pow2(e);
 }
 
 // Shared memory: [stages][weights | activations | their sums and scales | group scales | group zeros], the
@@ -245,8 +253,17 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int
   }
 }
 
+// Order-preserving bits of a logit, never 0; a NaN as -inf, -0 as 0.
+__device__ __forceinline__ unsigned key_of(float v) {
+  const unsigned b = __float_as_uint(isnan(v) ? __int_as_float(0xFF800000) : v + 0.f);
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float logit_of(unsigned key) {
+  return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);
+}
+
 // Softmax, top-k (equal logits: the lower index; a NaN ranks as -inf) and grouping by expert, by the
-// whole CTA; returns the number of chosen experts.  scratch: kThreads / 32 rows of `experts` floats.
+// whole CTA; returns the number of chosen experts.  scratch: a row of `experts` floats per warp.
 __device__ __forceinline__ int route(const Args& a, const Routing& r, float* scratch, int (*scan)[2], bool publish) {
   constexpr int kAll = kThreads / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -262,38 +279,33 @@ __device__ __forceinline__ int route(const Args& a, const Routing& r, float* scr
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-    for (int e = lane; e < a.experts; e += 32) sum += expf(row[e] - m);
+    for (int e = lane; e < a.experts; e += 32) {
+      sum += expf(row[e] - m);
+      row[e] = __uint_as_float(key_of(row[e]));
+    }
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    // the best expert after the last one in (value, index) order; there are experts >= topk of them
-    float last_v = inf, mine = 0.f;
-    int last_e = -1;
+    // topk times the best expert that has not been taken, equal ones by index: the largest key, then its
+    // lowest index; keys order the logits, NaN as -inf, and 0 marks the taken ones
+    float mine = 0.f;
     for (int j = 0; j < a.topk; ++j) {
-      float bv = -inf;
+      unsigned bk = 0u;
       int be = 0x7FFFFFFF;
       for (int e = lane; e < a.experts; e += 32) {
-        const float v = isnan(row[e]) ? -inf : row[e];
-        const bool after = v < last_v || (v == last_v && e > last_e);
-        if (after && (be == 0x7FFFFFFF || v > bv)) {
-          bv = v;
+        const unsigned k = __float_as_uint(row[e]);
+        if (k > bk) {
+          bk = k;
           be = e;
         }
       }
-#pragma unroll
-      for (int o = 16; o; o >>= 1) {
-        const float ov = __shfl_xor_sync(0xFFFFFFFFu, bv, o);
-        const int oe = __shfl_xor_sync(0xFFFFFFFFu, be, o);
-        if (oe != 0x7FFFFFFF && (be == 0x7FFFFFFF || ov > bv || (ov == bv && oe < be))) {
-          bv = ov;
-          be = oe;
-        }
-      }
-      const float pr = expf(bv - m) / sum;
+      const unsigned top = __reduce_max_sync(0xFFFFFFFFu, bk);
+      be = __reduce_min_sync(0xFFFFFFFFu, bk == top ? be : 0x7FFFFFFF);
+      const float pr = expf(logit_of(top) - m) / sum;
       kept += pr;
       if (lane == j) mine = pr;
       if (lane == 0) r.id[t * a.topk + j] = be;
-      last_v = bv;
-      last_e = be;
+      if (lane == (be & 31)) row[be] = 0.f;
+      __syncwarp();
     }
     if (a.renormalize) mine /= kept;
     if (lane < a.topk) r.w[t * a.topk + lane] = mine;
@@ -376,7 +388,7 @@ struct Cursor {
 };
 
 template <int BITS, int NB, bool DOWN>
-__global__ void __launch_bounds__(kThreads, (NB == 4 ? 1 : 2)) k_experts(const __grid_constant__ CUtensorMap tmW, const Args a) {
+__global__ void __launch_bounds__(kThreads, (ctas_of(NB))) k_experts(const __grid_constant__ CUtensorMap tmW, const Args a) {
   using P = Pack<BITS>;
   using C = Chunk<BITS>;
   using L = Layout<BITS>;
@@ -470,29 +482,27 @@ __global__ void __launch_bounds__(kThreads, (NB == 4 ? 1 : 2)) k_experts(const _
     // (one token, 4096 x 14336: 85 us).
     struct Put {
       Cursor x;
-      int item, slot, rows, w_row, act_row, g, g_at;       // g: the chunk's first group, g_at: k of the chunk in it
-      int col, sc_col, zc[2];
-      unsigned box_bytes;
+      int item, slot, rows, off, w_row, g, g_at;           // g: the chunk's first group, g_at: k of the chunk in it
+      int block, sc_col, zc[2];                            // block: the item's first 32 columns
       const __half* sc;
       const int32_t* zr[2];
-      const __half* act;
       const float* act_sc;
       const float* act_sum;
     };
     auto place = [&](Put& p) {                             // after a new item or expert
       if (p.item != p.x.item) {
         p.item = p.x.item;
-        p.col = lane < kWarps ? col_of(p.item, lane) : -1;
+        p.block = DOWN ? p.item * kWarps : (p.item % a.jblocks) * (kWarps / 2);
         p.sc_col = col_of(p.item, lane >> 2);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int w = lane + 32 * i;
           p.zc[i] = w < C::kZeroWords ? col_of(p.item, w / BITS) : -1;
         }
-        p.box_bytes = __popc(__ballot_sync(0xFFFFFFFFu, p.col >= 0)) * (C::kRows * 128);
       }
       p.slot = p.x.s;
       const int expert = rt.slot_expert[p.slot], off = rt.slot_off[p.slot];
+      p.off = off;
       p.rows = rt.slot_off[p.slot + 1] - off;
       const int k0 = p.x.kc * C::kK;
       p.g = k0 / a.group;
@@ -503,7 +513,6 @@ __global__ void __launch_bounds__(kThreads, (NB == 4 ? 1 : 2)) k_experts(const _
 #pragma unroll
       for (int i = 0; i < 2; ++i) p.zr[i] = a.qzeros + grow * a.zwords + p.zc[i] / 32 * BITS + (lane + 32 * i) % BITS;
       const int row = lane < p.rows ? (DOWN ? off + lane : rt.row_token[off + lane]) : 0;
-      p.act = a.act + static_cast<long long>(row) * a.K + k0;
       p.act_sc = a.act_scale + static_cast<long long>(row) * a.act_runs + k0 / kRun;
       p.act_sum = a.act_sum + static_cast<long long>(row) * (a.K / C::kTileK) + k0 / C::kTileK;
     };
@@ -515,7 +524,6 @@ __global__ void __launch_bounds__(kThreads, (NB == 4 ? 1 : 2)) k_experts(const _
         return;
       }
       p.w_row += C::kRows;
-      p.act += C::kK;
       p.act_sum += C::kTiles;
       p.act_sc += C::kK >= kRun ? C::kRunsOf : 1 - (p.x.kc & 1);
       p.g_at += C::kK;
@@ -532,9 +540,13 @@ __global__ void __launch_bounds__(kThreads, (NB == 4 ? 1 : 2)) k_experts(const _
     auto put_weights = [&](const Put& p, int st) {
       const uint32_t to = smem_a + st * stage_bytes;
       const int left = a.K - p.x.kc * C::kK, ck = left < C::kK ? left : C::kK;
-      if (lane == 0) ptx::mbar_arrive_expect_tx(full(st), p.box_bytes + p.rows * ck * 2);
+      if (lane == 0) {
+        // box rows past the matrix and columns past its end arrive as zeros, and count
+        ptx::mbar_arrive_expect_tx(full(st), kWarps * C::kRows * 128);
+        tma_load_3d(to, &tmW, 0, p.w_row, p.block, full(st), policy);
+        if (!DOWN) tma_load_3d(to + kWarps / 2 * C::kSlot, &tmW, 0, p.w_row, a.inter / 32 + p.block, full(st), policy);
+      }
       __syncwarp();
-      if (p.col >= 0) ptx::tma_load_2d_hint(to + lane * C::kSlot, &tmW, p.col, p.w_row, full(st), policy);
       const __half* sc = p.sc;
       const int32_t* z0 = p.zr[0];
       const int32_t* z1 = p.zr[1];
@@ -553,12 +565,25 @@ __global__ void __launch_bounds__(kThreads, (NB == 4 ? 1 : 2)) k_experts(const _
     auto put_acts = [&](const Put& p, int st) {
       const uint32_t to = smem_a + st * stage_bytes;
       const int left = a.K - p.x.kc * C::kK, ck = left < C::kK ? left : C::kK;
+      // 16-byte pieces of the rows, then each row's sums and scales
+      constexpr int kPieces = C::kK / 8;
+      const int pieces = p.rows * kPieces;
+      for (int i = lane; i < pieces; i += 32) {
+        const int m = i / kPieces, piece = i % kPieces;
+        const int row = DOWN ? p.off + m : rt.row_token[p.off + m];
+        if (piece * 8 < ck)
+          cp_async16(to + L::act() + m * C::kActRow + piece * 16,
+                     a.act + static_cast<long long>(row) * a.K + p.x.kc * C::kK + piece * 8);
+      }
       if (lane < p.rows) {
-        bulk_load(to + L::act() + lane * C::kActRow, p.act, ck * 2, full(st));
         const uint32_t info = to + L::info(a.tokens) + lane * C::kInfo * 4;
+        if (C::kTiles == 4 && a.K % (4 * C::kTileK) == 0) {
+          cp_async16(info, p.act_sum);
+        } else {
 #pragma unroll
-        for (int i = 0; i < C::kTiles; ++i)
-          if (i * C::kTileK < ck) cp_async4(info + 4 * i, p.act_sum + i);
+          for (int i = 0; i < C::kTiles; ++i)
+            if (i * C::kTileK < ck) cp_async4(info + 4 * i, p.act_sum + i);
+        }
 #pragma unroll
         for (int i = 0; i < C::kRunsOf; ++i)
           if (i * kRun < ck) cp_async4(info + 4 * (C::kTiles + i), p.act_sc + i);
@@ -652,8 +677,9 @@ __global__ void __launch_bounds__(kThreads, (NB == 4 ? 1 : 2)) k_experts(const _
         for (int i = 0; i < 4; ++i) {
           const int m = 8 * nb + 2 * tq + (i & 1), c = col0 + 2 * t + (i >> 1);
           if (m < rows) {
-            if constexpr (DOWN) tile[tok[nb][i & 1] * kCols + c] += wt[nb][i & 1] * acc[t][nb][i];
-            else tile[m * kCols + c] = acc[t][nb][i];
+            const float v = acc[t][nb][i] * 16777216.f;    // the codes' 2^-24
+            if constexpr (DOWN) tile[tok[nb][i & 1] * kCols + c] += wt[nb][i & 1] * v;
+            else tile[m * kCols + c] = v;
           }
         }
   };
@@ -710,8 +736,9 @@ __global__ void __launch_bounds__(kThreads, (NB == 4 ? 1 : 2)) k_experts(const _
     // the part goes to the workspace; threads take (row, 4 columns)
     const int first = run_of(first_chunk);
     const int c4 = 4 * (threadIdx.x % (kCols / 4)), m0 = threadIdx.x / (kCols / 4);
+    constexpr int kStep = kConsumers / (kCols / 4);
     float* to = slot_of(run, first);
-    for (int m = m0; m < live; m += kConsumers / (kCols / 4))
+    for (int m = m0; m < live; m += kStep)
       __stcg(reinterpret_cast<float4*>(to + m * kCols + c4), *reinterpret_cast<const float4*>(tile + m * kCols + c4));
     if (DOWN) {                                            // summed by a kernel of its own
       consumer_sync();
@@ -727,7 +754,7 @@ __global__ void __launch_bounds__(kThreads, (NB == 4 ? 1 : 2)) k_experts(const _
     consumer_sync();
     if (sm_last) {                                         // the last to arrive adds the parts in run order
       constexpr int kBatch = 8;
-      for (int m = m0; m < live; m += kConsumers / (kCols / 4)) {
+      for (int m = m0; m < live; m += kStep) {
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int c0 = first; c0 <= last; c0 += kBatch) {
           float4 p[kBatch];
@@ -754,49 +781,63 @@ __global__ void __launch_bounds__(kThreads, (NB == 4 ? 1 : 2)) k_experts(const _
 
   long long first_chunk = begin + start.u - start.c;       // of the current item, on the line
   open_item();
+  // this thread's places in a stage: its pieces of the weights (tile l at w_at[l & 1] + 512 l; the swizzle
+  // goes by the 128-byte line within the stage), scales and zeros, and its rows' activations and sums
+  int w_at[BITS == 3 ? ROWS : 2], act_at[NB], info_at[NB][2];
+  const int scales_at = L::scales(a.tokens) + 2 * col0, zeros_at = L::zeros(a.tokens, a.gmax) + 4 * warp * BITS;
+#pragma unroll
+  for (int i = 0; i < (BITS == 3 ? ROWS : 2); ++i) {
+    const int row = BITS == 3 ? tq * ROWS + i : 4 * i + tq, line = warp * C::kRows + row;
+    w_at[i] = line * 128 + ((quad ^ (line & 7)) << 4) - (BITS == 3 ? 0 : 512 * i);
+  }
+  const float zero_base = 8388608.f - static_cast<float>(a.zero_offset);
+  const uint8_t* base = smem;                              // of the stage
   int st = 0, g_at = 0;                                    // g_at: k of the chunk within its first group
   unsigned round = 0;
   while (x.u < limit) {
     if (x.s != cur) {
       open_slot();
       g_at = x.kc * C::kK % a.group;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {                    // rows past the slot's read its last one
+        const int m = 8 * nb + gq;
+        act_at[nb] = L::act() + (m < rows ? m : rows - 1) * C::kActRow + tq * (NP * 4);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int mi = 8 * nb + 2 * tq + i;
+          info_at[nb][i] = L::info(a.tokens) + (mi < rows ? mi : rows - 1) * (C::kInfo * 4);
+        }
+      }
     }
-    const bool ok = __all_sync(0xFFFFFFFFu, wait(full(st), round, &sm_abort, a.status));
-    if (ok) {
-      const uint8_t* base = smem + st * stage_bytes;
-      const uint8_t* slot = base + warp * C::kSlot;
-      const float* info = reinterpret_cast<const float*>(base + L::info(a.tokens));
-      const __half* scales = reinterpret_cast<const __half*>(base + L::scales(a.tokens)) + col0;
-      const uint32_t* zeros = reinterpret_cast<const uint32_t*>(base + L::zeros(a.tokens, a.gmax)) + warp * BITS;
+    if (__all_sync(0xFFFFFFFFu, wait(full(st), round, &sm_abort, a.status))) {
+      const __half* scales = reinterpret_cast<const __half*>(base + scales_at);
+      const uint32_t* zeros = reinterpret_cast<const uint32_t*>(base + zeros_at);
       const int k0 = x.kc * C::kK;
       const int tiles = a.K - k0 < C::kK ? (a.K - k0) / C::kTileK : C::kTiles;
       float gs[4], gz[4];                                  // scales and zeros of this thread's 4 columns
       auto load_group = [&](int g) {
         const uint2 s = *reinterpret_cast<const uint2*>(scales + g * kCols);
-        constexpr float up = 16777216.f;                   // the codes' 2^-24
-        gs[0] = __half2float(__ushort_as_half(lo16(s.x))) * up;
-        gs[1] = __half2float(__ushort_as_half(hi16(s.x))) * up;
-        gs[2] = __half2float(__ushort_as_half(lo16(s.y))) * up;
-        gs[3] = __half2float(__ushort_as_half(hi16(s.y))) * up;
+        gs[0] = __half2float(__ushort_as_half(lo16(s.x)));
+        gs[1] = __half2float(__ushort_as_half(hi16(s.x)));
+        gs[2] = __half2float(__ushort_as_half(lo16(s.y)));
+        gs[3] = __half2float(__ushort_as_half(hi16(s.y)));
         const uint32_t* zw = zeros + g * C::kZeroWords;
         const int bit = BITS * quad * 4;
         uint32_t zf = zw[bit >> 5] >> (bit & 31);
         if (BITS == 3 && (bit & 31) + 12 > 32) zf = __funnelshift_r(zw[bit >> 5], zw[(bit >> 5) + 1], bit & 31);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) gz[c] = static_cast<float>(static_cast<int>((zf >> (BITS * c)) & P::kMask) + a.zero_offset);
+        for (int c = 0; c < 4; ++c)                        // 2^23 + z - 2^23
+          gz[c] = __uint_as_float(0x4B000000u | ((zf >> (BITS * c)) & P::kMask)) - zero_base;
       };
-      const uint8_t* act[NB];
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        const int m = 8 * nb + gq;
-        act[nb] = base + L::act() + (m < rows ? m : rows - 1) * C::kActRow + tq * (NP * 4);
-      }
       auto tile_mma = [&](int l) {
         uint4 w[ROWS];
 #pragma unroll
         for (int r = 0; r < ROWS; ++r) {
-          const int row = (l * 4 + tq) * ROWS + r;
-          w[r] = *reinterpret_cast<const uint4*>(slot + row * 128 + ((quad ^ (row & 7)) << 4));
+          if constexpr (BITS == 3) {
+            w[r] = *reinterpret_cast<const uint4*>(base + w_at[r]);
+          } else {
+            w[r] = *reinterpret_cast<const uint4*>(base + w_at[l & 1] + l * 512);
+          }
         }
         uint32_t d[4][NP];
 #pragma unroll
@@ -808,7 +849,7 @@ __global__ void __launch_bounds__(kThreads, (NB == 4 ? 1 : 2)) k_experts(const _
         for (int nb = 0; nb < NB; ++nb) {
           if (nb == 0 || 8 * nb < rows) {
             uint32_t b[NP];
-            const uint8_t* src = act[nb] + l * (NP * 16);
+            const uint8_t* src = base + act_at[nb] + l * (NP * 16);
             if constexpr (NP % 4 == 0) {
 #pragma unroll
               for (int i = 0; i < NP / 4; ++i) {
@@ -828,7 +869,7 @@ __global__ void __launch_bounds__(kThreads, (NB == 4 ? 1 : 2)) k_experts(const _
           }
         }
       };
-      // tiles l0 .. l1 are done: acc += scale 2^24 (act_scale c - zero 2^-24 sum a)
+      // tiles l0 .. l1 are done: acc += scale (act_scale c - zero 2^-24 sum a)
       auto fold = [&](int l0, int l1) {
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
@@ -836,12 +877,15 @@ __global__ void __launch_bounds__(kThreads, (NB == 4 ? 1 : 2)) k_experts(const _
             float s[2], sum[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              const int m = 8 * nb + 2 * tq + i;
-              const float* row = info + (m < rows ? m : rows - 1) * C::kInfo;
+              const float* row = reinterpret_cast<const float*>(base + info_at[nb][i]);
               s[i] = row[C::kTiles + l0 * C::kTileK / kRun];
-              sum[i] = row[l0];
-              for (int l = l0 + 1; l <= l1; ++l) sum[i] += row[l];
-              sum[i] *= 1.f / 16777216.f;
+              if (C::kTiles == 4 && l0 == 0 && l1 == 3) {
+                const float4 v = *reinterpret_cast<const float4*>(row);
+                sum[i] = (v.x + v.y) + (v.z + v.w);
+              } else {
+                sum[i] = row[l0];
+                for (int l = l0 + 1; l <= l1; ++l) sum[i] += row[l];
+              }
             }
 #pragma unroll
             for (int t = 0; t < 2; ++t)
@@ -885,9 +929,11 @@ __global__ void __launch_bounds__(kThreads, (NB == 4 ? 1 : 2)) k_experts(const _
     }
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(empty(st));
+    base += stage_bytes;
     if (++st == a.stages) {
       st = 0;
       round ^= 1;
+      base = smem;
     }
     g_at += C::kK;
     while (g_at >= a.group) g_at -= a.group;
@@ -954,31 +1000,31 @@ cudaError_t launch_experts(Args a, const int32_t* qweight, int experts, int* run
   else if (C::kK % a.group == 0) a.gmax = C::kK / a.group;
   a.stage_bytes = L::stage(a.tokens, a.gmax);
   const int pairs = a.tokens * a.topk;
-  // two CTAs on an SM where their rings hold three chunks each, else one
-  int per_sm = NB == 4 ? 1 : 2;
+  int per_sm = ctas_of(NB);
   auto fit = [&](int ctas) {
-    const int budget = ctas == 2 ? 233472 / 2 - 1024 - 256 : 227 * 1024 - 256;   // less the static part
+    const int budget = ctas > 1 ? 233472 / ctas - 1024 - 512 : 227 * 1024 - 512;   // less the static part
     return (budget - L::fixed(a.tokens, pairs, experts)) / (a.stage_bytes + 16);
   };
   a.stages = fit(per_sm);
-  if (per_sm == 2 && a.stages < 3) a.stages = fit(per_sm = 1);
+  while (per_sm > 1 && a.stages < 3) a.stages = fit(--per_sm);
   if (a.stages > kMaxStages) a.stages = kMaxStages;
   // the router's scratch lies over the ring
   if (a.stages < 2 || a.stages * a.stage_bytes < kThreads / 32 * experts * 4) return cudaErrorInvalidConfiguration;
   const int smem = L::fixed(a.tokens, pairs, experts) + a.stages * (a.stage_bytes + 16);
   static std::atomic<unsigned long long> opted_in{0};       // per device
   if (dev.device >= 64 || !(opted_in.load(std::memory_order_relaxed) & (1ull << dev.device))) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024 - 256);
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024 - 512);
     if (e != cudaSuccess) return e;
     if (dev.device < 64) opted_in.fetch_or(1ull << dev.device, std::memory_order_relaxed);
   }
   CUtensorMap tmW = {};
-  const uint64_t dims[2] = {static_cast<uint64_t>(a.N), static_cast<uint64_t>(a.units) * Pack<BITS>::kRowsPerUnit * experts};
-  const uint64_t strides[1] = {static_cast<uint64_t>(a.N) * 4};
-  const uint32_t box[2] = {32, static_cast<uint32_t>(C::kRows)};
-  const uint32_t estr[2] = {1, 1};
-  if (!encode_tensor_map(&tmW, CU_TENSOR_MAP_DATA_TYPE_INT32, const_cast<int32_t*>(qweight), dims, strides, box, estr,
-                         CU_TENSOR_MAP_SWIZZLE_128B))
+  // (column of 32, packed row, block of 32 columns): a box lands block by block, as the warps read it
+  const uint64_t dims[3] = {32, static_cast<uint64_t>(a.units) * Pack<BITS>::kRowsPerUnit * experts, static_cast<uint64_t>(a.N) / 32};
+  const uint64_t strides[2] = {static_cast<uint64_t>(a.N) * 4, 128};
+  const uint32_t box[3] = {32, static_cast<uint32_t>(C::kRows), DOWN ? kWarps : kWarps / 2};
+  const uint32_t estr[3] = {1, 1, 1};
+  if (!encode_tensor_map_nd(&tmW, CU_TENSOR_MAP_DATA_TYPE_INT32, 3, const_cast<int32_t*>(qweight), dims, strides, box, estr,
+                            CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
   int grid = dev.sm_count * per_sm;
   if (grid > kMaxRuns) grid = kMaxRuns;
