@@ -4,7 +4,7 @@
 // keeps a prefix of that order: the first top_k, then those before which less than top_p of the mass
 // lies, then those with w >= min_p.  So the kept set is "logits above a threshold, and the first few of
 // those equal to it", and the token is found by cumulating the kept masses in index order.  Nothing is
-// sorted but the few tokens around a threshold.  Masses are integers of 2^-32 of the best token's, whose
+// sorted but the few tokens around a threshold.  Masses are integers of 2^-31 of the best token's, whose
 // sums do not depend on their order: atomics and splits do not change a result.
 //
 // Bound: the logits are read once from HBM (a cluster of CTAs holds a row in its shared memory); what
@@ -37,7 +37,8 @@ constexpr int kList = 2048;                        // tokens that are sorted, at
 constexpr int kShortK = 1024;
 constexpr int kMaxCluster = 8;
 constexpr int kMaxSlice = 65535;                   // tokens of a CTA whose 16-bit half masses fit 32-bit sums
-constexpr float kReach = 24.f;                     // e^-24 2^32 rounds to no mass
+constexpr float kReach = 24.f;                     // e^-24 2^31 rounds to no mass
+constexpr float kOne = 2147483648.f;               // the best token's mass
 
 // Order-preserving bits of a logit: NaN lowest (0), -0 as 0.
 __device__ __forceinline__ uint32_t key_of(float l) {
@@ -54,7 +55,32 @@ __device__ __forceinline__ float load_logit(const void* p, int i) {
   else if constexpr (DT == 1) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
   else return static_cast<const float*>(p)[i];
 }
-__device__ __forceinline__ u64 mass_of(float w) { return __float2ull_rn(w * 4294967296.f); }
+template <int DT>
+__device__ __forceinline__ void unpack(const uint4& x, float (&l)[DT == 2 ? 4 : 8]) {
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const uint32_t u = (&x.x)[w];
+    if constexpr (DT == 2) {
+      l[w] = __uint_as_float(u);
+    } else if constexpr (DT == 1) {
+      l[2 * w] = __uint_as_float(u << 16);
+      l[2 * w + 1] = __uint_as_float(u & 0xFFFF0000u);
+    } else {
+      l[2 * w] = __half2float(__ushort_as_half(lo16(u)));
+      l[2 * w + 1] = __half2float(__ushort_as_half(hi16(u)));
+    }
+  }
+}
+__device__ __forceinline__ uint32_t mass_of(float w) { return __float2uint_rn(w * kOne); }
+
+// Comparisons of whole masses with a fraction of a total, as whole numbers (fp64 is slow here):
+// m < fraction * total is m < below_part, and cum > fraction * total is cum >= beyond_part.
+__device__ __forceinline__ u64 below_part(float fraction, u64 total) {
+  return static_cast<u64>(ceil(static_cast<double>(fraction) * static_cast<double>(total)));
+}
+__device__ __forceinline__ u64 beyond_part(float fraction, u64 total) {
+  return static_cast<u64>(floor(static_cast<double>(fraction) * static_cast<double>(total))) + 1;
+}
 
 __device__ __forceinline__ u64 warp_sum(u64 v) {
 #pragma unroll
@@ -79,7 +105,7 @@ struct Shared {
   };
   u64 list[kList];
   u64 slots[2][kMaxCluster];       // cluster sums, every CTA's part in every CTA
-  uint2 range[kMaxCluster];        // largest and smallest key of each CTA
+  float2 range[kMaxCluster];       // largest logit of each CTA, and the smallest of a sample of its tokens
   u64 part_m[kMaxCluster];         // kept mass above the threshold, and ties, of each CTA
   int part_t[kMaxCluster];
   u64 warp_m[kWarps];
@@ -90,14 +116,29 @@ struct Shared {
   int bin_lo, bin_hi, verdict;     // from CTA 0: the bins to list; what happens next
   uint32_t thr;                    // from CTA 0: keys above thr are kept, and the first `ties` of key thr
   int ties;
-  int found;
-  uint32_t found_key;
 };
 
 enum Verdict { kGather = 1, kBisect = 2, kReady = 3 };
 
 // The list's first n entries in descending order (padded with zeros to a power of two).
 __device__ void sort_list(u64* list, int n) {
+  // a few entries go straight to their places, each the number of larger ones (they differ all): 256
+  // take 0.7 us so, and 3 us in the 36 steps below
+  if (n <= kThreads) {
+    const int i = threadIdx.x;
+    u64 e = 0;
+    int at = 0;
+    __syncthreads();
+    if ((i & ~31) < n) {
+      e = i < n ? list[i] : 0ull;
+#pragma unroll 4
+      for (int j = 0; j < n; ++j) at += list[j] > e;
+    }
+    __syncthreads();
+    if (i < n) list[at] = e;
+    __syncthreads();
+    return;
+  }
   int size = 1;
   while (size < n) size <<= 1;
   for (int i = n + static_cast<int>(threadIdx.x); i < size; i += kThreads) list[i] = 0ull;
@@ -117,7 +158,7 @@ __device__ void sort_list(u64* list, int n) {
 }
 
 template <int DT>
-__global__ void __launch_bounds__(kThreads) k_sample(const SampleProblem p, int held) {
+__global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleProblem p, int held) {
   __shared__ Shared sh;
   extern __shared__ __align__(16) unsigned char dyn[];
   cg::cluster_group cluster = cg::this_cluster();
@@ -134,79 +175,78 @@ __global__ void __launch_bounds__(kThreads) k_sample(const SampleProblem p, int 
   const int start = static_cast<int>(static_cast<long long>(p.vocab) * rank / cs);
   const int n = static_cast<int>(static_cast<long long>(p.vocab) * (rank + 1) / cs) - start;
   const char* src = static_cast<const char*>(p.logits) + (row * p.row_stride + start) * kSize;
-  const void* data = src;
-  uint32_t best = 0u, least = 0xFFFFFFFFu;
-  auto see = [&](float l) {
-    const uint32_t k = key_of(l);
-    best = max(best, k);
-    if (k > 0x007FFFFFu) least = min(least, k);            // not NaN, not -inf
-  };
-  {
-    // 16 bytes at a time between the ends, kept at the same place modulo 16 in shared memory
-    const int head = min(n, static_cast<int>((16 - (reinterpret_cast<uintptr_t>(src) & 15)) & 15) / kSize);
-    const int vecs = (n - head) / kVec;
-    unsigned char* to = dyn + (reinterpret_cast<uintptr_t>(src) & 15);
-    auto one = [&](int i) {
-      const float l = load_logit<DT>(src, i);
-      see(l);
-      if (held) {
-        if constexpr (DT == 2) reinterpret_cast<float*>(to)[i] = l;
-        else reinterpret_cast<uint16_t*>(to)[i] = reinterpret_cast<const uint16_t*>(src)[i];
-      }
-    };
-    if (static_cast<int>(threadIdx.x) < head) one(threadIdx.x);
-    const int tail = head + vecs * kVec + static_cast<int>(threadIdx.x);
-    if (tail < n) one(tail);
-    const uint4* from = reinterpret_cast<const uint4*>(src + head * kSize);
-    uint4* into = reinterpret_cast<uint4*>(to + head * kSize);
-#pragma unroll 4
-    for (int v = threadIdx.x; v < vecs; v += kThreads) {
-      const uint4 x = __ldg(from + v);
-      if (held) into[v] = x;
+  // vectors of 16 bytes from the address below src that is a multiple of 16: token i is element i + skew.
+  // What lies before token 0 and after token n - 1 reads as NaN, which no rule keeps.
+  const int skew = static_cast<int>(reinterpret_cast<uintptr_t>(src) & 15) / kSize;
+  const int vecs = (n + skew + kVec - 1) / kVec;
+  const char* base = src - skew * kSize;
+  auto edge_vec = [&](int v, float (&l)[kVec]) {           // from global memory, token by token
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const uint32_t u = (&x.x)[w];
-        if constexpr (DT == 2) {
-          see(__uint_as_float(u));
-        } else if constexpr (DT == 1) {
-          see(__uint_as_float(u << 16));
-          see(__uint_as_float(u & 0xFFFF0000u));
-        } else {
-          see(__half2float(__ushort_as_half(lo16(u))));
-          see(__half2float(__ushort_as_half(hi16(u))));
+    for (int j = 0; j < kVec; ++j) {
+      const int i = v * kVec + j - skew;
+      l[j] = i >= 0 && i < n ? load_logit<DT>(src, i) : CUDART_NAN_F;
+    }
+  };
+  float top = -CUDART_INF_F, low = CUDART_INF_F;           // fmaxf and fminf pass over NaN
+  {
+    uint4* to = reinterpret_cast<uint4*>(dyn);
+    const int inner0 = skew ? 1 : 0, inner1 = (n + skew) / kVec;   // whole vectors
+#pragma unroll 4
+    for (int v = inner0 + static_cast<int>(threadIdx.x); v < inner1; v += kThreads) {
+      const uint4 x = __ldg(reinterpret_cast<const uint4*>(base) + v);
+      if (held) to[v] = x;
+      float l[kVec];
+      unpack<DT>(x, l);
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) top = fmaxf(top, l[j]);
+      low = fminf(low, l[0] > -CUDART_INF_F ? l[0] : low);
+    }
+    if (threadIdx.x < 2) {                                 // the first and the last, where they are not whole
+      const int v = threadIdx.x == 0 ? 0 : vecs - 1;
+      if (v < inner0 || v >= inner1) {
+        float l[kVec];
+        edge_vec(v, l);
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) {
+          top = fmaxf(top, l[j]);
+          low = fminf(low, l[j] > -CUDART_INF_F ? l[j] : low);
+          const int i = v * kVec + j - skew;
+          if (held) {
+            if constexpr (DT == 2) reinterpret_cast<float*>(dyn)[i + skew] = l[j];
+            else reinterpret_cast<uint16_t*>(dyn)[i + skew] = i >= 0 && i < n ? reinterpret_cast<const uint16_t*>(src)[i] : uint16_t(0x7FFF);
+          }
         }
       }
     }
-    if (held) data = to;
   }
-  best = __reduce_max_sync(0xFFFFFFFFu, best);
-  least = __reduce_min_sync(0xFFFFFFFFu, least);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    low = fminf(low, __shfl_xor_sync(0xFFFFFFFFu, low, o));
+  }
   if (lane == 0) {
-    sh.scan_c[warp] = best;
-    sh.warp_t[warp] = static_cast<int>(least);
+    sh.scan_c[warp] = __float_as_uint(top);
+    sh.warp_t[warp] = __float_as_int(low);
   }
   for (int i = threadIdx.x; i < kBins; i += kThreads) sh.count[i] = sh.hi[i] = sh.lo[i] = 0u;
-  if (threadIdx.x == 0) {
-    sh.listed = 0;
-    sh.found = -1;
-  }
+  if (threadIdx.x == 0) sh.listed = 0;
   __syncthreads();
   asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
   if (static_cast<int>(threadIdx.x) < cs) {
     for (int w = 0; w < kWarps; ++w) {
-      best = max(best, sh.scan_c[w]);
-      least = min(least, static_cast<uint32_t>(sh.warp_t[w]));
+      top = fmaxf(top, __uint_as_float(sh.scan_c[w]));
+      low = fminf(low, __int_as_float(sh.warp_t[w]));
     }
-    cluster.map_shared_rank(&sh, threadIdx.x)->range[rank] = make_uint2(best, least);
+    cluster.map_shared_rank(&sh, threadIdx.x)->range[rank] = make_float2(top, low);
   }
   cluster.sync();
   for (int r = 0; r < cs; ++r) {
-    best = max(best, sh.range[r].x);
-    least = min(least, sh.range[r].y);
+    top = fmaxf(top, sh.range[r].x);
+    low = fminf(low, sh.range[r].y);
   }
   // +inf logits share the mass: they count as 0 and the others as -inf
-  const bool has_inf = best == key_of(CUDART_INF_F);
-  if (best <= key_of(-CUDART_INF_F)) {                     // nothing above -inf
+  const bool has_inf = top == CUDART_INF_F;
+  if (top == -CUDART_INF_F) {                              // nothing above -inf
     if (rank == 0 && threadIdx.x == 0) {
       p.token[row] = -1;
       if (p.logprob) p.logprob[row] = CUDART_NAN_F;
@@ -214,9 +254,9 @@ __global__ void __launch_bounds__(kThreads) k_sample(const SampleProblem p, int 
     }
     return;
   }
-  const float top = has_inf ? 0.f : logit_of(best);
-  best = key_of(top);
-  const float low = has_inf ? 0.f : logit_of(least);
+  if (has_inf) top = low = 0.f;
+  top += 0.f;                                              // -0 as 0
+  const uint32_t best = key_of(top);
   float temp = p.temperature ? p.temperature[row] : 1.f;
   const float top_p = p.top_p ? p.top_p[row] : 1.f, min_p = p.min_p ? p.min_p[row] : 0.f;
   float u = p.uniform[row];
@@ -227,14 +267,40 @@ __global__ void __launch_bounds__(kThreads) k_sample(const SampleProblem p, int 
     k = 1;
   }
   if (!(top_p > 0.f) || !(min_p <= 1.f)) k = 1;
-  auto value_at = [&](int i) {
-    const float l = load_logit<DT>(data, i);
-    return has_inf ? (l == CUDART_INF_F ? 0.f : -CUDART_INF_F) : l;
+  auto load_vec = [&](int v, float (&l)[kVec]) {
+    if (held) {
+      unpack<DT>(reinterpret_cast<const uint4*>(dyn)[v], l);
+    } else if (v * kVec >= skew && (v + 1) * kVec <= n + skew) {
+      unpack<DT>(__ldg(reinterpret_cast<const uint4*>(base) + v), l);
+    } else {
+      edge_vec(v, l);
+    }
+    if (has_inf)
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) l[j] = l[j] == CUDART_INF_F ? 0.f : -CUDART_INF_F;
   };
-  auto weight_at = [&](uint32_t key) { return expf((logit_of(key) - top) / temp); };
-  auto kept_mass = [&](uint32_t key) {                     // min_p's part of the rule included
-    const float w = weight_at(key);
-    return w >= min_p || key == best ? mass_of(w) : 0ull;
+  auto each = [&](auto f) {                                // f(logit, token), in any order
+#pragma unroll 2
+    for (int v = threadIdx.x; v < vecs; v += kThreads) {
+      float l[kVec];
+      load_vec(v, l);
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) f(l[j], start + v * kVec + j - skew);
+    }
+  };
+  // w = e^((l - top) / T) as a power of two: the exponent is rounded once more than in the definition,
+  // by 2^-24 of itself
+  const float rate = fminf(1.44269504088896341f / temp, 3e38f);
+  auto weight_of = [&](float l) {
+    float w;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"((l - top) * rate));   // 2 units in the last place
+    return w;
+  };
+  auto weight_at = [&](uint32_t key) { return weight_of(logit_of(key)); };
+  const bool by_min = min_p > 0.f;
+  auto kept_mass = [&](float l) {                          // min_p's part of the rule included
+    const float w = weight_of(l);
+    return !by_min || w >= min_p || l == top ? mass_of(w) : 0u;
   };
   Shared* const boss = cluster.map_shared_rank(&sh, 0);
   int parity = 0;
@@ -257,7 +323,7 @@ __global__ void __launch_bounds__(kThreads) k_sample(const SampleProblem p, int 
     p.token[row] = token;
     if (p.logprob)
       p.logprob[row] = static_cast<float>(static_cast<double>((logit_of(key) - top) / temp) -
-                                          log(static_cast<double>(total) / 4294967296.0));
+                                          log(static_cast<double>(total) / static_cast<double>(kOne)));
   };
 
   uint32_t thr = 0u;
@@ -268,27 +334,41 @@ __global__ void __launch_bounds__(kThreads) k_sample(const SampleProblem p, int 
   } else if (k < p.vocab || top_p < 1.f) {
     const bool short_k = k <= kShortK;
     // ---- the histogram of top - l over the reach of the masses
-    const float span = fminf(top - low, kReach * temp);
+    const float reach = kReach * temp, span = low <= top ? fminf(top - low, reach) : reach;
     const float scale = span > 0.f ? fminf((kOver - 0.5f) / span, 3e38f) : 0.f;
-    auto bin_of = [&](float l) {                           // NaN and -inf: the last
-      const float d = (top - l) * scale;
-      return d < static_cast<float>(kOver) ? static_cast<int>(d) : kOver;
+    // NaN, -inf and what has no mass: the last bin; what is lower than the sampled lowest: the one before
+    auto bin_of = [&](float l) {
+      const float d = top - l;
+      return d <= reach && d < CUDART_INF_F ? min(static_cast<int>(fminf(d * scale, static_cast<float>(kOver - 1))), kOver - 1) : kOver;
     };
     const bool by_mass = top_p < 1.f && !short_k;
     const bool fits = n <= kMaxSlice;
-#pragma unroll 4
-    for (int i = threadIdx.x; i < n; i += kThreads) {
-      const float l = value_at(i);
-      const int b = bin_of(l);
-      if (b < kOver) {
-        atomicAdd(&sh.count[b], 1u);
-        if (by_mass && fits) {
-          const u64 m = mass_of(expf((l - top) / temp));
-          atomicAdd(&sh.hi[b], static_cast<uint32_t>(m >> 16));
-          atomicAdd(&sh.lo[b], static_cast<uint32_t>(m & 0xFFFFu));
+    if (by_mass && fits)
+      each([&](float l, int) {
+        const int b = bin_of(l);
+        if (b < kOver) {
+          const uint32_t m = mass_of(weight_of(l));
+          if (k < p.vocab) atomicAdd(&sh.count[b], 1u);    // else the list's own count will do
+          atomicAdd(&sh.hi[b], m >> 16);
+          atomicAdd(&sh.lo[b], m & 0xFFFFu);
         }
+      });
+    else if (short_k && p.vocab / kVec >= 4 * k)
+      // the largest of each vector only: k vectors reach as far down as their k-th largest, so at least k
+      // tokens do, and what lies above is little more than k tokens
+      for (int v = threadIdx.x; v < vecs; v += kThreads) {
+        float l[kVec], most = -CUDART_INF_F;
+        load_vec(v, l);
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) most = fmaxf(most, l[j]);
+        const int b = bin_of(most);
+        if (b < kOver) atomicAdd(&sh.count[b], 1u);
       }
-    }
+    else
+      each([&](float l, int) {
+        const int b = bin_of(l);
+        if (b < kOver) atomicAdd(&sh.count[b], 1u);
+      });
     cluster.sync();
     // ---- CTA 0: running sums over the cluster's bins, 4 bins a thread
     u64 mass_total = 0;
@@ -363,14 +443,16 @@ __global__ void __launch_bounds__(kThreads) k_sample(const SampleProblem p, int 
     // all CTAs: the tokens of bins bin_lo .. bin_hi into CTA 0's list
     auto gather = [&]() {
       const int lo = sh.bin_lo, hi = sh.bin_hi;
-      for (int i = threadIdx.x; i < n; i += kThreads) {
-        const float l = value_at(i);
+      // most tokens are below: one comparison, with half a bin to spare for its rounding
+      const float floor = scale > 0.f && hi < kOver - 1 ? top - (hi + 1.5f) / scale * (1.f + 1e-5f) : -CUDART_INF_F;
+      each([&](float l, int token) {
+        if (!(l >= floor)) return;
         const int b = bin_of(l);
         if (b >= lo && b <= hi) {
           const int at = atomicAdd(&boss->listed, 1);
-          if (at < kList) boss->list[at] = static_cast<u64>(key_of(l)) << 32 | (0xFFFFFFFFu - static_cast<uint32_t>(start + i));
+          if (at < kList) boss->list[at] = static_cast<u64>(key_of(l)) << 32 | (0xFFFFFFFFu - static_cast<uint32_t>(token));
         }
-      }
+      });
     };
     auto key_in = [&](int i) { return static_cast<uint32_t>(sh.list[i] >> 32); };
     // CTA 0: the place of the threshold after the first r of the sorted list: its key, and how many of
@@ -394,7 +476,7 @@ __global__ void __launch_bounds__(kThreads) k_sample(const SampleProblem p, int 
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int i = 4 * threadIdx.x + j;
-        m[j] = i < r ? mass(i) : 0ull;
+        m[j] = i < r ? static_cast<u64>(mass(i)) : 0ull;
         before[j] = sum;
         sum += m[j];
       }
@@ -429,24 +511,51 @@ __global__ void __launch_bounds__(kThreads) k_sample(const SampleProblem p, int 
         tell(sh.cum_c[last] <= kList ? kGather : kBisect, 0, last);
       }
       cluster.sync();
+      bool listed = false;
       if (sh.verdict == kGather) {
         gather();
         cluster.sync();
+        listed = boss->listed <= kList;                    // (the bins counted vectors, not tokens)
+        cluster.sync();
+      }
+      if (listed) {
         if (rank != 0) return;                             // CTA 0 has everything that can be kept
-        int r = min(sh.listed, kList);
+        int r = sh.listed;
         sort_list(sh.list, r);
         r = min(r, k);
         u64 before[4], m[4];
         const u64 all = scan_list(r, [&](int i) { return mass_of(weight_at(key_in(i))); }, before, m);
-        const double limit = top_p < 1.f ? static_cast<double>(top_p) * static_cast<double>(all) : 2.0 * static_cast<double>(all);
+        const u64 limit = top_p < 1.f ? below_part(top_p, all) : ~0ull;
         int keep = 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int i = 4 * threadIdx.x + j;
-          keep += i < r && (i == 0 || (static_cast<double>(before[j]) < limit && weight_at(key_in(i)) >= min_p));
+          keep += i < r && (i == 0 || (before[j] < limit && weight_at(key_in(i)) >= min_p));
         }
         r = count_true(keep);                              // the kept ones are a prefix
-        // in index order: (index, key) ascending is (~index, key) descending
+        // in index order: by adding up, of a few, those of lower index
+        if (r <= kThreads) {
+          uint32_t* const mass = sh.cum_c;
+          const int i = threadIdx.x;
+          const u64 e = i < r ? sh.list[i] : 0ull;
+          const uint32_t mine = i < r ? mass_of(weight_at(static_cast<uint32_t>(e >> 32))) : 0u;
+          mass[i] = mine;
+          __syncthreads();
+          if ((i & ~31) < r) {
+            u64 lower = 0, total = 0;
+#pragma unroll 4
+            for (int j = 0; j < r; ++j) {
+              const uint32_t m_j = mass[j];
+              total += m_j;
+              if (static_cast<uint32_t>(sh.list[j]) > static_cast<uint32_t>(e)) lower += m_j;   // ~index
+            }
+            // the token whose masses reach past the target (u >= 1: the last one)
+            const u64 goal = min(beyond_part(u, total), total), end = lower + mine;
+            if (i < r && lower < goal && goal <= end) write(static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(e)), static_cast<uint32_t>(e >> 32), total);
+          }
+          return;
+        }
+        // or sorted: (index, key) ascending is (~index, key) descending
         for (int i = threadIdx.x; i < r; i += kThreads) {
           const u64 e = sh.list[i];
           sh.list[i] = e << 32 | e >> 32;
@@ -455,14 +564,11 @@ __global__ void __launch_bounds__(kThreads) k_sample(const SampleProblem p, int 
         sort_list(sh.list, r);
         auto low_key = [&](int i) { return static_cast<uint32_t>(sh.list[i]); };
         const u64 total = scan_list(r, [&](int i) { return mass_of(weight_at(low_key(i))); }, before, m);
-        const double target = static_cast<double>(u) * static_cast<double>(total);
-        const bool over = !(target < static_cast<double>(total));   // u >= 1: the last kept token
+        const u64 goal = min(beyond_part(u, total), total);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int i = 4 * threadIdx.x + j;
-          const u64 end = before[j] + m[j];
-          const bool hit = over ? end == total : static_cast<double>(before[j]) <= target && target < static_cast<double>(end);
-          if (i < r && m[j] > 0 && hit) write(static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(sh.list[i] >> 32)), low_key(i), total);
+          if (i < r && before[j] < goal && goal <= before[j] + m[j]) write(static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(sh.list[i] >> 32)), low_key(i), total);
         }
         return;
       }
@@ -475,8 +581,8 @@ __global__ void __launch_bounds__(kThreads) k_sample(const SampleProblem p, int 
           tell(in <= kList && (!by_mass || p.vocab <= kMaxSlice * cs) ? kGather : kBisect, b, b);
         } else if (by_mass) {
           // top_k cuts nothing that has a mass
-          const double limit = static_cast<double>(top_p) * static_cast<double>(mass_total);
-          const int pb = first_bin([&](int i) { return static_cast<double>(sh.cum_m[i]) >= limit; });
+          const u64 limit = below_part(top_p, mass_total);
+          const int pb = first_bin([&](int i) { return sh.cum_m[i] >= limit; });
           const uint32_t in = pb < kOver ? sh.cum_c[pb] - below(pb) : 0u;
           tell(p.vocab > kMaxSlice * cs || in > kList ? kBisect : (pb < kOver ? kGather : kReady), pb, pb);
         } else {
@@ -488,8 +594,11 @@ __global__ void __launch_bounds__(kThreads) k_sample(const SampleProblem p, int 
       if (sh.verdict == kGather) {
         gather();
         cluster.sync();
-        if (rank == 0) {
-          int bin = sh.bin_lo, r = min(sh.listed, kList);
+        if (rank == 0 && sh.listed > kList) {
+          __syncthreads();                                 // (every thread has read it)
+          tell(kBisect, 0, 0);
+        } else if (rank == 0) {
+          int bin = sh.bin_lo, r = sh.listed;
           sort_list(sh.list, r);
           bool again = false;
           u64 before[4], m[4];
@@ -501,8 +610,8 @@ __global__ void __launch_bounds__(kThreads) k_sample(const SampleProblem p, int 
             cut_after(within);
             if (by_mass) {
               goal_mass = below_m(bin) + scan_list(within, [&](int i) { return mass_of(weight_at(key_in(i))); }, before, m);
-              const double limit = static_cast<double>(top_p) * static_cast<double>(goal_mass);
-              const int pb = first_bin([&](int i) { return i >= bin || static_cast<double>(sh.cum_m[i]) >= limit; });
+              const u64 limit = below_part(top_p, goal_mass);
+              const int pb = first_bin([&](int i) { return i >= bin || sh.cum_m[i] >= limit; });
               if (pb < bin) {                              // top_p ends in an earlier bin: list that one
                 const uint32_t in = sh.cum_c[pb] - below(pb);
                 again = true;
@@ -516,12 +625,12 @@ __global__ void __launch_bounds__(kThreads) k_sample(const SampleProblem p, int 
           }
           if (!again) {
             if (by_mass) {
-              const double limit = static_cast<double>(top_p) * static_cast<double>(goal_mass);
+              const u64 limit = below_part(top_p, goal_mass);
               scan_list(within, [&](int i) { return mass_of(weight_at(key_in(i))); }, before, m);
               int keep = 0;
 #pragma unroll
               for (int j = 0; j < 4; ++j)
-                keep += 4 * static_cast<int>(threadIdx.x) + j < within && static_cast<double>(before[j] + below_m(bin)) < limit;
+                keep += 4 * static_cast<int>(threadIdx.x) + j < within && before[j] + below_m(bin) < limit;
               keep = count_true(keep);
               cut_after(keep > 0 ? keep : 1);
             }
@@ -533,15 +642,15 @@ __global__ void __launch_bounds__(kThreads) k_sample(const SampleProblem p, int 
           gather();
           cluster.sync();
           if (rank == 0) {
-            const int bin = sh.bin_lo, r = min(sh.listed, kList);
-            const double limit = static_cast<double>(top_p) * static_cast<double>(sh.slots[0][0]);
+            const int bin = sh.bin_lo, r = sh.listed;
+            const u64 limit = below_part(top_p, sh.slots[0][0]);
             sort_list(sh.list, r);
             u64 before[4], m[4];
             scan_list(r, [&](int i) { return mass_of(weight_at(key_in(i))); }, before, m);
             int keep = 0;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              keep += 4 * static_cast<int>(threadIdx.x) + j < r && static_cast<double>(before[j] + below_m(bin)) < limit;
+              keep += 4 * static_cast<int>(threadIdx.x) + j < r && before[j] + below_m(bin) < limit;
             keep = count_true(keep);
             cut_after(keep > 0 ? keep : 1);
             tell(kReady, 0, 0);
@@ -554,48 +663,46 @@ __global__ void __launch_bounds__(kThreads) k_sample(const SampleProblem p, int 
         ties = sh.ties;
       }
     }
-    if (sh.verdict == kBisect) {
+    if (short_k || sh.verdict == kBisect) {                // (a short top_k that could be listed has returned)
       thr = 0u;
       ties = p.vocab;
-      auto key_at = [&](int i) { return key_of(value_at(i)); };
-      auto mass_at = [&](uint32_t key) { return key ? mass_of(weight_at(key)) : 0ull; };
+      auto mass_at = [&](uint32_t key) { return key ? static_cast<u64>(mass_of(weight_at(key))) : 0ull; };
       if (k < p.vocab) {
         for (int bit = 31; bit >= 0; --bit) {
           const uint32_t cand = thr | (1u << bit);
           u64 c = 0;
-          for (int i = threadIdx.x; i < n; i += kThreads) c += key_at(i) >= cand;
+          each([&](float l, int) { c += key_of(l) >= cand; });
           if (cluster_sum(c) >= static_cast<u64>(k)) thr = cand;
         }
         u64 c = 0;
-        for (int i = threadIdx.x; i < n; i += kThreads) c += key_at(i) > thr;
+        each([&](float l, int) { c += key_of(l) > thr; });
         ties = k - static_cast<int>(cluster_sum(c));
       }
       if (top_p < 1.f) {
         auto above = [&](uint32_t v) {                     // mass of the keys above v
           u64 m = 0;
-          for (int i = threadIdx.x; i < n; i += kThreads) {
-            const uint32_t key = key_at(i);
+          each([&](float l, int) {
+            const uint32_t key = key_of(l);
             if (key > v) m += mass_at(key);
-          }
+          });
           return cluster_sum(m);
         };
         u64 at_thr = 0;
-        for (int i = threadIdx.x; i < n; i += kThreads) at_thr += key_at(i) == thr;
+        each([&](float l, int) { at_thr += key_of(l) == thr; });
         at_thr = cluster_sum(at_thr);
         if (at_thr > static_cast<u64>(ties)) at_thr = ties;
-        const double limit = static_cast<double>(top_p) * static_cast<double>(above(thr) + at_thr * mass_at(thr));
+        const u64 limit = below_part(top_p, above(thr) + at_thr * mass_at(thr));
         // the smallest key v >= thr with less than the limit above it
         uint32_t lo = thr, hi = best;
         while (lo < hi) {
           const uint32_t mid = lo + (hi - lo) / 2;
-          if (static_cast<double>(above(mid)) < limit) hi = mid;
+          if (above(mid) < limit) hi = mid;
           else lo = mid + 1;
         }
         const u64 a = above(lo), m = mass_at(lo);
         int r = lo == thr ? ties : p.vocab;
         if (m > 0) {                                       // ties i = 0, 1, ... stay while a + i m < limit
-          u64 q = static_cast<u64>(ceil((limit - static_cast<double>(a)) / static_cast<double>(m)));
-          if (q < 1) q = 1;
+          const u64 q = limit > a ? (limit - a + m - 1) / m : 1;
           if (q < static_cast<u64>(r)) r = static_cast<int>(q);
         }
         thr = lo;
@@ -606,27 +713,30 @@ __global__ void __launch_bounds__(kThreads) k_sample(const SampleProblem p, int 
 
   // ---- the kept masses in index order: each warp's run of this CTA's tokens, then the CTAs.  Ties have
   // one mass each, so a run needs only the mass above the threshold and its number of ties.
-  const int chunks = (n + 127) / 128;                      // a warp's run is whole chunks of 128 tokens
+  const float cut = thr ? logit_of(thr) : -CUDART_INF_F;   // (nothing is cut: ties of -inf have no mass)
+  const u64 tie_mass = thr ? kept_mass(cut) : 0ull;
+  const int chunks = (vecs + 31) / 32;                     // a warp's run is whole chunks of 32 vectors
   const int c0 = chunks * warp / kWarps, c1 = chunks * (warp + 1) / kWarps;
-  const u64 tie_mass = thr ? kept_mass(thr) : 0ull;
-  auto chunk_at = [&](int c, u64 (&m)[4], bool (&tie)[4]) {   // this lane's 4 tokens of chunk c
+  auto chunk_at = [&](int c, float (&l)[kVec]) {
+    if (c * 32 + lane < vecs) {
+      load_vec(c * 32 + lane, l);
+    } else {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int i = c * 128 + 4 * lane + j;
-      const uint32_t key = i < n ? key_of(value_at(i)) : 0u;
-      tie[j] = i < n && key == thr;
-      m[j] = key > thr ? kept_mass(key) : 0ull;
+      for (int j = 0; j < kVec; ++j) l[j] = CUDART_NAN_F;
     }
   };
   {
     u64 mine = 0;
     int t = 0;
+#pragma unroll 2
     for (int c = c0; c < c1; ++c) {
-      u64 m[4];
-      bool tie[4];
-      chunk_at(c, m, tie);
-      mine += (m[0] + m[1]) + (m[2] + m[3]);
-      t += tie[0] + tie[1] + tie[2] + tie[3];
+      float l[kVec];
+      chunk_at(c, l);
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) {
+        if (l[j] > cut) mine += kept_mass(l[j]);
+        t += l[j] == cut;
+      }
     }
     mine = warp_sum(mine);
     t = __reduce_add_sync(0xFFFFFFFFu, t);
@@ -667,15 +777,15 @@ __global__ void __launch_bounds__(kThreads) k_sample(const SampleProblem p, int 
     tied += sh.warp_t[w];
   }
   const u64 end = before + sh.warp_m[warp] + static_cast<u64>(kept_ties(tied, sh.warp_t[warp])) * tie_mass;
-  const double target = static_cast<double>(u) * static_cast<double>(total);
-  const bool over = !(target < static_cast<double>(total));   // u >= 1: the last kept token
-  // the run that holds the target (over: the run whose end is the total, with a mass of its own)
-  if (!(over ? end == total && end > before : static_cast<double>(before) <= target && target < static_cast<double>(end))) return;
+  // the run in which the kept masses reach past the target (u >= 1: the one where they end)
+  const u64 goal = min(beyond_part(u, total), total);
+  if (!(before < goal && goal <= end)) return;
   for (int c = c0; c < c1; ++c) {
-    u64 m[4];
-    bool tie[4];
-    chunk_at(c, m, tie);
-    const int t = tie[0] + tie[1] + tie[2] + tie[3];
+    float l[kVec];
+    chunk_at(c, l);
+    int t = 0;
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) t += l[j] == cut;
     int tscan = t;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -683,27 +793,24 @@ __global__ void __launch_bounds__(kThreads) k_sample(const SampleProblem p, int 
       if (lane >= o) tscan += v;
     }
     int at = tied + tscan - t;
-    u64 sum = 0;
+    u64 m[kVec], sum = 0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (tie[j] && at++ < ties) m[j] = tie_mass;
+    for (int j = 0; j < kVec; ++j) {
+      m[j] = l[j] > cut ? static_cast<u64>(kept_mass(l[j])) : 0ull;
+      if (l[j] == cut && at++ < ties) m[j] = tie_mass;
       sum += m[j];
     }
     const u64 incl = warp_scan(sum);
     u64 run = before + incl - sum;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < kVec; ++j) {
       const u64 e = run + m[j];
-      const bool hit = over ? e == total : static_cast<double>(run) <= target && target < static_cast<double>(e);
-      if (m[j] > 0 && hit) {
-        const int i = c * 128 + 4 * lane + j;
-        write(start + i, key_of(value_at(i)), total);
-      }
+      if (run < goal && goal <= e) write(start + (c * 32 + lane) * kVec + j - skew, key_of(l[j]), total);
       run = e;
     }
     before += __shfl_sync(0xFFFFFFFFu, incl, 31);
     tied += __shfl_sync(0xFFFFFFFFu, tscan, 31);
-    if (over ? before == total : target < static_cast<double>(before)) break;
+    if (before >= goal) break;
   }
 }
 
@@ -711,14 +818,16 @@ template <int DT>
 cudaError_t launch(const SampleProblem& p, cudaStream_t stream) {
   constexpr int kSize = DT == 2 ? 4 : 2;
   const DeviceInfo& dev = device_info();
-  // CTAs per row: enough to fill the GPU and to hold the row in shared memory with exact histograms
+  // CTAs per row: as many as run at once, two on an SM, and more where the row's masses need them for
+  // exact sums of 32 bits; at most 2 * kThreads tokens a CTA are too few to split
   int cs = 1;
-  auto bytes = [&](int c) { return (static_cast<size_t>(p.vocab) / c + 1) * kSize + 16; };
-  while (cs < kMaxCluster && (static_cast<long long>(p.batch) * cs < 2 * dev.sm_count || p.vocab > kMaxSlice * cs || bytes(cs) > 96 * 1024) &&
-         p.vocab / cs > 2 * kThreads)
+  while (cs < kMaxCluster && p.vocab / cs > 2 * kThreads &&
+         (static_cast<long long>(p.batch) * 2 * cs <= 2 * dev.sm_count || p.vocab > kMaxSlice * cs))
     cs *= 2;
-  size_t smem = bytes(cs);
-  const bool held = smem <= 160 * 1024;
+  // the row stays in shared memory where that leaves room for as many CTAs; else it is read again from L2
+  size_t smem = ((static_cast<size_t>(p.vocab) / cs + 1) * kSize + 31) & ~static_cast<size_t>(15);
+  const bool one_each = static_cast<long long>(p.batch) * cs <= dev.sm_count;
+  const bool held = smem <= (one_each ? 160 : 72) * 1024;
   if (!held) smem = 0;
   auto kern = k_sample<DT>;
   static std::atomic<unsigned long long> opted_in{0};       // per device

@@ -101,7 +101,7 @@ int gptq_moe(const void* x, int tokens, int hidden, int inter, int dtype, const 
  *   stays while the mass before it is < top_p * total); of these those with w >= min_p (the best
  *   token always stays);
  *   token = the first kept index, in index order, whose cumulated w exceeds uniform * (kept mass).
- * l is taken to fp32 and x and w are fp32; masses are summed exactly, as integers of 2^-32 of the
+ * l is taken to fp32 and x and w are fp32; masses are summed exactly, as integers of 2^-31 of the
  * best token's w, so that the result does not depend on an order of summation.
  *   logits       [batch, vocab] of dtype (GPTQ_F16, GPTQ_BF16, GPTQ_F32), rows row_stride elements
  *                apart; aligned to the element
