@@ -35,6 +35,7 @@ constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kBins = 2048, kOver = kBins - 1;     // the last bin: logits too low to have a mass
 constexpr int kList = 2048;                        // tokens that are sorted, at most
 constexpr int kShortK = 1024;
+constexpr int kSubs = 128;                         // sub-runs of a CTA's tokens, 8 a warp
 constexpr int kMaxCluster = 8;
 constexpr int kMaxSlice = 65535;                   // tokens of a CTA whose 16-bit half masses fit 32-bit sums
 constexpr float kReach = 24.f;                     // e^-24 2^31 rounds to no mass
@@ -110,6 +111,8 @@ struct Shared {
   int part_t[kMaxCluster];
   u64 warp_m[kWarps];
   int warp_t[kWarps];
+  u64 sub_m[kSubs];                // the same of each sub-run of this CTA's tokens
+  int sub_t[kSubs];
   u64 scan_m[kWarps];
   uint32_t scan_c[kWarps];
   int listed;                      // CTA 0: entries of the list
@@ -280,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleProblem p, i
       for (int j = 0; j < kVec; ++j) l[j] = l[j] == CUDART_INF_F ? 0.f : -CUDART_INF_F;
   };
   auto each = [&](auto f) {                                // f(logit, token), in any order
-#pragma unroll 2
+#pragma unroll 4
     for (int v = threadIdx.x; v < vecs; v += kThreads) {
       float l[kVec];
       load_vec(v, l);
@@ -322,8 +325,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleProblem p, i
   auto write = [&](int token, uint32_t key, u64 total) {
     p.token[row] = token;
     if (p.logprob)
-      p.logprob[row] = static_cast<float>(static_cast<double>((logit_of(key) - top) / temp) -
-                                          log(static_cast<double>(total) / static_cast<double>(kOne)));
+      p.logprob[row] = (logit_of(key) - top) / temp - logf(static_cast<float>(total) * (1.f / kOne));
   };
 
   uint32_t thr = 0u;
@@ -443,10 +445,11 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleProblem p, i
     // all CTAs: the tokens of bins bin_lo .. bin_hi into CTA 0's list
     auto gather = [&]() {
       const int lo = sh.bin_lo, hi = sh.bin_hi;
-      // most tokens are below: one comparison, with half a bin to spare for its rounding
+      // most tokens are below or above: two comparisons, with half a bin to spare for their rounding
       const float floor = scale > 0.f && hi < kOver - 1 ? top - (hi + 1.5f) / scale * (1.f + 1e-5f) : -CUDART_INF_F;
+      const float roof = scale > 0.f ? top - (lo - 0.5f) / scale * (1.f - 1e-5f) : CUDART_INF_F;
       each([&](float l, int token) {
-        if (!(l >= floor)) return;
+        if (!(l >= floor && l <= roof)) return;
         const int b = bin_of(l);
         if (b >= lo && b <= hi) {
           const int at = atomicAdd(&boss->listed, 1);
@@ -711,12 +714,12 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleProblem p, i
     }
   }
 
-  // ---- the kept masses in index order: each warp's run of this CTA's tokens, then the CTAs.  Ties have
-  // one mass each, so a run needs only the mass above the threshold and its number of ties.
+  // ---- the kept masses in index order: sub-runs of this CTA's tokens, then the CTAs.  Ties have one
+  // mass each, so a sub-run needs only the mass above the threshold and its number of ties.
   const float cut = thr ? logit_of(thr) : -CUDART_INF_F;   // (nothing is cut: ties of -inf have no mass)
   const u64 tie_mass = thr ? kept_mass(cut) : 0ull;
-  const int chunks = (vecs + 31) / 32;                     // a warp's run is whole chunks of 32 vectors
-  const int c0 = chunks * warp / kWarps, c1 = chunks * (warp + 1) / kWarps;
+  const int chunks = (vecs + 31) / 32;                     // a sub-run is whole chunks of 32 vectors
+  auto sub_begin = [&](int q) { return static_cast<int>(static_cast<long long>(chunks) * q / kSubs); };
   auto chunk_at = [&](int c, float (&l)[kVec]) {
     if (c * 32 + lane < vecs) {
       load_vec(c * 32 + lane, l);
@@ -725,11 +728,12 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleProblem p, i
       for (int j = 0; j < kVec; ++j) l[j] = CUDART_NAN_F;
     }
   };
-  {
+  for (int q = warp * (kSubs / kWarps); q < (warp + 1) * (kSubs / kWarps); ++q) {
     u64 mine = 0;
     int t = 0;
+    const int c1 = sub_begin(q + 1);
 #pragma unroll 2
-    for (int c = c0; c < c1; ++c) {
+    for (int c = sub_begin(q); c < c1; ++c) {
       float l[kVec];
       chunk_at(c, l);
 #pragma unroll
@@ -740,28 +744,33 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleProblem p, i
     }
     mine = warp_sum(mine);
     t = __reduce_add_sync(0xFFFFFFFFu, t);
-    __syncthreads();
     if (lane == 0) {
-      sh.warp_m[warp] = mine;
-      sh.warp_t[warp] = t;
+      sh.sub_m[q] = mine;
+      sh.sub_t[q] = t;
     }
-    __syncthreads();
-    if (static_cast<int>(threadIdx.x) < cs) {
-      u64 all = 0;
-      int ties_here = 0;
-      for (int w = 0; w < kWarps; ++w) {
-        all += sh.warp_m[w];
-        ties_here += sh.warp_t[w];
-      }
-      Shared* s = cluster.map_shared_rank(&sh, threadIdx.x);
+  }
+  __syncthreads();
+  // warp 0 goes on alone: 4 sub-runs a lane, summed for the cluster
+  if (warp == 0) {
+    u64 all = 0;
+    int ties_here = 0;
+#pragma unroll
+    for (int j = 0; j < kSubs / 32; ++j) {
+      all += sh.sub_m[lane * (kSubs / 32) + j];
+      ties_here += sh.sub_t[lane * (kSubs / 32) + j];
+    }
+    all = warp_sum(all);
+    ties_here = __reduce_add_sync(0xFFFFFFFFu, ties_here);
+    if (lane < cs) {
+      Shared* s = cluster.map_shared_rank(&sh, lane);
       s->part_m[rank] = all;
       s->part_t[rank] = ties_here;
     }
   }
   cluster.sync();                                          // the last access to another CTA's memory
-  u64 before = 0, total = 0;                               // kept mass before this warp's run, in all
-  int tied = 0;                                            // ties before this warp's run
-  int seen = 0;
+  if (warp != 0) return;
+  u64 before = 0, total = 0;                               // kept mass before this CTA's tokens, in all
+  int tied = 0, seen = 0;                                  // ties before them
   auto kept_ties = [&](int from, int count) { return max(0, min(count, ties - from)); };
   for (int r = 0; r < cs; ++r) {
     const u64 m = sh.part_m[r] + static_cast<u64>(kept_ties(seen, sh.part_t[r])) * tie_mass;
@@ -772,15 +781,51 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleProblem p, i
     total += m;
     seen += sh.part_t[r];
   }
-  for (int w = 0; w < warp; ++w) {
-    before += sh.warp_m[w] + static_cast<u64>(kept_ties(tied, sh.warp_t[w])) * tie_mass;
-    tied += sh.warp_t[w];
-  }
-  const u64 end = before + sh.warp_m[warp] + static_cast<u64>(kept_ties(tied, sh.warp_t[warp])) * tie_mass;
-  // the run in which the kept masses reach past the target (u >= 1: the one where they end)
+  // the sub-run in which the kept masses reach past the target (u >= 1: the one where they end)
   const u64 goal = min(beyond_part(u, total), total);
-  if (!(before < goal && goal <= end)) return;
-  for (int c = c0; c < c1; ++c) {
+  int q = -1;
+  {
+    constexpr int kEach = kSubs / 32;
+    int t[kEach], lane_t = 0;
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) lane_t += t[j] = sh.sub_t[lane * kEach + j];
+    int from = lane_t;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xFFFFFFFFu, from, o);
+      if (lane >= o) from += v;
+    }
+    from += tied - lane_t;
+    u64 m[kEach], lane_m = 0;
+    int f = from;
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+      m[j] = sh.sub_m[lane * kEach + j] + static_cast<u64>(kept_ties(f, t[j])) * tie_mass;
+      f += t[j];
+      lane_m += m[j];
+    }
+    u64 at = before + warp_scan(lane_m) - lane_m;
+    f = from;
+    int mine = -1;
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+      if (at < goal && goal <= at + m[j]) {
+        mine = lane * kEach + j;
+        before = at;
+        tied = f;
+      }
+      at += m[j];
+      f += t[j];
+    }
+    const unsigned who = __ballot_sync(0xFFFFFFFFu, mine >= 0);
+    if (who == 0) return;                                  // in another CTA's tokens
+    const int owner = __ffs(who) - 1;
+    q = __shfl_sync(0xFFFFFFFFu, mine, owner);
+    before = __shfl_sync(0xFFFFFFFFu, before, owner);
+    tied = __shfl_sync(0xFFFFFFFFu, tied, owner);
+  }
+  const int c1 = sub_begin(q + 1);
+  for (int c = sub_begin(q); c < c1; ++c) {
     float l[kVec];
     chunk_at(c, l);
     int t = 0;
