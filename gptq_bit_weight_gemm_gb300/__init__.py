@@ -465,8 +465,37 @@ def strerror(code):
 
 
 # ------------------------------------------------------------------ the rest of a decode step
-def _cuda(t, dtype, shape, name):
-    """The address of a contiguous CUDA tensor of this type and shape."""
+# A decode step is tens of these calls, some of a few microseconds on the GPU, so each checks its
+# tensors in one expression (attribute reads, about 0.1 us each) and calls the library; only where the
+# expression fails are they looked at one by one, to say what is wrong.
+class _Runtime:
+    """What the calls below use of torch, looked up once."""
+
+    def __init__(self):
+        torch = _torch()
+        self.int32, self.float32, self.float16 = torch.int32, torch.float32, torch.float16
+        self.codes = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32}
+        self.lib = lib()
+        raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+        if raw is None or device is None:
+            self.stream = lambda: torch.cuda.current_stream().cuda_stream
+        else:
+            torch.cuda.init()
+            self.stream = lambda: raw(device())
+
+
+_rt = None
+
+
+def _runtime():
+    global _rt
+    if _rt is None:
+        _rt = _Runtime()
+    return _rt
+
+
+def _look(t, dtype, shape, name):
+    """Raises what is wrong with a tensor that should be a contiguous CUDA tensor of this type and shape."""
     if not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
     if t.dtype != dtype:
@@ -475,6 +504,11 @@ def _cuda(t, dtype, shape, name):
         raise ValueError("%s must have the shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
+
+
+def _address(t, dtype, shape, name):
+    if not (t.is_cuda and t.dtype == dtype and t.shape == shape and t.is_contiguous()):
+        _look(t, dtype, shape, name)
     return t.data_ptr()
 
 
@@ -483,6 +517,13 @@ def _buffer(nbytes, zeroed, what):
         raise GPTQError(-2, what)
     make = _torch().zeros if zeroed else _torch().empty
     return make(nbytes, dtype=_torch().uint8, device="cuda")
+
+
+def _workspace(t):
+    """(address, bytes) of a workspace tensor."""
+    if not (t.is_cuda and t.is_contiguous()):
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    return t.data_ptr(), t.nbytes
 
 
 def paged_attention_workspace_size(heads, kv_heads, head_dim):
@@ -495,8 +536,8 @@ def paged_attention_workspace(heads, kv_heads, head_dim):
     return _buffer(paged_attention_workspace_size(heads, kv_heads, head_dim), True, "gptq_paged_attention_workspace_size")
 
 
-def _token_rows(t, dtype, shape, name):
-    """(address, stride between sequences) of [batch, heads, dim] rows that are contiguous within a sequence."""
+def _look_rows(t, dtype, shape, name):
+    """Raises what is wrong with [batch, heads, dim] rows that should be contiguous within a sequence."""
     if not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
     if t.dtype != dtype:
@@ -506,7 +547,15 @@ def _token_rows(t, dtype, shape, name):
     stride = t.stride()
     if stride[2] != 1 or (shape[1] > 1 and stride[1] != shape[2]):
         raise ValueError("%s: the heads of a sequence must be contiguous" % name)
-    return t.data_ptr(), stride[0] if shape[0] > 1 else 0
+
+
+def _look_cache(t, dtype, shape, name):
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.shape != shape or t.stride()[3] != 1:
+        raise ValueError("%s must be [pages, page_size, kv_heads, dim] = %s with contiguous rows" % (name, tuple(shape)))
 
 
 def paged_attention(q, k_cache, v_cache, block_table, seq_lens, *, scale=None, window=0, k_new=None, v_new=None,
@@ -518,46 +567,59 @@ def paged_attention(q, k_cache, v_cache, block_table, seq_lens, *, scale=None, w
     only the last `window` keys.  scale: dim ** -0.5 where not given.  lse [batch, heads] fp32 takes
     the log of each row's exponential sum.  A workspace (paged_attention_workspace) is made here
     when none is given."""
-    torch = _torch()
-    batch, heads, dim = q.shape
-    pages, page_size, kv_heads, _ = k_cache.shape
-    dtype, code = q.dtype, _dtype_code(q)
-    q_ptr, q_stride = _token_rows(q, dtype, q.shape, "q")
-    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if not t.is_cuda:
-            raise ValueError("%s must be a CUDA tensor" % name)
-        if t.dtype != dtype:
-            raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-        if t.shape != (pages, page_size, kv_heads, dim) or t.stride(3) != 1:
-            raise ValueError("%s must be [pages, page_size, kv_heads, dim] with contiguous rows" % name)
-    if (k_new is None) != (v_new is None):
-        raise ValueError("k_new and v_new go together")
+    rt = _rt or _runtime()
+    batch, heads, dim = shape = q.shape
+    pages, page_size, kv_heads, _ = cache_shape = k_cache.shape
+    dtype, i32 = q.dtype, rt.int32
+    code = rt.codes.get(dtype, F32)
+    if code == F32:
+        raise TypeError("q must be float16 or bfloat16, got %s" % dtype)
+    table_shape, lens_shape = block_table.shape, seq_lens.shape
+    qs, ks, vs = q.stride(), k_cache.stride(), v_cache.stride()
+    if not (q.is_cuda and qs[2] == 1 and (qs[1] == dim or heads == 1)):
+        _look_rows(q, dtype, shape, "q")
+    if not (k_cache.is_cuda and v_cache.is_cuda and k_cache.dtype == dtype and v_cache.dtype == dtype
+            and v_cache.shape == cache_shape and cache_shape[3] == dim and ks[3] == 1 and vs[3] == 1):
+        for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+            _look_cache(t, dtype, (pages, page_size, kv_heads, dim), name)
+    if not (block_table.is_cuda and seq_lens.is_cuda and block_table.dtype == i32 and seq_lens.dtype == i32
+            and len(table_shape) == 2 and table_shape[0] == batch and len(lens_shape) == 1 and lens_shape[0] == batch
+            and block_table.is_contiguous() and seq_lens.is_contiguous()):
+        if len(table_shape) != 2:
+            raise ValueError("block_table must be [batch, width]")
+        _look(block_table, i32, (batch, table_shape[1]), "block_table")
+        _look(seq_lens, i32, (batch,), "seq_lens")
     kn = vn = None
     kn_stride = vn_stride = 0
-    if k_new is not None:
-        kn, kn_stride = _token_rows(k_new, dtype, (batch, kv_heads, dim), "k_new")
-        vn, vn_stride = _token_rows(v_new, dtype, (batch, kv_heads, dim), "v_new")
-    if block_table.dim() != 2 or block_table.shape[0] != batch:
-        raise ValueError("block_table must be [batch, width]")
-    table_ptr = _cuda(block_table, torch.int32, block_table.shape, "block_table")
-    lens_ptr = _cuda(seq_lens, torch.int32, (batch,), "seq_lens")
+    if k_new is not None or v_new is not None:
+        if k_new is None or v_new is None:
+            raise ValueError("k_new and v_new go together")
+        new_shape = (batch, kv_heads, dim)
+        ns, nv = k_new.stride(), v_new.stride()
+        if not (k_new.is_cuda and v_new.is_cuda and k_new.dtype == dtype and v_new.dtype == dtype and k_new.shape == new_shape
+                and v_new.shape == new_shape and ns[2] == 1 and nv[2] == 1 and ns[1] == dim and nv[1] == dim):
+            _look_rows(k_new, dtype, new_shape, "k_new")
+            _look_rows(v_new, dtype, new_shape, "v_new")
+        kn, vn, kn_stride, vn_stride = k_new.data_ptr(), v_new.data_ptr(), ns[0], nv[0]
     if out is None:
-        out = torch.empty((batch, heads, dim), dtype=dtype, device=q.device)
+        out = q.new_empty(shape)
         out_ptr = out.data_ptr()
     else:
-        out_ptr = _cuda(out, dtype, (batch, heads, dim), "out")
-    lse_ptr = None if lse is None else _cuda(lse, torch.float32, (batch, heads), "lse")
+        out_ptr = _address(out, dtype, shape, "out")
+    lse_ptr = None if lse is None else _address(lse, rt.float32, (batch, heads), "lse")
     if workspace is None:
         workspace = paged_attention_workspace(heads, kv_heads, dim)
-    k_stride, v_stride = k_cache.stride(), v_cache.stride()
-    strides = _Strides(q_stride, kn_stride, vn_stride, k_stride[0], k_stride[1], k_stride[2], v_stride[0], v_stride[1],
-                       v_stride[2])
-    rc = lib().gptq_paged_attention(q_ptr, batch, heads, code, k_cache.data_ptr(), v_cache.data_ptr(), pages, page_size,
-                                    kv_heads, dim, strides, table_ptr, block_table.shape[1], lens_ptr, kn, vn,
-                                    dim ** -0.5 if scale is None else scale, window, out_ptr, lse_ptr,
-                                    _ptr(workspace, name="workspace"), workspace.numel() * workspace.element_size(),
-                                    _stream(stream))
-    _check(rc, "gptq_paged_attention")
+    ws, ws_bytes = _workspace(workspace)
+    if batch == 1:                     # the strides of a dimension of one may be anything
+        strides = _Strides(0, 0, 0, ks[0], ks[1], ks[2], vs[0], vs[1], vs[2])
+    else:
+        strides = _Strides(qs[0], kn_stride, vn_stride, ks[0], ks[1], ks[2], vs[0], vs[1], vs[2])
+    rc = rt.lib.gptq_paged_attention(q.data_ptr(), batch, heads, code, k_cache.data_ptr(), v_cache.data_ptr(), pages, page_size,
+                                     kv_heads, dim, strides, block_table.data_ptr(), table_shape[1], seq_lens.data_ptr(), kn, vn,
+                                     dim ** -0.5 if scale is None else scale, window, out_ptr, lse_ptr, ws, ws_bytes,
+                                     rt.stream() if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "gptq_paged_attention")
     return out
 
 
@@ -580,36 +642,54 @@ def moe_layer(x, router, up, down, *, topk, bits, group, fmt=V2, renormalize=Tru
     first `inter` columns, down = (qweight [E, inter*bits/32, hidden], qzeros, scales); layouts as
     for gemm_grouped.  Returns out [tokens, hidden], or (out, ids, weights) with return_routing.  A
     workspace (moe_workspace) is made here when none is given."""
-    torch = _torch()
-    tokens, hidden = x.shape
+    rt = _rt or _runtime()
+    tokens, hidden = shape = x.shape
     experts = router.shape[0]
-    inter = up[0].shape[2] // 2
-    dtype, code = x.dtype, _dtype_code(x)
-    x_ptr = _cuda(x, dtype, (tokens, hidden), "x")
-    router_ptr = _cuda(router, dtype, (experts, hidden), "router")
-    ptrs = []
-    for weight, K, N, name in ((up, hidden, 2 * inter, "up"), (down, inter, hidden, "down")):
-        G = 1 if group == -1 else K // max(1, group)
-        ptrs.append(_cuda(weight[0], torch.int32, (experts, K * bits // 32, N), name + " qweight"))
-        ptrs.append(_cuda(weight[1], torch.int32, (experts, G, N * bits // 32), name + " qzeros"))
-        ptrs.append(_cuda(weight[2], torch.float16, (experts, G, N), name + " scales"))
+    uq, uz, us = up
+    dq, dz, ds = down
+    inter = uq.shape[2] // 2
+    dtype, i32, f16 = x.dtype, rt.int32, rt.float16
+    code = rt.codes.get(dtype, F32)
+    if code == F32:
+        raise TypeError("x must be float16 or bfloat16, got %s" % dtype)
+    Gu, Gd = (1, 1) if group == -1 else (hidden // max(1, group), inter // max(1, group))
+    if not (x.is_cuda and router.is_cuda and router.dtype == dtype and router.shape == (experts, hidden)
+            and x.is_contiguous() and router.is_contiguous()):
+        _look(x, dtype, shape, "x")
+        _look(router, dtype, (experts, hidden), "router")
+    if not (uq.is_cuda and uz.is_cuda and us.is_cuda and dq.is_cuda and dz.is_cuda and ds.is_cuda
+            and uq.dtype == i32 and uz.dtype == i32 and us.dtype == f16 and dq.dtype == i32 and dz.dtype == i32 and ds.dtype == f16
+            and uq.shape == (experts, hidden * bits // 32, 2 * inter) and uz.shape == (experts, Gu, inter * bits // 16)
+            and us.shape == (experts, Gu, 2 * inter) and dq.shape == (experts, inter * bits // 32, hidden)
+            and dz.shape == (experts, Gd, hidden * bits // 32) and ds.shape == (experts, Gd, hidden)
+            and uq.is_contiguous() and uz.is_contiguous() and us.is_contiguous()
+            and dq.is_contiguous() and dz.is_contiguous() and ds.is_contiguous()):
+        for weight, K, N, G, name in ((up, hidden, 2 * inter, Gu, "up"), (down, inter, hidden, Gd, "down")):
+            _look(weight[0], i32, (experts, K * bits // 32, N), name + " qweight")
+            _look(weight[1], i32, (experts, G, N * bits // 32), name + " qzeros")
+            _look(weight[2], f16, (experts, G, N), name + " scales")
     if out is None:
-        out = torch.empty((tokens, hidden), dtype=dtype, device=x.device)
+        out = x.new_empty(shape)
         out_ptr = out.data_ptr()
     else:
-        out_ptr = _cuda(out, dtype, (tokens, hidden), "out")
-    ids = weights = None
+        out_ptr = _address(out, dtype, shape, "out")
+    ids = weights = ids_ptr = weights_ptr = None
     if return_routing:
-        ids = torch.empty((tokens, topk), dtype=torch.int32, device=x.device)
-        weights = torch.empty((tokens, topk), dtype=torch.float32, device=x.device)
+        # the choices and their weights share an allocation: two 4-byte values each
+        both = x.new_empty((2, tokens, topk), dtype=i32)
+        ids, weights = both[0], both[1].view(rt.float32)
+        ids_ptr = both.data_ptr()
+        weights_ptr = ids_ptr + 4 * tokens * topk
+    ws = ws_bytes = 0
     if workspace is None and tokens > 0:
         workspace = moe_workspace(tokens, hidden, inter, experts, topk)
-    rc = lib().gptq_moe(x_ptr, tokens, hidden, inter, code, router_ptr, experts, topk, int(bool(renormalize)), *ptrs,
-                        bits, group, fmt, out_ptr, None if ids is None else ids.data_ptr(),
-                        None if weights is None else weights.data_ptr(),
-                        None if workspace is None else _ptr(workspace, name="workspace"),
-                        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream))
-    _check(rc, "gptq_moe")
+    if workspace is not None:
+        ws, ws_bytes = _workspace(workspace)
+    rc = rt.lib.gptq_moe(x.data_ptr(), tokens, hidden, inter, code, router.data_ptr(), experts, topk, 1 if renormalize else 0,
+                         uq.data_ptr(), uz.data_ptr(), us.data_ptr(), dq.data_ptr(), dz.data_ptr(), ds.data_ptr(), bits, group,
+                         fmt, out_ptr, ids_ptr, weights_ptr, ws, ws_bytes, rt.stream() if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "gptq_moe")
     return (out, ids, weights) if return_routing else out
 
 
@@ -619,24 +699,33 @@ def sample(logits, uniform, *, temperature=None, top_k=None, top_p=None, min_p=N
     fp32; top_k int32; None: off) -> (token [batch] int32, logprob [batch] fp32), written into `out` =
     (token, logprob) when given.  Among the kept tokens the first, in index order, whose cumulated
     probability exceeds the uniform number."""
-    torch = _torch()
+    rt = _rt or _runtime()
     batch, vocab = logits.shape
-    code = F32 if logits.dtype == torch.float32 else _dtype_code(logits)
+    code = rt.codes.get(logits.dtype)
+    if code is None:
+        raise TypeError("logits must be float16, bfloat16 or float32, got %s" % logits.dtype)
+    row, col = logits.stride()
     if not logits.is_cuda:
         raise ValueError("logits must be a CUDA tensor")
-    if vocab > 1 and logits.stride(1) != 1:
+    if col != 1 and vocab > 1:
         raise ValueError("logits: a row must be contiguous")
-    row = logits.stride(0) if batch > 1 else vocab
-    ptrs = [_cuda(uniform, torch.float32, (batch,), "uniform")]
-    for t, dtype, name in ((temperature, torch.float32, "temperature"), (top_k, torch.int32, "top_k"),
-                           (top_p, torch.float32, "top_p"), (min_p, torch.float32, "min_p")):
-        ptrs.append(None if t is None else _cuda(t, dtype, (batch,), name))
+    f32, one = rt.float32, (batch,)
+    u_ptr = _address(uniform, f32, one, "uniform")
+    t_ptr = None if temperature is None else _address(temperature, f32, one, "temperature")
+    k_ptr = None if top_k is None else _address(top_k, rt.int32, one, "top_k")
+    p_ptr = None if top_p is None else _address(top_p, f32, one, "top_p")
+    m_ptr = None if min_p is None else _address(min_p, f32, one, "min_p")
     if out is None:
-        token = torch.empty(batch, dtype=torch.int32, device=logits.device)
-        logprob = torch.empty(batch, dtype=torch.float32, device=logits.device)
+        # a token and a log probability, 4 bytes each, in one allocation
+        both = logits.new_empty((2, batch), dtype=rt.int32)
+        token, logprob = both[0], both[1].view(f32)
+        token_ptr = both.data_ptr()
+        logprob_ptr = token_ptr + 4 * batch
     else:
         token, logprob = out
-    rc = lib().gptq_sample(logits.data_ptr(), batch, vocab, row, code, *ptrs, _cuda(token, torch.int32, (batch,), "token"),
-                           _cuda(logprob, torch.float32, (batch,), "logprob"), _stream(stream))
-    _check(rc, "gptq_sample")
+        token_ptr, logprob_ptr = _address(token, rt.int32, one, "token"), _address(logprob, f32, one, "logprob")
+    rc = rt.lib.gptq_sample(logits.data_ptr(), batch, vocab, row if batch > 1 else vocab, code, u_ptr, t_ptr, k_ptr, p_ptr, m_ptr,
+                            token_ptr, logprob_ptr, rt.stream() if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "gptq_sample")
     return token, logprob
