@@ -220,6 +220,24 @@ __device__ __forceinline__ void store_run(const float (&v)[4], int j0, int K, __
   if (lane % (tile / 4) == 0 && j < K) sums[4 * lane / tile] = sum * (1.f / 16777216.f) * pow2(e);
 }
 
+// Loads from shared memory by 32-bit address (a generic pointer costs 64-bit additions in the main loop);
+// volatile, so that none moves ahead of the wait for its stage.
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+
 // Shared memory: [stages][weights | activations | their sums and scales | group scales | group zeros], the
 // output tile [tokens][kCols] floats, 2 mbarriers per stage, the routing.
 template <int BITS>
@@ -784,14 +802,15 @@ __global__ void __launch_bounds__(kThreads, (ctas_of(NB))) k_experts(const __gri
   // this thread's places in a stage: its pieces of the weights (tile l at w_at[l & 1] + 512 l; the swizzle
   // goes by the 128-byte line within the stage), scales and zeros, and its rows' activations and sums
   int w_at[BITS == 3 ? ROWS : 2], act_at[NB], info_at[NB][2];
-  const int scales_at = L::scales(a.tokens) + 2 * col0, zeros_at = L::zeros(a.tokens, a.gmax) + 4 * warp * BITS;
+  const int scales_at = L::scales(a.tokens) + 2 * col0;
+  const int zeros_at = L::zeros(a.tokens, a.gmax) + 4 * (warp * BITS + BITS * quad * 4 / 32), zero_shift = BITS * quad * 4 % 32;
 #pragma unroll
   for (int i = 0; i < (BITS == 3 ? ROWS : 2); ++i) {
     const int row = BITS == 3 ? tq * ROWS + i : 4 * i + tq, line = warp * C::kRows + row;
     w_at[i] = line * 128 + ((quad ^ (line & 7)) << 4) - (BITS == 3 ? 0 : 512 * i);
   }
   const float zero_base = 8388608.f - static_cast<float>(a.zero_offset);
-  const uint8_t* base = smem;                              // of the stage
+  uint32_t base = smem_a;                                  // of the stage
   int st = 0, g_at = 0;                                    // g_at: k of the chunk within its first group
   unsigned round = 0;
   while (x.u < limit) {
@@ -810,21 +829,18 @@ __global__ void __launch_bounds__(kThreads, (ctas_of(NB))) k_experts(const __gri
       }
     }
     if (__all_sync(0xFFFFFFFFu, wait(full(st), round, &sm_abort, a.status))) {
-      const __half* scales = reinterpret_cast<const __half*>(base + scales_at);
-      const uint32_t* zeros = reinterpret_cast<const uint32_t*>(base + zeros_at);
       const int k0 = x.kc * C::kK;
       const int tiles = a.K - k0 < C::kK ? (a.K - k0) / C::kTileK : C::kTiles;
       float gs[4], gz[4];                                  // scales and zeros of this thread's 4 columns
       auto load_group = [&](int g) {
-        const uint2 s = *reinterpret_cast<const uint2*>(scales + g * kCols);
+        const uint2 s = lds64(base + scales_at + g * (kCols * 2));
         gs[0] = __half2float(__ushort_as_half(lo16(s.x)));
         gs[1] = __half2float(__ushort_as_half(hi16(s.x)));
         gs[2] = __half2float(__ushort_as_half(lo16(s.y)));
         gs[3] = __half2float(__ushort_as_half(hi16(s.y)));
-        const uint32_t* zw = zeros + g * C::kZeroWords;
-        const int bit = BITS * quad * 4;
-        uint32_t zf = zw[bit >> 5] >> (bit & 31);
-        if (BITS == 3 && (bit & 31) + 12 > 32) zf = __funnelshift_r(zw[bit >> 5], zw[(bit >> 5) + 1], bit & 31);
+        const uint32_t zw = base + zeros_at + g * (C::kZeroWords * 4);
+        uint32_t zf = lds32(zw) >> zero_shift;
+        if (BITS == 3) zf = zero_shift + 12 > 32 ? zf | lds32(zw + 4) << (32 - zero_shift) : zf;
 #pragma unroll
         for (int c = 0; c < 4; ++c)                        // 2^23 + z - 2^23
           gz[c] = __uint_as_float(0x4B000000u | ((zf >> (BITS * c)) & P::kMask)) - zero_base;
@@ -834,9 +850,9 @@ __global__ void __launch_bounds__(kThreads, (ctas_of(NB))) k_experts(const __gri
 #pragma unroll
         for (int r = 0; r < ROWS; ++r) {
           if constexpr (BITS == 3) {
-            w[r] = *reinterpret_cast<const uint4*>(base + w_at[r]);
+            w[r] = lds128(base + w_at[r]);
           } else {
-            w[r] = *reinterpret_cast<const uint4*>(base + w_at[l & 1] + l * 512);
+            w[r] = lds128(base + w_at[l & 1] + l * 512);
           }
         }
         uint32_t d[4][NP];
@@ -849,15 +865,15 @@ __global__ void __launch_bounds__(kThreads, (ctas_of(NB))) k_experts(const __gri
         for (int nb = 0; nb < NB; ++nb) {
           if (nb == 0 || 8 * nb < rows) {
             uint32_t b[NP];
-            const uint8_t* src = base + act_at[nb] + l * (NP * 16);
+            const uint32_t src = base + act_at[nb] + l * (NP * 16);
             if constexpr (NP % 4 == 0) {
 #pragma unroll
               for (int i = 0; i < NP / 4; ++i) {
-                const uint4 v = reinterpret_cast<const uint4*>(src)[i];
+                const uint4 v = lds128(src + 16 * i);
                 b[4 * i] = v.x; b[4 * i + 1] = v.y; b[4 * i + 2] = v.z; b[4 * i + 3] = v.w;
               }
             } else {
-              const uint2 v = *reinterpret_cast<const uint2*>(src);
+              const uint2 v = lds64(src);
               b[0] = v.x; b[1] = v.y;
             }
 #pragma unroll
@@ -877,14 +893,14 @@ __global__ void __launch_bounds__(kThreads, (ctas_of(NB))) k_experts(const __gri
             float s[2], sum[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              const float* row = reinterpret_cast<const float*>(base + info_at[nb][i]);
-              s[i] = row[C::kTiles + l0 * C::kTileK / kRun];
+              const uint32_t row = base + info_at[nb][i];
+              s[i] = __uint_as_float(lds32(row + 4 * (C::kTiles + l0 * C::kTileK / kRun)));
               if (C::kTiles == 4 && l0 == 0 && l1 == 3) {
-                const float4 v = *reinterpret_cast<const float4*>(row);
-                sum[i] = (v.x + v.y) + (v.z + v.w);
+                const uint4 v = lds128(row);
+                sum[i] = (__uint_as_float(v.x) + __uint_as_float(v.y)) + (__uint_as_float(v.z) + __uint_as_float(v.w));
               } else {
-                sum[i] = row[l0];
-                for (int l = l0 + 1; l <= l1; ++l) sum[i] += row[l];
+                sum[i] = __uint_as_float(lds32(row + 4 * l0));
+                for (int l = l0 + 1; l <= l1; ++l) sum[i] += __uint_as_float(lds32(row + 4 * l));
               }
             }
 #pragma unroll
@@ -933,7 +949,7 @@ __global__ void __launch_bounds__(kThreads, (ctas_of(NB))) k_experts(const __gri
     if (++st == a.stages) {
       st = 0;
       round ^= 1;
-      base = smem;
+      base = smem_a;
     }
     g_at += C::kK;
     while (g_at >= a.group) g_at -= a.group;
