@@ -1,5 +1,7 @@
 // moe.cuh -- the expert products of the mixture-of-experts layer (gptq_moe) for up to 32 tokens.
 //
+// An expert's rows are taken in blocks of 8 NB; a block, with its expert, is a slot.
+//
 // Two launches after the router's (moe.cu, which leaves the logits): UP writes h = silu(x Wg) * (x Wu) for every (expert,
 // token) row, DOWN writes out[t] = sum over t's experts of w * (h Wd).  Both are a stream of packed
 // weights -- those of the chosen experts, each read once -- against a few activations, bound by HBM or,
@@ -50,8 +52,7 @@ constexpr int kItemUnits = 2;            // what opening and writing an item tak
 constexpr int kMinShare = 4;             // chunks of a run, at least: a join of more parts costs more than it saves
 constexpr int kMaxStages = 12;
 
-// CTAs on an SM, by what the registers allow
-__host__ __device__ constexpr int ctas_of(int nb) { return nb == 4 ? 1 : 2; }
+constexpr int kCtas = 2;                 // on an SM
 
 template <int BITS>
 struct Chunk {
@@ -77,12 +78,15 @@ struct Routing {
   int* id;               // [pairs] expert of (token, choice)
   float* w;              // [pairs] its weight
   int* count;            // [experts] rows, then first row
-  int* slot_expert;      // [slots] chosen experts in order
+  int* slot_expert;      // [slots] chosen experts in order, as often as they have blocks of rows
   int* slot_off;         // [slots + 1] their rows: [slot_off[s], slot_off[s + 1])
   int* row_token;        // [pairs] rows by expert, an expert's by token
   float* row_weight;
+  __host__ __device__ static int most_slots(int pairs, int experts) {
+    return (pairs < experts ? pairs : experts) + pairs / 8;
+  }
   __host__ __device__ static int bytes(int pairs, int experts) {
-    return (16 * pairs + 4 * experts + 8 * (pairs < experts ? pairs : experts) + 4 + 15) & ~15;
+    return (16 * pairs + 4 * experts + 8 * most_slots(pairs, experts) + 4 + 15) & ~15;
   }
 };
 
@@ -90,7 +94,8 @@ struct Args {
   int K, N, group, G, zero_offset, zwords, units;
   const int32_t* qzeros;
   const __half* scales;
-  int tokens;            // rows of the ring's activation part
+  int tokens;
+  int rows;              // of a slot, at most; of the ring's activation part
   int experts, topk, renormalize;
   const float* logits;   // [tokens][experts]
   int32_t* ids;          // UP, nullable: the caller's copies
@@ -239,21 +244,21 @@ __device__ __forceinline__ uint32_t lds32(uint32_t a) {
 }
 
 // Shared memory: [stages][weights | activations | their sums and scales | group scales | group zeros], the
-// output tile [tokens][kCols] floats, 2 mbarriers per stage, the routing.
+// output tile [tokens (DOWN) or rows][kCols] floats, 2 mbarriers per stage, the routing.
 template <int BITS>
 struct Layout {
   using C = Chunk<BITS>;
   __host__ __device__ static constexpr int act() { return kWarps * C::kSlot; }
-  __host__ __device__ static int info(int tokens) { return act() + tokens * C::kActRow; }
-  __host__ __device__ static int scales(int tokens) { return info(tokens) + tokens * C::kInfo * 4; }
-  __host__ __device__ static int zeros(int tokens, int gmax) { return scales(tokens) + gmax * kCols * 2; }
-  __host__ __device__ static int stage(int tokens, int gmax) {
-    return (zeros(tokens, gmax) + gmax * C::kZeroWords * 4 + 1023) & ~1023;
+  __host__ __device__ static int info(int rows) { return act() + rows * C::kActRow; }
+  __host__ __device__ static int scales(int rows) { return info(rows) + rows * C::kInfo * 4; }
+  __host__ __device__ static int zeros(int rows, int gmax) { return scales(rows) + gmax * kCols * 2; }
+  __host__ __device__ static int stage(int rows, int gmax) {
+    return (zeros(rows, gmax) + gmax * C::kZeroWords * 4 + 1023) & ~1023;
   }
-  __host__ __device__ static int tile_bytes(int tokens) { return tokens * kCols * 4; }
+  __host__ __device__ static int tile_bytes(int rows) { return rows * kCols * 4; }
   // less the stages and their mbarriers
-  __host__ __device__ static int fixed(int tokens, int pairs, int experts) {
-    return 1024 + tile_bytes(tokens) + Routing::bytes(pairs, experts);
+  __host__ __device__ static int fixed(int tile_rows, int pairs, int experts) {
+    return 1024 + tile_bytes(tile_rows) + Routing::bytes(pairs, experts);
   }
 };
 
@@ -282,7 +287,7 @@ __device__ __forceinline__ float logit_of(unsigned key) {
 
 // Softmax, top-k (equal logits: the lower index; a NaN ranks as -inf) and grouping by expert, by the
 // whole CTA; returns the number of chosen experts.  scratch: a row of `experts` floats per warp.
-__device__ __forceinline__ int route(const Args& a, const Routing& r, float* scratch, int (*scan)[2], bool publish) {
+__device__ __forceinline__ int route(const Args& a, const Routing& r, float* scratch, int* scan, bool publish) {
   constexpr int kAll = kThreads / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const float inf = __int_as_float(0x7F800000);
@@ -337,34 +342,35 @@ __device__ __forceinline__ int route(const Args& a, const Routing& r, float* scr
     if (publish && a.weights) a.weights[p] = r.w[p];
   }
   __syncthreads();
-  // experts with rows, in order: a scan of (chosen, rows), a CTA's threads at a time
+  // experts with rows, in order: a scan of (blocks, rows), a CTA's threads at a time
   int slots = 0, rows = 0;
   for (int e0 = 0; e0 < a.experts; e0 += kThreads) {
     const int e = e0 + static_cast<int>(threadIdx.x), n = e < a.experts ? r.count[e] : 0;
-    const unsigned chosen = __ballot_sync(0xFFFFFFFFu, n > 0);
-    int c = n;
+    const int mine = n | (n + a.rows - 1) / a.rows << 16;  // rows, and blocks of them
+    int c = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int v = __shfl_up_sync(0xFFFFFFFFu, c, o);
       if (lane >= o) c += v;
     }
-    if (lane == 31) {
-      scan[warp][0] = __popc(chosen);
-      scan[warp][1] = c;
-    }
+    if (lane == 31) scan[warp] = c;
     __syncthreads();
-    int s = slots + __popc(chosen & ((1u << lane) - 1u)), off = rows + c - n;
+    int at = c - mine;
     for (int w = 0; w < kAll; ++w) {
-      if (w < warp) {
-        s += scan[w][0];
-        off += scan[w][1];
-      }
-      slots += scan[w][0];
-      rows += scan[w][1];
+      if (w < warp) at += scan[w];
+    }
+    at += slots << 16 | rows;
+    for (int w = 0; w < kAll; ++w) {
+      slots += scan[w] >> 16;
+      rows += scan[w] & 0xFFFF;
     }
     if (n > 0) {
-      r.slot_expert[s] = e;
-      r.slot_off[s] = off;
+      const int off = at & 0xFFFF;
+      int s = at >> 16;
+      for (int m = 0; m < n; m += a.rows, ++s) {
+        r.slot_expert[s] = e;
+        r.slot_off[s] = off + m;
+      }
       r.count[e] = off;
     }
     __syncthreads();
@@ -406,33 +412,33 @@ struct Cursor {
 };
 
 template <int BITS, int NB, bool DOWN>
-__global__ void __launch_bounds__(kThreads, (ctas_of(NB))) k_experts(const __grid_constant__ CUtensorMap tmW, const Args a) {
+__global__ void __launch_bounds__(kThreads, kCtas) k_experts(const __grid_constant__ CUtensorMap tmW, const Args a) {
   using P = Pack<BITS>;
   using C = Chunk<BITS>;
   using L = Layout<BITS>;
   using RP = RawPairs<BITS>;
   constexpr int NP = RP::kPairs, ROWS = P::kRowsPerUnit;
   extern __shared__ __align__(128) unsigned char smem_raw[];
-  __shared__ int sm_abort, sm_last, sm_scan[kThreads / 32][2];
+  __shared__ int sm_abort, sm_last, sm_scan[kThreads / 32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   uint8_t* smem = smem_raw + ((1024u - (ptx::smem_addr(smem_raw) & 1023u)) & 1023u);
   const uint32_t smem_a = ptx::smem_addr(smem);
   const int stage_bytes = a.stage_bytes;
   float* tile = reinterpret_cast<float*>(smem + a.stages * stage_bytes);
-  const uint32_t bars = ptx::smem_addr(tile) + L::tile_bytes(a.tokens);
+  const uint32_t bars = ptx::smem_addr(tile) + L::tile_bytes(DOWN ? a.tokens : a.rows);
   auto full = [&](int s) { return bars + 16u * s; };
   auto empty = [&](int s) { return bars + 16u * s + 8u; };
   Routing rt;
   {
-    const int pairs = a.tokens * a.topk, most = pairs < a.experts ? pairs : a.experts;
-    rt.id = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(tile) + L::tile_bytes(a.tokens) + 16 * a.stages);
+    const int pairs = a.tokens * a.topk;
+    rt.id = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(tile) + L::tile_bytes(DOWN ? a.tokens : a.rows) + 16 * a.stages);
     rt.w = reinterpret_cast<float*>(rt.id + pairs);
     rt.row_token = reinterpret_cast<int*>(rt.w + pairs);
     rt.row_weight = reinterpret_cast<float*>(rt.row_token + pairs);
     rt.count = reinterpret_cast<int*>(rt.row_weight + pairs);
     rt.slot_expert = rt.count + a.experts;
-    rt.slot_off = rt.slot_expert + most;
+    rt.slot_off = rt.slot_expert + Routing::most_slots(pairs, a.experts);
   }
   // UP waits for the router's kernel and only then lets DOWN start; so the logits are final for DOWN from
   // its first instruction, and it streams its first weights while UP still runs.
@@ -568,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, (ctas_of(NB))) k_experts(const __gri
       const __half* sc = p.sc;
       const int32_t* z0 = p.zr[0];
       const int32_t* z1 = p.zr[1];
-      uint32_t sc_to = to + L::scales(a.tokens) + lane * 16, z_to = to + L::zeros(a.tokens, a.gmax) + lane * 4;
+      uint32_t sc_to = to + L::scales(a.rows) + lane * 16, z_to = to + L::zeros(a.rows, a.gmax) + lane * 4;
       for (int at = -p.g_at; at < ck; at += a.group) {      // the groups that the chunk touches
         if (p.sc_col >= 0) cp_async16(sc_to, sc);
         if (p.zc[0] >= 0) cp_async4(z_to, z0);
@@ -594,7 +600,7 @@ __global__ void __launch_bounds__(kThreads, (ctas_of(NB))) k_experts(const __gri
                      a.act + static_cast<long long>(row) * a.K + p.x.kc * C::kK + piece * 8);
       }
       if (lane < p.rows) {
-        const uint32_t info = to + L::info(a.tokens) + lane * C::kInfo * 4;
+        const uint32_t info = to + L::info(a.rows) + lane * C::kInfo * 4;
         if (C::kTiles == 4 && a.K % (4 * C::kTileK) == 0) {
           cp_async16(info, p.act_sum);
         } else {
@@ -802,8 +808,8 @@ __global__ void __launch_bounds__(kThreads, (ctas_of(NB))) k_experts(const __gri
   // this thread's places in a stage: its pieces of the weights (tile l at w_at[l & 1] + 512 l; the swizzle
   // goes by the 128-byte line within the stage), scales and zeros, and its rows' activations and sums
   int w_at[BITS == 3 ? ROWS : 2], act_at[NB], info_at[NB][2];
-  const int scales_at = L::scales(a.tokens) + 2 * col0;
-  const int zeros_at = L::zeros(a.tokens, a.gmax) + 4 * (warp * BITS + BITS * quad * 4 / 32), zero_shift = BITS * quad * 4 % 32;
+  const int scales_at = L::scales(a.rows) + 2 * col0;
+  const int zeros_at = L::zeros(a.rows, a.gmax) + 4 * (warp * BITS + BITS * quad * 4 / 32), zero_shift = BITS * quad * 4 % 32;
 #pragma unroll
   for (int i = 0; i < (BITS == 3 ? ROWS : 2); ++i) {
     const int row = BITS == 3 ? tq * ROWS + i : 4 * i + tq, line = warp * C::kRows + row;
@@ -824,7 +830,7 @@ __global__ void __launch_bounds__(kThreads, (ctas_of(NB))) k_experts(const __gri
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int mi = 8 * nb + 2 * tq + i;
-          info_at[nb][i] = L::info(a.tokens) + (mi < rows ? mi : rows - 1) * (C::kInfo * 4);
+          info_at[nb][i] = L::info(a.rows) + (mi < rows ? mi : rows - 1) * (C::kInfo * 4);
         }
       }
     }
@@ -1011,22 +1017,23 @@ cudaError_t launch_experts(Args a, const int32_t* qweight, int experts, int* run
   const DeviceInfo& dev = device_info();
   a.units = a.K / Pack<BITS>::kPerUnit;
   a.zwords = a.N / 32 * BITS;
+  a.rows = a.tokens < 8 * NB ? a.tokens : 8 * NB;
   a.gmax = (C::kK - 1) / a.group + 2;
   if (a.group % C::kK == 0) a.gmax = 1;
   else if (C::kK % a.group == 0) a.gmax = C::kK / a.group;
-  a.stage_bytes = L::stage(a.tokens, a.gmax);
+  a.stage_bytes = L::stage(a.rows, a.gmax);
   const int pairs = a.tokens * a.topk;
-  int per_sm = ctas_of(NB);
+  int per_sm = kCtas;
   auto fit = [&](int ctas) {
     const int budget = ctas > 1 ? 233472 / ctas - 1024 - 512 : 227 * 1024 - 512;   // less the static part
-    return (budget - L::fixed(a.tokens, pairs, experts)) / (a.stage_bytes + 16);
+    return (budget - L::fixed(DOWN ? a.tokens : a.rows, pairs, experts)) / (a.stage_bytes + 16);
   };
   a.stages = fit(per_sm);
   while (per_sm > 1 && a.stages < 3) a.stages = fit(--per_sm);
   if (a.stages > kMaxStages) a.stages = kMaxStages;
   // the router's scratch lies over the ring
   if (a.stages < 2 || a.stages * a.stage_bytes < kThreads / 32 * experts * 4) return cudaErrorInvalidConfiguration;
-  const int smem = L::fixed(a.tokens, pairs, experts) + a.stages * (a.stage_bytes + 16);
+  const int smem = L::fixed(DOWN ? a.tokens : a.rows, pairs, experts) + a.stages * (a.stage_bytes + 16);
   static std::atomic<unsigned long long> opted_in{0};       // per device
   if (dev.device >= 64 || !(opted_in.load(std::memory_order_relaxed) & (1ull << dev.device))) {
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024 - 512);
@@ -1060,9 +1067,10 @@ cudaError_t launch_experts(Args a, const int32_t* qweight, int experts, int* run
 
 template <int BITS, bool DOWN>
 cudaError_t launch_blocks(const Args& a, const int32_t* qweight, int experts, int* runs, cudaStream_t stream) {
-  if (a.tokens <= 8) return launch_experts<BITS, 1, DOWN>(a, qweight, experts, runs, stream);
-  if (a.tokens <= 16) return launch_experts<BITS, 2, DOWN>(a, qweight, experts, runs, stream);
-  return launch_experts<BITS, 4, DOWN>(a, qweight, experts, runs, stream);
+  // blocks of 8 rows where few experts have more: the others' weights are read once for each block
+  // (16 tokens, 2 of 8 experts each: 204 us in blocks of 16)
+  if (a.tokens <= 8 || a.tokens * a.topk <= 4 * a.experts) return launch_experts<BITS, 1, DOWN>(a, qweight, experts, runs, stream);
+  return launch_experts<BITS, 2, DOWN>(a, qweight, experts, runs, stream);
 }
 
 template <int BITS>
