@@ -49,7 +49,7 @@ constexpr int kCols = kWarps * 32;       // columns of a CTA's tile
 constexpr int kRun = 128;                // activations that share a power of two
 constexpr int kMaxRuns = 480;            // CTAs, at most
 constexpr int kItemUnits = 2;            // what opening and writing an item takes, in chunks
-constexpr int kMinShare = 4;             // chunks of a run, at least: a join of more parts costs more than it saves
+constexpr int kMinShare = 2;             // chunks and units of a run, at least (5 tokens on 6 small experts: 23 us; 4: 27, 8: 36)
 constexpr int kMaxStages = 12;
 
 constexpr int kCtas = 2;                 // on an SM
@@ -241,6 +241,13 @@ __device__ __forceinline__ uint32_t lds32(uint32_t a) {
   uint32_t v;
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
   return v;
+}
+
+// Not volatile: the products of one k-tile move freely among the loads and unpacking of the next.
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 // Shared memory: [stages][weights | activations | their sums and scales | group scales | group zeros], the
@@ -454,6 +461,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_experts(const __grid_consta
   }
   // ---- this CTA's run.  All items of a call are equally long.
   const int slots = route(a, rt, reinterpret_cast<float*>(smem), sm_scan, !DOWN && blockIdx.x == 0);
+  if (DOWN && blockIdx.x == 0 && threadIdx.x == 0) *a.slots = slots;   // (its run may hold no chunk)
   const int nk = (a.K + C::kK - 1) / C::kK;                // chunks of one expert's K
   const int per = DOWN ? slots * nk : nk;                  // chunks of an item
   const int items = DOWN ? a.jblocks : slots * a.jblocks;
@@ -801,8 +809,6 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_experts(const __grid_consta
     }
     consumer_sync();
   };
-  if (DOWN && run == 0 && threadIdx.x == 0) *a.slots = slots;
-
   long long first_chunk = begin + start.u - start.c;       // of the current item, on the line
   open_item();
   // this thread's places in a stage: its pieces of the weights (tile l at w_at[l & 1] + 512 l; the swizzle
@@ -851,16 +857,28 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_experts(const __grid_consta
         for (int c = 0; c < 4; ++c)                        // 2^23 + z - 2^23
           gz[c] = __uint_as_float(0x4B000000u | ((zf >> (BITS * c)) & P::kMask)) - zero_base;
       };
-      auto tile_mma = [&](int l) {
-        uint4 w[ROWS];
+      auto load_tile = [&](int l, uint4 (&w)[ROWS]) {
 #pragma unroll
         for (int r = 0; r < ROWS; ++r) {
-          if constexpr (BITS == 3) {
-            w[r] = lds128(base + w_at[r]);
-          } else {
-            w[r] = lds128(base + w_at[l & 1] + l * 512);
-          }
+          if constexpr (BITS == 3) w[r] = lds128(base + w_at[r]);
+          else w[r] = lds128(base + w_at[l & 1] + l * 512);
         }
+      };
+      auto load_acts = [&](int l, int nb, uint32_t (&b)[NP]) {
+        const uint32_t src = base + act_at[nb] + l * (NP * 16);
+        if constexpr (NP % 4 == 0) {
+#pragma unroll
+          for (int i = 0; i < NP / 4; ++i) {
+            const uint4 v = lds128(src + 16 * i);
+            b[4 * i] = v.x; b[4 * i + 1] = v.y; b[4 * i + 2] = v.z; b[4 * i + 3] = v.w;
+          }
+        } else {
+          const uint2 v = lds64(src);
+          b[0] = v.x; b[1] = v.y;
+        }
+      };
+      // the products of one k-tile; b0: its activations of the first 8 rows
+      auto multiply = [&](int l, const uint4 (&w)[ROWS], const uint32_t (&b0)[NP]) {
         uint32_t d[4][NP];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -871,25 +889,26 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_experts(const __grid_consta
         for (int nb = 0; nb < NB; ++nb) {
           if (nb == 0 || 8 * nb < rows) {
             uint32_t b[NP];
-            const uint32_t src = base + act_at[nb] + l * (NP * 16);
-            if constexpr (NP % 4 == 0) {
+            if (nb == 0) {
 #pragma unroll
-              for (int i = 0; i < NP / 4; ++i) {
-                const uint4 v = lds128(src + 16 * i);
-                b[4 * i] = v.x; b[4 * i + 1] = v.y; b[4 * i + 2] = v.z; b[4 * i + 3] = v.w;
-              }
+              for (int i = 0; i < NP; ++i) b[i] = b0[i];
             } else {
-              const uint2 v = lds64(src);
-              b[0] = v.x; b[1] = v.y;
+              load_acts(l, nb, b);
             }
 #pragma unroll
             for (int j = 0; j < NP / 2; ++j)
 #pragma unroll
               for (int t = 0; t < 2; ++t)
-                decode::mma16816(cg[t][nb], d[2 * t][2 * j], d[2 * t + 1][2 * j], d[2 * t][2 * j + 1], d[2 * t + 1][2 * j + 1],
-                                 b[2 * j], b[2 * j + 1], __half());
+                mma(cg[t][nb], d[2 * t][2 * j], d[2 * t + 1][2 * j], d[2 * t][2 * j + 1], d[2 * t + 1][2 * j + 1], b[2 * j], b[2 * j + 1]);
           }
         }
+      };
+      auto tile_mma = [&](int l) {
+        uint4 w[ROWS];
+        uint32_t b[NP];
+        load_tile(l, w);
+        load_acts(l, 0, b);
+        multiply(l, w, b);
       };
       // tiles l0 .. l1 are done: acc += scale (act_scale c - zero 2^-24 sum a)
       auto fold = [&](int l0, int l1) {
@@ -923,8 +942,21 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_experts(const __grid_consta
         for (int l0 = 0; l0 < C::kTiles; l0 += C::kSegTiles) {
           load_group(l0 == 0 || g_at + l0 * C::kTileK < a.group ? 0 : (g_at + l0 * C::kTileK) / a.group);
           clear(cg);
+          // a segment's tiles are loaded ahead of their products (2-bit tiles hold 64 k and go one by one)
+          if constexpr (BITS == 4 || BITS == 8) {
+            uint4 w[C::kSegTiles][ROWS];
+            uint32_t b[C::kSegTiles][NP];
 #pragma unroll
-          for (int l = l0; l < l0 + C::kSegTiles; ++l) tile_mma(l);
+            for (int l = 0; l < C::kSegTiles; ++l) {
+              load_tile(l0 + l, w[l]);
+              load_acts(l0 + l, 0, b[l]);
+            }
+#pragma unroll
+            for (int l = 0; l < C::kSegTiles; ++l) multiply(l0 + l, w[l], b[l]);
+          } else {
+#pragma unroll
+            for (int l = l0; l < l0 + C::kSegTiles; ++l) tile_mma(l);
+          }
           fold(l0, l0 + C::kSegTiles - 1);
         }
       } else {
