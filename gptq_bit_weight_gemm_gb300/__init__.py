@@ -675,11 +675,8 @@ def moe_layer(x, router, up, down, *, topk, bits, group, fmt=V2, renormalize=Tru
         out_ptr = _address(out, dtype, shape, "out")
     ids = weights = ids_ptr = weights_ptr = None
     if return_routing:
-        # the choices and their weights share an allocation: two 4-byte values each
-        both = x.new_empty((2, tokens, topk), dtype=i32)
-        ids, weights = both[0], both[1].view(rt.float32)
-        ids_ptr = both.data_ptr()
-        weights_ptr = ids_ptr + 4 * tokens * topk
+        ids, weights = x.new_empty((tokens, topk), dtype=i32), x.new_empty((tokens, topk), dtype=rt.float32)
+        ids_ptr, weights_ptr = ids.data_ptr(), weights.data_ptr()
     ws = ws_bytes = 0
     if workspace is None and tokens > 0:
         workspace = moe_workspace(tokens, hidden, inter, experts, topk)
@@ -716,11 +713,8 @@ def sample(logits, uniform, *, temperature=None, top_k=None, top_p=None, min_p=N
     p_ptr = None if top_p is None else _address(top_p, f32, one, "top_p")
     m_ptr = None if min_p is None else _address(min_p, f32, one, "min_p")
     if out is None:
-        # a token and a log probability, 4 bytes each, in one allocation
-        both = logits.new_empty((2, batch), dtype=rt.int32)
-        token, logprob = both[0], both[1].view(f32)
-        token_ptr = both.data_ptr()
-        logprob_ptr = token_ptr + 4 * batch
+        token, logprob = uniform.new_empty(one, dtype=rt.int32), uniform.new_empty(one)
+        token_ptr, logprob_ptr = token.data_ptr(), logprob.data_ptr()
     else:
         token, logprob = out
         token_ptr, logprob_ptr = _address(token, rt.int32, one, "token"), _address(logprob, f32, one, "logprob")
