@@ -201,6 +201,49 @@ def test_wide_flat_distribution():
                             int(tok[b]), float(lp[b])), (b, kw)
 
 
+@pytest.mark.parametrize("kw", [dict(p=[0.9] * 2), dict(k=[40] * 2, p=[0.8] * 2), dict(k=[5000] * 2), dict(k=[30000] * 2, p=[0.3] * 2)])
+def test_row_longer_than_the_histograms_hold(kw):
+    # 8 CTAs of more than 65535 tokens each: masses do not go into 32-bit sums
+    x = logits_of(2, 600001, torch.float16, 6)
+    u = np.array([0.31, 0.87], np.float32)
+    tok, lp = run(x.to(DEV), u, **kw)
+    for b in range(2):
+        assert accepted(x[b].float().numpy(), float(u[b]), 1.0, kw.get("k", [0])[0], float(np.float32(kw.get("p", [1.0])[0])), 0.0,
+                        int(tok[b]), float(lp[b])), b
+
+
+def test_masked_vocabulary():
+    # all but a few tokens at the type's lowest value or -inf, as a grammar leaves them
+    x = torch.full((4, 100003), torch.finfo(torch.float16).min, dtype=torch.float16)
+    x[1::2] = float("-inf")
+    keep = [3, 17, 50001, 77777, 100002]
+    x[:, keep] = torch.tensor([0.0, 1.0, -1.0, 2.0, 0.5], dtype=torch.float16)
+    w = np.exp(np.float64([0.0, 1.0, -1.0, 2.0, 0.5]))
+    edges = np.cumsum(w) / w.sum()
+    mids = ((np.concatenate([[0], edges[:-1]]) + edges) / 2).astype(np.float32)
+    for kw in ({}, dict(k=[100] * 4), dict(p=[0.9999] * 4), dict(k=[2000] * 4, p=[0.9999] * 4)):
+        for i in range(5):
+            tok, _ = run(x.to(DEV), [mids[i]] * 4, **kw)
+            assert tok.tolist() == [keep[i]] * 4, (kw, i, tok)
+
+
+@pytest.mark.parametrize("temperature", [1e-38, 1e-6, 1e-3, 50.0, 1e30])
+def test_extreme_temperatures(temperature):
+    x = torch.zeros((3, 5000))
+    x[:, 100:110] = 1.0                               # ten equal best tokens
+    u = [0.05, 0.55, 0.95]
+    for kw in (dict(), dict(k=[30] * 3), dict(p=[0.5] * 3)):
+        tok, lp = run(x.to(DEV), u, t=[temperature] * 3, **kw)
+        if temperature <= 1e-3:
+            n = 5 if "p" in kw else 10
+            assert tok.tolist() == [100 + int(n * np.float32(v)) for v in u], (kw, tok)
+        else:
+            rows = x.numpy()
+            for b in range(3):
+                assert accepted(rows[b], float(np.float32(u[b])), temperature, kw.get("k", [0])[0], kw.get("p", [1.0])[0], 0.0,
+                                int(tok[b]), float(lp[b])), (kw, b)
+
+
 def test_side_stream_and_repeatable():
     x = logits_of(4, 20000, torch.float32, 1).to(DEV)
     u = torch.rand(4, device=DEV)
