@@ -16,6 +16,9 @@
 //   4. the kept masses summed and searched in index order.
 // Rows whose threshold bin holds more tokens than the list (equal or nearly equal logits by the
 // thousand) bisect the threshold over the 32 bits of the logit, a pass each.
+//
+// Measured (GB300): 64 rows of 131072 bf16 logits 18 us without a threshold, 25 us with top_k, 43 us with
+// top_p alone (two shared atomics a token, and exponentials in both passes); one row of 32000 10.5 us.
 #include <cooperative_groups.h>
 #include <math_constants.h>
 
