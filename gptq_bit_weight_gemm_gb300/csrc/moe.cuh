@@ -300,32 +300,62 @@ __device__ __forceinline__ int route(const Args& a, const Routing& r, float* scr
   const float inf = __int_as_float(0x7F800000);
   for (int e = threadIdx.x; e < a.experts; e += kThreads) r.count[e] = 0;
   for (int t = warp; t < a.tokens; t += kAll) {
+    // keys order the logits (a NaN as -inf); 0 marks absent and taken ones.  Up to kHeld experts a lane stay
+    // in registers, more in shared memory.
+    constexpr int kHeld = 4;
+    const float* logits = a.logits + t * a.experts;
     float* row = scratch + warp * a.experts;
-    float m = -inf, sum = 0.f, kept = 0.f;
-    for (int e = lane; e < a.experts; e += 32) {
-      const float v = __ldcg(a.logits + t * a.experts + e);
-      row[e] = v;
-      m = fmaxf(m, v);
-    }
+    const bool held = a.experts <= 32 * kHeld;
+    unsigned key[kHeld];
+    float m = -inf, sum = 0.f, kept = 0.f, mine = 0.f;
+    if (held) {
+      float v[kHeld];
 #pragma unroll
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-    for (int e = lane; e < a.experts; e += 32) {
-      sum += expf(row[e] - m);
-      row[e] = __uint_as_float(key_of(row[e]));
+      for (int i = 0; i < kHeld; ++i) {
+        v[i] = lane + 32 * i < a.experts ? __ldcg(logits + lane + 32 * i) : -inf;
+        m = fmaxf(m, v[i]);
+      }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) {
+        const bool in = lane + 32 * i < a.experts;
+        if (in) sum += expf(v[i] - m);
+        key[i] = in ? key_of(v[i]) : 0u;
+      }
+    } else {
+      for (int e = lane; e < a.experts; e += 32) {
+        const float v = __ldcg(logits + e);
+        row[e] = v;
+        m = fmaxf(m, v);
+      }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+      for (int e = lane; e < a.experts; e += 32) {
+        sum += expf(row[e] - m);
+        row[e] = __uint_as_float(key_of(row[e]));
+      }
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    // topk times the best expert that has not been taken, equal ones by index: the largest key, then its
-    // lowest index; keys order the logits, NaN as -inf, and 0 marks the taken ones
-    float mine = 0.f;
+    // topk times the largest key, its lowest index first
     for (int j = 0; j < a.topk; ++j) {
       unsigned bk = 0u;
       int be = 0x7FFFFFFF;
-      for (int e = lane; e < a.experts; e += 32) {
-        const unsigned k = __float_as_uint(row[e]);
-        if (k > bk) {
-          bk = k;
-          be = e;
+      if (held) {
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i)
+          if (key[i] > bk) {
+            bk = key[i];
+            be = lane + 32 * i;
+          }
+      } else {
+        for (int e = lane; e < a.experts; e += 32) {
+          const unsigned k = __float_as_uint(row[e]);
+          if (k > bk) {
+            bk = k;
+            be = e;
+          }
         }
       }
       const unsigned top = __reduce_max_sync(0xFFFFFFFFu, bk);
@@ -334,19 +364,37 @@ __device__ __forceinline__ int route(const Args& a, const Routing& r, float* scr
       kept += pr;
       if (lane == j) mine = pr;
       if (lane == 0) r.id[t * a.topk + j] = be;
-      if (lane == (be & 31)) row[be] = 0.f;
-      __syncwarp();
+      if (held) {
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i)
+          if (be == lane + 32 * i) key[i] = 0u;
+      } else {
+        if (lane == (be & 31)) row[be] = 0.f;
+        __syncwarp();
+      }
     }
     if (a.renormalize) mine /= kept;
     if (lane < a.topk) r.w[t * a.topk + lane] = mine;
-    __syncwarp();
   }
   __syncthreads();
+  // a pair's place among its expert's rows: warp 0 takes the pairs in order, 32 at a time
   const int pairs = a.tokens * a.topk;
-  for (int p = threadIdx.x; p < pairs; p += kThreads) {
-    atomicAdd(&r.count[r.id[p]], 1);
-    if (publish && a.ids) a.ids[p] = r.id[p];
-    if (publish && a.weights) a.weights[p] = r.w[p];
+  int* rank = reinterpret_cast<int*>(scratch);
+  if (warp == 0) {
+    for (int p0 = 0; p0 < pairs; p0 += 32) {
+      const int p = p0 + lane, e = p < pairs ? r.id[p] : 0x7FFFFFFF;
+      const unsigned same = __match_any_sync(0xFFFFFFFFu, e);
+      const int before = __popc(same & ((1u << lane) - 1u));
+      if (p < pairs) {
+        const int base = r.count[e];
+        rank[p] = base + before;
+        if (publish && a.ids) a.ids[p] = e;
+        if (publish && a.weights) a.weights[p] = r.w[p];
+      }
+      __syncwarp();
+      if (p < pairs && before == 0) r.count[e] += __popc(same);
+      __syncwarp();
+    }
   }
   __syncthreads();
   // experts with rows, in order: a scan of (blocks, rows), a CTA's threads at a time
@@ -383,13 +431,10 @@ __device__ __forceinline__ int route(const Args& a, const Routing& r, float* scr
     __syncthreads();
   }
   if (threadIdx.x == 0) r.slot_off[slots] = rows;
-  // a pair's place among its expert's rows: the pairs before it with the same expert
   for (int p = threadIdx.x; p < pairs; p += kThreads) {
-    const int e = r.id[p];
-    int rank = 0;
-    for (int q = 0; q < p; ++q) rank += r.id[q] == e;
-    r.row_token[r.count[e] + rank] = p / a.topk;
-    r.row_weight[r.count[e] + rank] = r.w[p];
+    const int at = r.count[r.id[p]] + rank[p];
+    r.row_token[at] = p / a.topk;
+    r.row_weight[at] = r.w[p];
   }
   ptx::fence_proxy_async_smem();                           // the scratch lies where the ring's copies will land
   __syncthreads();
@@ -1064,7 +1109,7 @@ cudaError_t launch_experts(Args a, const int32_t* qweight, int experts, int* run
   while (per_sm > 1 && a.stages < 3) a.stages = fit(--per_sm);
   if (a.stages > kMaxStages) a.stages = kMaxStages;
   // the router's scratch lies over the ring
-  if (a.stages < 2 || a.stages * a.stage_bytes < kThreads / 32 * experts * 4) return cudaErrorInvalidConfiguration;
+  if (a.stages < 2 || a.stages * a.stage_bytes < kThreads / 32 * experts * 4 || a.stages * a.stage_bytes < pairs * 4) return cudaErrorInvalidConfiguration;
   const int smem = L::fixed(DOWN ? a.tokens : a.rows, pairs, experts) + a.stages * (a.stage_bytes + 16);
   static std::atomic<unsigned long long> opted_in{0};       // per device
   if (dev.device >= 64 || !(opted_in.load(std::memory_order_relaxed) & (1ull << dev.device))) {
