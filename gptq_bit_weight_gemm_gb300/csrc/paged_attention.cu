@@ -154,6 +154,9 @@ __device__ __forceinline__ int tile_count(const AttentionProblem& p, int n) {
 // joining and writing it takes, in tiles.  Without it a run of many short items ends last (16
 // sequences of 40 to 2048 keys, 32 kv heads: the last run at 39 us, the median at 30 us).
 constexpr int kItemUnits = 2;
+// Units of a run, at least: shorter runs leave more parts to join than they save (one sequence of 4000
+// keys: 14.3 us at 1, 11.6 at 2, 12.1 at 4; of 997: 8.3, 8.4, 10.3, a tile alone taking about 1 us).
+constexpr int kMinShare = 2;
 
 // A place on the line: u units after the run's begin, tile t of nt of item h of sequence b, whose live
 // keys are [lo, n).
@@ -237,7 +240,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, R>::kCtas)) k_attention(c
   };
   long long total = 0;
   for (int b0 = 0; b0 < p.batch; b0 += kThreads) total = scan_chunk(b0, total);
-  const int runs = total < static_cast<long long>(gridDim.x) ? static_cast<int>(total) : static_cast<int>(gridDim.x);
+  const long long most = total >= kMinShare ? divide(total, kMinShare) : 1;
+  const int runs = most < static_cast<long long>(gridDim.x) ? static_cast<int>(most) : static_cast<int>(gridDim.x);
   const int run = blockIdx.x;
   if (run >= runs) return;
   // runs of `share` tiles, the first `extra` of them one longer
