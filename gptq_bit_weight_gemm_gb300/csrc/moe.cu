@@ -209,7 +209,7 @@ cudaError_t launch_moe(const MoeProblem& p, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const int chunk = p.bits == 2 ? moe::Chunk<2>::kK : p.bits == 3 ? moe::Chunk<3>::kK : p.bits == 4 ? moe::Chunk<4>::kK : moe::Chunk<8>::kK;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(down.jblocks, (p.tokens + 3) / 4);
+  cfg.gridDim = dim3(down.jblocks, p.tokens);
   cfg.blockDim = dim3(moe::kCols);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];

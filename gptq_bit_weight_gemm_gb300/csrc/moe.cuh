@@ -1050,38 +1050,53 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_experts(const __grid_consta
   }
 }
 
-// out = the parts of each 256 columns in run order, rounded once.  A CTA takes 4 tokens of an item, a
-// thread 4 columns of one.  (In DOWN itself the last CTA to arrive would add up to 40 parts of tokens x
-// 256 values alone: 16 tokens of 2048 columns took 60 us that way.)
+// out = the parts of each 256 columns, rounded once.  A CTA takes a token of an item, a thread 4 columns
+// and a quarter of the parts, each quarter in run order and the quarters in theirs, so the sum does not
+// depend on timing.  (In DOWN itself the last CTA to arrive would add up to 40 parts of tokens x 256
+// values alone: 16 tokens of 2048 columns took 60 us that way.)
 template <typename T>
 __global__ void __launch_bounds__(kCols) k_sum_parts(const float* partials, const int* slots, int nk, int items, int grid,
                                                      int tokens, int hidden, T* out) {
+  constexpr int kQuads = kCols / 4, kShares = 4, kBatch = 16;
+  __shared__ float4 sm[kShares - 1][kQuads];
   decode::pdl_wait();
   decode::pdl_launch_dependents();
-  const int per = *slots * nk, item = blockIdx.x;
+  const int per = *slots * nk, item = blockIdx.x, m = blockIdx.y;
   const Line line(static_cast<long long>(items) * (per + kItemUnits), grid);
   const long long first_chunk = static_cast<long long>(item) * (per + kItemUnits) + kItemUnits;
   const int first = line.run_of(first_chunk), last = line.run_of(first_chunk + per - 1);
-  const int c4 = 4 * (threadIdx.x % (kCols / 4)), m = blockIdx.y * 4 + threadIdx.x / (kCols / 4), n = item * kCols + c4;
-  if (m >= tokens || n >= hidden || first == last) return;   // (DOWN wrote an item inside one run itself)
+  if (first == last) return;   // (DOWN wrote an item inside one run itself)
+  const int quad = threadIdx.x % kQuads, share = threadIdx.x / kQuads, n = item * kCols + 4 * quad;
+  const int each = (last - first + kShares) / kShares, from = first + share * each;
+  const int to = from + each <= last ? from + each : last + 1;
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-  constexpr int kBatch = 16;
-  for (int c0 = first; c0 <= last; c0 += kBatch) {
+  for (int c0 = from; c0 < to; c0 += kBatch) {
     float4 p[kBatch];
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
-      const int r = c0 + j <= last ? c0 + j : last;
-      p[j] = __ldcg(reinterpret_cast<const float4*>(
-          partials + ((static_cast<size_t>(r) * 2 + (r == first ? 1 : 0)) * tokens + m) * kCols + c4));
+      const int r = c0 + j;
+      p[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r < to)
+        p[j] = __ldcg(reinterpret_cast<const float4*>(
+            partials + ((static_cast<size_t>(r) * 2 + (r == first ? 1 : 0)) * tokens + m) * kCols + 4 * quad));
     }
 #pragma unroll
-    for (int j = 0; j < kBatch; ++j)
-      if (c0 + j <= last) {
-        v.x += p[j].x;
-        v.y += p[j].y;
-        v.z += p[j].z;
-        v.w += p[j].w;
-      }
+    for (int j = 0; j < kBatch; ++j) {
+      v.x += p[j].x;
+      v.y += p[j].y;
+      v.z += p[j].z;
+      v.w += p[j].w;
+    }
+  }
+  if (share > 0) sm[share - 1][quad] = v;
+  __syncthreads();
+  if (share > 0 || n >= hidden) return;
+#pragma unroll
+  for (int i = 0; i < kShares - 1; ++i) {
+    v.x += sm[i][quad].x;
+    v.y += sm[i][quad].y;
+    v.z += sm[i][quad].z;
+    v.w += sm[i][quad].w;
   }
   *reinterpret_cast<uint2*>(out + static_cast<long long>(m) * hidden + n) = make_uint2(pack2(v.x, v.y, T()), pack2(v.z, v.w, T()));
 }
