@@ -303,10 +303,11 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleProblem p, i
     return w;
   };
   auto weight_at = [&](uint32_t key) { return weight_of(logit_of(key)); };
-  const bool by_min = min_p > 0.f;
-  auto kept_mass = [&](float l) {                          // min_p's part of the rule included
+  // the mass with min_p's part of the rule (the best token, of weight 1, always has it); NaN has none
+  const float least = min_p > 0.f ? fminf(min_p, 1.f) : 0.f;
+  auto kept_mass = [&](float l) {
     const float w = weight_of(l);
-    return !by_min || w >= min_p || l == top ? mass_of(w) : 0u;
+    return mass_of(w >= least ? w : 0.f);
   };
   Shared* const boss = cluster.map_shared_rank(&sh, 0);
   int parity = 0;
@@ -731,21 +732,25 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleProblem p, i
       for (int j = 0; j < kVec; ++j) l[j] = CUDART_NAN_F;
     }
   };
+#pragma unroll 2
   for (int q = warp * (kSubs / kWarps); q < (warp + 1) * (kSubs / kWarps); ++q) {
     u64 mine = 0;
     int t = 0;
     const int c1 = sub_begin(q + 1);
-#pragma unroll 2
+#pragma unroll 1
     for (int c = sub_begin(q); c < c1; ++c) {
       float l[kVec];
       chunk_at(c, l);
 #pragma unroll
       for (int j = 0; j < kVec; ++j) {
-        if (l[j] > cut) mine += kept_mass(l[j]);
+        const uint32_t m = kept_mass(l[j]);                // (without a branch around it)
+        mine += l[j] > cut ? m : 0u;
         t += l[j] == cut;
       }
     }
-    mine = warp_sum(mine);
+    // a lane's sum is below 2^54: 2^19 tokens of a sub-run in it at most
+    const u64 part = __reduce_add_sync(0xFFFFFFFFu, static_cast<uint32_t>(mine) & 0x7FFFFFFu);
+    mine = (static_cast<u64>(__reduce_add_sync(0xFFFFFFFFu, static_cast<uint32_t>(mine >> 27))) << 27) + part;
     t = __reduce_add_sync(0xFFFFFFFFu, t);
     if (lane == 0) {
       sh.sub_m[q] = mine;
