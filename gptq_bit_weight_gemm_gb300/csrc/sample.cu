@@ -107,7 +107,7 @@ struct Shared {
     struct { uint32_t count[kBins], hi[kBins], lo[kBins]; };
     struct { uint32_t cum_c[kBins]; u64 cum_m[kBins]; };
   };
-  u64 list[kList];
+  alignas(16) u64 list[kList];
   u64 slots[2][kMaxCluster];       // cluster sums, every CTA's part in every CTA
   float2 range[kMaxCluster];       // largest logit of each CTA, and the smallest of a sample of its tokens
   u64 part_m[kMaxCluster];         // kept mass above the threshold, and ties, of each CTA
@@ -135,10 +135,16 @@ __device__ void sort_list(u64* list, int n) {
     u64 e = 0;
     int at = 0;
     __syncthreads();
+    if (i < 16 && n + i < kList) list[n + i] = 0ull;
+    __syncthreads();
     if ((i & ~31) < n) {
       e = i < n ? list[i] : 0ull;
-#pragma unroll 4
-      for (int j = 0; j < n; ++j) at += list[j] > e;
+      for (int j = 0; j < n; j += 16)
+#pragma unroll
+        for (int o = 0; o < 16; o += 2) {
+          const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(list + j + o);
+          at += (x.x > e) + (x.y > e);
+        }
     }
     __syncthreads();
     if (i < n) list[at] = e;
@@ -286,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleProblem p, i
       for (int j = 0; j < kVec; ++j) l[j] = l[j] == CUDART_INF_F ? 0.f : -CUDART_INF_F;
   };
   auto each = [&](auto f) {                                // f(logit, token), in any order
-#pragma unroll 4
+#pragma unroll 2
     for (int v = threadIdx.x; v < vecs; v += kThreads) {
       float l[kVec];
       load_vec(v, l);
@@ -340,12 +346,12 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleProblem p, i
   } else if (k < p.vocab || top_p < 1.f) {
     const bool short_k = k <= kShortK;
     // ---- the histogram of top - l over the reach of the masses
-    const float reach = kReach * temp, span = low <= top ? fminf(top - low, reach) : reach;
+    const float reach = fminf(kReach * temp, 3.402823466e38f), span = low <= top ? fminf(top - low, reach) : reach;
     const float scale = span > 0.f ? fminf((kOver - 0.5f) / span, 3e38f) : 0.f;
     // NaN, -inf and what has no mass: the last bin; what is lower than the sampled lowest: the one before
     auto bin_of = [&](float l) {
       const float d = top - l;
-      return d <= reach && d < CUDART_INF_F ? min(static_cast<int>(fminf(d * scale, static_cast<float>(kOver - 1))), kOver - 1) : kOver;
+      return d <= reach ? static_cast<int>(fminf(d * scale, static_cast<float>(kOver - 1))) : kOver;
     };
     const bool by_mass = top_p < 1.f && !short_k;
     const bool fits = n <= kMaxSlice;
@@ -383,6 +389,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleProblem p, i
       static_assert(kPer == 4, "a uint4 of bins per thread");
       u64 m[4] = {};
       uint32_t c[4] = {};
+#pragma unroll 4
       for (int r = 0; r < cs; ++r) {
         const Shared* s = cluster.map_shared_rank(&sh, r);
         const uint4 x = reinterpret_cast<const uint4*>(s->count)[threadIdx.x];
@@ -446,20 +453,39 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleProblem p, i
     };
     auto below = [&](int b) { return b > 0 ? sh.cum_c[b - 1] : 0u; };
     auto below_m = [&](int b) { return b > 0 ? sh.cum_m[b - 1] : 0ull; };
-    // all CTAs: the tokens of bins bin_lo .. bin_hi into CTA 0's list
+    // all CTAs: the tokens of bins bin_lo .. bin_hi into CTA 0's list, from a list of this CTA's own (an
+    // atomic on another CTA's memory takes most of a microsecond, one after the other in a warp)
     auto gather = [&]() {
       const int lo = sh.bin_lo, hi = sh.bin_hi;
       // most tokens are below or above: two comparisons, with half a bin to spare for their rounding
       const float floor = scale > 0.f && hi < kOver - 1 ? top - (hi + 1.5f) / scale * (1.f + 1e-5f) : -CUDART_INF_F;
       const float roof = scale > 0.f ? top - (lo - 0.5f) / scale * (1.f - 1e-5f) : CUDART_INF_F;
-      each([&](float l, int token) {
-        if (!(l >= floor && l <= roof)) return;
-        const int b = bin_of(l);
-        if (b >= lo && b <= hi) {
-          const int at = atomicAdd(&boss->listed, 1);
-          if (at < kList) boss->list[at] = static_cast<u64>(key_of(l)) << 32 | (0xFFFFFFFFu - static_cast<uint32_t>(token));
+#pragma unroll 2
+      for (int v = threadIdx.x; v < vecs; v += kThreads) {
+        float l[kVec];
+        load_vec(v, l);
+        bool any = false;
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) any |= l[j] >= floor && l[j] <= roof;
+        if (!any) continue;
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) {
+          const int b = bin_of(l[j]);
+          if (b >= lo && b <= hi) {
+            const int at = atomicAdd(&sh.listed, 1), token = start + v * kVec + j - skew;
+            if (at < kList) sh.list[at] = static_cast<u64>(key_of(l[j])) << 32 | (0xFFFFFFFFu - static_cast<uint32_t>(token));
+          }
         }
-      });
+      }
+      if (rank != 0) {
+        __syncthreads();
+        const int count = sh.listed;
+        if (threadIdx.x == 0) sh.bin_lo = count > 0 ? atomicAdd(&boss->listed, count) : 0;
+        __syncthreads();
+        const int at = sh.bin_lo;
+        for (int i = threadIdx.x; i < count && at + i < kList && i < kList; i += kThreads) boss->list[at + i] = sh.list[i];
+        if (threadIdx.x == 0) sh.listed = 0;
+      }
     };
     auto key_in = [&](int i) { return static_cast<uint32_t>(sh.list[i] >> 32); };
     // CTA 0: the place of the threshold after the first r of the sorted list: its key, and how many of
@@ -550,11 +576,15 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleProblem p, i
           __syncthreads();
           if ((i & ~31) < r) {
             u64 lower = 0, total = 0;
-#pragma unroll 4
-            for (int j = 0; j < r; ++j) {
-              const uint32_t m_j = mass[j];
-              total += m_j;
-              if (static_cast<uint32_t>(sh.list[j]) > static_cast<uint32_t>(e)) lower += m_j;   // ~index
+#pragma unroll 2
+            for (int j0 = 0; j0 < r; j0 += 4) {            // (past r the masses are 0)
+              const uint4 four = *reinterpret_cast<const uint4*>(mass + j0);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const uint32_t m_j = (&four.x)[j];
+                total += m_j;
+                if (static_cast<uint32_t>(sh.list[j0 + j]) > static_cast<uint32_t>(e)) lower += m_j;   // ~index
+              }
             }
             // the token whose masses reach past the target (u >= 1: the last one)
             const u64 goal = min(beyond_part(u, total), total), end = lower + mine;
