@@ -28,7 +28,11 @@ Beside the GEMMs, the rest of a decode step (include/gptq_serving.h):
                                                              (with k_new, v_new: appended first)
   moe_layer(x, router, up, down, topk, bits, group)          -> router, experts on packed weights and sum
   sample(logits, uniform, temperature, top_k, top_p, min_p)  -> (token, log probability) of each row
+
+Every call on the device runs on `stream` (None: the current one).  With a stream that is not the current
+one, the caller has its inputs ready there; what the call allocates (outputs, workspaces) belongs to it.
 """
+import contextlib
 import ctypes
 import os
 import re
@@ -125,7 +129,8 @@ def header_functions(header=HEADER):
 def selftest_wait_timeout(limit_ns=50_000_000, stream=None):
     """Run the bounded-wait self-test; returns (waited_out, status bits)."""
     torch = _torch()
-    flag = torch.zeros(1, dtype=torch.int32, device="cuda")
+    with _on(stream):
+        flag = torch.zeros(1, dtype=torch.int32, device="cuda")
     _check(lib().gptq_selftest_wait_timeout(int(limit_ns), _ptr(flag), _stream(stream)),
            "gptq_selftest_wait_timeout")
     status = device_status(stream)
@@ -169,9 +174,29 @@ def _stream(stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _on(stream):
+    """Within it, what a call allocates belongs to the stream that the call runs on: a fill precedes the
+    kernels, and memory that is released when the call returns is not handed out to another stream
+    while they use it."""
+    return contextlib.nullcontext() if stream is None else _torch().cuda.stream(stream)
+
+
+def _new(stream, like, shape, dtype=None):
+    """An output for the caller, of like's device and (unless given) type.  The caller's current stream
+    may use it as well."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    with _on(stream):
+        t = like.new_empty(shape, dtype=dtype)
+    here = _torch().cuda.current_stream()
+    if here != stream:
+        t.record_stream(here)
+    return t
+
+
 def gemm(A, qweight, qzeros, scales, g_idx=None, *, bits, group, fmt=V2, out=None, workspace=None,
          sort_rows=True, stream=None):
-    """C[M, N] = A[M, K] @ dequant(qweight, qzeros, scales, g_idx) on the current stream.  When no
+    """C[M, N] = A[M, K] @ dequant(qweight, qzeros, scales, g_idx).  When no
     workspace is given one is allocated here: act-order (g_idx) with sort_rows, where the shape
     qualifies, takes act_order_workspace_size(...) bytes (rows sorted by group on the device);
     otherwise bf16 activations take workspace_size(...) bytes."""
@@ -179,13 +204,14 @@ def gemm(A, qweight, qzeros, scales, g_idx=None, *, bits, group, fmt=V2, out=Non
     M, K = A.shape
     N = qweight.shape[1]
     if out is None:
-        out = torch.empty((M, N), dtype=A.dtype, device=A.device)
+        out = _new(stream, A, (M, N))
     if workspace is None and M > 0:
         size = act_order_workspace_size(M, K, N, bits, group) if (g_idx is not None and sort_rows) else 0
         if size == 0 and A.dtype == torch.bfloat16:
             size = workspace_size(M, K, N, bits, group)
         if size:
-            workspace = torch.empty(size, dtype=torch.uint8, device=A.device)
+            with _on(stream):
+                workspace = torch.empty(size, dtype=torch.uint8, device=A.device)
     ws_ptr = _ptr(workspace, name="workspace") if workspace is not None else None
     ws_len = workspace.numel() * workspace.element_size() if workspace is not None else 0
     rc = lib().gptq_gemm(_ptr(A, name="A"), M, K, _dtype_code(A),
@@ -291,7 +317,7 @@ def dequant(qweight, qzeros, scales, g_idx=None, *, K, bits, group, fmt=V2, dtyp
     dtype = torch.float16 if dtype is None else dtype
     N = qweight.shape[1]
     if out is None:
-        out = torch.empty((K, N), dtype=dtype, device=qweight.device)
+        out = _new(stream, qweight, (K, N), dtype)
     code = F16 if dtype == torch.float16 else BF16
     rc = lib().gptq_dequant(_ptr(qweight, torch.int32, "qweight"), _ptr(qzeros, torch.int32, "qzeros"),
                             _ptr(scales, torch.float16, "scales"), _ptr(g_idx, torch.int32, "g_idx"),
@@ -309,9 +335,9 @@ def quantize_rtn(W, *, bits, group, g_idx=None, sym=False, fmt=V2, out=None, str
     if out is not None:
         qweight, qzeros, scales = out
     else:
-        qweight = torch.empty((K * bits // 32, N), dtype=torch.int32, device=W.device)
-        qzeros = torch.empty((G, N * bits // 32), dtype=torch.int32, device=W.device)
-        scales = torch.empty((G, N), dtype=torch.float16, device=W.device)
+        qweight = _new(stream, W, (K * bits // 32, N), torch.int32)
+        qzeros = _new(stream, W, (G, N * bits // 32), torch.int32)
+        scales = _new(stream, W, (G, N), torch.float16)
     if (tuple(qweight.shape) != (K * bits // 32, N) or tuple(qzeros.shape) != (G, N * bits // 32)
             or tuple(scales.shape) != (G, N)):
         raise ValueError("quantize_rtn: output buffers of the wrong shape")
@@ -359,9 +385,10 @@ def prepack_act_order_device(qweight, g_idx, *, K, N, bits, group, workspace=Non
     if ws_bytes == 0:
         raise GPTQError(-2, "gptq_prepack_act_order_device")
     if workspace is None:
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=qweight.device)
-    out = torch.empty_like(qweight)
-    perm = torch.empty(K, dtype=torch.int32, device=qweight.device)
+        with _on(stream):
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=qweight.device)
+    out = _new(stream, qweight, qweight.shape)
+    perm = _new(stream, qweight, (K,))
     rc = lib().gptq_prepack_act_order_device(_ptr(qweight, torch.int32, "qweight"), _ptr(g_idx, torch.int32, "g_idx"),
                                              K, N, bits, group, _ptr(out, torch.int32, "qweight_out"),
                                              _ptr(perm, torch.int32, "perm"), _ptr(workspace, name="workspace"),
@@ -382,10 +409,11 @@ def gemm_perm(A, perm, qweight, qzeros, scales, *, bits, group, fmt=V2, out=None
     M, K = A.shape
     N = qweight.shape[1]
     if out is None:
-        out = torch.empty((M, N), dtype=A.dtype, device=A.device)
+        out = _new(stream, A, (M, N))
     ws_bytes = gemm_perm_workspace_size(M, K)
     if ws_bytes and workspace is None:
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=A.device)
+        with _on(stream):
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=A.device)
     ws_ptr = _ptr(workspace, name="workspace") if ws_bytes else None
     ws_len = workspace.numel() * workspace.element_size() if ws_bytes else 0
     rc = lib().gptq_gemm_perm(_ptr(A, name="A"), M, K, _dtype_code(A), _ptr(perm, torch.int32, "perm"),
@@ -411,10 +439,11 @@ def gemm_interleaved(A, qweight_il, qzeros, scales, perm=None, *, N, bits, group
     torch = _torch()
     M, K = A.shape
     if out is None:
-        out = torch.empty((M, N), dtype=A.dtype, device=A.device)
+        out = _new(stream, A, (M, N))
     ws_bytes = gemm_perm_workspace_size(M, K) if perm is not None else 0
     if ws_bytes and workspace is None:
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=A.device)
+        with _on(stream):
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=A.device)
     ws_ptr = _ptr(workspace, name="workspace") if ws_bytes else None
     ws_len = workspace.numel() * workspace.element_size() if ws_bytes else 0
     rc = lib().gptq_gemm_interleaved(_ptr(A, name="A"), M, K, _dtype_code(A), _ptr(perm, torch.int32, "perm"),
@@ -435,7 +464,7 @@ def gemm_grouped(A, offsets, qweight, qzeros, scales, *, bits, group, max_m, fmt
     rows, K = A.shape
     E, _, N = qweight.shape
     if out is None:
-        out = torch.empty((rows, N), dtype=A.dtype, device=A.device)
+        out = _new(stream, A, (rows, N))
     rc = lib().gptq_gemm_grouped(_ptr(A, name="A"), rows, K, _dtype_code(A),
                                  _ptr(offsets, torch.int32, "offsets"), E, max_m,
                                  _ptr(qweight, torch.int32, "qweight"), _ptr(qzeros, torch.int32, "qzeros"),
@@ -602,13 +631,14 @@ def paged_attention(q, k_cache, v_cache, block_table, seq_lens, *, scale=None, w
             _look_rows(v_new, dtype, new_shape, "v_new")
         kn, vn, kn_stride, vn_stride = k_new.data_ptr(), v_new.data_ptr(), ns[0], nv[0]
     if out is None:
-        out = q.new_empty(shape)
+        out = q.new_empty(shape) if stream is None else _new(stream, q, shape)
         out_ptr = out.data_ptr()
     else:
         out_ptr = _address(out, dtype, shape, "out")
     lse_ptr = None if lse is None else _address(lse, rt.float32, (batch, heads), "lse")
     if workspace is None:
-        workspace = paged_attention_workspace(heads, kv_heads, dim)
+        with _on(stream):
+            workspace = paged_attention_workspace(heads, kv_heads, dim)
     ws, ws_bytes = _workspace(workspace)
     if batch == 1:                     # the strides of a dimension of one may be anything
         strides = _Strides(0, 0, 0, ks[0], ks[1], ks[2], vs[0], vs[1], vs[2])
@@ -669,17 +699,18 @@ def moe_layer(x, router, up, down, *, topk, bits, group, fmt=V2, renormalize=Tru
             _look(weight[1], i32, (experts, G, N * bits // 32), name + " qzeros")
             _look(weight[2], f16, (experts, G, N), name + " scales")
     if out is None:
-        out = x.new_empty(shape)
+        out = x.new_empty(shape) if stream is None else _new(stream, x, shape)
         out_ptr = out.data_ptr()
     else:
         out_ptr = _address(out, dtype, shape, "out")
     ids = weights = ids_ptr = weights_ptr = None
     if return_routing:
-        ids, weights = x.new_empty((tokens, topk), dtype=i32), x.new_empty((tokens, topk), dtype=rt.float32)
+        ids, weights = _new(stream, x, (tokens, topk), i32), _new(stream, x, (tokens, topk), rt.float32)
         ids_ptr, weights_ptr = ids.data_ptr(), weights.data_ptr()
     ws = ws_bytes = 0
     if workspace is None and tokens > 0:
-        workspace = moe_workspace(tokens, hidden, inter, experts, topk)
+        with _on(stream):
+            workspace = moe_workspace(tokens, hidden, inter, experts, topk)
     if workspace is not None:
         ws, ws_bytes = _workspace(workspace)
     rc = rt.lib.gptq_moe(x.data_ptr(), tokens, hidden, inter, code, router.data_ptr(), experts, topk, 1 if renormalize else 0,
@@ -713,7 +744,7 @@ def sample(logits, uniform, *, temperature=None, top_k=None, top_p=None, min_p=N
     p_ptr = None if top_p is None else _address(top_p, f32, one, "top_p")
     m_ptr = None if min_p is None else _address(min_p, f32, one, "min_p")
     if out is None:
-        token, logprob = uniform.new_empty(one, dtype=rt.int32), uniform.new_empty(one)
+        token, logprob = _new(stream, uniform, one, rt.int32), _new(stream, uniform, one)
         token_ptr, logprob_ptr = token.data_ptr(), logprob.data_ptr()
     else:
         token, logprob = out
