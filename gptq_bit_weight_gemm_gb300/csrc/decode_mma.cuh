@@ -219,8 +219,13 @@ __global__ void __launch_bounds__(kThreads, (MT <= 16 && BITS != 3 ? 5 : 1))
   constexpr int NB = (MT + 7) / 8;                    // token blocks of 8
   extern __shared__ __align__(128) unsigned char smem_raw[];
 
-  // a flag-gated launch whose flag says no: every CTA leaves before any barrier or copy
-  if (args.run_flag != nullptr && *args.run_flag != args.run_when) return;
+  // a flag-gated launch whose flag says no: every CTA leaves before any barrier or copy.  The grid's first
+  // CTA waits for the kernels before this one first: whatever follows on the stream waits for this grid
+  // alone, so the grid must not be complete while the kernel that did the work still runs.
+  if (args.run_flag != nullptr && *args.run_flag != args.run_when) {
+    if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) pdl_wait();
+    return;
+  }
   pdl_launch_dependents();
   // Grouped: the expert e of slot blockIdx.z multiplies rows [offsets[e], offsets[e + 1]) of A
   // into the same rows of C, with its own scales, zeros and packed rows (e * K * bits / 32 onward

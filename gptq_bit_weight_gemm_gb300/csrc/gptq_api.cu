@@ -234,7 +234,8 @@ bool act_order_shape_ok(int K, int G, int group, int bits) {
 // wrote.  The per-row decode reads nothing the group-wise GEMM writes, and the flag is final once
 // that GEMM has started (the sort had completed before the repack finished), so it is a
 // programmatic dependent: with flag 1 its CTAs leave as slots free at the group-wise GEMM's tail
-// instead of costing a launch after it.
+// instead of costing a launch after it, all but the first, which waits for the GEMM so that the
+// grid completes after it (the next kernel on the stream waits for this grid).
 int gemm_act_order(const Problem& p, cudaStream_t s) {
   const ActOrderLayout l = act_order_layout(p.M, p.K, p.N, p.bits);
   unsigned char* ws = static_cast<unsigned char*>(p.workspace);
