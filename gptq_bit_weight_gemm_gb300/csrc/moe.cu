@@ -25,7 +25,7 @@ constexpr size_t kCounterBytes = 4096;   // UP's runs
 static_assert(kMaxRuns * 4 <= kCounterBytes, "counters");
 
 struct Space {
-  size_t slots, logits, act, act_scale, act_sum, h, h_scale, h_sum, partials, total;
+  size_t slots, logits, act, act_scale, h, h_scale, partials, total;
 };
 Space space(int tokens, int hidden, int inter, int experts, int topk) {
   auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
@@ -35,12 +35,9 @@ Space space(int tokens, int hidden, int inter, int experts, int topk) {
   s.logits = s.slots + 256;
   s.act = s.logits + up(static_cast<size_t>(tokens) * experts * 4);
   s.act_scale = s.act + up(static_cast<size_t>(tokens) * hidden * 2);
-  // sums per k-tile: 16 k values at least
-  s.act_sum = s.act_scale + up(static_cast<size_t>(tokens) * ((hidden + kRun - 1) / kRun) * 4);
-  s.h = s.act_sum + up(static_cast<size_t>(tokens) * (hidden / 16) * 4);
+  s.h = s.act_scale + up(static_cast<size_t>(tokens) * ((hidden + kRun - 1) / kRun) * 4);
   s.h_scale = s.h + up(rows * inter * 2);
-  s.h_sum = s.h_scale + up(rows * ((inter + kRun - 1) / kRun) * 4);
-  s.partials = s.h_sum + up(rows * (inter / 16) * 4);
+  s.partials = s.h_scale + up(rows * ((inter + kRun - 1) / kRun) * 4);
   s.total = s.partials + static_cast<size_t>(kMaxRuns) * 2 * tokens * kCols * 4;
   return s;
 }
@@ -52,7 +49,6 @@ struct RouteArgs {
   float* logits;
   __half* act;
   float* act_scale;
-  float* act_sum;
   unsigned* counters;
 };
 
@@ -120,9 +116,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) k_route(const RouteArgs a) {
     v[2] = F16Traits<T>::to_f32(F16Traits<T>::from_bits(lo16(w.y)));
     v[3] = F16Traits<T>::to_f32(F16Traits<T>::from_bits(hi16(w.y)));
   }
-  constexpr int tile = 4 * Pack<BITS>::kPerUnit;
-  store_run<BITS>(v, j0, a.hidden, a.act + static_cast<long long>(t) * a.hidden, a.act_scale + static_cast<long long>(t) * runs + j0 / kRun,
-                  a.act_sum + static_cast<long long>(t) * (a.hidden / tile) + j0 / tile);
+  store_run<BITS>(v, j0, a.hidden, a.act + static_cast<long long>(t) * a.hidden, a.act_scale + static_cast<long long>(t) * runs + j0 / kRun);
 }
 
 template <typename T>
@@ -164,7 +158,6 @@ cudaError_t launch_moe(const MoeProblem& p, cudaStream_t stream) {
   ra.act = reinterpret_cast<__half*>(ws + s.act);
   ra.act_scale = reinterpret_cast<float*>(ws + s.act_scale);
   ra.counters = counters;
-  ra.act_sum = reinterpret_cast<float*>(ws + s.act_sum);
   const int tblocks = (p.tokens + moe::kRouteTokens - 1) / moe::kRouteTokens;
   const int runs = (p.hidden + kRun - 1) / kRun;
   const int grid = p.experts * tblocks + (p.tokens * runs + moe::kRouteWarps - 1) / moe::kRouteWarps;
@@ -180,12 +173,11 @@ cudaError_t launch_moe(const MoeProblem& p, cudaStream_t stream) {
   up.experts = p.experts; up.topk = p.topk; up.renormalize = p.renormalize;
   up.logits = ra.logits;
   up.ids = p.ids; up.weights = p.weights;
-  up.act = ra.act; up.act_scale = ra.act_scale; up.act_sum = ra.act_sum; up.act_runs = runs;
+  up.act = ra.act; up.act_scale = ra.act_scale; up.act_runs = runs;
   up.jblocks = (p.inter + moe::kCols / 2 - 1) / (moe::kCols / 2);
   up.inter = p.inter;
   up.h = reinterpret_cast<__half*>(ws + s.h);
   up.h_scale = reinterpret_cast<float*>(ws + s.h_scale);
-  up.h_sum = reinterpret_cast<float*>(ws + s.h_sum);
   up.h_runs = (p.inter + kRun - 1) / kRun;
   up.counters = counters;
   up.partials = reinterpret_cast<float*>(ws + s.partials);
@@ -194,7 +186,7 @@ cudaError_t launch_moe(const MoeProblem& p, cudaStream_t stream) {
   down.K = p.inter; down.N = p.hidden; down.group = p.group_down; down.G = p.inter / p.group_down;
   down.qzeros = p.down.qzeros;
   down.scales = static_cast<const __half*>(p.down.scales);
-  down.act = up.h; down.act_scale = up.h_scale; down.act_sum = up.h_sum; down.act_runs = up.h_runs;
+  down.act = up.h; down.act_scale = up.h_scale; down.act_runs = up.h_runs;
   down.jblocks = (p.hidden + moe::kCols - 1) / moe::kCols;
   down.out = p.out;
   down.dtype = p.dtype;

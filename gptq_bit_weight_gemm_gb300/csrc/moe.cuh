@@ -21,17 +21,16 @@
 // activations and its groups' scales and zeros (cp.async), all arriving on one mbarrier.  (A box for
 // each 32 columns and a bulk copy for each row cost the producer about 100 cycles each, which bounded
 // everything: one token 83 us.)  A consumer warp owns 32 columns and multiplies on the tensor cores (m16n8k16, weights as
-// the A operand).  Unpacking is what the SM runs out of first (with exact q - zero pairs, 9 operations
-// per word of 8 codes, eight tokens took 227 us at 61 % of the issue slots), so a code is only masked:
-// in the low mantissa bits of a half, s bits up, it reads as the subnormal q 2^(s - 24), which the MMA
-// multiplies exactly.  The activations of the codes s bits up are stored times 2^-s, and the zero comes
-// off per group:  sum (q - z) a = 2^24 c - z sum a,  with the rows' sums of a stored beside them.  The
-// difference costs the accuracy of fp32 sums of 15 |a| in place of |q - z| |a|.
+// the A operand).  Unpacking is what the SM runs out of first.  A code masked into the low mantissa bits of
+// a half, s bits up, reads as the subnormal q 2^(s - 24), and one fma with 2^(14 - s) and -z 2^-10 makes
+// it (q - z) 2^-10, exactly: 9 operations per word of 8 codes.  (Without the fma, with the zero taken off
+// per group as sum q a - z sum a, a group whose codes equal its zero would leave the fp32 error of two
+// sums of up to 255 |a| where the result is 0: 0.2 at 8 bits with outlier channels.)
 //
 // Activations are fp16 in both stages: every row's run of 128 values is stored as fp16 times a power
-// of two chosen for the run (11 bits relative to the run's largest value for values above 2^-20 of it;
-// exact for fp16 input in that range), already in the pair order of the codes.  So h may exceed fp16's
-// range, and bf16 models lose nothing to the multiply.
+// of two chosen for the run (11 bits of each value above 2^-28 of the run's largest; exact for fp16 and
+// bf16 input in that range), already in the pair order of the codes.  So h may exceed fp16's range, and
+// bf16 models lose nothing to the multiply.
 #pragma once
 
 #include <cuda.h>
@@ -66,7 +65,7 @@ struct Chunk {
   // fall into distinct banks
   static constexpr int kActRow = kK * 2 + (BITS == 4 ? 64 : BITS == 8 ? 32 : 16);
   static constexpr int kZeroWords = kWarps * BITS;                        // zeros of 256 columns
-  static constexpr int kInfo = kTiles + kRunsOf > 4 ? 8 : 4;              // floats per row: k-tile sums, run scales
+  static constexpr int kInfo = kRunsOf;                                   // floats per row: run scales
   // tiles that share a run of activations (and a group, where groups are multiples of their length)
   static constexpr int kSegTiles = kTileK * kTiles < kRun ? kTiles : kRun / kTileK;
   static constexpr int kSegK = kSegTiles * kTileK;
@@ -102,13 +101,11 @@ struct Args {
   float* weights;
   const __half* act;     // UP: [tokens][K] in pair order; DOWN: [rows][K]
   const float* act_scale;   // [row][act_runs]
-  const float* act_sum;     // [row][K / k-tile]
   int act_runs;
   int jblocks;           // column blocks: UP ceil(inter / 128), DOWN ceil(hidden / 256)
   int inter;
   __half* h;             // UP
   float* h_scale;
-  float* h_sum;
   int h_runs;
   void* out;             // DOWN
   int dtype;
@@ -136,7 +133,7 @@ __device__ __forceinline__ int pair_pos(int k) {
   }
 }
 
-// How far up (bits) the code at halfword `pos` of a unit sits in its half after RawPairs.
+// How far up (bits) the code at halfword `pos` of a unit sits in its half once masked (ScaledPairs).
 template <int BITS>
 __host__ __device__ constexpr int pair_shift(int pos) {
   const int p = pos >> 1;
@@ -146,30 +143,38 @@ __host__ __device__ constexpr int pair_shift(int pos) {
   return 0;
 }
 
-// The codes of a unit as pairs of fp16 subnormals q 2^(shift - 24), in DiffPairs' order.
+// fp16 bits of (2^(14 - s), 2^(14 - s')), s and s' the shifts of pair p's codes
 template <int BITS>
-struct RawPairs {
+__host__ __device__ constexpr uint32_t pair_scale(int p) {
+  return static_cast<uint32_t>(29 - pair_shift<BITS>(2 * p)) << 10 | static_cast<uint32_t>(29 - pair_shift<BITS>(2 * p + 1)) << 26;
+}
+// -z 2^-10 in both halves: z as a subnormal, z 2^-24, times -2^14
+__device__ __forceinline__ uint32_t zero_pair(uint32_t z) { return fma2(z * 0x00010001u, 0xF400F400u, 0x80008000u, __half()); }
+
+// (q - z) 2^-10 of the codes of a unit as pairs of halves, in DiffPairs' order; zero: zero_pair(z).
+template <int BITS>
+struct ScaledPairs {
   static constexpr int kPairs = 16 / BITS;
-  __device__ static __forceinline__ void run(uint32_t w, uint32_t (&d)[kPairs]) {
+  __device__ static __forceinline__ void run(uint32_t w, uint32_t zero, uint32_t (&d)[kPairs]) {
     constexpr uint32_t mask = Pack<BITS>::kMask * 0x00010001u;
     constexpr int low = 8 / BITS;                          // pairs below bit 8
 #pragma unroll
     for (int p = 0; p < low; ++p) {
-      d[p] = w & (mask << (BITS * p));
-      d[low + p] = (w >> 8) & (mask << (BITS * p));
+      d[p] = fma2(w & (mask << (BITS * p)), pair_scale<BITS>(p), zero, __half());
+      d[low + p] = fma2((w >> 8) & (mask << (BITS * p)), pair_scale<BITS>(low + p), zero, __half());
     }
   }
 };
 template <>
-struct RawPairs<3> {
+struct ScaledPairs<3> {
   static constexpr int kPairs = 16;
-  __device__ static __forceinline__ void run3(uint32_t w0, uint32_t w1, uint32_t w2, uint32_t (&d)[kPairs]) {
+  __device__ static __forceinline__ void run3(uint32_t w0, uint32_t w1, uint32_t w2, uint32_t zero, uint32_t (&d)[kPairs]) {
     const uint32_t x[9] = {w0, w0 >> 4, __funnelshift_r(w0, w1, 10), w1, w1 >> 3, w1 >> 6, __funnelshift_r(w1, w2, 26), w2, w2 >> 6};
 #pragma unroll
     for (int p = 0; p < kPairs; ++p) {
       const int s = code3_pair(p, 2);
       const int xi = s == 0 ? 0 : s == 4 ? 1 : s == 10 ? 2 : s == 32 ? 3 : s == 35 ? 4 : s == 38 ? 5 : s == 58 ? 6 : s == 64 ? 7 : 8;
-      d[p] = x[xi] & ((7u << CodePairs<__half, 3>::shift_lo(p)) | (7u << (16 + CodePairs<__half, 3>::shift_hi(p))));
+      d[p] = fma2(x[xi] & ((7u << CodePairs<__half, 3>::shift_lo(p)) | (7u << (16 + CodePairs<__half, 3>::shift_hi(p)))), pair_scale<3>(p), zero, __half());
     }
   }
 };
@@ -200,29 +205,20 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int 
 __device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory"); }
 
 // One warp stores a run of a row: lane l holds values 4 l .. 4 l + 3 (zeros past K).  act: the row; the
-// run's power of two goes to *scale, and 2^-24 of the sums of the stored values over each k-tile, times
-// it, to sums[0 ..].
+// run's power of two goes to *scale.
 template <int BITS>
-__device__ __forceinline__ void store_run(const float (&v)[4], int j0, int K, __half* act, float* scale, float* sums) {
-  constexpr int per = Pack<BITS>::kPerUnit, tile = 4 * per;
+__device__ __forceinline__ void store_run(const float (&v)[4], int j0, int K, __half* act, float* scale) {
+  constexpr int per = Pack<BITS>::kPerUnit;
   const int lane = threadIdx.x & 31, j = j0 + 4 * lane;
   float top = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
 #pragma unroll
   for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
   const int e = run_exponent(top);
   const float inv = pow2(-e);
-  float sum = 0.f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int pos = pair_pos<BITS>((j + i) % per);
-    const __half x = __float2half_rn(v[i] * inv);
-    sum += __half2float(x);
-    if (j < K) act[(j + i) / per * per + pos] = __float2half_rn(__half2float(x) * pow2(-pair_shift<BITS>(pos)));
-  }
-#pragma unroll
-  for (int o = 1; o < tile / 4; o <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+  for (int i = 0; i < 4; ++i)
+    if (j < K) act[(j + i) / per * per + pair_pos<BITS>((j + i) % per)] = __float2half_rn(v[i] * inv);
   if (lane == 0) *scale = pow2(e);
-  if (lane % (tile / 4) == 0 && j < K) sums[4 * lane / tile] = sum * (1.f / 16777216.f) * pow2(e);
 }
 
 // Loads from shared memory by 32-bit address (a generic pointer costs 64-bit additions in the main loop);
@@ -250,14 +246,14 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Shared memory: [stages][weights | activations | their sums and scales | group scales | group zeros], the
+// Shared memory: [stages][weights | activations | their scales | group scales | group zeros], the
 // output tile [tokens (DOWN) or rows][kCols] floats, 2 mbarriers per stage, the routing.
 template <int BITS>
 struct Layout {
   using C = Chunk<BITS>;
   __host__ __device__ static constexpr int act() { return kWarps * C::kSlot; }
   __host__ __device__ static int info(int rows) { return act() + rows * C::kActRow; }
-  __host__ __device__ static int scales(int rows) { return info(rows) + rows * C::kInfo * 4; }
+  __host__ __device__ static int scales(int rows) { return (info(rows) + rows * C::kInfo * 4 + 15) & ~15; }
   __host__ __device__ static int zeros(int rows, int gmax) { return scales(rows) + gmax * kCols * 2; }
   __host__ __device__ static int stage(int rows, int gmax) {
     return (zeros(rows, gmax) + gmax * C::kZeroWords * 4 + 1023) & ~1023;
@@ -468,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_experts(const __grid_consta
   using P = Pack<BITS>;
   using C = Chunk<BITS>;
   using L = Layout<BITS>;
-  using RP = RawPairs<BITS>;
+  using RP = ScaledPairs<BITS>;
   constexpr int NP = RP::kPairs, ROWS = P::kRowsPerUnit;
   extern __shared__ __align__(128) unsigned char smem_raw[];
   __shared__ int sm_abort, sm_last, sm_scan[kThreads / 32];
@@ -564,7 +560,6 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_experts(const __grid_consta
       const __half* sc;
       const int32_t* zr[2];
       const float* act_sc;
-      const float* act_sum;
     };
     auto place = [&](Put& p) {                             // after a new item or expert
       if (p.item != p.x.item) {
@@ -591,7 +586,6 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_experts(const __grid_consta
       for (int i = 0; i < 2; ++i) p.zr[i] = a.qzeros + grow * a.zwords + p.zc[i] / 32 * BITS + (lane + 32 * i) % BITS;
       const int row = lane < p.rows ? (DOWN ? off + lane : rt.row_token[off + lane]) : 0;
       p.act_sc = a.act_scale + static_cast<long long>(row) * a.act_runs + k0 / kRun;
-      p.act_sum = a.act_sum + static_cast<long long>(row) * (a.K / C::kTileK) + k0 / C::kTileK;
     };
     auto step = [&](Put& p) {                              // to the next chunk
       const int item = p.x.item, slot = p.x.s;
@@ -601,7 +595,6 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_experts(const __grid_consta
         return;
       }
       p.w_row += C::kRows;
-      p.act_sum += C::kTiles;
       p.act_sc += C::kK >= kRun ? C::kRunsOf : 1 - (p.x.kc & 1);
       p.g_at += C::kK;
       while (p.g_at >= a.group) {
@@ -642,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_experts(const __grid_consta
     auto put_acts = [&](const Put& p, int st) {
       const uint32_t to = smem_a + st * stage_bytes;
       const int left = a.K - p.x.kc * C::kK, ck = left < C::kK ? left : C::kK;
-      // 16-byte pieces of the rows, then each row's sums and scales
+      // 16-byte pieces of the rows, then each row's scales
       constexpr int kPieces = C::kK / 8;
       const int pieces = p.rows * kPieces;
       for (int i = lane; i < pieces; i += 32) {
@@ -654,16 +647,9 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_experts(const __grid_consta
       }
       if (lane < p.rows) {
         const uint32_t info = to + L::info(a.rows) + lane * C::kInfo * 4;
-        if (C::kTiles == 4 && a.K % (4 * C::kTileK) == 0) {
-          cp_async16(info, p.act_sum);
-        } else {
-#pragma unroll
-          for (int i = 0; i < C::kTiles; ++i)
-            if (i * C::kTileK < ck) cp_async4(info + 4 * i, p.act_sum + i);
-        }
 #pragma unroll
         for (int i = 0; i < C::kRunsOf; ++i)
-          if (i * kRun < ck) cp_async4(info + 4 * (C::kTiles + i), p.act_sc + i);
+          if (i * kRun < ck) cp_async4(info + 4 * i, p.act_sc + i);
       }
       cp_async_arrive(full(st));
     };
@@ -754,7 +740,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_experts(const __grid_consta
         for (int i = 0; i < 4; ++i) {
           const int m = 8 * nb + 2 * tq + (i & 1), c = col0 + 2 * t + (i >> 1);
           if (m < rows) {
-            const float v = acc[t][nb][i] * 16777216.f;    // the codes' 2^-24
+            const float v = acc[t][nb][i] * 1024.f;        // the differences' 2^-10
             if constexpr (DOWN) tile[tok[nb][i & 1] * kCols + c] += wt[nb][i & 1] * v;
             else tile[m * kCols + c] = v;
           }
@@ -792,8 +778,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_experts(const __grid_consta
         h[i] = j < a.inter ? gi / (1.f + expf(-gi)) * (&u.x)[i] : 0.f;
       }
       const long long row = off + m;
-      store_run<BITS>(h, j0, a.inter, a.h + row * a.inter, a.h_scale + row * a.h_runs + j0 / kRun,
-                      a.h_sum + row * (a.inter / C::kTileK) + j0 / C::kTileK);
+      store_run<BITS>(h, j0, a.inter, a.h + row * a.inter, a.h_scale + row * a.h_runs + j0 / kRun);
     }
   };
   // runs first .. last hold an item; the first leaves its part in its slot 1, the others in slot 0
@@ -857,7 +842,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_experts(const __grid_consta
   long long first_chunk = begin + start.u - start.c;       // of the current item, on the line
   open_item();
   // this thread's places in a stage: its pieces of the weights (tile l at w_at[l & 1] + 512 l; the swizzle
-  // goes by the 128-byte line within the stage), scales and zeros, and its rows' activations and sums
+  // goes by the 128-byte line within the stage), scales and zeros, and its rows' activations and scales
   int w_at[BITS == 3 ? ROWS : 2], act_at[NB], info_at[NB][2];
   const int scales_at = L::scales(a.rows) + 2 * col0;
   const int zeros_at = L::zeros(a.rows, a.gmax) + 4 * (warp * BITS + BITS * quad * 4 / 32), zero_shift = BITS * quad * 4 % 32;
@@ -866,7 +851,6 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_experts(const __grid_consta
     const int row = BITS == 3 ? tq * ROWS + i : 4 * i + tq, line = warp * C::kRows + row;
     w_at[i] = line * 128 + ((quad ^ (line & 7)) << 4) - (BITS == 3 ? 0 : 512 * i);
   }
-  const float zero_base = 8388608.f - static_cast<float>(a.zero_offset);
   uint32_t base = smem_a;                                  // of the stage
   int st = 0, g_at = 0;                                    // g_at: k of the chunk within its first group
   unsigned round = 0;
@@ -888,7 +872,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_experts(const __grid_consta
     if (__all_sync(0xFFFFFFFFu, wait(full(st), round, &sm_abort, a.status))) {
       const int k0 = x.kc * C::kK;
       const int tiles = a.K - k0 < C::kK ? (a.K - k0) / C::kTileK : C::kTiles;
-      float gs[4], gz[4];                                  // scales and zeros of this thread's 4 columns
+      float gs[4];                                         // scales and zeros of this thread's 4 columns
+      uint32_t gz[4];
       auto load_group = [&](int g) {
         const uint2 s = lds64(base + scales_at + g * (kCols * 2));
         gs[0] = __half2float(__ushort_as_half(lo16(s.x)));
@@ -899,8 +884,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_experts(const __grid_consta
         uint32_t zf = lds32(zw) >> zero_shift;
         if (BITS == 3) zf = zero_shift + 12 > 32 ? zf | lds32(zw + 4) << (32 - zero_shift) : zf;
 #pragma unroll
-        for (int c = 0; c < 4; ++c)                        // 2^23 + z - 2^23
-          gz[c] = __uint_as_float(0x4B000000u | ((zf >> (BITS * c)) & P::kMask)) - zero_base;
+        for (int c = 0; c < 4; ++c) gz[c] = zero_pair(((zf >> (BITS * c)) & P::kMask) + a.zero_offset);
       };
       auto load_tile = [&](int l, uint4 (&w)[ROWS]) {
 #pragma unroll
@@ -927,8 +911,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_experts(const __grid_consta
         uint32_t d[4][NP];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          if constexpr (BITS == 3) RP::run3((&w[0].x)[c], (&w[1].x)[c], (&w[2].x)[c], d[c]);
-          else RP::run((&w[0].x)[c], d[c]);
+          if constexpr (BITS == 3) RP::run3((&w[0].x)[c], (&w[1].x)[c], (&w[2].x)[c], gz[c], d[c]);
+          else RP::run((&w[0].x)[c], gz[c], d[c]);
         }
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
@@ -955,29 +939,19 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_experts(const __grid_consta
         load_acts(l, 0, b);
         multiply(l, w, b);
       };
-      // tiles l0 .. l1 are done: acc += scale (act_scale c - zero 2^-24 sum a)
-      auto fold = [&](int l0, int l1) {
+      // tiles of the run that tile l0 lies in are done: acc += scale act_scale c
+      auto fold = [&](int l0) {
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
           if (nb == 0 || 8 * nb < rows) {
-            float s[2], sum[2];
+            float s[2];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const uint32_t row = base + info_at[nb][i];
-              s[i] = __uint_as_float(lds32(row + 4 * (C::kTiles + l0 * C::kTileK / kRun)));
-              if (C::kTiles == 4 && l0 == 0 && l1 == 3) {
-                const uint4 v = lds128(row);
-                sum[i] = (__uint_as_float(v.x) + __uint_as_float(v.y)) + (__uint_as_float(v.z) + __uint_as_float(v.w));
-              } else {
-                sum[i] = __uint_as_float(lds32(row + 4 * l0));
-                for (int l = l0 + 1; l <= l1; ++l) sum[i] += __uint_as_float(lds32(row + 4 * l));
-              }
-            }
+            for (int i = 0; i < 2; ++i) s[i] = __uint_as_float(lds32(base + info_at[nb][i] + 4 * (l0 * C::kTileK / kRun)));
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
               for (int i = 0; i < 4; ++i)
-                acc[t][nb][i] = fmaf(gs[2 * t + (i >> 1)], fmaf(-gz[2 * t + (i >> 1)], sum[i & 1], s[i & 1] * cg[t][nb][i]), acc[t][nb][i]);
+                acc[t][nb][i] = fmaf(gs[2 * t + (i >> 1)], s[i & 1] * cg[t][nb][i], acc[t][nb][i]);
           }
         }
       };
@@ -1002,10 +976,10 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_experts(const __grid_consta
 #pragma unroll
             for (int l = l0; l < l0 + C::kSegTiles; ++l) tile_mma(l);
           }
-          fold(l0, l0 + C::kSegTiles - 1);
+          fold(l0);
         }
       } else {
-        int g = 0, l0 = 0, g_end = k0 - g_at + a.group;
+        int g = 0, g_end = k0 - g_at + a.group;
         clear(cg);
         load_group(0);
 #pragma unroll
@@ -1014,9 +988,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_experts(const __grid_consta
             tile_mma(l);
             const int k = k0 + (l + 1) * C::kTileK;
             if (k == g_end || k % kRun == 0 || l + 1 == tiles) {   // a group, a run or the chunk ends
-              fold(l0, l);
+              fold(l);
               clear(cg);
-              l0 = l + 1;
               if (k == g_end && l + 1 < tiles) {
                 load_group(++g);
                 g_end += a.group;
