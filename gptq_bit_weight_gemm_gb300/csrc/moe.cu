@@ -36,7 +36,7 @@ Space space(int tokens, int hidden, int inter, int experts, int topk) {
   s.act = s.logits + up(static_cast<size_t>(tokens) * experts * 4);
   s.act_scale = s.act + up(static_cast<size_t>(tokens) * hidden * 2);
   s.h = s.act_scale + up(static_cast<size_t>(tokens) * ((hidden + kRun - 1) / kRun) * 4);
-  s.h_scale = s.h + up(rows * inter * 2);
+  s.h_scale = s.h + up(rows * 2 * inter * 2);              // two parts at most
   s.partials = s.h_scale + up(rows * ((inter + kRun - 1) / kRun) * 4);
   s.total = s.partials + static_cast<size_t>(kMaxRuns) * 2 * tokens * kCols * 4;
   return s;
@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) k_route(const RouteArgs a) {
     v[2] = F16Traits<T>::to_f32(F16Traits<T>::from_bits(lo16(w.y)));
     v[3] = F16Traits<T>::to_f32(F16Traits<T>::from_bits(hi16(w.y)));
   }
-  store_run<BITS>(v, j0, a.hidden, a.act + static_cast<long long>(t) * a.hidden, a.act_scale + static_cast<long long>(t) * runs + j0 / kRun);
+  store_run<BITS>(v, j0, a.hidden, 1, a.act + static_cast<long long>(t) * a.hidden, a.act_scale + static_cast<long long>(t) * runs + j0 / kRun);
 }
 
 template <typename T>
@@ -170,6 +170,8 @@ cudaError_t launch_moe(const MoeProblem& p, cudaStream_t stream) {
   up.qzeros = p.up.qzeros;
   up.scales = static_cast<const __half*>(p.up.scales);
   up.tokens = p.tokens;
+  up.parts = 1;
+  up.h_parts = p.dtype == 0 ? 2 : 1;
   up.experts = p.experts; up.topk = p.topk; up.renormalize = p.renormalize;
   up.logits = ra.logits;
   up.ids = p.ids; up.weights = p.weights;
@@ -183,6 +185,7 @@ cudaError_t launch_moe(const MoeProblem& p, cudaStream_t stream) {
   up.partials = reinterpret_cast<float*>(ws + s.partials);
   up.status = p.status;
   moe::Args down = up;
+  down.parts = up.h_parts;
   down.K = p.inter; down.N = p.hidden; down.group = p.group_down; down.G = p.inter / p.group_down;
   down.qzeros = p.down.qzeros;
   down.scales = static_cast<const __half*>(p.down.scales);

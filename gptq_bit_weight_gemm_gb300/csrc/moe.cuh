@@ -30,7 +30,10 @@
 // Activations are fp16 in both stages: every row's run of 128 values is stored as fp16 times a power
 // of two chosen for the run (11 bits of each value above 2^-28 of the run's largest; exact for fp16 and
 // bf16 input in that range), already in the pair order of the codes.  So h may exceed fp16's range, and
-// bf16 models lose nothing to the multiply.
+// bf16 models lose nothing to the multiply.  Where the output is fp16 too, 11 bits of h would show in it
+// (relative error 2.9e-4 against the 2.1e-4 of the output's own rounding), so h goes in two parts there,
+// its rounding and what the rounding left, as two rows of the products: free where a block of 8 rows has
+// room for them.
 #pragma once
 
 #include <cuda.h>
@@ -82,7 +85,7 @@ struct Routing {
   int* row_token;        // [pairs] rows by expert, an expert's by token
   float* row_weight;
   __host__ __device__ static int most_slots(int pairs, int experts) {
-    return (pairs < experts ? pairs : experts) + pairs / 8;
+    return (pairs < experts ? pairs : experts) + pairs / 4;   // (4 rows a slot at least, unless there are fewer)
   }
   __host__ __device__ static int bytes(int pairs, int experts) {
     return (16 * pairs + 4 * experts + 8 * most_slots(pairs, experts) + 4 + 15) & ~15;
@@ -94,12 +97,15 @@ struct Args {
   const int32_t* qzeros;
   const __half* scales;
   int tokens;
-  int rows;              // of a slot, at most; of the ring's activation part
+  int rows;              // of a slot, at most
+  int parts;             // fp16 rows of a row's activations: 1, or 2 (DOWN)
+  int ring_rows;         // of the ring's activation part: rows * parts
+  int h_parts;           // UP: DOWN's parts
   int experts, topk, renormalize;
   const float* logits;   // [tokens][experts]
   int32_t* ids;          // UP, nullable: the caller's copies
   float* weights;
-  const __half* act;     // UP: [tokens][K] in pair order; DOWN: [rows][K]
+  const __half* act;     // UP: [tokens][K] in pair order; DOWN: [rows][parts][K]
   const float* act_scale;   // [row][act_runs]
   int act_runs;
   int jblocks;           // column blocks: UP ceil(inter / 128), DOWN ceil(hidden / 256)
@@ -204,10 +210,10 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int 
 }
 __device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory"); }
 
-// One warp stores a run of a row: lane l holds values 4 l .. 4 l + 3 (zeros past K).  act: the row; the
-// run's power of two goes to *scale.
+// One warp stores a run of a row: lane l holds values 4 l .. 4 l + 3 (zeros past K).  act: the row, or in
+// two parts the two rows of its roundings and of what they left; the run's power of two goes to *scale.
 template <int BITS>
-__device__ __forceinline__ void store_run(const float (&v)[4], int j0, int K, __half* act, float* scale) {
+__device__ __forceinline__ void store_run(const float (&v)[4], int j0, int K, int parts, __half* act, float* scale) {
   constexpr int per = Pack<BITS>::kPerUnit;
   const int lane = threadIdx.x & 31, j = j0 + 4 * lane;
   float top = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
@@ -216,8 +222,14 @@ __device__ __forceinline__ void store_run(const float (&v)[4], int j0, int K, __
   const int e = run_exponent(top);
   const float inv = pow2(-e);
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (j < K) act[(j + i) / per * per + pair_pos<BITS>((j + i) % per)] = __float2half_rn(v[i] * inv);
+  for (int i = 0; i < 4; ++i) {
+    const int at = (j + i) / per * per + pair_pos<BITS>((j + i) % per);
+    const __half x = __float2half_rn(v[i] * inv);
+    if (j < K) {
+      act[at] = x;
+      if (parts == 2) act[K + at] = __float2half_rn(v[i] * inv - __half2float(x));
+    }
+  }
   if (lane == 0) *scale = pow2(e);
 }
 
@@ -574,8 +586,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_experts(const __grid_consta
       }
       p.slot = p.x.s;
       const int expert = rt.slot_expert[p.slot], off = rt.slot_off[p.slot];
-      p.off = off;
-      p.rows = rt.slot_off[p.slot + 1] - off;
+      p.off = off * a.parts;
+      p.rows = (rt.slot_off[p.slot + 1] - off) * a.parts;
       const int k0 = p.x.kc * C::kK;
       p.g = k0 / a.group;
       p.g_at = k0 - p.g * a.group;
@@ -584,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_experts(const __grid_consta
       p.sc = a.scales + grow * a.N + p.sc_col + 8 * (lane & 3);
 #pragma unroll
       for (int i = 0; i < 2; ++i) p.zr[i] = a.qzeros + grow * a.zwords + p.zc[i] / 32 * BITS + (lane + 32 * i) % BITS;
-      const int row = lane < p.rows ? (DOWN ? off + lane : rt.row_token[off + lane]) : 0;
+      const int row = lane < p.rows ? (DOWN ? off + (a.parts == 2 ? lane >> 1 : lane) : rt.row_token[off + lane]) : 0;
       p.act_sc = a.act_scale + static_cast<long long>(row) * a.act_runs + k0 / kRun;
     };
     auto step = [&](Put& p) {                              // to the next chunk
@@ -620,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_experts(const __grid_consta
       const __half* sc = p.sc;
       const int32_t* z0 = p.zr[0];
       const int32_t* z1 = p.zr[1];
-      uint32_t sc_to = to + L::scales(a.rows) + lane * 16, z_to = to + L::zeros(a.rows, a.gmax) + lane * 4;
+      uint32_t sc_to = to + L::scales(a.ring_rows) + lane * 16, z_to = to + L::zeros(a.ring_rows, a.gmax) + lane * 4;
       for (int at = -p.g_at; at < ck; at += a.group) {      // the groups that the chunk touches
         if (p.sc_col >= 0) cp_async16(sc_to, sc);
         if (p.zc[0] >= 0) cp_async4(z_to, z0);
@@ -646,7 +658,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_experts(const __grid_consta
                      a.act + static_cast<long long>(row) * a.K + p.x.kc * C::kK + piece * 8);
       }
       if (lane < p.rows) {
-        const uint32_t info = to + L::info(a.rows) + lane * C::kInfo * 4;
+        const uint32_t info = to + L::info(a.ring_rows) + lane * C::kInfo * 4;
 #pragma unroll
         for (int i = 0; i < C::kRunsOf; ++i)
           if (i * kRun < ck) cp_async4(info + 4 * i, p.act_sc + i);
@@ -711,26 +723,28 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_experts(const __grid_consta
         for (int i = 0; i < 4; ++i) x[t][nb][i] = 0.f;
   };
   Cursor x = start;
-  int cur = -1, rows = 0, off = 0;
+  int cur = -1, rows = 0, off = 0;                         // rows: of the products (a row's parts count each)
   int tok[NB][2];
   float wt[NB][2];
   auto open_slot = [&]() {
     cur = x.s;
     off = rt.slot_off[cur];
-    rows = rt.slot_off[cur + 1] - off;
+    const int count = rt.slot_off[cur + 1] - off;
+    rows = count * a.parts;
     if constexpr (DOWN) {
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const int m = 8 * nb + 2 * tq + i;
-          tok[nb][i] = m < rows ? rt.row_token[off + m] : 0;
-          wt[nb][i] = m < rows ? rt.row_weight[off + m] : 0.f;
+          const int m = a.parts == 2 ? 4 * nb + tq : 8 * nb + 2 * tq + i;
+          tok[nb][i] = m < count ? rt.row_token[off + m] : 0;
+          wt[nb][i] = m < count ? rt.row_weight[off + m] : 0.f;
         }
     }
     clear(acc);
   };
-  // the finished rows of a slot into the tile: UP stores [row][column], DOWN adds w * y to [token]
+  // the finished rows of a slot into the tile: UP stores [row][column], DOWN adds w * y to [token] (both
+  // parts of a row are one thread's)
   auto close_slot = [&]() {
 #pragma unroll
     for (int t = 0; t < 2; ++t)
@@ -778,7 +792,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_experts(const __grid_consta
         h[i] = j < a.inter ? gi / (1.f + expf(-gi)) * (&u.x)[i] : 0.f;
       }
       const long long row = off + m;
-      store_run<BITS>(h, j0, a.inter, a.h + row * a.inter, a.h_scale + row * a.h_runs + j0 / kRun);
+      store_run<BITS>(h, j0, a.inter, a.h_parts, a.h + row * a.h_parts * a.inter, a.h_scale + row * a.h_runs + j0 / kRun);
     }
   };
   // runs first .. last hold an item; the first leaves its part in its slot 1, the others in slot 0
@@ -844,8 +858,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_experts(const __grid_consta
   // this thread's places in a stage: its pieces of the weights (tile l at w_at[l & 1] + 512 l; the swizzle
   // goes by the 128-byte line within the stage), scales and zeros, and its rows' activations and scales
   int w_at[BITS == 3 ? ROWS : 2], act_at[NB], info_at[NB][2];
-  const int scales_at = L::scales(a.rows) + 2 * col0;
-  const int zeros_at = L::zeros(a.rows, a.gmax) + 4 * (warp * BITS + BITS * quad * 4 / 32), zero_shift = BITS * quad * 4 % 32;
+  const int scales_at = L::scales(a.ring_rows) + 2 * col0;
+  const int zeros_at = L::zeros(a.ring_rows, a.gmax) + 4 * (warp * BITS + BITS * quad * 4 / 32), zero_shift = BITS * quad * 4 % 32;
 #pragma unroll
   for (int i = 0; i < (BITS == 3 ? ROWS : 2); ++i) {
     const int row = BITS == 3 ? tq * ROWS + i : 4 * i + tq, line = warp * C::kRows + row;
@@ -865,7 +879,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_experts(const __grid_consta
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int mi = 8 * nb + 2 * tq + i;
-          info_at[nb][i] = L::info(a.rows) + (mi < rows ? mi : rows - 1) * (C::kInfo * 4);
+          info_at[nb][i] = L::info(a.ring_rows) + (mi < rows ? mi : rows - 1) * (C::kInfo * 4);
         }
       }
     }
@@ -1082,11 +1096,12 @@ cudaError_t launch_experts(Args a, const int32_t* qweight, int experts, int* run
   const DeviceInfo& dev = device_info();
   a.units = a.K / Pack<BITS>::kPerUnit;
   a.zwords = a.N / 32 * BITS;
-  a.rows = a.tokens < 8 * NB ? a.tokens : 8 * NB;
+  a.rows = a.tokens < 8 * NB / a.parts ? a.tokens : 8 * NB / a.parts;
+  a.ring_rows = a.rows * a.parts;
   a.gmax = (C::kK - 1) / a.group + 2;
   if (a.group % C::kK == 0) a.gmax = 1;
   else if (C::kK % a.group == 0) a.gmax = C::kK / a.group;
-  a.stage_bytes = L::stage(a.rows, a.gmax);
+  a.stage_bytes = L::stage(a.ring_rows, a.gmax);
   const int pairs = a.tokens * a.topk;
   int per_sm = kCtas;
   auto fit = [&](int ctas) {
@@ -1132,9 +1147,12 @@ cudaError_t launch_experts(Args a, const int32_t* qweight, int experts, int* run
 
 template <int BITS, bool DOWN>
 cudaError_t launch_blocks(const Args& a, const int32_t* qweight, int experts, int* runs, cudaStream_t stream) {
-  // blocks of 8 rows where few experts have more: the others' weights are read once for each block
-  // (16 tokens, 2 of 8 experts each: 204 us in blocks of 16)
-  if (a.tokens <= 8 || a.tokens * a.topk <= 4 * a.experts) return launch_experts<BITS, 1, DOWN>(a, qweight, experts, runs, stream);
+  // single blocks (8 rows, or 4 in two parts) where few experts have more: the others' weights are read once
+  // for each block (4-bit wide layer, 2 of 8 experts a token, in single and double blocks: 8 tokens in two
+  // parts 172 and 184 us, 16 tokens in one 187 and 204)
+  constexpr int kBlock = 8;
+  const int room = kBlock / a.parts;
+  if (a.tokens <= room || 2 * a.tokens * a.topk <= room * a.experts) return launch_experts<BITS, 1, DOWN>(a, qweight, experts, runs, stream);
   return launch_experts<BITS, 2, DOWN>(a, qweight, experts, runs, stream);
 }
 

@@ -72,9 +72,10 @@ int gptq_paged_attention(const void* q, int batch, int heads, int dtype, void* k
  *   p = softmax(router x),  S = the topk experts of largest p (equal p: the lower index first),
  *   w_e = p_e (renormalize: p_e / sum_{S} p),
  *   out = sum_{e in S} w_e * down_e( silu(gate_e x) * up_e x ).
- * Every weight of an expert that no token chose is left unread.  Products accumulate in fp32; the
- * inner activation silu(g) * u is rounded once to fp16 times a power of two for each row's run of
- * 128 values (11 significant bits relative to the run's largest, for both dtypes), out once.
+ * Every weight of an expert that no token chose is left unread.  Products are of exact (q - zero)
+ * and accumulate in fp32; the inner activation silu(g) * u is kept as fp16 times a power of two for
+ * each row's run of 128 values, in 11 significant bits for bf16 and in 22 (a sum of two) for fp16;
+ * out is rounded once.
  *   x        [tokens, hidden] of dtype          router [experts, hidden] of dtype
  *   up_*     packed as for gptq_gemm_grouped, K = hidden, N = 2 * inter: columns [0, inter) are the
  *            gate, [inter, 2 * inter) the up projection

@@ -1,5 +1,5 @@
 """gptq_moe where the arithmetic, not the layout, decides: groups whose codes equal their zero under
-large scales, with activations that have outlier channels.
+large scales, activations with outlier channels, and the accuracy of the whole layer against 64 bits.
 
 The bounds of `test_gpu_moe.check` are proportional to sum |x w|, which is 0 for a column of such groups:
 what the layer returns there has to be 0 up to fp16's smallest step, whatever the scale and the
@@ -73,3 +73,32 @@ def test_groups_of_zeros_stay_zero(bits, group, fmt, dtype, tokens):
     out = check(a, Wu, Wd)
     assert float(out[:, DEAD + [513, 1023]].abs().max()) <= 2.0 ** -24
     assert float(out.abs().max()) > 0
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("tokens,E,topk,H,I,bits,group", [(1, 4, 2, 1024, 512, 4, 128), (3, 8, 2, 2048, 384, 4, -1), (8, 8, 2, 1024, 320, 8, 32),
+                                                          (16, 16, 4, 1024, 512, 8, 128), (32, 4, 2, 512, 1024, 4, 64),
+                                                          (32, 8, 2, 1024, 512, 3, 128), (5, 6, 1, 1024, 512, 2, 64)])
+def test_only_the_output_is_rounded_to_16_bits(tokens, E, topk, H, I, bits, group, dtype):
+    """The 2-norm of the error against 64 bits is that of rounding the exact result once, r, within a
+    tenth.  What else there is: fp32 sums of up to 2048 products, 2^-24 each step of a sum that grows as a
+    random walk, so some 2^-22 of sum |h w|, which for random signs is sqrt(I) < 32 times the result
+    (2^-17), and an inner activation of at least 20 significant bits (2^-21 each): with r = 2^-12.2 in
+    fp16 the sum of squares grows by 2^-9."""
+    rng = np.random.default_rng(tokens + H)
+    up, Wu = packed(rng, E, H, 2 * I, bits, group, g.V2, 0.1 / 2 ** bits, [])
+    down, Wd = packed(rng, E, I, H, bits, group, g.V2, 0.1 / 2 ** bits, [])
+    x = torch.from_numpy(rng.standard_normal((tokens, H))).to(dtype).to(DEV)
+    router = torch.from_numpy(rng.standard_normal((E, H)) * 2 / H ** 0.5).to(dtype).to(DEV)
+    out, ids, w = g.moe_layer(x, router, up, down, topk=topk, bits=bits, group=group, return_routing=True)
+    p = torch.softmax(x.double() @ router.double().T, -1).gather(1, ids.long())
+    p = p / p.sum(-1, keepdim=True)
+    ref = torch.zeros((tokens, H), dtype=torch.float64, device=DEV)
+    for t in range(tokens):
+        for j in range(topk):
+            e = int(ids[t, j])
+            y = x[t].double() @ Wu[e]
+            ref[t] += p[t, j] * ((torch.nn.functional.silu(y[:I]) * y[I:]) @ Wd[e])
+    own = float((ref.to(dtype).double() - ref).norm() / ref.norm())
+    err = float((out.double() - ref).norm() / ref.norm())
+    assert err <= 1.1 * own, (err, own)
