@@ -27,6 +27,12 @@
 // dimensions of key g as the B fragments of two k-steps of q k^T, and the query fragments are loaded in
 // the same order.  The scores' C fragment is the A fragment of p v as it stands.
 //
+// The probabilities go to the tensor cores in two parts, their rounding to 16 bits and what it left (16
+// significant bits for bf16, 22 for fp16; one part shows in the output: relative error 2.2e-3 in bf16, 1.7e-3
+// so).  The second parts are the A rows 8 .. 15 where an item has at most 8 query heads, and products of their
+// own where it has more.  They are taken 2^15 times as large, as l and o are throughout: one part in 2^25
+// of the largest, of which a long flat tail may have thousands, would be nothing in fp16.
+//
 // Measured (GB300, bf16, 32 query and 8 kv heads of 128): 64 sequences of 512 to 8192 keys 120 us,
 // 6.3 TB/s; one of 131072 keys 89 us, 6.0 TB/s; one of 997 keys 8 us, the latencies of launch, lengths,
 // table, keys, partial and join one after the other.
@@ -45,6 +51,7 @@ namespace attention {
 constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kWarpKeys = 16, kTileKeys = kWarps * kWarpKeys;
 constexpr int kMaxRows = 16;             // query heads of one item
+constexpr float kLift = 15.f;            // probabilities are taken times 2^kLift
 constexpr int kMaxCtas = 512;            // runs, at most
 constexpr size_t kControlBytes = 4096;   // arrival counters, one per run
 
@@ -445,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, R>::kCtas)) k_attention(c
             R == 2 ? q[R - 1][4 * blk + 3] : 0u, v.z, v.w, T());
       }
     }
-    uint32_t pa[2][2];                                     // [row block][key half]: the A fragment of p v
+    uint32_t pa[2][2], rest[R][2];                         // [row block][key half]: the A fragment of p v
     bool moved = false;
     float alpha[R];
 #pragma unroll
@@ -460,24 +467,26 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, R>::kCtas)) k_attention(c
       float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
       top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-      const float mn = fmaxf(m[r], top), base = mn == -CUDART_INF_F ? 0.f : mn;
+      const float mn = fmaxf(m[r], top), base = mn == -CUDART_INF_F ? 0.f : mn, low = base - kLift;
       alpha[r] = exp2f(m[r] - base);
       moved |= mn != m[r];
       m[r] = mn;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] = exp2f(x[i] - base);
+      for (int i = 0; i < 4; ++i) x[i] = exp2f(x[i] - low);
       l[r] = l[r] * alpha[r] + ((x[0] + x[1]) + (x[2] + x[3]));
-      // the probabilities are rounded to 16 bits for the tensor cores (relative 2^-11 / 2^-8, as the
-      // values they multiply); their sum l is not
-      pa[r][0] = pack2(x[0], x[1], T());
-      pa[r][1] = pack2(x[2], x[3], T());
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t h = pack2(x[2 * i], x[2 * i + 1], T());
+        pa[r][i] = h;
+        rest[r][i] = pack2(x[2 * i] - Tr::to_f32(Tr::from_bits(lo16(h))), x[2 * i + 1] - Tr::to_f32(Tr::from_bits(hi16(h))), T());
+      }
     }
-    if (R == 1) pa[1][0] = pa[1][1] = 0u;
+    if (R == 1) pa[1][0] = rest[0][0], pa[1][1] = rest[0][1];
     if (__any_sync(0xFFFFFFFFu, moved)) {
 #pragma unroll
       for (int i = 0; i < S::kCols; ++i)
 #pragma unroll
-        for (int c = 0; c < 2 * R; ++c) o[i][c] *= alpha[c >> 1];
+        for (int c = 0; c < 4; ++c) o[i][c] *= alpha[R == 2 ? c >> 1 : 0];
     }
 #pragma unroll
     for (int i = 0; i < S::kCols; i += 2) {                // keys 0..7 and 8..15 of two column tiles
@@ -485,6 +494,10 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, R>::kCtas)) k_attention(c
       ldsm4_trans(v, v_at[(i >> 1) & 3] + at + (i >> 3) * 128);
       mma(o[i], pa[0][0], pa[1][0], pa[0][1], pa[1][1], v[0], v[1], T());
       mma(o[i + 1], pa[0][0], pa[1][0], pa[0][1], pa[1][1], v[2], v[3], T());
+      if (R == 2) {
+        mma(o[i], rest[0][0], rest[R - 1][0], rest[0][1], rest[R - 1][1], v[0], v[1], T());
+        mma(o[i + 1], rest[0][0], rest[R - 1][0], rest[0][1], rest[R - 1][1], v[2], v[3], T());
+      }
     }
   };
 
@@ -521,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, R>::kCtas)) k_attention(c
         const int d = (warp * kMine + i) * 8 + 2 * t;
         if (d < p.head_dim) *reinterpret_cast<uint32_t*>(out + d) = pack2(sum[i][0] * inv, sum[i][1] * inv, T());
       }
-      if (p.lse && warp == 0 && t == 0) p.lse[at] = M * 0.693147180559945f + logf(L);
+      if (p.lse && warp == 0 && t == 0) p.lse[at] = M * 0.693147180559945f + logf(L * (1.f / 32768.f));   // 2^-kLift
     };
     float M[R], L[R];
 #pragma unroll
@@ -539,7 +552,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, R>::kCtas)) k_attention(c
       float sum[kMine][2];
 #pragma unroll
       for (int i = 0; i < S::kCols; ++i) {
-        const float2 v = make_float2(o[i][2 * r] * f, o[i][2 * r + 1] * f);
+        const float2 v = R == 2 ? make_float2(o[i][2 * r] * f, o[i][2 * r + 1] * f)
+                                : make_float2((o[i][0] + o[i][2]) * f, (o[i][1] + o[i][3]) * f);
         const int owner = i / kMine, from = (warp - owner + kWarps - 1) % kWarps;   // 0 .. 2, 3 for the owner
         if (warp == owner) {
           sum[i % kMine][0] = v.x;

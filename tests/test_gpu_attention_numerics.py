@@ -1,0 +1,60 @@
+"""gptq_paged_attention's probabilities: they reach the product with v in more bits than the result has.
+
+The error's 2-norm against 64 bits is that of rounding the exact result once, r, within a tenth.  What
+else there is: scores as fp32 sums, off by some 2^-21 of |s| < 8, and probabilities of at least 16
+significant bits (2^-17): against r = 2^-9.2 (bf16) and 2^-12.2 (fp16) the sum of squares grows by less
+than 2^-8."""
+import numpy as np
+import pytest
+import torch
+
+import gptq_bit_weight_gemm_gb300 as g
+from test_gpu_paged_attention import Case, LENS, check
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from gptq_bit_weight_gemm_gb300 import build as lib_build
+    lib_build.build()
+    assert torch.cuda.is_available()
+    yield
+    assert g.device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("heads,kv,dim", [(8, 2, 64), (8, 8, 128), (32, 8, 128), (16, 1, 96), (24, 1, 128), (40, 1, 64), (4, 4, 256),
+                                          (12, 1, 256)])
+def test_only_the_output_is_rounded_to_16_bits(dtype, heads, kv, dim):
+    c = Case(LENS + [3000], heads, kv, dim, 16, dtype, seed=dim + heads)
+    out = check(c).double().cpu()
+    ref = c.ref(dim ** -0.5, 0)[0]
+    own = float((ref.to(dtype).double() - ref).norm() / ref.norm())
+    err = float((out - ref).norm() / ref.norm())
+    assert err <= 1.1 * own, (err, own)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("group", [1, 12])
+@pytest.mark.parametrize("halvings", [12, 16, 20, 23.5, 25.5, 28])
+def test_a_peak_over_a_flat_tail(dtype, group, halvings):
+    """One key of probability near 1 and value 0 before thousands of equal ones with value 1: the result
+    is the tail's mass, each of whose terms is 2^-halvings of the peak's."""
+    B, kv, n, dim, page = 48, 8, 4001, 64, 32
+    pages = -(-n // page)
+    k = torch.zeros((pages, page, kv, dim), dtype=dtype, device=DEV)
+    v = torch.ones_like(k)
+    q = torch.zeros((B, kv * group, dim), dtype=dtype, device=DEV)
+    q[:, :, 0] = 4.0
+    k[0, 0, :, 0] = halvings * np.log(2.0) / 4.0
+    v[0, 0] = 0.0
+    table = torch.arange(pages, dtype=torch.int32, device=DEV).repeat(B, 1)
+    out = g.paged_attention(q, k, v, table, torch.full((B,), n, dtype=torch.int32, device=DEV), scale=1.0)
+    s = float(k[0, 0, 0, 0]) * 4.0
+    ref = (n - 1) * np.exp(-s) / (1.0 + (n - 1) * np.exp(-s))
+    # the tolerance of the attention tests: A = ref, as all values that count are 1
+    u = 2.0 ** (-11 if dtype == torch.float16 else -8)
+    tol = (2 * u + 2.0 ** -16 * (1 + s)) * ref + 2.0 ** -24
+    assert float((out.double() - ref).abs().max()) <= tol, (float(out.min()), float(out.max()), ref)
