@@ -308,8 +308,10 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, R>::kCtas)) k_attention(c
     const int entry = static_cast<int>(static_cast<unsigned long long>(static_cast<unsigned>(key)) * a.page_mul >> a.page_shift);
     slot = key - entry * p.page_size;
     page = want ? __ldg(p.table + static_cast<long long>(put.b) * p.table_width + entry) : -1;
-    // the new token's own row comes from k_new and v_new: fetched here, a tile ahead
+    // the new token's own row comes from k_new and v_new: fetched here, a tile ahead.  Past the block table
+    // it has no slot: the last one holds an older key
     fresh_row = p.k_new && put.n > kb && put.n <= kb + kWarpKeys ? put.n - 1 - kb : -1;
+    if (fresh_row >= 0 && put.n == p.table_width * p.page_size && p.lens[put.b] != put.n) fresh_row = -1;
     if (fresh_row >= 0) {
 #pragma unroll
       for (int i = 0; i < kFresh; ++i) {

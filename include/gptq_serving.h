@@ -30,7 +30,8 @@ extern "C" {
 #define GPTQ_DEV_PAGE_RANGE 0x20u     /* gptq_paged_attention: a live key's block-table entry was
                                          outside [0, pages); its page's keys were left out       */
 #define GPTQ_DEV_SEQ_LEN 0x40u        /* gptq_paged_attention: a length was negative (taken as 0)
-                                         or longer than the block table (cut to it)              */
+                                         or longer than the block table (cut to it, and its new
+                                         token neither appended nor used)                        */
 #define GPTQ_DEV_NO_TOKEN 0x80u       /* gptq_sample: a row held no logit above -inf; its token
                                          is -1                                                   */
 

@@ -58,3 +58,22 @@ def test_a_peak_over_a_flat_tail(dtype, group, halvings):
     u = 2.0 ** (-11 if dtype == torch.float16 else -8)
     tol = (2 * u + 2.0 ** -16 * (1 + s)) * ref + 2.0 ** -24
     assert float((out.double() - ref).abs().max()) <= tol, (float(out.min()), float(out.max()), ref)
+
+
+def test_a_cut_length_appends_nothing():
+    """A length past the block table is cut to it and flagged; the new token then has no slot: neither the
+    cache nor the result takes it."""
+    c = Case([30, 64, 48], 8, 2, 64, 16, torch.float16, seed=11, width=4)
+    a = c.gpu()
+    gen = torch.Generator().manual_seed(1)
+    new = [torch.randn((3, 2, 64), generator=gen).half().to(DEV) for _ in range(2)]
+    a["seq_lens"][1] = 65                             # four pages of 16 hold 64 keys
+    keys, values = a["k_cache"].clone(), a["v_cache"].clone()
+    out = g.paged_attention(**dict(a, k_new=new[0], v_new=new[1]))
+    assert g.device_status() == g.DEV_SEQ_LEN
+    ref, tol, _, _ = c.ref(64 ** -0.5, 0)             # sequence 1: its 64 cached keys
+    assert bool(((out[1].double().cpu() - ref[1]).abs() <= tol[1]).all())
+    for cache, old, fresh in ((a["k_cache"], keys, new[0]), (a["v_cache"], values, new[1])):
+        for b, n in ((0, 30), (2, 48)):               # the others' new tokens are in their slots
+            old[int(c.table[b, (n - 1) // 16]), (n - 1) % 16] = fresh[b]
+        assert torch.equal(cache.view(torch.int16), old.view(torch.int16))
