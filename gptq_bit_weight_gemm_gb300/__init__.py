@@ -640,10 +640,7 @@ def paged_attention(q, k_cache, v_cache, block_table, seq_lens, *, scale=None, w
         with _on(stream):
             workspace = paged_attention_workspace(heads, kv_heads, dim)
     ws, ws_bytes = _workspace(workspace)
-    if batch == 1:                     # the strides of a dimension of one may be anything
-        strides = _Strides(0, 0, 0, ks[0], ks[1], ks[2], vs[0], vs[1], vs[2])
-    else:
-        strides = _Strides(qs[0], kn_stride, vn_stride, ks[0], ks[1], ks[2], vs[0], vs[1], vs[2])
+    strides = _Strides(qs[0], kn_stride, vn_stride, ks[0], ks[1], ks[2], vs[0], vs[1], vs[2])
     rc = rt.lib.gptq_paged_attention(q.data_ptr(), batch, heads, code, k_cache.data_ptr(), v_cache.data_ptr(), pages, page_size,
                                      kv_heads, dim, strides, block_table.data_ptr(), table_shape[1], seq_lens.data_ptr(), kn, vn,
                                      dim ** -0.5 if scale is None else scale, window, out_ptr, lse_ptr, ws, ws_bytes,

@@ -46,13 +46,18 @@ extern "C" int gptq_paged_attention(const void* q, int batch, int heads, int dty
   if (static_cast<long long>(batch) * heads > (1ll << 24)) return GPTQ_ERR_SHAPE;
   if (batch == 0) return GPTQ_OK;
   if (!q || !k_cache || !v_cache || !block_table || !seq_lens || !out || !workspace) return GPTQ_ERR_ARG;
-  for (int i = 0; i < 9; ++i)
-    if (strides[i] < 0 || strides[i] % 8) return GPTQ_ERR_ALIGN;
+  // a dimension of one is never stepped over, whatever its stride
+  const int steps[9] = {batch, batch, batch, pages, page_size, kv_heads, pages, page_size, kv_heads};
+  long long st[9];
+  for (int i = 0; i < 9; ++i) {
+    st[i] = steps[i] > 1 ? strides[i] : 0;
+    if (st[i] < 0 || st[i] % 8) return GPTQ_ERR_ALIGN;
+  }
   // rows of a cache are found by 32-bit offsets in 16-byte units
   for (int i = 3; i < 9; i += 3) {
-    if (strides[i] > (1ll << 40) || strides[i + 1] > (1ll << 40) || strides[i + 2] > (1ll << 40)) return GPTQ_ERR_SHAPE;
-    const __int128 last = static_cast<__int128>(pages - 1) * strides[i] + static_cast<__int128>(page_size - 1) * strides[i + 1] +
-                          static_cast<__int128>(kv_heads - 1) * strides[i + 2] + head_dim;
+    if (st[i] > (1ll << 40) || st[i + 1] > (1ll << 40) || st[i + 2] > (1ll << 40)) return GPTQ_ERR_SHAPE;
+    const __int128 last = static_cast<__int128>(pages - 1) * st[i] + static_cast<__int128>(page_size - 1) * st[i + 1] +
+                          static_cast<__int128>(kv_heads - 1) * st[i + 2] + head_dim;
     if (last > (static_cast<__int128>(1) << 35)) return GPTQ_ERR_SHAPE;
   }
   if (!aligned_to(q, 16) || !aligned_to(k_cache, 16) || !aligned_to(v_cache, 16) || !aligned_to(k_new, 16) ||
@@ -66,9 +71,9 @@ extern "C" int gptq_paged_attention(const void* q, int batch, int heads, int dty
   p.q = q; p.batch = batch; p.heads = heads; p.dtype = dtype;
   p.k_cache = k_cache; p.v_cache = v_cache; p.pages = pages; p.page_size = page_size;
   p.kv_heads = kv_heads; p.head_dim = head_dim;
-  p.q_batch = strides[0]; p.kn_batch = strides[1]; p.vn_batch = strides[2];
-  p.k_page = strides[3]; p.k_slot = strides[4]; p.k_head = strides[5];
-  p.v_page = strides[6]; p.v_slot = strides[7]; p.v_head = strides[8];
+  p.q_batch = st[0]; p.kn_batch = st[1]; p.vn_batch = st[2];
+  p.k_page = st[3]; p.k_slot = st[4]; p.k_head = st[5];
+  p.v_page = st[6]; p.v_slot = st[7]; p.v_head = st[8];
   p.table = block_table; p.table_width = table_width; p.lens = seq_lens;
   p.k_new = k_new; p.v_new = v_new; p.scale = scale; p.window = window;
   p.out = out; p.lse = lse; p.workspace = workspace;

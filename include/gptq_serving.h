@@ -53,14 +53,16 @@ extern "C" {
  *   q            [batch, heads, head_dim]: rows of a sequence contiguous, sequences q_stride apart
  *   k/v_cache    [pages, page_size, kv_heads, head_dim] in any order of the first three, each
  *                head_dim values contiguous
- *   strides      HOST array of 9 strides in elements, multiples of 8: q batch, k_new batch,
- *                v_new batch, k page, k slot, k head, v page, v slot, v head
+ *   strides      HOST array of 9 strides in elements, multiples of 8 (anything where the dimension
+ *                is one): q batch, k_new batch, v_new batch, k page, k slot, k head, v page, v slot,
+ *                v head
  *   block_table  [batch, table_width] int32, seq_lens [batch] int32 (4-byte aligned)
  *   out          [batch, heads, head_dim] contiguous
  *   lse          nullable [batch, heads] fp32: log sum_j exp(scale * q . k_j), -inf for length 0
  * Everything 16-bit is of `dtype` and 16-byte aligned.  head_dim: a multiple of 8 up to 256; heads a
- * multiple of kv_heads; a cache spans at most 2^35 elements (64 GiB; GPTQ_ERR_SHAPE).  workspace: gptq_paged_attention_workspace_size() bytes, 16-byte aligned,
- * control block zero (above).  batch == 0 is a no-op.
+ * multiple of kv_heads; a cache spans at most 2^35 elements (64 GiB; GPTQ_ERR_SHAPE).  workspace:
+ * gptq_paged_attention_workspace_size() bytes, 16-byte aligned, control block zero (above).
+ * batch == 0 is a no-op.
  */
 size_t gptq_paged_attention_workspace_size(int heads, int kv_heads, int head_dim);
 int gptq_paged_attention(const void* q, int batch, int heads, int dtype, void* k_cache, void* v_cache,

@@ -77,3 +77,19 @@ def test_a_cut_length_appends_nothing():
         for b, n in ((0, 30), (2, 48)):               # the others' new tokens are in their slots
             old[int(c.table[b, (n - 1) // 16]), (n - 1) % 16] = fresh[b]
         assert torch.equal(cache.view(torch.int16), old.view(torch.int16))
+
+
+def test_strides_of_dimensions_of_one():
+    """A dimension of one is never stepped over: its stride may be anything."""
+    gen = torch.Generator(device=DEV).manual_seed(3)
+    q = torch.randn((1, 4, 64), generator=gen, device=DEV).half()
+    k, v = (torch.randn((3, 16, 1, 64), generator=gen, device=DEV).half() for _ in range(2))
+    table = torch.tensor([[2, 0, 1]], dtype=torch.int32, device=DEV)
+    lens = torch.tensor([41], dtype=torch.int32, device=DEV)
+    want = g.paged_attention(q, k, v, table, lens)
+    odd = lambda t: torch.as_strided(t, t.shape, (16 * 64, 64, 3, 1))  # noqa: E731
+    assert torch.equal(g.paged_attention(q, odd(k), odd(v), table, lens), want)
+    one = [t[2:3].contiguous() for t in (k, v)]       # one page of one head
+    odd = [torch.as_strided(t, t.shape, (5, 64, 7, 1)) for t in one]
+    args = (torch.zeros((1, 1), dtype=torch.int32, device=DEV), torch.tensor([13], dtype=torch.int32, device=DEV))
+    assert torch.equal(g.paged_attention(q, *odd, *args), g.paged_attention(q, *one, *args))
