@@ -4,8 +4,10 @@
 // keeps a prefix of that order: the first top_k, then those before which less than top_p of the mass
 // lies, then those with w >= min_p.  So the kept set is "logits above a threshold, and the first few of
 // those equal to it", and the token is found by cumulating the kept masses in index order.  Nothing is
-// sorted but the few tokens around a threshold.  Masses are integers of 2^-31 of the best token's, whose
-// sums do not depend on their order: atomics and splits do not change a result.
+// sorted but the few tokens around a threshold.  Masses are integers of 2^-39 of the best token's, whose
+// sums do not depend on their order: atomics and splits do not change a result.  Rounding them loses at
+// most 2^-40 a token, 2^-18 of the total at 2^22 tokens; units of 2^-31 lost a tail of 131072 tokens 22.3
+// below the best altogether, 2.7e-5 of the total.
 //
 // Bound: the logits are read once from HBM (a cluster of CTAs holds a row in its shared memory); what
 // costs time is the passes over the row on chip and the cluster's barriers between them.
@@ -17,9 +19,9 @@
 // Rows whose threshold bin holds more tokens than the list (equal or nearly equal logits by the
 // thousand) bisect the threshold over the 32 bits of the logit, a pass each.
 //
-// Measured (GB300): 64 rows of 131072 bf16 logits 13.6 us without a threshold, 22 us with top_k, 37 us with
-// top_p alone (some 20 instructions a token in each of two passes are the most of it, the histogram's two
-// shared atomics a token 3 us; one atomic of 64 bits instead: 59 us); one row of 32000 11 us.
+// Measured (GB300): 64 rows of 131072 bf16 logits 15 us without a threshold, 23 us with top_k, 39.5 us with
+// top_p alone (one 64-bit shared atomic a token instead of the histogram's two: 59 us); one row of 32000
+// 11.5 us.
 #include <cooperative_groups.h>
 #include <math_constants.h>
 
@@ -43,8 +45,9 @@ constexpr int kShortK = 1024;
 constexpr int kSubs = 128;                         // sub-runs of a CTA's tokens, 8 a warp
 constexpr int kMaxCluster = 8;
 constexpr int kMaxSlice = 65535;                   // tokens of a CTA whose 16-bit half masses fit 32-bit sums
-constexpr float kReach = 24.f;                     // e^-24 2^31 rounds to no mass
-constexpr float kOne = 2147483648.f;               // the best token's mass
+constexpr float kReach = 28.f;                     // e^-28 2^39 rounds to no mass
+constexpr float kOne = 549755813888.f;             // 2^39, the best token's mass
+constexpr float kNearDepth = 5.1986039f;           // 7.5 ln 2: a weight of 2^-7.5 lies so far below the best, times T
 
 // Order-preserving bits of a logit: NaN lowest (0), -0 as 0.
 __device__ __forceinline__ uint32_t key_of(float l) {
@@ -77,7 +80,23 @@ __device__ __forceinline__ void unpack(const uint4& x, float (&l)[DT == 2 ? 4 : 
     }
   }
 }
-__device__ __forceinline__ uint32_t mass_of(float w) { return __float2uint_rn(w * kOne); }
+// w (at most 1.5) to the nearest whole number of 2^-(U + V), as hi 2^-U + lo 2^-(U + V), added to hi and (signed)
+// lo: adding 2^(23 - U) leaves the multiple of 2^-U in the low bits, and what is left of w is exact.
+template <int U, int V>
+__device__ __forceinline__ void add_parts(float w, uint32_t& hi, uint32_t& lo) {
+  constexpr uint32_t kBase = static_cast<uint32_t>(127 + 23 - U) << 23, kRest = static_cast<uint32_t>(127 + 23 - U - V) << 23 | 0x400000u;
+  const float t = w + __uint_as_float(kBase);
+  hi += __float_as_uint(t) - kBase;
+  lo += __float_as_uint((w - (t - __uint_as_float(kBase))) + __uint_as_float(kRest)) - kRest;
+}
+__device__ __forceinline__ u64 joined(uint32_t hi, uint32_t lo, int v) {
+  return (static_cast<u64>(hi) << v) + static_cast<u64>(static_cast<long long>(static_cast<int>(lo)));
+}
+__device__ __forceinline__ u64 mass_of(float w) {
+  uint32_t hi = 0, lo = 0;
+  add_parts<20, 19>(w, hi, lo);
+  return joined(hi, lo, 19);
+}
 
 // Comparisons of whole masses with a fraction of a total, as whole numbers (fp64 is slow here):
 // m < fraction * total is m < below_part, and cum > fraction * total is cum >= beyond_part.
@@ -294,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleProblem p, i
       for (int j = 0; j < kVec; ++j) l[j] = l[j] == CUDART_INF_F ? 0.f : -CUDART_INF_F;
   };
   auto each = [&](auto f) {                                // f(logit, token), in any order
-#pragma unroll 2
+#pragma unroll 1
     for (int v = threadIdx.x; v < vecs; v += kThreads) {
       float l[kVec];
       load_vec(v, l);
@@ -349,22 +368,37 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleProblem p, i
     const bool short_k = k <= kShortK;
     // ---- the histogram of top - l over the reach of the masses
     const float reach = fminf(kReach * temp, 3.402823466e38f), span = low <= top ? fminf(top - low, reach) : reach;
-    const float scale = span > 0.f ? fminf((kOver - 0.5f) / span, 3e38f) : 0.f;
-    // NaN, -inf and what has no mass: the last bin; what is lower than the sampled lowest: the one before
+    // bins a unit of the logits: the span's, but none finer than weights can tell (1e-9 T)
+    const float scale = fminf(fminf((kOver - 0.5f) / span, 1e9f / temp), 3e38f);
+    // NaN, -inf and what has no mass: the last bin; what is lower than the sampled lowest: the two before.
+    // Bins below `edge`, a whole number of them or all but those of tokens past it, hold masses in units of
+    // 2^-31, which weights of 2^-8 and more are multiples of, the others, below 2^-7, 2^8 times finer ones
+    // (edge lies at weights of 2^-7.5, and a bin is far narrower than that).  So the sums over 65535 tokens of
+    // the two halves of either take 32 bits each
+    const float at_near = kNearDepth * (temp * scale);
+    const float edge = at_near < kOver - 2 ? fmaxf(floorf(at_near), 1.f) : fmaxf(at_near, kOver - 1.f);
+    auto place_of = [&](float l, bool& near) {             // (not called past the reach)
+      const float x = (top - l) * scale;
+      near = x < edge;
+      return static_cast<int>(fminf(x, near ? kOver - 2.f : kOver - 1.f));
+    };
     auto bin_of = [&](float l) {
-      const float d = top - l;
-      return d <= reach ? static_cast<int>(fminf(d * scale, static_cast<float>(kOver - 1))) : kOver;
+      bool near;
+      return top - l <= reach ? place_of(l, near) : kOver;
     };
     const bool by_mass = top_p < 1.f && !short_k;
     const bool fits = n <= kMaxSlice;
     if (by_mass && fits)
       each([&](float l, int) {
-        const int b = bin_of(l);
-        if (b < kOver) {
-          const uint32_t m = mass_of(weight_of(l));
+        if (top - l <= reach) {
+          bool near;
+          const int b = place_of(l, near);
+          const float w = weight_of(l);
+          uint32_t hi = 0, lo = 0;
+          add_parts<15, 16>(near ? w : 256.f * w, hi, lo);
           if (k < p.vocab) atomicAdd(&sh.count[b], 1u);    // else the list's own count will do
-          atomicAdd(&sh.hi[b], m >> 16);
-          atomicAdd(&sh.lo[b], m & 0xFFFFu);
+          atomicAdd(&sh.hi[b], hi);
+          atomicAdd(&sh.lo[b], lo);
         }
       });
     else if (short_k && p.vocab / kVec >= 4 * k)
@@ -399,7 +433,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleProblem p, i
         if (by_mass) {
           const uint4 h = reinterpret_cast<const uint4*>(s->hi)[threadIdx.x], l = reinterpret_cast<const uint4*>(s->lo)[threadIdx.x];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) m[j] += (static_cast<u64>((&h.x)[j]) << 16) + (&l.x)[j];
+          for (int j = 0; j < 4; ++j) {
+            const u64 sum = joined((&h.x)[j], (&l.x)[j], 16);
+            m[j] += static_cast<float>(4 * threadIdx.x + j) < fminf(edge, kOver - 1.f) ? sum << 8 : sum;
+          }
         }
       }
 #pragma unroll
@@ -463,8 +500,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleProblem p, i
     auto gather = [&](auto few) {
       const int lo = sh.bin_lo, hi = sh.bin_hi;
       // most tokens are below or above: two comparisons, with half a bin to spare for their rounding
-      const float floor = scale > 0.f && hi < kOver - 1 ? top - (hi + 1.5f) / scale * (1.f + 1e-5f) : -CUDART_INF_F;
-      const float roof = scale > 0.f ? top - (lo - 0.5f) / scale * (1.f - 1e-5f) : CUDART_INF_F;
+      const float floor = hi < kOver - 2 ? top - (hi + 1.5f) / scale * (1.f + 1e-5f) : -CUDART_INF_F;
+      const float roof = top - (lo - 0.5f) / scale * (1.f - 1e-5f);
 #pragma unroll 2
       for (int v = threadIdx.x; v < vecs; v += kThreads) {
         float l[kVec];
@@ -529,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleProblem p, i
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int i = 4 * threadIdx.x + j;
-        m[j] = i < r ? static_cast<u64>(mass(i)) : 0ull;
+        m[j] = i < r ? mass(i) : 0ull;
         before[j] = sum;
         sum += m[j];
       }
@@ -586,25 +623,27 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleProblem p, i
           keep += i < r && (i == 0 || (before[j] < limit && weight_at(key_in(i)) >= min_p));
         }
         r = count_true(keep);                              // the kept ones are a prefix
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (4 * static_cast<int>(threadIdx.x) + j == r - 1) sh.slots[0][0] = before[j] + m[j];   // their mass
         // in index order: by adding up, of a few, those of lower index
         if (r <= kThreads) {
-          uint32_t* const mass = sh.cum_c;
+          u64* const mass = sh.cum_m;
           const int i = threadIdx.x;
           const u64 e = i < r ? sh.list[i] : 0ull;
-          const uint32_t mine = i < r ? mass_of(weight_at(static_cast<uint32_t>(e >> 32))) : 0u;
+          const u64 mine = i < r ? mass_of(weight_at(static_cast<uint32_t>(e >> 32))) : 0ull;
           mass[i] = mine;
           __syncthreads();
           if ((i & ~31) < r) {
-            u64 lower = 0, total = 0;
+            const u64 total = sh.slots[0][0];
+            u64 lower = 0;
 #pragma unroll 2
             for (int j0 = 0; j0 < r; j0 += 4) {            // (past r the masses are 0)
-              const uint4 four = *reinterpret_cast<const uint4*>(mass + j0);
+              const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(mass + j0), b = *reinterpret_cast<const ulonglong2*>(mass + j0 + 2);
+              const u64 four[4] = {a.x, a.y, b.x, b.y};
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const uint32_t m_j = (&four.x)[j];
-                total += m_j;
-                if (static_cast<uint32_t>(sh.list[j0 + j]) > static_cast<uint32_t>(e)) lower += m_j;   // ~index
-              }
+              for (int j = 0; j < 4; ++j)
+                if (static_cast<uint32_t>(sh.list[j0 + j]) > static_cast<uint32_t>(e)) lower += four[j];   // ~index
             }
             // the token whose masses reach past the target (u >= 1: the last one)
             const u64 goal = min(beyond_part(u, total), total), end = lower + mine;
@@ -723,7 +762,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleProblem p, i
     if (short_k || sh.verdict == kBisect) {                // (a short top_k that could be listed has returned)
       thr = 0u;
       ties = p.vocab;
-      auto mass_at = [&](uint32_t key) { return key ? static_cast<u64>(mass_of(weight_at(key))) : 0ull; };
+      auto mass_at = [&](uint32_t key) { return key ? mass_of(weight_at(key)) : 0ull; };
       if (k < p.vocab) {
         for (int bit = 31; bit >= 0; --bit) {
           const uint32_t cand = thr | (1u << bit);
@@ -784,7 +823,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleProblem p, i
   };
 #pragma unroll 2
   for (int q = warp * (kSubs / kWarps); q < (warp + 1) * (kSubs / kWarps); ++q) {
-    u64 mine = 0;
+    uint32_t hi = 0, lo = 0;
     int t = 0;
     const int c1 = sub_begin(q + 1);
 #pragma unroll 1
@@ -793,12 +832,13 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleProblem p, i
       chunk_at(c, l);
 #pragma unroll
       for (int j = 0; j < kVec; ++j) {
-        const uint32_t m = kept_mass(l[j]);                // (without a branch around it)
-        mine += l[j] > cut ? m : 0u;
+        const float w = weight_of(l[j]);                   // (without a branch around it)
+        add_parts<20, 19>(l[j] > cut && w >= least ? w : 0.f, hi, lo);
         t += l[j] == cut;
       }
     }
-    // a lane's sum is below 2^54: 2^19 tokens of a sub-run in it at most
+    // a sub-run holds less than 2^13 tokens, a lane of it less than 2^9: hi stays below 2^29, lo below 2^28
+    u64 mine = joined(hi, lo, 19);
     const u64 part = __reduce_add_sync(0xFFFFFFFFu, static_cast<uint32_t>(mine) & 0x7FFFFFFu);
     mine = (static_cast<u64>(__reduce_add_sync(0xFFFFFFFFu, static_cast<uint32_t>(mine >> 27))) << 27) + part;
     t = __reduce_add_sync(0xFFFFFFFFu, t);
@@ -899,7 +939,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleProblem p, i
     u64 m[kVec], sum = 0;
 #pragma unroll
     for (int j = 0; j < kVec; ++j) {
-      m[j] = l[j] > cut ? static_cast<u64>(kept_mass(l[j])) : 0ull;
+      m[j] = l[j] > cut ? kept_mass(l[j]) : 0ull;
       if (l[j] == cut && at++ < ties) m[j] = tie_mass;
       sum += m[j];
     }

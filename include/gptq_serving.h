@@ -106,8 +106,9 @@ int gptq_moe(const void* x, int tokens, int hidden, int inter, int dtype, const 
  *   stays while the mass before it is < top_p * total); of these those with w >= min_p (the best
  *   token always stays);
  *   token = the first kept index, in index order, whose cumulated w exceeds uniform * (kept mass).
- * l is taken to fp32 and x and w are fp32; masses are summed exactly, as integers of 2^-31 of the
- * best token's w, so that the result does not depend on an order of summation.
+ * l is taken to fp32 and x and w are fp32; each w is rounded to a whole multiple of 2^-39 of the best
+ * token's (vocab * 2^-40 of the total at most) and these are summed exactly, so that the result does
+ * not depend on an order of summation.
  *   logits       [batch, vocab] of dtype (GPTQ_F16, GPTQ_BF16, GPTQ_F32), rows row_stride elements
  *                apart; aligned to the element
  *   uniform      [batch] fp32 in [0, 1) (below 0 or NaN: 0; 1 and above: the last kept token)
