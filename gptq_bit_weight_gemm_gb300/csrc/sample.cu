@@ -145,6 +145,13 @@ struct Shared {
   int ties;
 };
 
+// What a CTA may hold of its row so that two share an SM, or that one has all of it: an SM has 228 KB, of
+// which each CTA's launch takes 1 KB
+constexpr size_t kSmSmem = 228 * 1024, kCtaSmem = sizeof(Shared) + 1024;
+constexpr size_t kHeldOfTwo = (kSmSmem / 2 - kCtaSmem) & ~static_cast<size_t>(15), kHeldOfOne = 160 * 1024;
+static_assert(2 * (kHeldOfTwo + kCtaSmem) <= kSmSmem && kHeldOfTwo > 64 * 1024, "two CTAs an SM");
+static_assert(kHeldOfOne + kCtaSmem <= kSmSmem, "one CTA an SM");
+
 enum Verdict { kGather = 1, kBisect = 2, kReady = 3 };
 
 // The list's first n entries in descending order (padded with zeros to a power of two).
@@ -968,14 +975,16 @@ cudaError_t launch(const SampleProblem& p, cudaStream_t stream) {
          (static_cast<long long>(p.batch) * 2 * cs <= 2 * dev.sm_count || p.vocab > kMaxSlice * cs))
     cs *= 2;
   // the row stays in shared memory where that leaves room for as many CTAs; else it is read again from L2
+  // (256 rows of 36000 / 36500 fp16 logits, mixed settings: 36 us held and 39 read again; held all the same,
+  // with one CTA an SM, 36500 took 43)
   size_t smem = ((static_cast<size_t>(p.vocab) / cs + 1) * kSize + 31) & ~static_cast<size_t>(15);
   const bool one_each = static_cast<long long>(p.batch) * cs <= dev.sm_count;
-  const bool held = smem <= (one_each ? 160 : 72) * 1024;
+  const bool held = smem <= (one_each ? kHeldOfOne : kHeldOfTwo);
   if (!held) smem = 0;
   auto kern = k_sample<DT>;
   static std::atomic<unsigned long long> opted_in{0};       // per device
   if (dev.device >= 64 || !(opted_in.load(std::memory_order_relaxed) & (1ull << dev.device))) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kHeldOfOne));
     if (e != cudaSuccess) return e;
     if (dev.device < 64) opted_in.fetch_or(1ull << dev.device, std::memory_order_relaxed);
   }
