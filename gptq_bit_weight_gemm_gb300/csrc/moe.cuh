@@ -2,17 +2,18 @@
 //
 // An expert's rows are taken in blocks of 8 NB; a block, with its expert, is a slot.
 //
-// Two launches after the router's (moe.cu, which leaves the logits): UP writes h = silu(x Wg) * (x Wu) for every (expert,
-// token) row, DOWN writes out[t] = sum over t's experts of w * (h Wd).  Both are a stream of packed
-// weights -- those of the chosen experts, each read once -- against a few activations, bound by HBM or,
-// with more than a few rows an expert, by unpacking.  One kernel template runs both.
+// Three launches after the router's (moe.cu, which leaves the logits): UP writes h = silu(x Wg) * (x Wu) for every
+// (expert, token) row, DOWN out[t] = sum over t's experts of w * (h Wd), in parts that the third adds
+// (k_sum_parts).  UP and DOWN are a stream of packed weights -- those of the chosen experts, each read once --
+// against a few activations.  HBM is their floor; what they take more goes to the instructions that unpack,
+// multiply and fold, to the ends of items and to the chain of launches.  One kernel template runs both.
 //
 // Split: a call's work is a line of chunks (32 columns x 8 warps wide, kRows packed rows deep).  UP's
 // items are (expert, 128 gate and the same 128 up columns), DOWN's are 256 output columns, whose line
 // runs through all experts one after the other, so that the sum over experts stays in the CTA and needs
-// neither atomics nor a pass of its own.  The line is cut into equal runs, one per resident CTA,
-// whatever the experts the tokens chose; an item that spans runs leaves one partial tile per run in the
-// workspace, and the last CTA to arrive adds them in run order.
+// no atomics.  The line is cut into equal runs, one per resident CTA, whatever the experts the tokens
+// chose; an item that spans runs leaves one partial tile per run in the workspace.  UP's are added in run
+// order by the last CTA to arrive, DOWN's by k_sum_parts.
 //
 // A CTA is one producer warp and 8 consumer warps around a ring of chunks.  Two CTAs share an SM, so that
 // one computes while the other writes an item: one CTA of 16 or 24 consumer warps took 75 and 83 us for
@@ -501,7 +502,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_experts(const __grid_consta
     rt.slot_off = rt.slot_expert + Routing::most_slots(pairs, a.experts);
   }
   // UP waits for the router's kernel and only then lets DOWN start; so the logits are final for DOWN from
-  // its first instruction, and it streams its first weights while UP still runs.
+  // its first instruction.  A DOWN CTA starts where a UP CTA has left its SM (either's ring takes half of it)
+  // and streams its first weights while the last runs of UP end.
   if (!DOWN) decode::pdl_wait();
   decode::pdl_launch_dependents();
   if (threadIdx.x == 0) {
@@ -1147,12 +1149,16 @@ cudaError_t launch_experts(Args a, const int32_t* qweight, int experts, int* run
 
 template <int BITS, bool DOWN>
 cudaError_t launch_blocks(const Args& a, const int32_t* qweight, int experts, int* runs, cudaStream_t stream) {
-  // single blocks (8 rows, or 4 in two parts) where few experts have more: the others' weights are read once
-  // for each block (4-bit wide layer, 2 of 8 experts a token, in single and double blocks: 8 tokens in two
-  // parts 172 and 184 us, 16 tokens in one 187 and 204)
+  // Single blocks (8 rows, or 4 in two parts) unless the experts have as many rows on average: a further block
+  // of an expert reads its weights again, a double one multiplies rows that are not there and has 96 registers
+  // for twice the accumulators.  At 8 bits, where reading is most of it, unless they have half as many.
+  // Single and double, wide layer of 8 experts, top-2, bf16: 18 tokens 182 and 217 us, 24 206 and 232, 32 250 and
+  // 247; 24 at 2, 3 and 8 bits 198 and 263, 224 and 385, 362 and 324.  fp16, down alone: 8 tokens 172 and 184,
+  // 16 196 and 198, 32 at 8 bits 472 and 383.
   constexpr int kBlock = 8;
-  const int room = kBlock / a.parts;
-  if (a.tokens <= room || 2 * a.tokens * a.topk <= room * a.experts) return launch_experts<BITS, 1, DOWN>(a, qweight, experts, runs, stream);
+  const int room = kBlock / a.parts, pairs = a.tokens * a.topk;
+  if (a.tokens <= room || (BITS == 8 ? 2 * pairs <= room * a.experts : pairs < room * a.experts))
+    return launch_experts<BITS, 1, DOWN>(a, qweight, experts, runs, stream);
   return launch_experts<BITS, 2, DOWN>(a, qweight, experts, runs, stream);
 }
 
