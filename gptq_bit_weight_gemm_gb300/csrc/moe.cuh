@@ -33,8 +33,8 @@
 // bf16 input in that range), already in the pair order of the codes.  So h may exceed fp16's range, and
 // bf16 models lose nothing to the multiply.  Where the output is fp16 too, 11 bits of h would show in it
 // (relative error 2.9e-4 against the 2.1e-4 of the output's own rounding), so h goes in two parts there,
-// its rounding and what the rounding left, as two rows of the products: free where a block of 8 rows has
-// room for them.
+// its rounding and what the rounding left: as two rows of the products, free where a block of 8 rows has
+// room for them, or multiplied one after the other (TWICE).
 #pragma once
 
 #include <cuda.h>
@@ -472,7 +472,9 @@ struct Cursor {
   int u, item, c, s, kc;
 };
 
-template <int BITS, int NB, bool DOWN>
+// TWICE: the activations' two parts are multiplied one after the other into the same sums, instead of as two
+// rows.
+template <int BITS, int NB, bool DOWN, bool TWICE>
 __global__ void __launch_bounds__(kThreads, kCtas) k_experts(const __grid_constant__ CUtensorMap tmW, const Args a) {
   using P = Pack<BITS>;
   using C = Chunk<BITS>;
@@ -725,20 +727,21 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_experts(const __grid_consta
         for (int i = 0; i < 4; ++i) x[t][nb][i] = 0.f;
   };
   Cursor x = start;
-  int cur = -1, rows = 0, off = 0;                         // rows: of the products (a row's parts count each)
+  const int row_parts = TWICE ? 1 : a.parts;               // rows of the products to a row
+  int cur = -1, rows = 0, off = 0;                         // rows: of the products
   int tok[NB][2];
   float wt[NB][2];
   auto open_slot = [&]() {
     cur = x.s;
     off = rt.slot_off[cur];
     const int count = rt.slot_off[cur + 1] - off;
-    rows = count * a.parts;
+    rows = count * row_parts;
     if constexpr (DOWN) {
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const int m = a.parts == 2 ? 4 * nb + tq : 8 * nb + 2 * tq + i;
+          const int m = row_parts == 2 ? 4 * nb + tq : 8 * nb + 2 * tq + i;
           tok[nb][i] = m < count ? rt.row_token[off + m] : 0;
           wt[nb][i] = m < count ? rt.row_weight[off + m] : 0.f;
         }
@@ -877,11 +880,11 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_experts(const __grid_consta
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {                    // rows past the slot's read its last one
         const int m = 8 * nb + gq;
-        act_at[nb] = L::act() + (m < rows ? m : rows - 1) * C::kActRow + tq * (NP * 4);
+        act_at[nb] = L::act() + (m < rows ? m : rows - 1) * (TWICE ? 2 * C::kActRow : C::kActRow) + tq * (NP * 4);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int mi = 8 * nb + 2 * tq + i;
-          info_at[nb][i] = L::info(a.ring_rows) + (mi < rows ? mi : rows - 1) * (C::kInfo * 4);
+          info_at[nb][i] = L::info(a.ring_rows) + (mi < rows ? mi : rows - 1) * ((TWICE ? 2 : 1) * C::kInfo * 4);
         }
       }
     }
@@ -909,8 +912,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_experts(const __grid_consta
           else w[r] = lds128(base + w_at[l & 1] + l * 512);
         }
       };
-      auto load_acts = [&](int l, int nb, uint32_t (&b)[NP]) {
-        const uint32_t src = base + act_at[nb] + l * (NP * 16);
+      auto load_acts = [&](int l, int nb, uint32_t (&b)[NP], int part = 0) {
+        const uint32_t src = base + act_at[nb] + l * (NP * 16) + part * C::kActRow;
         if constexpr (NP % 4 == 0) {
 #pragma unroll
           for (int i = 0; i < NP / 4; ++i) {
@@ -941,10 +944,14 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_experts(const __grid_consta
               load_acts(l, nb, b);
             }
 #pragma unroll
-            for (int j = 0; j < NP / 2; ++j)
+            for (int part = 0; part < (TWICE ? 2 : 1); ++part) {
+              if (part) load_acts(l, nb, b, 1);
 #pragma unroll
-              for (int t = 0; t < 2; ++t)
-                mma(cg[t][nb], d[2 * t][2 * j], d[2 * t + 1][2 * j], d[2 * t][2 * j + 1], d[2 * t + 1][2 * j + 1], b[2 * j], b[2 * j + 1]);
+              for (int j = 0; j < NP / 2; ++j)
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+                  mma(cg[t][nb], d[2 * t][2 * j], d[2 * t + 1][2 * j], d[2 * t][2 * j + 1], d[2 * t + 1][2 * j + 1], b[2 * j], b[2 * j + 1]);
+            }
           }
         }
       };
@@ -1090,15 +1097,16 @@ __global__ void __launch_bounds__(kCols) k_sum_parts(const float* partials, cons
   *reinterpret_cast<uint2*>(out + static_cast<long long>(m) * hidden + n) = make_uint2(pack2(v.x, v.y, T()), pack2(v.z, v.w, T()));
 }
 
-template <int BITS, int NB, bool DOWN>
+template <int BITS, int NB, bool DOWN, bool TWICE = false>
 cudaError_t launch_experts(Args a, const int32_t* qweight, int experts, int* runs, cudaStream_t stream) {
   using C = Chunk<BITS>;
   using L = Layout<BITS>;
-  auto kern = k_experts<BITS, NB, DOWN>;
+  auto kern = k_experts<BITS, NB, DOWN, TWICE>;
   const DeviceInfo& dev = device_info();
   a.units = a.K / Pack<BITS>::kPerUnit;
   a.zwords = a.N / 32 * BITS;
-  a.rows = a.tokens < 8 * NB / a.parts ? a.tokens : 8 * NB / a.parts;
+  const int room = 8 * NB / (TWICE ? 1 : a.parts);
+  a.rows = a.tokens < room ? a.tokens : room;
   a.ring_rows = a.rows * a.parts;
   a.gmax = (C::kK - 1) / a.group + 2;
   if (a.group % C::kK == 0) a.gmax = 1;
@@ -1153,12 +1161,17 @@ cudaError_t launch_blocks(const Args& a, const int32_t* qweight, int experts, in
   // of an expert reads its weights again, a double one multiplies rows that are not there and has 96 registers
   // for twice the accumulators.  At 8 bits, where reading is most of it, unless they have half as many.
   // Single and double, wide layer of 8 experts, top-2, bf16: 18 tokens 182 and 217 us, 24 206 and 232, 32 250 and
-  // 247; 24 at 2, 3 and 8 bits 198 and 263, 224 and 385, 362 and 324.  fp16, down alone: 8 tokens 172 and 184,
-  // 16 196 and 198, 32 at 8 bits 472 and 383.
+  // 247; 24 at 2, 3 and 8 bits 198 and 263, 224 and 385, 362 and 324.
+  // In two parts a double block holds 8 rows as well, and so does a single one whose parts are multiplied one
+  // after the other.  Blocks of 4, double and single of 8 (fp16): 8 tokens 172, 183 and 173 us, 12 185, 193 and
+  // 186, 16 196, 199 and 195, 24 246, 227 and 220; 32 at 2, 3 and 8 bits, the last two, 331 and 293, 458 and
+  // 408, 383 and 370.
   constexpr int kBlock = 8;
   const int room = kBlock / a.parts, pairs = a.tokens * a.topk;
   if (a.tokens <= room || (BITS == 8 ? 2 * pairs <= room * a.experts : pairs < room * a.experts))
     return launch_experts<BITS, 1, DOWN>(a, qweight, experts, runs, stream);
+  if constexpr (DOWN)
+    if (a.parts == 2) return launch_experts<BITS, 1, DOWN, true>(a, qweight, experts, runs, stream);
   return launch_experts<BITS, 2, DOWN>(a, qweight, experts, runs, stream);
 }
 
