@@ -33,8 +33,8 @@
 // own where it has more.  They are taken 2^15 times as large, as l and o are throughout: one part in 2^25
 // of the largest, of which a long flat tail may have thousands, would be nothing in fp16.
 //
-// Measured (GB300, bf16, 32 query and 8 kv heads of 128): 64 sequences of 512 to 8192 keys 120 us,
-// 6.3 TB/s; one of 131072 keys 89 us, 6.0 TB/s; one of 997 keys 8 us, the latencies of launch, lengths,
+// Measured (GB300, bf16, 32 query and 8 kv heads of 128): 64 sequences of 512 to 8192 keys 124 us,
+// 6.1 TB/s; one of 131072 keys 90 us, 6.0 TB/s; one of 997 keys 8.5 us, the latencies of launch, lengths,
 // table, keys, partial and join one after the other.
 #include <math_constants.h>
 

@@ -10,7 +10,8 @@
 // below the best altogether, 2.7e-5 of the total.
 //
 // Bound: the logits are read once from HBM (a cluster of CTAs holds a row in its shared memory); what
-// costs time is the passes over the row on chip and the cluster's barriers between them.
+// costs time is the passes over the row on chip and, more, the cluster's barriers between them, at which the
+// others wait while CTA 0 joins the histograms, finds the bin, sorts its tokens and cuts them.
 //   1. load, largest and smallest logit;
 //   2. a histogram of max - l: counts, and masses where the mass decides (no top_k, or a long one);
 //   3. with a short top_k, everything down to the bin that holds the k-th goes to one CTA, which sorts
