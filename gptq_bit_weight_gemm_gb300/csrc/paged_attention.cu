@@ -27,9 +27,9 @@
 // dimensions of key g as the B fragments of two k-steps of q k^T, and the query fragments are loaded in
 // the same order.  The scores' C fragment is the A fragment of p v as it stands.
 //
-// The probabilities go to the tensor cores in two parts, their rounding to 16 bits and what it left (16
-// significant bits for bf16, 22 for fp16; one part shows in the output: relative error 2.2e-3 in bf16, 1.7e-3
-// so).  The second parts are the A rows 8 .. 15 where an item has at most 8 query heads, and products of their
+// The probabilities go to the tensor cores in two parts, 16 bits of a little less than each and what is left
+// (15 significant bits for bf16, 20 for fp16; one part shows in the output: relative error 2.2e-3 in bf16, 1.7e-3
+// so).  Both are above 0, so an infinite value stays infinite.  The second parts are the A rows 8 .. 15 where an item has at most 8 query heads, and products of their
 // own where it has more.  They are taken 2^15 times as large, as l and o are throughout: one part in 2^25
 // of the largest, of which a long flat tail may have thousands, would be nothing in fp16.
 //
@@ -39,6 +39,7 @@
 #include <math_constants.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "decode.cuh"
 #include "gptq_device.cuh"
@@ -476,9 +477,12 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, R>::kCtas)) k_attention(c
 #pragma unroll
       for (int i = 0; i < 4; ++i) x[i] = exp2f(x[i] - low);
       l[r] = l[r] * alpha[r] + ((x[0] + x[1]) + (x[2] + x[3]));
+      // below p whichever way it rounds, by u = 2^-8 (bf16) or 2^-11 (fp16) of itself at most: for u taken off
+      // p (1 - u) (1 + u / (1 + u)) = p (1 - 2 u^2 / (1 + u))
+      constexpr float kLess = std::is_same<T, __half>::value ? 1.f - 1.f / 1024.f : 1.f - 1.f / 256.f;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const uint32_t h = pack2(x[2 * i], x[2 * i + 1], T());
+        const uint32_t h = pack2(x[2 * i] * kLess, x[2 * i + 1] * kLess, T());
         pa[r][i] = h;
         rest[r][i] = pack2(x[2 * i] - Tr::to_f32(Tr::from_bits(lo16(h))), x[2 * i + 1] - Tr::to_f32(Tr::from_bits(hi16(h))), T());
       }

@@ -41,7 +41,7 @@ extern "C" {
  * [max(0, n - window), n) of sequence b, n = seq_lens[b] (window 0: all n), k and v of head
  * h / (heads / kv_heads).  Key j of sequence b is slot j % page_size of page
  * block_table[b, j / page_size].  Sums, maxima and accumulators are fp32, the probabilities enter
- * the product with v in 16 (bf16) or 22 (fp16) significant bits, out is rounded once.
+ * the product with v in 15 (bf16) or 20 (fp16) significant bits, out is rounded once.
  * A sequence of length 0 gives zeros.  Nothing past a sequence's length (or before its window) is
  * used, whatever it holds: neither cache slots nor block-table entries.
  *

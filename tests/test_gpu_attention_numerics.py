@@ -1,8 +1,8 @@
 """gptq_paged_attention's probabilities: they reach the product with v in more bits than the result has.
 
 The error's 2-norm against 64 bits is that of rounding the exact result once, r, within a tenth.  What
-else there is: scores as fp32 sums, off by some 2^-21 of |s| < 8, and probabilities of at least 16
-significant bits (2^-17): against r = 2^-9.2 (bf16) and 2^-12.2 (fp16) the sum of squares grows by less
+else there is: scores as fp32 sums, off by some 2^-21 of |s| < 8, and probabilities of at least 15
+significant bits (2^-16): against r = 2^-9.2 (bf16) and 2^-12.2 (fp16) the sum of squares grows by less
 than 2^-8."""
 import numpy as np
 import pytest
@@ -93,3 +93,28 @@ def test_strides_of_dimensions_of_one():
     odd = [torch.as_strided(t, t.shape, (5, 64, 7, 1)) for t in one]
     args = (torch.zeros((1, 1), dtype=torch.int32, device=DEV), torch.tensor([13], dtype=torch.int32, device=DEV))
     assert torch.equal(g.paged_attention(q, *odd, *args), g.paged_attention(q, *one, *args))
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("group", [1, 4, 12])
+def test_infinite_values_stay_infinite(dtype, group):
+    """An infinite value of a live key makes its dimension of the result infinite, with its sign, whatever the
+    key's probability (here from 2^-12 of the largest to 1); the other dimensions do not see it.  NaN
+    stays NaN, and two signs give NaN."""
+    n, kv, dim = 200, 2, 64
+    gen = torch.Generator(device=DEV).manual_seed(group)
+    q = torch.randn((1, kv * group, dim), generator=gen, device=DEV).to(dtype)
+    k = torch.randn((13, 16, kv, dim), generator=gen, device=DEV).to(dtype)
+    v = torch.randn((13, 16, kv, dim), generator=gen, device=DEV).to(dtype)
+    args = (torch.arange(13, dtype=torch.int32, device=DEV)[None], torch.tensor([n], dtype=torch.int32, device=DEV))
+    plain = g.paged_attention(q, k, v, *args)
+    inf = float("inf")
+    flat_v = v.view(-1, kv, dim)
+    flat_v[5, :, 3], flat_v[77, :, 9], flat_v[199, :, 17] = inf, -inf, inf
+    flat_v[20, :, 30], flat_v[21, :, 30], flat_v[100, :, 40] = inf, -inf, float("nan")
+    out = g.paged_attention(q, k, v, *args)[0].float()
+    for d, want in ((3, inf), (9, -inf), (17, inf)):
+        assert bool((out[:, d] == want).all()), (d, out[:, d])
+    assert bool(out[:, 30].isnan().all()) and bool(out[:, 40].isnan().all())
+    rest = [d for d in range(dim) if d not in (3, 9, 17, 30, 40)]
+    assert torch.equal(out[:, rest], plain[0].float()[:, rest])
