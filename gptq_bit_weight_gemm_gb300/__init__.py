@@ -29,6 +29,16 @@ Beside the GEMMs, the rest of a decode step (include/gptq_serving.h):
   moe_layer(x, router, up, down, topk, bits, group)          -> router, experts on packed weights and sum
   sample(logits, uniform, temperature, top_k, top_p, min_p)  -> (token, log probability) of each row
 
+And a step whose sequences bring chunks of prompts (include/gptq_prompt.h):
+
+  page_plan(cached, added, block_table, free_pages, free_count) -> lengths, rows, positions and slots of the step;
+                                                             pages taken from the free list and given back
+  rms_norm(x, weight, residual)                              -> the norm of residual + x
+  rotary_table(rot_dim, theta, scaling)                      -> frequencies for rotary, on the device
+  rotary(q, k, positions, turns)                             -> rotated queries and keys (with v, caches and slots:
+                                                             keys and values appended to the paged cache)
+  chunk_attention(q, k_cache, v_cache, block_table, seq_lens, cu_tokens) -> causal attention of each sequence's new tokens
+
 Every call on the device runs on `stream` (None: the current one).  With a stream that is not the current
 one, the caller has its inputs ready there; what the call allocates (outputs, workspaces) belongs to it.
 """
@@ -43,11 +53,14 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "_lib", "libgptq_gb300.so")
 HEADER = os.path.join(os.path.dirname(HERE), "include", "gptq.h")
 SERVING_HEADER = os.path.join(os.path.dirname(HERE), "include", "gptq_serving.h")
+PROMPT_HEADER = os.path.join(os.path.dirname(HERE), "include", "gptq_prompt.h")
 
 F16, BF16, F32 = 0, 1, 2
 V1, V2 = 1, 2
 DEV_TIMEOUT, DEV_GIDX_RANGE, DEV_SCALE_OVERFLOW, DEV_EXPERT_ROWS, DEV_GIDX_GROUPS = 0x1, 0x2, 0x4, 0x8, 0x10
 DEV_PAGE_RANGE, DEV_SEQ_LEN, DEV_NO_TOKEN = 0x20, 0x40, 0x80
+DEV_NO_PAGE, DEV_SLOT_RANGE, DEV_TOKEN_ROWS = 0x100, 0x200, 0x400
+ROTARY_SCALINGS = {"none": 0, "linear": 1, "base": 2, "ramp": 3, "bands": 4}
 DECODE_MAX_M = 32
 
 _STATUS = {0: "GPTQ_OK", -1: "GPTQ_ERR_ARG", -2: "GPTQ_ERR_SHAPE", -3: "GPTQ_ERR_ALIGN",
@@ -69,7 +82,9 @@ class GPTQError(RuntimeError):
 _lib = None
 
 _P, _I, _SZ, _F, _LL = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float, ctypes.c_longlong
+_D, _ULL = ctypes.c_double, ctypes.c_ulonglong
 _Strides = _LL * 9
+_RotaryStrides, _ChunkStrides = _LL * 11, _LL * 7
 _SIGNATURES = {
     "gptq_dequant": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P]),
     "gptq_gemm": (_I, [_P, _I, _I, _I, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _SZ, _P]),
@@ -100,6 +115,14 @@ _SIGNATURES = {
     "gptq_moe_workspace_size": (_SZ, [_I, _I, _I, _I, _I]),
     "gptq_moe": (_I, [_P, _I, _I, _I, _I, _P, _I, _I, _I, _P, _P, _P, _P, _P, _P, _I, _I, _I, _P, _P, _P, _P, _SZ, _P]),
     "gptq_sample": (_I, [_P, _I, _I, _LL, _I, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "gptq_page_plan": (_I, [_P, _P, _I, _I, _P, _I, _P, _I, _P, _P, _P, _P, _P, _P, _I, _P]),
+    "gptq_rms_norm": (_I, [_P, _I, _I, _LL, _I, _P, _LL, _I, _P, _LL, _P, _I, _F, _P, _LL, _I, _P]),
+    "gptq_rotary_table": (_I, [_I, _D, _I, _D, _D, _D, _D, ctypes.POINTER(_ULL), ctypes.POINTER(_D)]),
+    "gptq_rotary": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _I, _I, ctypes.POINTER(_LL), _P, _P, _F, _P, _P, _P, _P, _I, _I,
+                         _P, _P]),
+    "gptq_chunk_attention_workspace_size": (_SZ, [_I, _I, _I]),
+    "gptq_chunk_attention": (_I, [_P, _I, _I, _I, _P, _P, _I, _I, _I, _I, ctypes.POINTER(_LL), _P, _I, _P, _P, _I, _F, _I, _P,
+                                  _P, _P, _SZ, _P]),
 }
 
 
@@ -502,15 +525,17 @@ class _Runtime:
 
     def __init__(self):
         torch = _torch()
-        self.int32, self.float32, self.float16 = torch.int32, torch.float32, torch.float16
+        self.int32, self.float32, self.float16, self.int64 = torch.int32, torch.float32, torch.float16, torch.int64
         self.codes = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32}
         self.lib = lib()
         raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
         if raw is None or device is None:
             self.stream = lambda: torch.cuda.current_stream().cuda_stream
+            self.device = torch.cuda.current_device
         else:
             torch.cuda.init()
             self.stream = lambda: raw(device())
+            self.device = device
 
 
 _rt = None
@@ -751,3 +776,277 @@ def sample(logits, uniform, *, temperature=None, top_k=None, top_p=None, min_p=N
     if rc:
         _check(rc, "gptq_sample")
     return token, logprob
+
+
+# ------------------------------------------------------------------ a step with chunks of prompts
+# The calls below also refuse tensors of another device than the current one, which the kernels run on.
+def _look_here(t, dtype, shape, name, device, contiguous=True):
+    """Raises what is wrong with a tensor that should be one of this type and shape on the current device."""
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if t.get_device() != device:
+        raise ValueError("%s is on device %d, the current one is %d" % (name, t.get_device(), device))
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.shape != shape:
+        raise ValueError("%s must have the shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    if contiguous and not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+
+
+def _here(t, dtype, shape, name, device):
+    """The address of a contiguous tensor of this type and shape on the current device."""
+    if not (t.get_device() == device and t.dtype == dtype and t.shape == shape and t.is_contiguous()):
+        _look_here(t, dtype, shape, name, device)
+    return t.data_ptr()
+
+
+def _row_stride(t, dtype, shape, name, device):
+    """The stride of rows [tokens, heads, dim] whose heads are contiguous, on the current device."""
+    stride = t.stride()
+    if not (t.get_device() == device and t.dtype == dtype and t.shape == shape and stride[2] == 1
+            and (stride[1] == shape[2] or shape[1] == 1)):
+        _look_here(t, dtype, shape, name, device, contiguous=False)
+        raise ValueError("%s: the heads of a token must be contiguous" % name)
+    return stride[0]
+
+
+def _cache_strides(t, dtype, shape, name, device):
+    stride = t.stride()
+    if not (t.get_device() == device and t.dtype == dtype and t.shape == shape and stride[3] == 1):
+        _look_here(t, dtype, shape, name, device, contiguous=False)
+        raise ValueError("%s must be [pages, page_size, kv_heads, dim] with contiguous rows" % name)
+    return stride
+
+
+def _raw_stream(rt, stream, device):
+    if stream is None:
+        return rt.stream()
+    if stream.device_index != device:
+        raise ValueError("stream is of device %d, the current one is %d" % (stream.device_index, device))
+    return stream.cuda_stream
+
+
+def page_plan(cached, added, block_table, free_pages, free_count, *, page_size, max_tokens, seq_lens=None, free_count_out=None,
+              stream=None):
+    """The plan of a step: sequence b of `cached` [batch] tokens gets `added` [batch] more (negative: its last ones
+    are dropped; all int32 on the device).  Pages no longer needed go back to the free list free_pages
+    [capacity] (its first free_count [1] entries), pages needed are taken from its end and entered into
+    block_table [batch, width], both updated in place.  Returns (seq_lens [batch], cu_tokens [batch + 1],
+    positions [max_tokens], slots [max_tokens] int64): sequence b's new tokens are rows cu_tokens[b] ..
+    cu_tokens[b + 1]; rows behind the last have position 0 and slot -1.  seq_lens, when given, is written
+    there (it may be `cached`); the new count goes to free_count_out, where given, and to free_count itself."""
+    rt = _rt or _runtime()
+    device, i32 = rt.device(), rt.int32
+    (batch,) = cached.shape
+    table_shape, list_shape = block_table.shape, free_pages.shape
+    if len(table_shape) != 2 or table_shape[0] != batch:
+        raise ValueError("block_table must be [batch, width] = [%d, ...], got %s" % (batch, tuple(table_shape)))
+    if len(list_shape) != 1:
+        raise ValueError("free_pages must be [capacity], got %s" % (tuple(list_shape),))
+    if max_tokens < 0:
+        raise ValueError("max_tokens must not be negative")
+    c_ptr, a_ptr = _here(cached, i32, (batch,), "cached", device), _here(added, i32, (batch,), "added", device)
+    t_ptr, f_ptr = _here(block_table, i32, table_shape, "block_table", device), _here(free_pages, i32, list_shape, "free_pages", device)
+    n_ptr = _here(free_count, i32, (1,), "free_count", device)
+    n_out = n_ptr if free_count_out is None else _here(free_count_out, i32, (1,), "free_count_out", device)
+    raw = _raw_stream(rt, stream, device)
+    if seq_lens is None:
+        seq_lens = _new(stream, cached, (batch,))
+        l_ptr = seq_lens.data_ptr()
+    else:
+        l_ptr = _here(seq_lens, i32, (batch,), "seq_lens", device)
+    cu, positions = _new(stream, cached, (batch + 1,)), _new(stream, cached, (max_tokens,))
+    slots = _new(stream, cached, (max_tokens,), rt.int64)
+    rc = rt.lib.gptq_page_plan(c_ptr, a_ptr, batch, page_size, t_ptr, table_shape[1], f_ptr, list_shape[0], n_ptr, n_out, l_ptr,
+                               cu.data_ptr(), positions.data_ptr(), slots.data_ptr(), max_tokens, raw)
+    if rc:
+        _check(rc, "gptq_page_plan")
+    return seq_lens, cu, positions, slots
+
+
+def _look_matrix(t, dtype, shape, name, device):
+    """Raises what is wrong with [rows, hidden] rows that should be contiguous."""
+    _look_here(t, dtype, shape, name, device, contiguous=False)
+    raise ValueError("%s: a row must be contiguous" % name)
+
+
+def rms_norm(x, weight=None, *, residual=None, residual_out=None, eps=1e-6, dtype=None, out=None, stream=None):
+    """The root-mean-square norm of s = residual + x (x alone without a residual), row by row: s * weight /
+    sqrt(mean(s^2) + eps).  x [rows, hidden] and residual are float16, bfloat16 or float32 (rows may be
+    strided), weight [hidden] any of them.  s is written to residual_out, where given, and to residual
+    itself, in its type.  The result is of `dtype` (x's where not given), written into `out` when given
+    (which may be x)."""
+    rt = _rt or _runtime()
+    device, codes = rt.device(), rt.codes
+    rows, hidden = shape = x.shape
+    code = codes.get(x.dtype)
+    if code is None:
+        raise TypeError("x must be float16, bfloat16 or float32, got %s" % x.dtype)
+    xs = x.stride()
+    if not (x.get_device() == device and (xs[1] == 1 or hidden == 1)):
+        _look_matrix(x, x.dtype, shape, "x", device)
+    r_ptr = ro_ptr = w_ptr = None
+    r_stride = ro_stride = r_code = w_code = 0
+    if residual is not None:
+        r_code = codes.get(residual.dtype)
+        if r_code is None:
+            raise TypeError("residual must be float16, bfloat16 or float32, got %s" % residual.dtype)
+        if residual_out is None:
+            residual_out = residual
+        rs, ros = residual.stride(), residual_out.stride()
+        if not (residual.get_device() == device and residual.shape == shape and (rs[1] == 1 or hidden == 1)):
+            _look_matrix(residual, residual.dtype, shape, "residual", device)
+        if not (residual_out.get_device() == device and residual_out.dtype == residual.dtype and residual_out.shape == shape
+                and (ros[1] == 1 or hidden == 1)):
+            _look_matrix(residual_out, residual.dtype, shape, "residual_out", device)
+        r_ptr, ro_ptr, r_stride, ro_stride = residual.data_ptr(), residual_out.data_ptr(), rs[0], ros[0]
+    elif residual_out is not None:
+        raise ValueError("residual_out without a residual")
+    if weight is not None:
+        w_code = codes.get(weight.dtype)
+        if w_code is None:
+            raise TypeError("weight must be float16, bfloat16 or float32, got %s" % weight.dtype)
+        w_ptr = _here(weight, weight.dtype, (hidden,), "weight", device)
+    if dtype is None:
+        dtype = x.dtype if out is None else out.dtype
+    o_code = codes.get(dtype)
+    if o_code is None:
+        raise TypeError("the result must be float16, bfloat16 or float32, got %s" % dtype)
+    raw = _raw_stream(rt, stream, device)
+    if out is None:
+        out = x.new_empty(shape, dtype=dtype) if stream is None else _new(stream, x, shape, dtype)
+    os_ = out.stride()
+    if not (out.get_device() == device and out.dtype == dtype and out.shape == shape and (os_[1] == 1 or hidden == 1)):
+        _look_matrix(out, dtype, shape, "out", device)
+    rc = rt.lib.gptq_rms_norm(x.data_ptr(), rows, hidden, xs[0], code, r_ptr, r_stride, r_code, ro_ptr, ro_stride, w_ptr, w_code,
+                              eps, out.data_ptr(), os_[0], o_code, raw)
+    if rc:
+        _check(rc, "gptq_rms_norm")
+    return out
+
+
+def rotary_table(rot_dim, *, theta=10000.0, scaling="none", factor=1.0, original=0.0, low=1.0, high=32.0, device="cuda"):
+    """(turns, amplitude) of a rotary embedding of rot_dim dimensions, for `rotary`: turns [rot_dim / 2] int64 on
+    `device`, the frequencies in units of 2^-64 turns, made once on the host.  scaling: "none"; "linear"
+    (frequencies / factor); "base" (theta * factor^(rot_dim / (rot_dim - 2))); "ramp" and "bands": pairs that turn
+    `high` times and more over the `original` positions stay, those that turn `low` times and fewer are
+    divided by factor, and between them a mixture, linear in the pair ("ramp", with the amplitude 0.1
+    ln(factor) + 1) or in the turns ("bands")."""
+    if scaling not in ROTARY_SCALINGS:
+        raise ValueError("scaling must be one of %s, got %r" % (", ".join(ROTARY_SCALINGS), scaling))
+    turns = np.empty(max(0, rot_dim // 2), dtype=np.int64)
+    amplitude = _D(1.0)
+    _check(lib().gptq_rotary_table(rot_dim, theta, ROTARY_SCALINGS[scaling], factor, original, low, high,
+                                   turns.ctypes.data_as(ctypes.POINTER(_ULL)), ctypes.byref(amplitude)), "gptq_rotary_table")
+    return _torch().from_numpy(turns).to(device), amplitude.value
+
+
+def rotary(q, k, positions, turns, *, amplitude=1.0, interleaved=False, v=None, k_cache=None, v_cache=None, slots=None,
+           q_out=None, k_out=None, stream=None):
+    """The rotary embedding of q [tokens, heads, dim] and k [tokens, kv_heads, dim] (heads of a token contiguous) at
+    positions [tokens] int32: the first 2 * len(turns) dimensions of each head turned, in halves or, interleaved,
+    in neighbouring pairs (turns and amplitude from rotary_table).  With v, k_cache, v_cache [pages,
+    page_size, kv_heads, dim] and slots [tokens] int64 each row's rotated key and its value are written to
+    its slot (a negative one: not).  Returns (q_out, k_out); without caches k_out is made here when not
+    given, with them it stays None.  q_out may be q, k_out k."""
+    rt = _rt or _runtime()
+    device = rt.device()
+    tokens, heads, dim = shape = q.shape
+    kv_heads = k.shape[1]
+    dtype = q.dtype
+    code = rt.codes.get(dtype, F32)
+    if code == F32:
+        raise TypeError("q must be float16 or bfloat16, got %s" % dtype)
+    k_shape = (tokens, kv_heads, dim)
+    qs, ks = _row_stride(q, dtype, shape, "q", device), _row_stride(k, dtype, k_shape, "k", device)
+    p_ptr = _here(positions, rt.int32, (tokens,), "positions", device)
+    t_ptr = _here(turns, rt.int64, turns.shape, "turns", device)
+    v_ptr = kc_ptr = vc_ptr = s_ptr = None
+    vs = pages = page_size = 0
+    kc = vc = (0, 0, 0, 1)
+    if k_cache is not None:
+        if v is None or v_cache is None or slots is None:
+            raise ValueError("k_cache goes with v, v_cache and slots")
+        pages, page_size, _, _ = cache_shape = k_cache.shape
+        cache_shape = (pages, page_size, kv_heads, dim)
+        kc, vc = (_cache_strides(t, dtype, cache_shape, name, device) for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")))
+        vs = _row_stride(v, dtype, k_shape, "v", device)
+        s_ptr = _here(slots, rt.int64, (tokens,), "slots", device)
+        v_ptr, kc_ptr, vc_ptr = v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr()
+    elif v is not None or v_cache is not None or slots is not None:
+        raise ValueError("v, v_cache and slots go with k_cache")
+    raw = _raw_stream(rt, stream, device)
+    if q_out is None:
+        q_out = _new(stream, q, shape)
+    if k_out is None and k_cache is None:
+        k_out = _new(stream, k, k_shape)
+    qo = _row_stride(q_out, dtype, shape, "q_out", device)
+    ko = 0 if k_out is None else _row_stride(k_out, dtype, k_shape, "k_out", device)
+    strides = _RotaryStrides(qs, ks, vs, qo, ko, kc[0], kc[1], kc[2], vc[0], vc[1], vc[2])
+    rc = rt.lib.gptq_rotary(q.data_ptr(), k.data_ptr(), v_ptr, tokens, heads, kv_heads, dim, 2 * turns.numel(),
+                            1 if interleaved else 0, code, strides, p_ptr, t_ptr, amplitude, q_out.data_ptr(),
+                            None if k_out is None else k_out.data_ptr(), kc_ptr, vc_ptr, pages, page_size, s_ptr, raw)
+    if rc:
+        _check(rc, "gptq_rotary")
+    return q_out, k_out
+
+
+def chunk_attention_workspace_size(heads, kv_heads, head_dim):
+    return int(lib().gptq_chunk_attention_workspace_size(heads, kv_heads, head_dim))
+
+
+def chunk_attention_workspace(heads, kv_heads, head_dim):
+    """A workspace for chunk_attention with these heads: kept by the caller and given to one call after the
+    other on one stream, whatever their batch and lengths."""
+    return _buffer(chunk_attention_workspace_size(heads, kv_heads, head_dim), False, "gptq_chunk_attention_workspace_size")
+
+
+def chunk_attention(q, k_cache, v_cache, block_table, seq_lens, cu_tokens, *, scale=None, window=0, out=None, lse=None,
+                    workspace=None, stream=None):
+    """Causal attention of each sequence's new tokens over a paged cache that holds their keys and values
+    already: q [tokens, heads, dim] (heads of a token contiguous), sequence b's tokens in rows cu_tokens[b] ..
+    cu_tokens[b + 1] (int32 [batch + 1]), the last of seq_lens[b] (int32 [batch]) positions; k_cache / v_cache
+    [pages, page_size, kv_heads, dim] (views in any order of the first three), block_table [batch, width]
+    int32 -> out [tokens, heads, dim].  window > 0: only the last `window` keys up to a token's own.  scale: dim
+    ** -0.5 where not given.  lse [tokens, heads] fp32 takes the log of each row's exponential sum.  Rows outside
+    every sequence are left as they were.  A workspace (chunk_attention_workspace) is made here when none
+    is given."""
+    rt = _rt or _runtime()
+    device, i32 = rt.device(), rt.int32
+    tokens, heads, dim = shape = q.shape
+    pages, page_size, kv_heads, _ = k_cache.shape
+    cache_shape = (pages, page_size, kv_heads, dim)
+    dtype = q.dtype
+    code = rt.codes.get(dtype, F32)
+    if code == F32:
+        raise TypeError("q must be float16 or bfloat16, got %s" % dtype)
+    qs = _row_stride(q, dtype, shape, "q", device)
+    ks, vs = _cache_strides(k_cache, dtype, cache_shape, "k_cache", device), _cache_strides(v_cache, dtype, cache_shape, "v_cache", device)
+    table_shape = block_table.shape
+    if len(table_shape) != 2:
+        raise ValueError("block_table must be [batch, width]")
+    batch, width = table_shape
+    t_ptr = _here(block_table, i32, table_shape, "block_table", device)
+    l_ptr = _here(seq_lens, i32, (batch,), "seq_lens", device)
+    c_ptr = _here(cu_tokens, i32, (batch + 1,), "cu_tokens", device)
+    lse_ptr = None if lse is None else _here(lse, rt.float32, (tokens, heads), "lse", device)
+    raw = _raw_stream(rt, stream, device)
+    if out is None:
+        out = q.new_empty(shape) if stream is None else _new(stream, q, shape)
+        o_ptr = out.data_ptr()
+    else:
+        o_ptr = _here(out, dtype, shape, "out", device)
+    if workspace is None:
+        with _on(stream):
+            workspace = chunk_attention_workspace(heads, kv_heads, dim)
+    elif workspace.get_device() != device:
+        raise ValueError("workspace must be on the current device")
+    ws, ws_bytes = _workspace(workspace)
+    strides = _ChunkStrides(qs, ks[0], ks[1], ks[2], vs[0], vs[1], vs[2])
+    rc = rt.lib.gptq_chunk_attention(q.data_ptr(), tokens, heads, code, k_cache.data_ptr(), v_cache.data_ptr(), pages, page_size,
+                                     kv_heads, dim, strides, t_ptr, width, l_ptr, c_ptr, batch,
+                                     dim ** -0.5 if scale is None else scale, window, o_ptr, lse_ptr, ws, ws_bytes, raw)
+    if rc:
+        _check(rc, "gptq_chunk_attention")
+    return out
