@@ -2,119 +2,962 @@
 //   out = sum_j p_j v_j,  p = softmax_j(scale q . k_j),  over the keys j in [max(0, t - window + 1), t] of the
 // row at position t.
 //
-// With the maximum m, the sum l and the accumulator o of the keys so far, a new score s moves them to
-//   m' = max(m, s),  l' = l e^(m - m') + e^(s - m'),  o' = o e^(m - m') + e^(s - m') v.
+// One pass over the keys: with the maximum m, the sum l and the accumulator o of the keys so far, a block of scores
+// s moves them to  m' = max(m, max s),  l' = l e^(m - m') + sum e^(s - m'),  o' = o e^(m - m') + e^(s - m') v,
+// and two partial results of disjoint keys join the same way.
 //
-// A warp takes a row and head, a lane DP / 32 dimensions.
+// Bound: 4 flops per visible key, query head and dimension on the tensor cores, for chunks of some hundred rows and
+// more; the cache's bytes for fewer.
+//
+// Rows: the query heads that share a key head read the same keys, so the rows of an item are the pairs (token,
+// head of the group), 256 of them (128 for head_dim above 128) for one sequence and kv head: two
+// accumulators of 128 rows that share every tile of keys and values.
+//
+// Split: items cost what their visible key tiles cost, from 1 to thousands.  All of them, one after the
+// other, are a line of key tiles that is cut into as many equal runs as there are SMs, on the device, from the
+// lengths; an item cut by a run's end leaves partial results (m, l, o) in the workspace, two a run at most, and a
+// second kernel joins them, all SMs at work on the rows.
+//
+// A CTA: softmax warps 0-3 and 4-7 (one accumulator each, a thread a row), loader warps 8-11, and in the last
+// four one that issues the MMAs and one that walks the line.  S = q k^T goes to tensor memory; a softmax
+// thread reads its row, writes the probabilities back over it as 16-bit values, and these are the A operand
+// of p v straight from tensor memory.  While one accumulator's softmax runs, the tensor cores work for the
+// other.  The accumulator o is rescaled by the softmax threads themselves, only where a row's maximum has
+// grown by more than 2^8 since the last time: until then probabilities are simply larger than 1 (the
+// scores' MMA completes after the p v before it, so o is at rest then).  fp16 probabilities are taken 2^7
+// times as large, so that a long flat tail behind one large score is not lost in fp16's range.
+//
+// Keys and values come through cp.async, 16 bytes a lane, whole rows: pages of any size, anywhere.
+// Values that some row of the item must not see (later tokens', outside the window) could reach it as 0 x NaN:
+// in the tiles at the diagonal the loader replaces infinite and NaN values by 0, and the rows that do see
+// them get them added at the end.
 #include <math_constants.h>
+
+#include <atomic>
+#include <type_traits>
 
 #include "decode.cuh"
 #include "gptq_device.cuh"
 #include "gptq_internal.h"
 #include "prompt_internal.h"
+#include "sm100_ptx.cuh"
 
 namespace gptq {
 namespace chunk {
 
-constexpr int kWarps = 8, kThreads = kWarps * 32;
-
-template <typename T, int DP>
-__global__ void __launch_bounds__(kThreads) k_chunk(const ChunkProblem p) {
-  using Tr = F16Traits<T>;
-  constexpr int kDims = DP / 32;
-  decode::pdl_launch_dependents();
-  decode::pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const long long item = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  const int row = static_cast<int>(item / p.heads), h = static_cast<int>(item % p.heads);
-  const int kvh = h / (p.heads / p.kv_heads);
-  if (blockIdx.x == 0)
-    for (int s = threadIdx.x; s < p.batch; s += kThreads)
-      if (p.cu[s] < 0 || p.cu[s + 1] < p.cu[s] || p.cu[s + 1] > p.tokens) atomicOr(p.status, kStatusTokenRows);
-  if (row >= p.tokens) return;
-  // the row's sequence
-  int b = -1, first = 0, end = 0;
-  for (int s = 0; s < p.batch; ++s) {
-    const int c0 = p.cu[s], c1 = p.cu[s + 1];
-    first = min(max(c0, 0), p.tokens);
-    end = max(first, min(c1, p.tokens));
-    if (row >= first && row < end) {
-      b = s;
-      break;
-    }
-  }
-  if (b < 0) return;
-  const int most = p.table_width * p.page_size, raw = p.lens[b], n = min(max(raw, 0), most);
-  if (raw != n && lane == 0) atomicOr(p.status, kStatusSeqLen);
-  const int at = n - (end - first) + row - first;
-  const int lo = p.window > 0 ? max(0, at - p.window + 1) : 0;
-  float q[kDims], o[kDims] = {}, m = -CUDART_INF_F, l = 0.f;
-  const T* qp = static_cast<const T*>(p.q) + row * p.q_token + static_cast<long long>(h) * p.head_dim;
-#pragma unroll
-  for (int i = 0; i < kDims; ++i) {
-    const int d = lane + 32 * i;
-    q[i] = d < p.head_dim ? Tr::to_f32(qp[d]) : 0.f;
-  }
-  for (int j = lo; j <= at; ++j) {
-    const int page = p.table[static_cast<long long>(b) * p.table_width + j / p.page_size], slot = j % p.page_size;
-    if (page < 0 || page >= p.pages) {
-      if (lane == 0) atomicOr(p.status, kStatusPageRange);
-      continue;
-    }
-    const T* k = static_cast<const T*>(p.k_cache) + page * p.k_page + slot * p.k_slot + kvh * p.k_head;
-    const T* v = static_cast<const T*>(p.v_cache) + page * p.v_page + slot * p.v_slot + kvh * p.v_head;
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < kDims; ++i) {
-      const int d = lane + 32 * i;
-      if (d < p.head_dim) s += q[i] * Tr::to_f32(k[d]);
-    }
-#pragma unroll
-    for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, x);
-    s *= p.scale;
-    const float mn = fmaxf(m, s), base = mn == -CUDART_INF_F ? 0.f : mn;
-    const float keep = expf(m - base), e = expf(s - base);
-    m = mn;
-    l = l * keep + e;
-#pragma unroll
-    for (int i = 0; i < kDims; ++i) {
-      const int d = lane + 32 * i;
-      if (d < p.head_dim) o[i] = o[i] * keep + e * Tr::to_f32(v[d]);
-    }
-  }
-  const long long to = static_cast<long long>(row) * p.heads + h;
-  const float inv = l > 0.f || isnan(l) ? 1.f / l : 0.f;
-#pragma unroll
-  for (int i = 0; i < kDims; ++i) {
-    const int d = lane + 32 * i;
-    if (d < p.head_dim) static_cast<T*>(p.out)[to * p.head_dim + d] = Tr::from_f32(o[i] * inv);
-  }
-  if (p.lse && lane == 0) p.lse[to] = m + logf(l);
-}
+constexpr int kMaxRuns = 512;
+constexpr size_t kRecordBytes = kMaxRuns * 32;
+constexpr uint64_t kWaitLimitNs = 2000000000ull;
+constexpr float kGrow = 8.f;             // log2 of what a row's maximum may grow by before o is rescaled
+// An item counts as its tiles and kItemUnits more: opening and closing it.
+constexpr int kItemUnits = 3;
+constexpr int kMinShare = 2;             // units of a run, at least
 
 template <typename T>
-cudaError_t launch(const ChunkProblem& p, cudaStream_t stream) {
-  const long long items = static_cast<long long>(p.tokens) * p.heads;
+__host__ __device__ constexpr float lift() { return std::is_same<T, __half>::value ? 7.f : 0.f; }
+
+// Dimensions padded to DP (64, 128, 256).
+template <int DP>
+struct Shape {
+  static constexpr int kNQ = DP == 256 ? 1 : 2;            // accumulators of 128 rows
+  static constexpr int kRows = kNQ * 128;
+  static constexpr int kKeys = DP == 256 ? 64 : 128;       // of a tile
+  static constexpr int kStages = DP == 64 ? 8 : 5;         // tiles of keys or values in flight
+  static constexpr int kAhead = kStages - 2;               // loads left open behind the last one issued
+  static constexpr int kThreads = (kNQ + 2) * 128;
+  static constexpr int kLoadWarp0 = kNQ * 4, kMmaWarp = kLoadWarp0 + 4, kWalkWarp = kMmaWarp + 1;
+  static constexpr uint32_t kQBytes = 128 * DP * 2;        // queries of one accumulator
+  static constexpr uint32_t kTileBytes = kKeys * DP * 2;
+  static constexpr uint32_t kOffKV = kNQ * kQBytes;
+  static constexpr uint32_t kOffControl = kOffKV + kStages * kTileBytes;
+};
+
+// One item's part in a run.
+struct Item {
+  int kv_head;
+  int first;               // row of the sequence's first new token
+  int row0, rows;          // first packed row (token * group + head), live rows from there
+  int position0;           // position of the sequence's first new token
+  int b, key_lo, key_hi;   // keys any of its rows sees
+  int t0, t1;              // tiles of this run
+  int lo[2], hi[2];        // of them, those that each accumulator takes part in
+  int full_lo, full_hi;    // keys that every row sees
+  int slot;                // -1: the run holds all of the item; else where its partial goes
+  int bad;                 // an infinite or NaN value was replaced by 0 in a tile not seen by every row
+};
+
+template <int DP>
+struct Control {
+  unsigned long long full[Shape<DP>::kStages], empty[Shape<DP>::kStages];
+  unsigned long long qfull, qempty, sfull[2], pready[2], ofull[2], ifull[2], iempty[2], drain;
+  uint32_t valid[16][4];   // per tile: keys whose page could be read
+  Item item[2];
+  uint32_t tmem;
+  int abort;
+  int sequence;
+  long long sum[Shape<DP>::kThreads / 32], at, total;
+};
+
+// What is left of a cut item for the joining kernel, by the run that holds the item's first tile.
+struct Record {
+  int valid, first_run, last_run, kv_head, first, row0, rows, pad;
+};
+
+struct Args {
+  ChunkProblem p;
+  int group;
+  float scale_log2;        // |scale| * log2(e)
+  int negative;            // scale < 0
+  unsigned page_mul, page_shift;   // key / page_size = key * page_mul >> page_shift for keys below 2^30
+  unsigned k_page16, k_slot16, k_head16, v_page16, v_slot16, v_head16;   // strides in 16-byte units
+  Record* records;
+  float* partials;
+};
+
+// floats of one partial: accumulators [column / 4][row][4], then m and l per row
+template <int DP>
+__host__ __device__ constexpr size_t partial_floats() { return static_cast<size_t>(Shape<DP>::kRows) * (DP + 2); }
+
+// ------------------------------------------------------------------------------ small pieces
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// x * s + c of two values at a time
+__device__ __forceinline__ void fma2(float& a, float& b, float s, float c) {
+  uint64_t d;
+  const uint64_t x = (static_cast<uint64_t>(__float_as_uint(b)) << 32) | __float_as_uint(a);
+  const uint64_t y = (static_cast<uint64_t>(__float_as_uint(s)) << 32) | __float_as_uint(s);
+  const uint64_t z = (static_cast<uint64_t>(__float_as_uint(c)) << 32) | __float_as_uint(c);
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(x), "l"(y), "l"(z));
+  a = __uint_as_float(static_cast<uint32_t>(d));
+  b = __uint_as_float(static_cast<uint32_t>(d >> 32));
+}
+template <int N>
+__device__ __forceinline__ void grow_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void shrink_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+// Bounded wait on an mbarrier phase; false if the wait ran out or another role gave up.  All lanes agree.
+__device__ __forceinline__ bool wait_one(uint32_t bar, uint32_t parity, volatile int* abort, unsigned* status) {
+  if (ptx::mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = ptx::globaltimer();
+  while (true) {
+    if (ptx::mbar_try_wait_hint(bar, parity, 200000u)) return true;
+    if (*abort) return false;
+    if (ptx::globaltimer() - t0 > kWaitLimitNs) {
+      *abort = 1;
+      atomicOr(status, kStatusTimeout);
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int* abort, unsigned* status) {
+  return __all_sync(0xFFFFFFFFu, wait_one(bar, parity, abort, status));
+}
+
+// x / y of nonnegative numbers: mostly they fit 32 bits
+__device__ __forceinline__ long long divide(long long x, long long y) {
+  if (((x | y) >> 32) == 0) return static_cast<unsigned>(x) / static_cast<unsigned>(y);
+  return x / y;
+}
+
+// ------------------------------------------------------------------------------ the line
+struct Sequence {
+  int first, tokens, n, blocks;    // its rows, keys, blocks of packed rows
+};
+
+template <int DP>
+__device__ __forceinline__ Sequence sequence_of(const Args& a, int b, bool report) {
+  const ChunkProblem& p = a.p;
+  Sequence s;
+  const int c0 = p.cu[b], c1 = p.cu[b + 1], raw = p.lens[b], most = p.table_width * p.page_size;
+  s.first = min(max(c0, 0), p.tokens);
+  const int end = max(s.first, min(c1, p.tokens));
+  s.tokens = end - s.first;
+  s.n = min(max(raw, 0), most);
+  s.blocks = (s.tokens * a.group + Shape<DP>::kRows - 1) / Shape<DP>::kRows;
+  if (report) {
+    if (s.first != c0 || end != c1) atomicOr(p.status, kStatusTokenRows);
+    if (s.n != raw) atomicOr(p.status, kStatusSeqLen);
+  }
+  return s;
+}
+
+// Keys [lo, hi) that the packed rows r0 .. r1 of a sequence see.
+__device__ __forceinline__ void keys_of(const Args& a, const Sequence& s, int r0, int r1, int* lo, int* hi) {
+  const int position0 = s.n - s.tokens;
+  *hi = max(0, position0 + r1 / a.group + 1);
+  *lo = a.p.window > 0 ? max(0, position0 + r0 / a.group - a.p.window + 1) : 0;
+}
+
+template <int DP>
+__device__ __forceinline__ int units_of(const Args& a, const Sequence& s, int block) {
+  using S = Shape<DP>;
+  const int r0 = block * S::kRows, r1 = min(r0 + S::kRows, s.tokens * a.group) - 1;
+  int lo, hi;
+  keys_of(a, s, r0, r1, &lo, &hi);
+  const int tiles = hi > lo ? (hi + S::kKeys - 1) / S::kKeys - lo / S::kKeys : 0;
+  return kItemUnits + max(tiles, 1);       // (an item without keys still writes its zeros)
+}
+
+// Units of one kv head's items of each lane's sequence; sequences of many blocks are summed by the warp.
+template <int DP>
+__device__ __forceinline__ long long head_units(const Args& a, const Sequence& s, int lane) {
+  long long sum = 0;
+  if (s.blocks <= 4)
+    for (int i = 0; i < s.blocks; ++i) sum += units_of<DP>(a, s, i);
+  unsigned many = __ballot_sync(0xFFFFFFFFu, s.blocks > 4);
+  while (many) {
+    const int from = __ffs(many) - 1;
+    many &= many - 1;
+    Sequence o;
+    o.first = __shfl_sync(0xFFFFFFFFu, s.first, from);
+    o.tokens = __shfl_sync(0xFFFFFFFFu, s.tokens, from);
+    o.n = __shfl_sync(0xFFFFFFFFu, s.n, from);
+    o.blocks = __shfl_sync(0xFFFFFFFFu, s.blocks, from);
+    long long part = 0;
+    for (int i = lane; i < o.blocks; i += 32) part += units_of<DP>(a, o, i);
+#pragma unroll
+    for (int x = 16; x; x >>= 1) part += __shfl_xor_sync(0xFFFFFFFFu, part, x);
+    if (lane == from) sum = part;
+  }
+  return sum;
+}
+
+// ------------------------------------------------------------------------------ the kernel
+template <typename T, int DP>
+__global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_constant__ Args a) {
+  using S = Shape<DP>;
+  using C = Control<DP>;
+  using Tr = F16Traits<T>;
+  constexpr int kKeys = S::kKeys, kNQ = S::kNQ;
+  const ChunkProblem& p = a.p;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                         ~static_cast<uintptr_t>(1023));
+  const uint32_t sbase = ptx::smem_addr(smem);
+  C& c = *reinterpret_cast<C*>(smem + S::kOffControl);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, run = blockIdx.x;
+
+  decode::pdl_launch_dependents();
+  decode::pdl_wait();
+
+  // ---- this CTA's run of the line: a scan over the sequences gives its length, and the sequence that the run
+  // begins in
+  long long before = 0, upto = 0, units = 0;
+  auto scan_chunk = [&](int b0, long long base) {
+    const int b = b0 + static_cast<int>(threadIdx.x);
+    Sequence s = {0, 0, 0, 0};
+    if (b < p.batch) s = sequence_of<DP>(a, b, run == 0);
+    units = head_units<DP>(a, s, lane);
+    const long long w = units * p.kv_heads;
+    long long x = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xFFFFFFFFu, x, o);
+      if (lane >= o) x += v;
+    }
+    __syncthreads();                       // what the chunk before left has been read
+    if (lane == 31) c.sum[warp] = x;
+    if (threadIdx.x == 0) c.sequence = -1;
+    __syncthreads();
+    long long all = base;
+    for (int i = 0; i < S::kThreads / 32; ++i) {
+      if (i < warp) x += c.sum[i];
+      all += c.sum[i];
+    }
+    upto = base + x;
+    before = upto - w;
+    return all;
+  };
+  long long total = 0;
+  for (int b0 = 0; b0 < p.batch; b0 += S::kThreads) total = scan_chunk(b0, total);
+  const long long most = total >= kMinShare ? divide(total, kMinShare) : 1;
+  const int runs = most < static_cast<long long>(gridDim.x) ? static_cast<int>(most) : static_cast<int>(gridDim.x);
+  // runs of `share` units, the first `extra` of them one longer
+  const long long share = divide(total, runs), extra = total - share * runs;
+  const long long begin = share * run + (run < extra ? run : extra), end = begin + share + (run < extra ? 1 : 0);
+  if (run < runs && total > 0) {
+    long long at = 0;
+    for (int b0 = 0; b0 < p.batch; b0 += S::kThreads) {
+      if (p.batch > S::kThreads) at = scan_chunk(b0, at);
+      if (before <= begin && begin < upto) {
+        c.sequence = b0 + static_cast<int>(threadIdx.x);
+        c.at = before;
+        c.total = units;
+      }
+      __syncthreads();
+      if (c.sequence >= 0) break;
+    }
+  }
+  if (run >= runs || total == 0 || c.sequence < 0) {       // (the last: lengths written while this ran)
+    if (threadIdx.x == 0) a.records[run].valid = 0;
+    return;
+  }
+
+  // ---- set up
+  if (threadIdx.x == 0) {
+    auto init = [&](unsigned long long& bar, int count) { ptx::mbar_init(ptx::smem_addr(&bar), count); };
+    for (int i = 0; i < S::kStages; ++i) init(c.full[i], 4), init(c.empty[i], 1);
+    init(c.qfull, 4);
+    init(c.qempty, 1);
+    for (int i = 0; i < 2; ++i) {
+      init(c.sfull[i], 1);
+      init(c.pready[i], 4);
+      init(c.ofull[i], 1);
+      init(c.ifull[i], 1);
+      init(c.iempty[i], 4 * kNQ + 5);      // softmax and loader warps, the MMA thread
+    }
+    init(c.drain, 1);
+    c.abort = 0;
+    ptx::fence_mbar_init();
+  }
+  if (p.head_dim % 16) {                   // the MMAs read 16 dimensions at a time: those past head_dim stay zero
+    for (uint32_t i = threadIdx.x * 16; i < S::kOffControl; i += S::kThreads * 16)
+      *reinterpret_cast<uint4*>(smem + i) = make_uint4(0u, 0u, 0u, 0u);
+    ptx::fence_proxy_async_smem();
+  }
+  if (warp == S::kMmaWarp) {
+    ptx::tmem_alloc(ptx::smem_addr(&c.tmem), 512);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = c.tmem;
+  volatile int* const abort = &c.abort;
+  auto bar = [&](unsigned long long& b) { return ptx::smem_addr(&b); };
+  auto wait = [&](unsigned long long& b, uint32_t parity) { return wait_warp(bar(b), parity, abort, p.status); };
+  auto s_col = [&](int s) { return tmem + s * 128; };
+  auto o_col = [&](int s) { return tmem + 256 + s * DP; };
+
+  if (warp >= S::kMmaWarp) {
+    if constexpr (kNQ == 2) shrink_registers<64>();
+    if (warp == S::kWalkWarp) {
+      // -------------------------------------------------------------- the line's items, one after the other
+      int b = c.sequence, h, block = 0;
+      Sequence s = sequence_of<DP>(a, b, false);
+      long long start;                     // the item's first unit
+      {
+        const long long rel = begin - c.at;
+        h = static_cast<int>(divide(rel, c.total));
+        long long left = rel - h * c.total;                // units of the head's items before the run
+        // the block whose units hold it: a warp's scan at a time
+        for (int b0 = 0;; b0 += 32) {
+          const int u = b0 + lane < s.blocks ? units_of<DP>(a, s, b0 + lane) : 0;
+          int x = u;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xFFFFFFFFu, x, o);
+            if (lane >= o) x += v;
+          }
+          const unsigned past = __ballot_sync(0xFFFFFFFFu, x > left);
+          if (past || b0 + 32 >= s.blocks) {
+            const int i = past ? __ffs(past) - 1 : 31;
+            block = min(b0 + i, s.blocks - 1);
+            left -= __shfl_sync(0xFFFFFFFFu, x - u, i);
+            break;
+          }
+          left -= __shfl_sync(0xFFFFFFFFu, x, 31);
+        }
+        start = begin - left;
+      }
+      auto run_of = [&](long long unit) {
+        const long long cut = extra * (share + 1);
+        return static_cast<int>(unit < cut ? divide(unit, share + 1) : extra + divide(unit - cut, share));
+      };
+      Record record = {};
+      bool ok = true;
+      uint32_t n = 0;                      // items handed out
+      while (true) {
+        const int u = units_of<DP>(a, s, block);
+        const long long tile0 = start + kItemUnits, stop = start + u;
+        const bool done = tile0 >= end;
+        const int slot = n & 1;
+        if (!wait(c.iempty[slot], ((n >> 1) & 1) ^ 1)) {
+          ok = false;
+          break;
+        }
+        Item it;
+        it.b = done ? -1 : b;
+        if (!done) {
+          const int r0 = block * S::kRows, r1 = min(r0 + S::kRows, s.tokens * a.group) - 1;
+          it.kv_head = h;
+          it.first = s.first;
+          it.row0 = r0;
+          it.rows = r1 - r0 + 1;
+          it.position0 = s.n - s.tokens;
+          keys_of(a, s, r0, r1, &it.key_lo, &it.key_hi);
+          int x, y;
+          keys_of(a, s, r0, r0, &x, &it.full_hi);
+          keys_of(a, s, r1, r1, &it.full_lo, &y);
+          const bool any = it.key_hi > it.key_lo;
+          const int t_lo = it.key_lo / kKeys;
+          const long long from = tile0 > begin ? 0 : begin - tile0, to = (stop < end ? stop : end) - tile0;
+          it.t0 = any ? t_lo + static_cast<int>(from) : 0;
+          it.t1 = any ? t_lo + static_cast<int>(to) : 0;
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            it.lo[q] = it.hi[q] = 0;
+            if (q < kNQ && r0 + q * 128 <= r1) {
+              keys_of(a, s, r0 + q * 128, min(r0 + q * 128 + 127, r1), &x, &y);
+              if (y > x) {
+                it.lo[q] = max(x / kKeys, it.t0);
+                it.hi[q] = min((y + kKeys - 1) / kKeys, it.t1);
+              }
+            }
+          }
+          const bool whole = tile0 >= begin && stop <= end;
+          const int first_run = whole ? run : run_of(tile0);
+          it.slot = whole ? -1 : 2 * run + (first_run == run ? 1 : 0);
+          it.bad = 0;
+          if (!whole && first_run == run)
+            record = {1, first_run, run_of(stop - 1), h, s.first, r0, it.rows, 0};
+        }
+        if (lane == 0) {
+          c.item[slot] = it;
+          ptx::mbar_arrive(bar(c.ifull[slot]));
+        }
+        __syncwarp();
+        if (done) break;
+        ++n;
+        start = stop;
+        if (++block >= s.blocks) {
+          block = 0;
+          if (++h == p.kv_heads) {
+            h = 0;
+            do {
+              if (++b >= p.batch) break;
+              s = sequence_of<DP>(a, b, false);
+            } while (s.blocks == 0);
+            if (b >= p.batch) {            // the line's end: nothing follows
+              b = p.batch - 1;
+              start = end;
+            }
+          }
+        }
+      }
+      if (lane == 0) a.records[run] = record;
+      (void)ok;
+    } else if (warp == S::kMmaWarp && lane == 0) {
+      // -------------------------------------------------------------- MMAs
+      const int kd = (p.head_dim + 15) / 16;
+      constexpr uint32_t type = std::is_same<T, __half>::value ? 0u : 1u;
+      constexpr uint32_t idesc_s = ptx::umma_idesc_f16(type, 128u, kKeys);
+      const uint32_t idesc_o = ptx::umma_idesc_f16(type, 128u, kd * 16u) | ptx::kUmmaBMajorMN;
+      auto wait1 = [&](unsigned long long& b, uint32_t parity) { return wait_one(bar(b), parity, abort, p.status); };
+      int stage = 0;
+      uint32_t phase = 0, items = 0, queries = 0, p_phase[2] = {0, 0};
+      bool ok = true;
+      auto scores = [&](int s, int at) {   // S[s] = q[s] k^T
+        const uint32_t qa = sbase + s * S::kQBytes, ka = sbase + S::kOffKV + at * S::kTileBytes;
+        for (int k = 0; k < kd; ++k)
+          ptx::umma_f16(s_col(s), ptx::umma_desc_sw128_kmajor(qa + (k >> 2) * 128 * 128 + (k & 3) * 32),
+                        ptx::umma_desc_sw128_kmajor(ka + (k >> 2) * kKeys * 128 + (k & 3) * 32), idesc_s, k != 0);
+        ptx::umma_commit(bar(c.sfull[s]));
+      };
+      auto values = [&](int s, int at, bool more) {   // O[s] (+)= p[s] v
+        const uint32_t va = sbase + S::kOffKV + at * S::kTileBytes;
+#pragma unroll
+        for (int k = 0; k < kKeys / 16; ++k)
+          ptx::umma_f16_ta(o_col(s), s_col(s) + k * 8, ptx::umma_desc_sw128_mnmajor(va + k * 2048, kKeys * 128), idesc_o,
+                           more || k != 0);
+      };
+      auto next_stage = [&]() {
+        if (++stage == S::kStages) stage = 0, phase ^= 1;
+      };
+      while (ok) {
+        const int slot = items & 1;
+        if (!wait1(c.ifull[slot], (items >> 1) & 1)) { ok = false; break; }
+        ++items;
+        const Item it = c.item[slot];
+        if (it.b < 0) break;
+        ptx::mbar_arrive(bar(c.iempty[slot]));
+        if (it.t0 >= it.t1) continue;
+        auto live = [&](int s, int t) { return s < kNQ && t >= it.lo[s] && t < it.hi[s]; };
+        if (!wait1(c.qfull, queries & 1)) { ok = false; break; }
+        ++queries;
+        // the first tile's scores; from then on p v of a tile, then the scores of the next, accumulator by accumulator
+        if (!wait1(c.full[stage], phase)) { ok = false; break; }
+        ptx::tc_fence_after();
+#pragma unroll
+        for (int s = 0; s < kNQ; ++s)
+          if (live(s, it.t0)) scores(s, stage);
+        ptx::umma_commit(bar(c.empty[stage]));
+        if (it.t0 + 1 == it.t1) ptx::umma_commit(bar(c.qempty));
+        next_stage();
+        for (int t = it.t0; t < it.t1; ++t) {
+          const int v_stage = stage;
+          if (!wait1(c.full[stage], phase)) { ok = false; break; }
+          next_stage();
+          bool have_k = false;
+#pragma unroll
+          for (int s = 0; s < kNQ; ++s) {
+            if (live(s, t)) {
+              if (!wait1(c.pready[s], p_phase[s])) { ok = false; break; }
+              p_phase[s] ^= 1;
+              ptx::tc_fence_after();
+              values(s, v_stage, t > it.lo[s]);
+              if (t + 1 == it.hi[s]) ptx::umma_commit(bar(c.ofull[s]));
+            }
+            if (live(s, t + 1)) {
+              if (!have_k) {
+                if (!wait1(c.full[stage], phase)) { ok = false; break; }
+                ptx::tc_fence_after();
+                have_k = true;
+              }
+              scores(s, stage);
+            }
+          }
+          if (!ok) break;
+          ptx::umma_commit(bar(c.empty[v_stage]));
+          if (t + 1 < it.t1) {
+            if (!have_k && !wait1(c.full[stage], phase)) { ok = false; break; }
+            ptx::umma_commit(bar(c.empty[stage]));
+            if (t + 2 == it.t1) ptx::umma_commit(bar(c.qempty));
+            next_stage();
+          }
+        }
+      }
+      if (!ok) {
+        // wait (bounded) for the MMAs already issued before tensor memory is released
+        ptx::umma_commit(bar(c.drain));
+        const uint64_t t0 = ptx::globaltimer();
+        while (!ptx::mbar_try_wait(bar(c.drain), 0) && ptx::globaltimer() - t0 < kWaitLimitNs) {}
+      }
+    }
+  } else if (warp >= S::kLoadWarp0) {
+    // ---------------------------------------------------------------- loads
+    if constexpr (kNQ == 2) shrink_registers<64>();
+    constexpr int kPieces = DP / 8, kAtOnce = 32 / kPieces, kWarpKeys = kKeys / 4;   // pieces and rows of an instruction
+    const int lw = warp - S::kLoadWarp0;
+    const int piece = lane % kPieces, sub = lane / kPieces;
+    const bool in_dim = piece * 8 < p.head_dim;
+    // rows `rows0 + sub + kAtOnce i` of a block of kRowsIn rows: the swizzle is an exclusive or, and kAtOnce a power of two
+    auto place = [&](int rows_in, int row0) {
+      return static_cast<uint32_t>((piece >> 3) * rows_in * 128 + (row0 + sub) * 128 + (((piece & 7) ^ sub) << 4));
+    };
+    const uint32_t kv_at = sbase + S::kOffKV + place(kKeys, lw * kWarpKeys);
+    int stage = 0, old_stage = 0, open = 0;
+    uint32_t phase = 0, items = 0, queries = 0, tiles = 0;
+    unsigned long long meta = 0;           // per open load 4 bits, the oldest lowest: queries with it, values to look at, item slot
+    bool ok = true;
+    auto finish = [&]() {                  // the oldest open load has landed (the caller has waited)
+      const unsigned m = meta & 15;
+      meta >>= 4;
+      --open;
+      if (m & 2) {                         // this thread's own pieces: what is not finite leaves
+        unsigned bad = 0;
+#pragma unroll 4
+        for (int i = 0; i < kWarpKeys / kAtOnce; ++i) {
+          const uint32_t at = ((kv_at + old_stage * S::kTileBytes) ^ (((kAtOnce * i) & 7) << 4)) + kAtOnce * i * 128;
+          uint4* v = reinterpret_cast<uint4*>(smem + (at - sbase));
+          uint4 x = *v;
+          constexpr uint32_t kExp = std::is_same<T, __half>::value ? 0x7C007C00u : 0x7F807F80u;
+          unsigned here = 0;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const uint32_t hit = __vcmpeq2((&x.x)[w] & kExp, kExp);
+            (&x.x)[w] &= ~hit;
+            here |= hit;
+          }
+          if (here && in_dim) *v = x;
+          bad |= here;
+        }
+        if (bad && in_dim) *const_cast<volatile int*>(&c.item[m >> 2 & 1].bad) = 1;
+      }
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        ptx::mbar_arrive(bar(c.full[old_stage]));
+        if (m & 1) ptx::mbar_arrive(bar(c.qfull));
+      }
+      if (++old_stage == S::kStages) old_stage = 0;
+    };
+    auto flush = [&]() {
+      cp_wait<0>();
+      while (open) finish();
+    };
+    auto close = [&](unsigned m) {         // of a load whose copies have been issued
+      cp_commit();
+      meta |= static_cast<unsigned long long>(m) << (4 * open);
+      ++open;
+      if (++stage == S::kStages) stage = 0, phase ^= 1;
+      if (open > S::kAhead) {
+        cp_wait<S::kAhead>();
+        finish();
+      }
+    };
+    while (ok) {
+      const int slot = items & 1;
+      flush();                             // nothing may wait for what is open here while this waits
+      if (!wait(c.ifull[slot], (items >> 1) & 1)) break;
+      ++items;
+      const Item it = c.item[slot];
+      __syncwarp();
+      if (it.b < 0) break;
+      if (lane == 0) ptx::mbar_arrive(bar(c.iempty[slot]));
+      if (it.t0 >= it.t1) continue;
+      const int32_t* table = p.table + static_cast<long long>(it.b) * p.table_width;
+      int key = 0, entry = 0, page = -1;
+      bool want = false;
+      auto fetch = [&](int t) {            // lane's key of tile t: its page
+        key = t * kKeys + lw * kWarpKeys + lane;
+        want = lane < kWarpKeys && key >= it.key_lo && key < it.key_hi;
+        entry = static_cast<int>(static_cast<unsigned long long>(static_cast<unsigned>(key)) * a.page_mul >> a.page_shift);
+        page = want ? __ldg(table + entry) : -1;
+      };
+      fetch(it.t0);
+      if (!wait(c.qempty, (queries & 1) ^ 1)) break;
+      ++queries;
+      {                                    // queries: row r of the item is token r / group, head r % group
+        const T* q = static_cast<const T*>(p.q);
+#pragma unroll
+        for (int s = 0; s < kNQ; ++s) {
+          if (it.lo[s] >= it.hi[s]) continue;
+          const int r = s * 128 + lw * 32 + lane;
+          const int packed = it.row0 + r, token = packed / a.group, head = packed - token * a.group;
+          const long long off = (it.first + token) * p.q_token + static_cast<long long>(it.kv_head * a.group + head) * p.head_dim;
+          const unsigned rows = __ballot_sync(0xFFFFFFFFu, r < it.rows);
+          const uint32_t at = sbase + s * S::kQBytes + place(128, lw * 32);
+#pragma unroll 4
+          for (int i = 0; i < 32 / kAtOnce; ++i) {
+            const long long o = __shfl_sync(0xFFFFFFFFu, off, kAtOnce * i + sub);
+            if (in_dim && (rows >> (kAtOnce * i + sub) & 1))
+              cp_async16((at ^ (((kAtOnce * i) & 7) << 4)) + kAtOnce * i * 128, q + o + piece * 8, 16u);
+          }
+        }
+      }
+      for (int t = it.t0; ok && t < it.t1; ++t, ++tiles) {
+        const bool good = want && page >= 0 && page < p.pages;
+        if (want && !good) atomicOr(p.status, kStatusPageRange);
+        const unsigned rows = __ballot_sync(0xFFFFFFFFu, good), unread = __ballot_sync(0xFFFFFFFFu, want && !good);
+        if (lane == 0) c.valid[tiles & 15][lw] = ~unread;
+        const int place_in = key - entry * p.page_size;
+        const unsigned off_k = good ? page * a.k_page16 + place_in * a.k_slot16 + it.kv_head * a.k_head16 : 0u;
+        const unsigned off_v = good ? page * a.v_page16 + place_in * a.v_slot16 + it.kv_head * a.v_head16 : 0u;
+        if (t + 1 < it.t1) fetch(t + 1);
+        const bool full = t * kKeys >= it.full_lo && (t + 1) * kKeys <= it.full_hi;
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          if (!wait(c.empty[stage], phase ^ 1)) { ok = false; break; }
+          const uint4* base = static_cast<const uint4*>(kv ? p.v_cache : p.k_cache);
+          const uint32_t at = kv_at + stage * S::kTileBytes;
+#pragma unroll 8
+          for (int i = 0; i < kWarpKeys / kAtOnce; ++i) {
+            const unsigned o = __shfl_sync(0xFFFFFFFFu, kv ? off_v : off_k, kAtOnce * i + sub);
+            const bool on = rows >> (kAtOnce * i + sub) & 1;   // (a key without a page is zeros)
+            if (in_dim) cp_async16((at ^ (((kAtOnce * i) & 7) << 4)) + kAtOnce * i * 128, base + o + (on ? piece : 0), on ? 16u : 0u);
+          }
+          close((kv == 0 && t == it.t0 ? 1u : 0u) | (kv && !full ? 2u : 0u) | static_cast<unsigned>(slot) << 2);
+        }
+      }
+    }
+    cp_wait<0>();
+  } else {
+    // ---------------------------------------------------------------- softmax: a thread a row
+    if constexpr (kNQ == 2) grow_registers<192>();
+    const int s = warp >> 2, row = threadIdx.x & 127;
+    const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;   // the warp's 32 lanes of tensor memory
+    const uint32_t sc = s_col(s) + lanes, oc = o_col(s) + lanes;
+    const float scale = a.scale_log2;
+    uint32_t items = 0, tiles = 0, s_phase = 0, o_phase = 0;
+    while (true) {
+      const int slot = items & 1;
+      if (!wait(c.ifull[slot], (items >> 1) & 1)) break;
+      ++items;
+      const Item& it = c.item[slot];
+      if (it.b < 0) break;
+      const int r = s * 128 + row, packed = it.row0 + r;
+      const int token = packed / a.group, head = packed - token * a.group;
+      const bool live_row = r < it.rows, live_warp = s * 128 + (warp & 3) * 32 < it.rows;
+      const int position = it.position0 + token;
+      const int row_hi = position + 1, row_lo = p.window > 0 ? max(0, position - p.window + 1) : 0;
+      float m = -CUDART_INF_F, l = 0.f;
+      bool ok = true;
+      const int t0 = it.t0, t1 = it.t1, lo = it.lo[s], hi = it.hi[s];
+      for (int t = t0; t < t1; ++t, ++tiles) {
+        if (t < lo || t >= hi) continue;
+        if (!wait(c.sfull[s], s_phase)) { ok = false; break; }
+        s_phase ^= 1;
+        ptx::tc_fence_after();
+        if (live_warp) {
+          float x[kKeys];
+#pragma unroll
+          for (int i = 0; i < kKeys / 32; ++i) ptx::tmem_ld_32x32b_x32(sc + 32 * i, *reinterpret_cast<uint32_t(*)[32]>(x + 32 * i));
+          ptx::tmem_ld_wait();
+          if (a.negative) {
+#pragma unroll
+            for (int i = 0; i < kKeys; ++i) x[i] = -x[i];
+          }
+          // keys that the row does not see
+          const int key0 = t * kKeys;
+          if (__any_sync(0xFFFFFFFFu, key0 < row_lo || key0 + kKeys > row_hi)) {
+            const int from = row_lo - key0;
+            const unsigned count = static_cast<unsigned>(max(row_hi - row_lo, 0));
+#pragma unroll
+            for (int i = 0; i < kKeys; ++i)
+              if (static_cast<unsigned>(i - from) >= count) x[i] = -CUDART_INF_F;
+          }
+          const uint32_t* valid = c.valid[tiles & 15];
+          if ((valid[0] & valid[1] & valid[2] & valid[3]) != 0xFFFFFFFFu) {
+#pragma unroll
+            for (int i = 0; i < kKeys; ++i)
+              if (!(valid[i / (kKeys / 4)] >> (i % (kKeys / 4)) & 1)) x[i] = -CUDART_INF_F;
+          }
+          float top[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+          for (int i = 4; i < kKeys; ++i) top[i & 3] = fmaxf(top[i & 3], x[i]);
+          const float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
+          const bool grown = now > m + kGrow;
+          if (__any_sync(0xFFFFFFFFu, grown)) {
+            const float mn = grown ? now : m;
+            const float keep = grown ? ex2(m - mn) : 1.f;
+            m = mn;
+            l *= keep;
+            if (t > lo) {                  // o is at rest: the scores' MMA came after its last
+              for (int i = 0; i < p.head_dim; i += 32) {
+                uint32_t o[32];
+                ptx::tmem_ld_32x32b_x32(oc + i, o);
+                ptx::tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * keep);
+                ptx::tmem_st_32x32b_x32(oc + i, o);
+              }
+            }
+          }
+          const float base = lift<T>() - (m == -CUDART_INF_F ? 0.f : m);
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int i = 0; i < kKeys / 64; ++i) {
+            uint32_t w[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              float u = x[64 * i + 2 * j], v = x[64 * i + 2 * j + 1];
+              fma2(u, v, scale, base);
+              u = ex2(u);
+              v = ex2(v);
+              sum[j & 1] += u;
+              sum[2 + (j & 1)] += v;
+              w[j] = pack2(u, v, T());
+            }
+            ptx::tmem_st_32x32b_x32(sc + 32 * i, w);
+          }
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          ptx::tmem_st_wait();
+        }
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(c.pready[s]));
+      }
+      if (!ok) break;
+      const bool any = hi > lo;
+      if (any) {
+        if (!wait(c.ofull[s], o_phase)) break;
+        o_phase ^= 1;
+        ptx::tc_fence_after();
+      }
+      if (live_warp) {
+        const long long at = static_cast<long long>(it.first + token) * p.heads + it.kv_head * a.group + head;
+        const bool bad = *const_cast<const volatile int*>(&it.bad) != 0;
+        const float inv = it.slot >= 0 ? 1.f : (l > 0.f || isnan(l) ? 1.f / l : 0.f);
+        float* part = a.partials + static_cast<size_t>(max(it.slot, 0)) * partial_floats<DP>();
+#pragma unroll 1
+        for (int i = 0; i < p.head_dim; i += 32) {
+          uint32_t o[32];
+          if (any) {
+            ptx::tmem_ld_32x32b_x32(oc + i, o);
+            ptx::tmem_ld_wait();
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = 0;
+          }
+          if (bad && live_row) {
+            // values that are not finite, of the keys that this row sees in the tiles not seen by all
+#pragma unroll 1
+            for (int t = t0; t < t1; ++t) {
+              if (t * kKeys >= it.full_lo && (t + 1) * kKeys <= it.full_hi) continue;
+#pragma unroll 1
+              for (int key = max(t * kKeys, row_lo); key < min((t + 1) * kKeys, row_hi); ++key) {
+                const int page = p.table[static_cast<long long>(it.b) * p.table_width + key / p.page_size];
+                if (page < 0 || page >= p.pages) continue;
+                const T* v = static_cast<const T*>(p.v_cache) + page * p.v_page + key % p.page_size * p.v_slot +
+                             it.kv_head * p.v_head + i;
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                  if (i + j >= p.head_dim) continue;
+                  const float f = Tr::to_f32(v[j]);
+                  if (!isfinite(f)) o[j] = __float_as_uint(__uint_as_float(o[j]) + f);
+                }
+              }
+            }
+          }
+          if (it.slot < 0) {
+            if (live_row) {
+              uint4* to = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + at * p.head_dim + i);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                uint4 w;
+#pragma unroll
+                for (int y = 0; y < 4; ++y)
+                  (&w.x)[y] = pack2(__uint_as_float(o[8 * j + 2 * y]) * inv, __uint_as_float(o[8 * j + 2 * y + 1]) * inv, T());
+                if (i + 8 * j < p.head_dim) to[j] = w;
+              }
+            }
+          } else if (any) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              __stcg(reinterpret_cast<uint4*>(part) + (i / 4 + j) * S::kRows + r, make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]));
+          }
+        }
+        if (it.slot < 0) {
+          if (p.lse && live_row) p.lse[at] = m * 0.693147180559945f + logf(l * (std::is_same<T, __half>::value ? 1.f / 128.f : 1.f));
+        } else {
+          __stcg(reinterpret_cast<float2*>(part + static_cast<size_t>(S::kRows) * DP) + r, make_float2(any ? m : -CUDART_INF_F, l));
+        }
+        ptx::tc_fence_before();
+      }
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bar(c.iempty[slot]));
+    }
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == S::kMmaWarp) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, 512);
+  }
+}
+
+// The join: a CTA takes 16 columns of one cut item, a thread a row.
+constexpr int kJoinCols = 16;
+
+template <typename T, int DP>
+__global__ void __launch_bounds__(Shape<DP>::kRows) k_join(const __grid_constant__ Args a) {
+  using S = Shape<DP>;
+  const ChunkProblem& p = a.p;
+  decode::pdl_launch_dependents();
+  decode::pdl_wait();
+  const Record rec = a.records[blockIdx.x];
+  const int row = threadIdx.x, col = blockIdx.y * kJoinCols;
+  if (!rec.valid || row >= rec.rows || col >= p.head_dim) return;
+  auto part_of = [&](int run) {
+    return a.partials + static_cast<size_t>(2 * run + (run == rec.first_run ? 1 : 0)) * partial_floats<DP>();
+  };
+  auto ml_of = [&](int run) { return __ldcg(reinterpret_cast<const float2*>(part_of(run) + static_cast<size_t>(S::kRows) * DP) + row); };
+  float top = -CUDART_INF_F;
+  for (int run = rec.first_run; run <= rec.last_run; ++run) top = fmaxf(top, ml_of(run).x);
+  float l = 0.f, o[kJoinCols] = {};
+  for (int run = rec.first_run; run <= rec.last_run; ++run) {
+    const float2 ml = ml_of(run);
+    if (ml.x == -CUDART_INF_F && !isnan(ml.y)) continue;   // the run had no key of the row: its o says nothing
+    const float f = ex2(ml.x - (top == -CUDART_INF_F ? 0.f : top));
+    l += ml.y * f;
+    const float4* from = reinterpret_cast<const float4*>(part_of(run)) + static_cast<size_t>(col / 4) * S::kRows + row;
+#pragma unroll
+    for (int i = 0; i < kJoinCols / 4; ++i) {
+      const float4 v = __ldcg(from + static_cast<size_t>(i) * S::kRows);
+      o[4 * i] += v.x * f;
+      o[4 * i + 1] += v.y * f;
+      o[4 * i + 2] += v.z * f;
+      o[4 * i + 3] += v.w * f;
+    }
+  }
+  const int packed = rec.row0 + row, token = packed / a.group, head = packed - token * a.group;
+  const long long at = static_cast<long long>(rec.first + token) * p.heads + rec.kv_head * a.group + head;
+  const float inv = l > 0.f || isnan(l) ? 1.f / l : 0.f;
+  uint4* to = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + at * p.head_dim + col);
+#pragma unroll
+  for (int j = 0; j < kJoinCols / 8; ++j) {
+    uint4 w;
+#pragma unroll
+    for (int y = 0; y < 4; ++y) (&w.x)[y] = pack2(o[8 * j + 2 * y] * inv, o[8 * j + 2 * y + 1] * inv, T());
+    if (col + 8 * j < p.head_dim) to[j] = w;
+  }
+  if (p.lse && col == 0) p.lse[at] = top * 0.693147180559945f + logf(l * (std::is_same<T, __half>::value ? 1.f / 128.f : 1.f));
+}
+
+// ------------------------------------------------------------------------------ host side
+template <typename T, int DP>
+cudaError_t launch(const Args& a, cudaStream_t stream) {
+  using S = Shape<DP>;
+  constexpr size_t kSmem = S::kOffControl + sizeof(Control<DP>) + 1024;
+  static_assert(kSmem <= 232448, "the layout must fit one CTA's shared memory (227 KB)");
+  auto kern = k_chunk<T, DP>;
+  const DeviceInfo& dev = device_info();
+  static std::atomic<unsigned long long> opted_in{0};       // per device
+  if (dev.device >= 64 || !(opted_in.load(std::memory_order_relaxed) & (1ull << dev.device))) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
+    if (e != cudaSuccess) return e;
+    if (dev.device < 64) opted_in.fetch_or(1ull << dev.device, std::memory_order_relaxed);
+  }
+  const int grid = dev.sm_count < kMaxRuns ? dev.sm_count : kMaxRuns;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((items + kWarps - 1) / kWarps));
-  cfg.blockDim = dim3(kThreads);
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(S::kThreads);
+  cfg.dynamicSmemBytes = kSmem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (p.head_dim <= 64) return cudaLaunchKernelEx(&cfg, k_chunk<T, 64>, p);
-  if (p.head_dim <= 128) return cudaLaunchKernelEx(&cfg, k_chunk<T, 128>, p);
-  return cudaLaunchKernelEx(&cfg, k_chunk<T, 256>, p);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a);
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3(grid, DP / kJoinCols);
+  cfg.blockDim = dim3(S::kRows);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, k_join<T, DP>, a);
+}
+
+template <typename T>
+cudaError_t launch_dim(const Args& a, cudaStream_t stream) {
+  if (a.p.head_dim <= 64) return launch<T, 64>(a, stream);
+  if (a.p.head_dim <= 128) return launch<T, 128>(a, stream);
+  return launch<T, 256>(a, stream);
 }
 
 }  // namespace chunk
 
-size_t chunk_attention_workspace_bytes(int, int, int) { return 4096; }
+size_t chunk_attention_workspace_bytes(int, int, int head_dim) {
+  const size_t floats = head_dim <= 64 ? chunk::partial_floats<64>()
+                                       : (head_dim <= 128 ? chunk::partial_floats<128>() : chunk::partial_floats<256>());
+  return chunk::kRecordBytes + static_cast<size_t>(chunk::kMaxRuns) * 2 * floats * 4;
+}
 
 cudaError_t launch_chunk_attention(const ChunkProblem& p, cudaStream_t stream) {
-  return p.dtype == 0 ? chunk::launch<__half>(p, stream) : chunk::launch<__nv_bfloat16>(p, stream);
+  chunk::Args a;
+  a.p = p;
+  a.group = p.heads / p.kv_heads;
+  a.negative = p.scale < 0.f;
+  a.scale_log2 = (a.negative ? -p.scale : p.scale) * 1.44269504088896341f;
+  // hidden scores are -inf, which times 0 is no number
+  if (a.scale_log2 == 0.f) a.scale_log2 = 1.17549435e-38f;
+  // m = ceil(2^(30 + L) / d) with 2^L >= d: n m / 2^(30 + L) is off by less than 1 / d for n < 2^30
+  unsigned log = 0;
+  while ((1ull << log) < static_cast<unsigned>(p.page_size)) ++log;
+  a.page_shift = 30 + log;
+  a.page_mul = static_cast<unsigned>(((1ull << a.page_shift) + p.page_size - 1) / p.page_size);
+  a.k_page16 = static_cast<unsigned>(p.k_page / 8);
+  a.k_slot16 = static_cast<unsigned>(p.k_slot / 8);
+  a.k_head16 = static_cast<unsigned>(p.k_head / 8);
+  a.v_page16 = static_cast<unsigned>(p.v_page / 8);
+  a.v_slot16 = static_cast<unsigned>(p.v_slot / 8);
+  a.v_head16 = static_cast<unsigned>(p.v_head / 8);
+  a.records = static_cast<chunk::Record*>(p.workspace);
+  a.partials = reinterpret_cast<float*>(static_cast<char*>(p.workspace) + chunk::kRecordBytes);
+  return p.dtype == 0 ? chunk::launch_dim<__half>(a, stream) : chunk::launch_dim<__nv_bfloat16>(a, stream);
 }
 
 }  // namespace gptq
