@@ -63,7 +63,7 @@ struct Shape {
   static constexpr int kRows = kNQ * 128;
   static constexpr int kKeys = DP == 256 ? 64 : 128;       // of a tile
   static constexpr int kStages = DP == 64 ? 8 : 5;         // tiles of keys or values in flight
-  static constexpr int kAhead = kStages - 2;               // loads left open behind the last one issued
+  static constexpr int kAhead = kStages - 2;               // loads left open behind the last one issued (6 at most)
   static constexpr int kThreads = (kNQ + 2) * 128;
   static constexpr int kLoadWarp0 = kNQ * 4, kMmaWarp = kLoadWarp0 + 4, kWalkWarp = kMmaWarp + 1;
   static constexpr uint32_t kQBytes = 128 * DP * 2;        // queries of one accumulator
@@ -141,6 +141,13 @@ __device__ __forceinline__ void fma2(float& a, float& b, float s, float c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(x), "l"(y), "l"(z));
   a = __uint_as_float(static_cast<uint32_t>(d));
   b = __uint_as_float(static_cast<uint32_t>(d >> 32));
+}
+__device__ __forceinline__ float2 add2(float2 s, float a, float b) {
+  uint64_t d;
+  const uint64_t x = (static_cast<uint64_t>(__float_as_uint(s.y)) << 32) | __float_as_uint(s.x);
+  const uint64_t y = (static_cast<uint64_t>(__float_as_uint(b)) << 32) | __float_as_uint(a);
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
+  return make_float2(__uint_as_float(static_cast<uint32_t>(d)), __uint_as_float(static_cast<uint32_t>(d >> 32)));
 }
 template <int N>
 __device__ __forceinline__ void grow_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
@@ -342,7 +349,7 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
   auto o_col = [&](int s) { return tmem + 256 + s * DP; };
 
   if (warp >= S::kMmaWarp) {
-    if constexpr (kNQ == 2) shrink_registers<64>();
+    if constexpr (kNQ == 2) shrink_registers<80>();
     if (warp == S::kWalkWarp) {
       // -------------------------------------------------------------- the line's items, one after the other
       int b = c.sequence, h, block = 0;
@@ -459,19 +466,30 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
       int stage = 0;
       uint32_t phase = 0, items = 0, queries = 0, p_phase[2] = {0, 0};
       bool ok = true;
+      // Descriptors hold addresses in units of 16 bytes in their lowest bits: a step is an addition of a constant.  (With
+      // descriptors built anew in a loop the issue of one MMA took 140 cycles, twice its time on the tensor cores.)
+      const uint64_t q_desc = ptx::umma_desc_sw128_kmajor(sbase), k_desc = ptx::umma_desc_sw128_kmajor(sbase + S::kOffKV);
+      const uint64_t v_desc = ptx::umma_desc_sw128_mnmajor(sbase + S::kOffKV, kKeys * 128);
       auto scores = [&](int s, int at) {   // S[s] = q[s] k^T
-        const uint32_t qa = sbase + s * S::kQBytes, ka = sbase + S::kOffKV + at * S::kTileBytes;
-        for (int k = 0; k < kd; ++k)
-          ptx::umma_f16(s_col(s), ptx::umma_desc_sw128_kmajor(qa + (k >> 2) * 128 * 128 + (k & 3) * 32),
-                        ptx::umma_desc_sw128_kmajor(ka + (k >> 2) * kKeys * 128 + (k & 3) * 32), idesc_s, k != 0);
+        const uint64_t qd = q_desc + s * (S::kQBytes >> 4), kt = k_desc + at * (S::kTileBytes >> 4);
+        if (kd == DP / 16) {
+#pragma unroll
+          for (int k = 0; k < DP / 16; ++k)
+            ptx::umma_f16(s_col(s), qd + ((k >> 2) * 128 * 128 + (k & 3) * 32) / 16,
+                          kt + ((k >> 2) * kKeys * 128 + (k & 3) * 32) / 16, idesc_s, k != 0);
+        } else {
+#pragma unroll 1
+          for (int k = 0; k < kd; ++k)
+            ptx::umma_f16(s_col(s), qd + ((k >> 2) * 128 * 128 + (k & 3) * 32) / 16,
+                          kt + ((k >> 2) * kKeys * 128 + (k & 3) * 32) / 16, idesc_s, k != 0);
+        }
         ptx::umma_commit(bar(c.sfull[s]));
       };
       auto values = [&](int s, int at, bool more) {   // O[s] (+)= p[s] v
-        const uint32_t va = sbase + S::kOffKV + at * S::kTileBytes;
+        const uint64_t vt = v_desc + at * (S::kTileBytes >> 4);
 #pragma unroll
         for (int k = 0; k < kKeys / 16; ++k)
-          ptx::umma_f16_ta(o_col(s), s_col(s) + k * 8, ptx::umma_desc_sw128_mnmajor(va + k * 2048, kKeys * 128), idesc_o,
-                           more || k != 0);
+          ptx::umma_f16_ta(o_col(s), s_col(s) + k * 8, vt + k * (2048 / 16), idesc_o, more || k != 0);
       };
       auto next_stage = [&]() {
         if (++stage == S::kStages) stage = 0, phase ^= 1;
@@ -538,7 +556,7 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
     }
   } else if (warp >= S::kLoadWarp0) {
     // ---------------------------------------------------------------- loads
-    if constexpr (kNQ == 2) shrink_registers<64>();
+    if constexpr (kNQ == 2) shrink_registers<80>();
     constexpr int kPieces = DP / 8, kAtOnce = 32 / kPieces, kWarpKeys = kKeys / 4;   // pieces and rows of an instruction
     const int lw = warp - S::kLoadWarp0;
     const int piece = lane % kPieces, sub = lane / kPieces;
@@ -584,28 +602,40 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
       }
       if (++old_stage == S::kStages) old_stage = 0;
     };
-    auto flush = [&]() {
-      cp_wait<0>();
-      while (open) finish();
+    auto oldest = [&]() {                  // waits for the oldest open load and hands it on
+      if (open > 5) cp_wait<5>();
+      else if (open == 5) cp_wait<4>();
+      else if (open == 4) cp_wait<3>();
+      else if (open == 3) cp_wait<2>();
+      else if (open == 2) cp_wait<1>();
+      else cp_wait<0>();
+      finish();
+    };
+    // A wait in which open loads are handed on as they land: who releases the barrier may be waiting for them.
+    auto wait_open = [&](unsigned long long& b, uint32_t parity) {
+      while (open) {
+        if (__all_sync(0xFFFFFFFFu, ptx::mbar_try_wait(bar(b), parity))) return true;
+        oldest();
+      }
+      return wait(b, parity);
     };
     auto close = [&](unsigned m) {         // of a load whose copies have been issued
       cp_commit();
       meta |= static_cast<unsigned long long>(m) << (4 * open);
       ++open;
       if (++stage == S::kStages) stage = 0, phase ^= 1;
-      if (open > S::kAhead) {
-        cp_wait<S::kAhead>();
-        finish();
-      }
+      if (open > S::kAhead) oldest();
     };
     while (ok) {
       const int slot = items & 1;
-      flush();                             // nothing may wait for what is open here while this waits
-      if (!wait(c.ifull[slot], (items >> 1) & 1)) break;
+      if (!wait_open(c.ifull[slot], (items >> 1) & 1)) break;
       ++items;
       const Item it = c.item[slot];
       __syncwarp();
-      if (it.b < 0) break;
+      if (it.b < 0) {
+        while (open) oldest();
+        break;
+      }
       if (lane == 0) ptx::mbar_arrive(bar(c.iempty[slot]));
       if (it.t0 >= it.t1) continue;
       const int32_t* table = p.table + static_cast<long long>(it.b) * p.table_width;
@@ -618,7 +648,7 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
         page = want ? __ldg(table + entry) : -1;
       };
       fetch(it.t0);
-      if (!wait(c.qempty, (queries & 1) ^ 1)) break;
+      if (!wait_open(c.qempty, (queries & 1) ^ 1)) break;
       ++queries;
       {                                    // queries: row r of the item is token r / group, head r % group
         const T* q = static_cast<const T*>(p.q);
@@ -650,7 +680,7 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
         const bool full = t * kKeys >= it.full_lo && (t + 1) * kKeys <= it.full_hi;
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
-          if (!wait(c.empty[stage], phase ^ 1)) { ok = false; break; }
+          if (!wait_open(c.empty[stage], phase ^ 1)) { ok = false; break; }
           const uint4* base = static_cast<const uint4*>(kv ? p.v_cache : p.k_cache);
           const uint32_t at = kv_at + stage * S::kTileBytes;
 #pragma unroll 8
@@ -663,10 +693,10 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
         }
       }
     }
-    cp_wait<0>();
+    cp_wait<0>();                          // (where a wait was given up: nothing lands after the CTA)
   } else {
     // ---------------------------------------------------------------- softmax: a thread a row
-    if constexpr (kNQ == 2) grow_registers<192>();
+    if constexpr (kNQ == 2) grow_registers<176>();
     const int s = warp >> 2, row = threadIdx.x & 127;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;   // the warp's 32 lanes of tensor memory
     const uint32_t sc = s_col(s) + lanes, oc = o_col(s) + lanes;
@@ -717,7 +747,11 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
           }
           float top[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-          for (int i = 4; i < kKeys; ++i) top[i & 3] = fmaxf(top[i & 3], x[i]);
+          for (int i = 4; i + 8 <= kKeys; i += 8)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) top[j] = fmaxf(fmaxf(top[j], x[i + 2 * j]), x[i + 2 * j + 1]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) top[j] = fmaxf(top[j], x[kKeys - 4 + j]);
           const float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
           const bool grown = now > m + kGrow;
           if (__any_sync(0xFFFFFFFFu, grown)) {
@@ -726,18 +760,19 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
             m = mn;
             l *= keep;
             if (t > lo) {                  // o is at rest: the scores' MMA came after its last
-              for (int i = 0; i < p.head_dim; i += 32) {
-                uint32_t o[32];
-                ptx::tmem_ld_32x32b_x32(oc + i, o);
+#pragma unroll 1
+              for (int i = 0; i < p.head_dim; i += 16) {
+                uint32_t o[16];
+                ptx::tmem_ld_32x32b_x16(oc + i, o);
                 ptx::tmem_ld_wait();
 #pragma unroll
-                for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * keep);
-                ptx::tmem_st_32x32b_x32(oc + i, o);
+                for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * keep);
+                ptx::tmem_st_32x32b_x16(oc + i, o);
               }
             }
           }
           const float base = lift<T>() - (m == -CUDART_INF_F ? 0.f : m);
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          float2 sum[2] = {};
 #pragma unroll
           for (int i = 0; i < kKeys / 64; ++i) {
             uint32_t w[32];
@@ -747,13 +782,12 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
               fma2(u, v, scale, base);
               u = ex2(u);
               v = ex2(v);
-              sum[j & 1] += u;
-              sum[2 + (j & 1)] += v;
+              sum[j & 1] = add2(sum[j & 1], u, v);
               w[j] = pack2(u, v, T());
             }
             ptx::tmem_st_32x32b_x32(sc + 32 * i, w);
           }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
           ptx::tmem_st_wait();
         }
         ptx::tc_fence_before();
