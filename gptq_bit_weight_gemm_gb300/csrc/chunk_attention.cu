@@ -89,7 +89,7 @@ struct Item {
 template <int DP>
 struct Control {
   unsigned long long full[Shape<DP>::kStages], empty[Shape<DP>::kStages];
-  unsigned long long qfull, qempty, sfull[2], pready[2], ofull[2], ifull[2], iempty[2], drain;
+  unsigned long long qfull, qempty, sfull[2], pready[2][2], ofull[2], ifull[2], iempty[2], drain;
   uint32_t valid[16][4];   // per tile: keys whose page could be read
   Item item[2];
   uint32_t tmem;
@@ -121,6 +121,9 @@ __host__ __device__ constexpr size_t partial_floats() { return static_cast<size_
 // ------------------------------------------------------------------------------ small pieces
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -254,7 +257,7 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
                                                          ~static_cast<uintptr_t>(1023));
   const uint32_t sbase = ptx::smem_addr(smem);
   C& c = *reinterpret_cast<C*>(smem + S::kOffControl);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, run = blockIdx.x;
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31, run = blockIdx.x;
 
   decode::pdl_launch_dependents();
   decode::pdl_wait();
@@ -320,7 +323,8 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
     init(c.qempty, 1);
     for (int i = 0; i < 2; ++i) {
       init(c.sfull[i], 1);
-      init(c.pready[i], 4);
+      init(c.pready[i][0], 4);
+      init(c.pready[i][1], 4);
       init(c.ofull[i], 1);
       init(c.ifull[i], 1);
       init(c.iempty[i], 4 * kNQ + 5);      // softmax and loader warps, the MMA thread
@@ -341,7 +345,7 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  const uint32_t tmem = c.tmem;
+  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, c.tmem, 0);
   volatile int* const abort = &c.abort;
   auto bar = [&](unsigned long long& b) { return ptx::smem_addr(&b); };
   auto wait = [&](unsigned long long& b, uint32_t parity) { return wait_warp(bar(b), parity, abort, p.status); };
@@ -456,18 +460,18 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
       }
       if (lane == 0) a.records[run] = record;
       (void)ok;
-    } else if (warp == S::kMmaWarp && lane == 0) {
+    } else if (warp == S::kMmaWarp) {
       // -------------------------------------------------------------- MMAs
       const int kd = (p.head_dim + 15) / 16;
       constexpr uint32_t type = std::is_same<T, __half>::value ? 0u : 1u;
       constexpr uint32_t idesc_s = ptx::umma_idesc_f16(type, 128u, kKeys);
       const uint32_t idesc_o = ptx::umma_idesc_f16(type, 128u, kd * 16u) | ptx::kUmmaBMajorMN;
-      auto wait1 = [&](unsigned long long& b, uint32_t parity) { return wait_one(bar(b), parity, abort, p.status); };
+      const uint32_t leader = ptx::elect_one();
+      auto commit = [&](unsigned long long& b) { ptx::umma_commit_by(leader, bar(b)); };
       int stage = 0;
       uint32_t phase = 0, items = 0, queries = 0, p_phase[2] = {0, 0};
       bool ok = true;
-      // Descriptors hold addresses in units of 16 bytes in their lowest bits: a step is an addition of a constant.  (With
-      // descriptors built anew in a loop the issue of one MMA took 140 cycles, twice its time on the tensor cores.)
+      // Descriptors hold addresses in units of 16 bytes in their lowest bits: a step is an addition of a constant.
       const uint64_t q_desc = ptx::umma_desc_sw128_kmajor(sbase), k_desc = ptx::umma_desc_sw128_kmajor(sbase + S::kOffKV);
       const uint64_t v_desc = ptx::umma_desc_sw128_mnmajor(sbase + S::kOffKV, kKeys * 128);
       auto scores = [&](int s, int at) {   // S[s] = q[s] k^T
@@ -475,62 +479,68 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
         if (kd == DP / 16) {
 #pragma unroll
           for (int k = 0; k < DP / 16; ++k)
-            ptx::umma_f16(s_col(s), qd + ((k >> 2) * 128 * 128 + (k & 3) * 32) / 16,
+            ptx::umma_f16_by(leader, s_col(s), qd + ((k >> 2) * 128 * 128 + (k & 3) * 32) / 16,
                           kt + ((k >> 2) * kKeys * 128 + (k & 3) * 32) / 16, idesc_s, k != 0);
         } else {
 #pragma unroll 1
           for (int k = 0; k < kd; ++k)
-            ptx::umma_f16(s_col(s), qd + ((k >> 2) * 128 * 128 + (k & 3) * 32) / 16,
+            ptx::umma_f16_by(leader, s_col(s), qd + ((k >> 2) * 128 * 128 + (k & 3) * 32) / 16,
                           kt + ((k >> 2) * kKeys * 128 + (k & 3) * 32) / 16, idesc_s, k != 0);
         }
-        ptx::umma_commit(bar(c.sfull[s]));
+        commit(c.sfull[s]);
       };
-      auto values = [&](int s, int at, bool more) {   // O[s] (+)= p[s] v
-        const uint64_t vt = v_desc + at * (S::kTileBytes >> 4);
+      auto values = [&](int s, int at, int half, bool more) {   // O[s] (+)= p[s] v, over half of the tile's keys
+        const uint64_t vt = v_desc + at * (S::kTileBytes >> 4) + half * (kKeys / 32) * (2048 / 16);
+        const uint32_t pt = s_col(s) + half * (kKeys / 4);
 #pragma unroll
-        for (int k = 0; k < kKeys / 16; ++k)
-          ptx::umma_f16_ta(o_col(s), s_col(s) + k * 8, vt + k * (2048 / 16), idesc_o, more || k != 0);
+        for (int k = 0; k < kKeys / 32; ++k)
+          ptx::umma_f16_ta_by(leader, o_col(s), pt + k * 8, vt + k * (2048 / 16), idesc_o, more || k != 0);
       };
       auto next_stage = [&]() {
         if (++stage == S::kStages) stage = 0, phase ^= 1;
       };
       while (ok) {
         const int slot = items & 1;
-        if (!wait1(c.ifull[slot], (items >> 1) & 1)) { ok = false; break; }
+        if (!wait(c.ifull[slot], (items >> 1) & 1)) { ok = false; break; }
         ++items;
-        const Item it = c.item[slot];
-        if (it.b < 0) break;
-        ptx::mbar_arrive(bar(c.iempty[slot]));
+        const Item& from = c.item[slot];
+        if (from.b < 0) break;
+        struct { int t0, t1, lo[2], hi[2]; } it = {from.t0, from.t1, {from.lo[0], from.lo[1]}, {from.hi[0], from.hi[1]}};
+        __syncwarp();
+        if (leader) ptx::mbar_arrive(bar(c.iempty[slot]));
         if (it.t0 >= it.t1) continue;
         auto live = [&](int s, int t) { return s < kNQ && t >= it.lo[s] && t < it.hi[s]; };
-        if (!wait1(c.qfull, queries & 1)) { ok = false; break; }
+        if (!wait(c.qfull, queries & 1)) { ok = false; break; }
         ++queries;
         // the first tile's scores; from then on p v of a tile, then the scores of the next, accumulator by accumulator
-        if (!wait1(c.full[stage], phase)) { ok = false; break; }
+        if (!wait(c.full[stage], phase)) { ok = false; break; }
         ptx::tc_fence_after();
 #pragma unroll
         for (int s = 0; s < kNQ; ++s)
           if (live(s, it.t0)) scores(s, stage);
-        ptx::umma_commit(bar(c.empty[stage]));
-        if (it.t0 + 1 == it.t1) ptx::umma_commit(bar(c.qempty));
+        commit(c.empty[stage]);
+        if (it.t0 + 1 == it.t1) commit(c.qempty);
         next_stage();
         for (int t = it.t0; t < it.t1; ++t) {
           const int v_stage = stage;
-          if (!wait1(c.full[stage], phase)) { ok = false; break; }
+          if (!wait(c.full[stage], phase)) { ok = false; break; }
           next_stage();
           bool have_k = false;
 #pragma unroll
           for (int s = 0; s < kNQ; ++s) {
             if (live(s, t)) {
-              if (!wait1(c.pready[s], p_phase[s])) { ok = false; break; }
+              if (!wait(c.pready[s][0], p_phase[s])) { ok = false; break; }
+              ptx::tc_fence_after();
+              values(s, v_stage, 0, t > it.lo[s]);
+              if (!wait(c.pready[s][1], p_phase[s])) { ok = false; break; }
               p_phase[s] ^= 1;
               ptx::tc_fence_after();
-              values(s, v_stage, t > it.lo[s]);
-              if (t + 1 == it.hi[s]) ptx::umma_commit(bar(c.ofull[s]));
+              values(s, v_stage, 1, true);
+              if (t + 1 == it.hi[s]) commit(c.ofull[s]);
             }
             if (live(s, t + 1)) {
               if (!have_k) {
-                if (!wait1(c.full[stage], phase)) { ok = false; break; }
+                if (!wait(c.full[stage], phase)) { ok = false; break; }
                 ptx::tc_fence_after();
                 have_k = true;
               }
@@ -538,34 +548,37 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
             }
           }
           if (!ok) break;
-          ptx::umma_commit(bar(c.empty[v_stage]));
+          commit(c.empty[v_stage]);
           if (t + 1 < it.t1) {
-            if (!have_k && !wait1(c.full[stage], phase)) { ok = false; break; }
-            ptx::umma_commit(bar(c.empty[stage]));
-            if (t + 2 == it.t1) ptx::umma_commit(bar(c.qempty));
+            if (!have_k && !wait(c.full[stage], phase)) { ok = false; break; }
+            commit(c.empty[stage]);
+            if (t + 2 == it.t1) commit(c.qempty);
             next_stage();
           }
         }
       }
       if (!ok) {
         // wait (bounded) for the MMAs already issued before tensor memory is released
-        ptx::umma_commit(bar(c.drain));
+        commit(c.drain);
         const uint64_t t0 = ptx::globaltimer();
         while (!ptx::mbar_try_wait(bar(c.drain), 0) && ptx::globaltimer() - t0 < kWaitLimitNs) {}
+        __syncwarp();
       }
     }
   } else if (warp >= S::kLoadWarp0) {
     // ---------------------------------------------------------------- loads
     if constexpr (kNQ == 2) shrink_registers<80>();
-    constexpr int kPieces = DP / 8, kAtOnce = 32 / kPieces, kWarpKeys = kKeys / 4;   // pieces and rows of an instruction
+    // An instruction copies 128 bytes of 4 rows, 8 lanes each.  Row r's pieces sit at piece ^ r % 8, which for row 4 i + sub
+    // is piece ^ sub ^ 4 (i % 2).
+    constexpr int kWarpKeys = kKeys / 4, kGroups = kWarpKeys / 4, kHalves = DP / 64;
     const int lw = warp - S::kLoadWarp0;
-    const int piece = lane % kPieces, sub = lane / kPieces;
-    const bool in_dim = piece * 8 < p.head_dim;
-    // rows `rows0 + sub + kAtOnce i` of a block of kRowsIn rows: the swizzle is an exclusive or, and kAtOnce a power of two
-    auto place = [&](int rows_in, int row0) {
-      return static_cast<uint32_t>((piece >> 3) * rows_in * 128 + (row0 + sub) * 128 + (((piece & 7) ^ sub) << 4));
+    const int piece = lane & 7, sub = lane >> 3;
+    const int halves = (p.head_dim - piece * 8 + 63) / 64;   // 128-byte blocks of a row that hold a piece of this lane
+    const uint32_t lane_at = static_cast<uint32_t>(sub * 128 + ((piece ^ sub) << 4));
+    auto place = [&](uint32_t block0, int rows_in, int i, int half) {   // of rows 4 i .. 4 i + 3 of a block of `rows_in`
+      return ((block0 + lane_at) ^ static_cast<uint32_t>((i & 1) << 6)) + i * 512 + half * rows_in * 128;
     };
-    const uint32_t kv_at = sbase + S::kOffKV + place(kKeys, lw * kWarpKeys);
+    const uint32_t kv_at = sbase + S::kOffKV + lw * kWarpKeys * 128;
     int stage = 0, old_stage = 0, open = 0;
     uint32_t phase = 0, items = 0, queries = 0, tiles = 0;
     unsigned long long meta = 0;           // per open load 4 bits, the oldest lowest: queries with it, values to look at, item slot
@@ -576,23 +589,26 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
       --open;
       if (m & 2) {                         // this thread's own pieces: what is not finite leaves
         unsigned bad = 0;
-#pragma unroll 4
-        for (int i = 0; i < kWarpKeys / kAtOnce; ++i) {
-          const uint32_t at = ((kv_at + old_stage * S::kTileBytes) ^ (((kAtOnce * i) & 7) << 4)) + kAtOnce * i * 128;
-          uint4* v = reinterpret_cast<uint4*>(smem + (at - sbase));
-          uint4 x = *v;
-          constexpr uint32_t kExp = std::is_same<T, __half>::value ? 0x7C007C00u : 0x7F807F80u;
-          unsigned here = 0;
+#pragma unroll 1
+        for (int i = 0; i < kGroups; ++i) {
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            const uint32_t hit = __vcmpeq2((&x.x)[w] & kExp, kExp);
-            (&x.x)[w] &= ~hit;
-            here |= hit;
+          for (int h = 0; h < kHalves; ++h) {
+            if (h >= halves) continue;
+            uint4* v = reinterpret_cast<uint4*>(smem + (place(kv_at + old_stage * S::kTileBytes, kKeys, i, h) - sbase));
+            uint4 x = *v;
+            constexpr uint32_t kExp = std::is_same<T, __half>::value ? 0x7C007C00u : 0x7F807F80u;
+            unsigned here = 0;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const uint32_t hit = __vcmpeq2((&x.x)[w] & kExp, kExp);
+              (&x.x)[w] &= ~hit;
+              here |= hit;
+            }
+            if (here) *v = x;
+            bad |= here;
           }
-          if (here && in_dim) *v = x;
-          bad |= here;
         }
-        if (bad && in_dim) *const_cast<volatile int*>(&c.item[m >> 2 & 1].bad) = 1;
+        if (bad) *const_cast<volatile int*>(&c.item[m >> 2 & 1].bad) = 1;
       }
       ptx::fence_proxy_async_smem();
       __syncwarp();
@@ -659,12 +675,14 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
           const int packed = it.row0 + r, token = packed / a.group, head = packed - token * a.group;
           const long long off = (it.first + token) * p.q_token + static_cast<long long>(it.kv_head * a.group + head) * p.head_dim;
           const unsigned rows = __ballot_sync(0xFFFFFFFFu, r < it.rows);
-          const uint32_t at = sbase + s * S::kQBytes + place(128, lw * 32);
-#pragma unroll 4
-          for (int i = 0; i < 32 / kAtOnce; ++i) {
-            const long long o = __shfl_sync(0xFFFFFFFFu, off, kAtOnce * i + sub);
-            if (in_dim && (rows >> (kAtOnce * i + sub) & 1))
-              cp_async16((at ^ (((kAtOnce * i) & 7) << 4)) + kAtOnce * i * 128, q + o + piece * 8, 16u);
+          const uint32_t at = sbase + s * S::kQBytes + lw * 32 * 128;
+#pragma unroll 2
+          for (int i = 0; i < 8; ++i) {
+            const long long o = __shfl_sync(0xFFFFFFFFu, off, 4 * i + sub);
+            const bool on = rows >> (4 * i + sub) & 1;
+#pragma unroll
+            for (int h = 0; h < kHalves; ++h)
+              if (on && h < halves) cp_async16(place(at, 128, i, h), q + o + piece * 8 + 64 * h);
           }
         }
       }
@@ -683,11 +701,25 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
           if (!wait_open(c.empty[stage], phase ^ 1)) { ok = false; break; }
           const uint4* base = static_cast<const uint4*>(kv ? p.v_cache : p.k_cache);
           const uint32_t at = kv_at + stage * S::kTileBytes;
-#pragma unroll 8
-          for (int i = 0; i < kWarpKeys / kAtOnce; ++i) {
-            const unsigned o = __shfl_sync(0xFFFFFFFFu, kv ? off_v : off_k, kAtOnce * i + sub);
-            const bool on = rows >> (kAtOnce * i + sub) & 1;   // (a key without a page is zeros)
-            if (in_dim) cp_async16((at ^ (((kAtOnce * i) & 7) << 4)) + kAtOnce * i * 128, base + o + (on ? piece : 0), on ? 16u : 0u);
+          const unsigned off = kv ? off_v : off_k;
+          if (rows == static_cast<unsigned>((1ull << kWarpKeys) - 1)) {
+            const uint4* from = base + piece;
+#pragma unroll
+            for (int i = 0; i < kGroups; ++i) {
+              const uint4* row = from + __shfl_sync(0xFFFFFFFFu, off, 4 * i + sub);
+#pragma unroll
+              for (int h = 0; h < kHalves; ++h)
+                if (h < halves) cp_async16(place(at, kKeys, i, h), row + 8 * h);
+            }
+          } else {                         // a key without a page, or that no row sees, is zeros
+#pragma unroll 2
+            for (int i = 0; i < kGroups; ++i) {
+              const uint4* row = base + __shfl_sync(0xFFFFFFFFu, off, 4 * i + sub);
+              const bool on = rows >> (4 * i + sub) & 1;
+#pragma unroll
+              for (int h = 0; h < kHalves; ++h)
+                if (h < halves) cp_async16(place(at, kKeys, i, h), row + (on ? piece + 8 * h : 0), on ? 16u : 0u);
+            }
           }
           close((kv == 0 && t == it.t0 ? 1u : 0u) | (kv && !full ? 2u : 0u) | static_cast<unsigned>(slot) << 2);
         }
@@ -708,11 +740,10 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
       ++items;
       const Item& it = c.item[slot];
       if (it.b < 0) break;
-      const int r = s * 128 + row, packed = it.row0 + r;
-      const int token = packed / a.group, head = packed - token * a.group;
+      const int r = s * 128 + row;
       const bool live_row = r < it.rows, live_warp = s * 128 + (warp & 3) * 32 < it.rows;
-      const int position = it.position0 + token;
-      const int row_hi = position + 1, row_lo = p.window > 0 ? max(0, position - p.window + 1) : 0;
+      const int row_hi = it.position0 + (it.row0 + r) / a.group + 1;
+      const int row_lo = p.window > 0 ? max(0, row_hi - p.window) : 0;
       float m = -CUDART_INF_F, l = 0.f;
       bool ok = true;
       const int t0 = it.t0, t1 = it.t1, lo = it.lo[s], hi = it.hi[s];
@@ -774,25 +805,31 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
           const float base = lift<T>() - (m == -CUDART_INF_F ? 0.f : m);
           float2 sum[2] = {};
 #pragma unroll
-          for (int i = 0; i < kKeys / 64; ++i) {
-            uint32_t w[32];
+          for (int half = 0; half < 2; ++half) {           // p v of the first half starts while the second is made
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              float u = x[64 * i + 2 * j], v = x[64 * i + 2 * j + 1];
-              fma2(u, v, scale, base);
-              u = ex2(u);
-              v = ex2(v);
-              sum[j & 1] = add2(sum[j & 1], u, v);
-              w[j] = pack2(u, v, T());
+            for (int i = half * kKeys / 64; i < (half + 1) * kKeys / 64; ++i) {
+              uint32_t w[16];
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                float u = x[32 * i + 2 * j], v = x[32 * i + 2 * j + 1];
+                fma2(u, v, scale, base);
+                u = ex2(u);
+                v = ex2(v);
+                sum[j & 1] = add2(sum[j & 1], u, v);
+                w[j] = pack2(u, v, T());
+              }
+              ptx::tmem_st_32x32b_x16(sc + 16 * i, w);
             }
-            ptx::tmem_st_32x32b_x32(sc + 32 * i, w);
+            ptx::tmem_st_wait();
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(bar(c.pready[s][half]));
           }
           l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-          ptx::tmem_st_wait();
+        } else if (lane == 0) {
+          ptx::mbar_arrive(bar(c.pready[s][0]));
+          ptx::mbar_arrive(bar(c.pready[s][1]));
         }
-        ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bar(c.pready[s]));
       }
       if (!ok) break;
       const bool any = hi > lo;
@@ -802,6 +839,7 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
         ptx::tc_fence_after();
       }
       if (live_warp) {
+        const int packed = it.row0 + r, token = packed / a.group, head = packed - token * a.group;
         const long long at = static_cast<long long>(it.first + token) * p.heads + it.kv_head * a.group + head;
         const bool bad = *const_cast<const volatile int*>(&it.bad) != 0;
         const float inv = it.slot >= 0 ? 1.f : (l > 0.f || isnan(l) ? 1.f / l : 0.f);
@@ -815,26 +853,6 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
           } else {
 #pragma unroll
             for (int j = 0; j < 32; ++j) o[j] = 0;
-          }
-          if (bad && live_row) {
-            // values that are not finite, of the keys that this row sees in the tiles not seen by all
-#pragma unroll 1
-            for (int t = t0; t < t1; ++t) {
-              if (t * kKeys >= it.full_lo && (t + 1) * kKeys <= it.full_hi) continue;
-#pragma unroll 1
-              for (int key = max(t * kKeys, row_lo); key < min((t + 1) * kKeys, row_hi); ++key) {
-                const int page = p.table[static_cast<long long>(it.b) * p.table_width + key / p.page_size];
-                if (page < 0 || page >= p.pages) continue;
-                const T* v = static_cast<const T*>(p.v_cache) + page * p.v_page + key % p.page_size * p.v_slot +
-                             it.kv_head * p.v_head + i;
-#pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                  if (i + j >= p.head_dim) continue;
-                  const float f = Tr::to_f32(v[j]);
-                  if (!isfinite(f)) o[j] = __float_as_uint(__uint_as_float(o[j]) + f);
-                }
-              }
-            }
           }
           if (it.slot < 0) {
             if (live_row) {
@@ -858,6 +876,31 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
           if (p.lse && live_row) p.lse[at] = m * 0.693147180559945f + logf(l * (std::is_same<T, __half>::value ? 1.f / 128.f : 1.f));
         } else {
           __stcg(reinterpret_cast<float2*>(part + static_cast<size_t>(S::kRows) * DP) + r, make_float2(any ? m : -CUDART_INF_F, l));
+        }
+        if (bad && live_row) {
+          // values that are not finite, of the keys that this row sees in the tiles not seen by all
+#pragma unroll 1
+          for (int t = t0; t < t1; ++t) {
+            if (t * kKeys >= it.full_lo && (t + 1) * kKeys <= it.full_hi) continue;
+#pragma unroll 1
+            for (int key = max(t * kKeys, row_lo); key < min((t + 1) * kKeys, row_hi); ++key) {
+              const int page = p.table[static_cast<long long>(it.b) * p.table_width + key / p.page_size];
+              if (page < 0 || page >= p.pages) continue;
+              const T* v = static_cast<const T*>(p.v_cache) + page * p.v_page + key % p.page_size * p.v_slot + it.kv_head * p.v_head;
+#pragma unroll 1
+              for (int d = 0; d < p.head_dim; ++d) {
+                const float f = Tr::to_f32(v[d]);
+                if (isfinite(f)) continue;
+                if (it.slot < 0) {
+                  T* to = static_cast<T*>(p.out) + at * p.head_dim + d;
+                  *to = Tr::from_f32(Tr::to_f32(*to) + f);
+                } else {
+                  float* to = part + ((d / 4) * S::kRows + r) * 4 + d % 4;
+                  __stcg(to, __ldcg(to) + f);
+                }
+              }
+            }
+          }
         }
         ptx::tc_fence_before();
       }
