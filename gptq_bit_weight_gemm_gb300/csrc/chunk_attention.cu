@@ -31,6 +31,7 @@
 // Values that some row of the item must not see (later tokens', outside the window) could reach it as 0 x NaN:
 // in the tiles at the diagonal the loader replaces infinite and NaN values by 0, and the rows that do see
 // them get them added at the end.
+#include <cuda.h>
 #include <math_constants.h>
 
 #include <atomic>
@@ -110,6 +111,8 @@ struct Args {
   int negative;            // scale < 0
   unsigned page_mul, page_shift;   // key / page_size = key * page_mul >> page_shift for keys below 2^30
   unsigned k_page16, k_slot16, k_head16, v_page16, v_slot16, v_head16;   // strides in 16-byte units
+  int box_rows;            // keys of a TMA box: 0 where the cache is not read by TMA
+  int box_order[3];        // which coordinate is the box's second, third and fourth: 0 slot, 1 head, 2 page
   Record* records;
   float* partials;
 };
@@ -246,7 +249,7 @@ __device__ __forceinline__ long long head_units(const Args& a, const Sequence& s
 
 // ------------------------------------------------------------------------------ the kernel
 template <typename T, int DP>
-__global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const __grid_constant__ Args a) {
   using S = Shape<DP>;
   using C = Control<DP>;
   using Tr = F16Traits<T>;
@@ -579,15 +582,17 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
       return ((block0 + lane_at) ^ static_cast<uint32_t>((i & 1) << 6)) + i * 512 + half * rows_in * 128;
     };
     const uint32_t kv_at = sbase + S::kOffKV + lw * kWarpKeys * 128;
-    int stage = 0, old_stage = 0, open = 0;
+    int stage = 0, open = 0;
     uint32_t phase = 0, items = 0, queries = 0, tiles = 0;
-    unsigned long long meta = 0;           // per open load 4 bits, the oldest lowest: queries with it, values to look at, item slot
+    unsigned long long meta = 0;           // of each open copy a byte, the oldest lowest: kLook, kQueries, the item's slot, the stage
+    constexpr unsigned kLook = 1, kQueries = 2, kSlot = 4;
     bool ok = true;
-    auto finish = [&]() {                  // the oldest open load has landed (the caller has waited)
-      const unsigned m = meta & 15;
-      meta >>= 4;
+    auto finish = [&]() {                  // the oldest open copy has landed (the caller has waited)
+      const unsigned m = meta & 255;
+      const int old_stage = m >> 3;
+      meta >>= 8;
       --open;
-      if (m & 2) {                         // this thread's own pieces: what is not finite leaves
+      if (m & kLook) {                     // this thread's own pieces: what is not finite leaves
         unsigned bad = 0;
 #pragma unroll 1
         for (int i = 0; i < kGroups; ++i) {
@@ -608,17 +613,13 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
             bad |= here;
           }
         }
-        if (bad) *const_cast<volatile int*>(&c.item[m >> 2 & 1].bad) = 1;
+        if (bad) *const_cast<volatile int*>(&c.item[m & kSlot ? 1 : 0].bad) = 1;
       }
       ptx::fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) {
-        ptx::mbar_arrive(bar(c.full[old_stage]));
-        if (m & 1) ptx::mbar_arrive(bar(c.qfull));
-      }
-      if (++old_stage == S::kStages) old_stage = 0;
+      if (lane == 0) ptx::mbar_arrive(m & kQueries ? bar(c.qfull) : bar(c.full[old_stage]));
     };
-    auto oldest = [&]() {                  // waits for the oldest open load and hands it on
+    auto oldest = [&]() {                  // waits for the oldest open copy and hands it on
       if (open > 5) cp_wait<5>();
       else if (open == 5) cp_wait<4>();
       else if (open == 4) cp_wait<3>();
@@ -627,7 +628,7 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
       else cp_wait<0>();
       finish();
     };
-    // A wait in which open loads are handed on as they land: who releases the barrier may be waiting for them.
+    // A wait in which open copies are handed on as they land: who releases the barrier may be waiting for them.
     auto wait_open = [&](unsigned long long& b, uint32_t parity) {
       while (open) {
         if (__all_sync(0xFFFFFFFFu, ptx::mbar_try_wait(bar(b), parity))) return true;
@@ -635,16 +636,18 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
       }
       return wait(b, parity);
     };
-    auto close = [&](unsigned m) {         // of a load whose copies have been issued
+    auto close = [&](unsigned m) {         // of a copy that has been issued
       cp_commit();
-      meta |= static_cast<unsigned long long>(m) << (4 * open);
+      meta |= static_cast<unsigned long long>(m) << (8 * open);
       ++open;
-      if (++stage == S::kStages) stage = 0, phase ^= 1;
       if (open > S::kAhead) oldest();
     };
+    const int blocks = (p.head_dim + 63) / 64;
+    uint32_t boxed = 0, boxed_phase = 0;   // stages that boxes were sent to, and in which phase
+    const bool boxes = a.box_rows > 0 && lane < kWarpKeys && lane % max(a.box_rows, 1) == 0;   // this lane's key begins a box
     while (ok) {
       const int slot = items & 1;
-      if (!wait_open(c.ifull[slot], (items >> 1) & 1)) break;
+      if (!wait_open(c.ifull[slot], (items >> 1) & 1)) { ok = false; break; }
       ++items;
       const Item it = c.item[slot];
       __syncwarp();
@@ -664,7 +667,7 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
         page = want ? __ldg(table + entry) : -1;
       };
       fetch(it.t0);
-      if (!wait_open(c.qempty, (queries & 1) ^ 1)) break;
+      if (!wait_open(c.qempty, (queries & 1) ^ 1)) { ok = false; break; }
       ++queries;
       {                                    // queries: row r of the item is token r / group, head r % group
         const T* q = static_cast<const T*>(p.q);
@@ -685,13 +688,14 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
               if (on && h < halves) cp_async16(place(at, 128, i, h), q + o + piece * 8 + 64 * h);
           }
         }
+        close(kQueries);
       }
       for (int t = it.t0; ok && t < it.t1; ++t, ++tiles) {
         const bool good = want && page >= 0 && page < p.pages;
         if (want && !good) atomicOr(p.status, kStatusPageRange);
         const unsigned rows = __ballot_sync(0xFFFFFFFFu, good), unread = __ballot_sync(0xFFFFFFFFu, want && !good);
         if (lane == 0) c.valid[tiles & 15][lw] = ~unread;
-        const int place_in = key - entry * p.page_size;
+        const int place_in = key - entry * p.page_size, now = page;
         const unsigned off_k = good ? page * a.k_page16 + place_in * a.k_slot16 + it.kv_head * a.k_head16 : 0u;
         const unsigned off_v = good ? page * a.v_page16 + place_in * a.v_slot16 + it.kv_head * a.v_head16 : 0u;
         if (t + 1 < it.t1) fetch(t + 1);
@@ -702,7 +706,21 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
           const uint4* base = static_cast<const uint4*>(kv ? p.v_cache : p.k_cache);
           const uint32_t at = kv_at + stage * S::kTileBytes;
           const unsigned off = kv ? off_v : off_k;
-          if (rows == static_cast<unsigned>((1ull << kWarpKeys) - 1)) {
+          const bool all = rows == static_cast<unsigned>((1ull << kWarpKeys) - 1), look = kv && !full;
+          if (a.box_rows && all && !look) {
+            if (lane == 0) ptx::mbar_arrive_expect_tx(bar(c.full[stage]), kWarpKeys * 128 * blocks);
+            boxed |= 1u << stage;
+            boxed_phase = (boxed_phase & ~(1u << stage)) | phase << stage;
+            __syncwarp();
+            if (boxes) {
+              auto coordinate = [&](int which) { return which == 0 ? place_in : (which == 1 ? it.kv_head : now); };
+              const int y = coordinate(a.box_order[0]), z = coordinate(a.box_order[1]), w = coordinate(a.box_order[2]);
+#pragma unroll
+              for (int h = 0; h < kHalves; ++h)
+                if (h < blocks)
+                  ptx::tma_load_4d(at + lane * 128 + h * kKeys * 128, kv ? &map_v : &map_k, 64 * h, y, z, w, bar(c.full[stage]));
+            }
+          } else if (all) {
             const uint4* from = base + piece;
 #pragma unroll
             for (int i = 0; i < kGroups; ++i) {
@@ -721,11 +739,20 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
                 if (h < halves) cp_async16(place(at, kKeys, i, h), row + (on ? piece + 8 * h : 0), on ? 16u : 0u);
             }
           }
-          close((kv == 0 && t == it.t0 ? 1u : 0u) | (kv && !full ? 2u : 0u) | static_cast<unsigned>(slot) << 2);
+          if (!(a.box_rows && all && !look)) close((look ? kLook : 0u) | (slot ? kSlot : 0u) | static_cast<unsigned>(stage) << 3);
+          if (++stage == S::kStages) stage = 0, phase ^= 1;
         }
       }
     }
-    cp_wait<0>();                          // (where a wait was given up: nothing lands after the CTA)
+    if (!ok) {
+      // nothing may land after the CTA: wait (bounded) for the copies already issued
+      cp_wait<0>();
+      const uint64_t t0 = ptx::globaltimer();
+      for (int i = 0; i < S::kStages; ++i)
+        if (boxed >> i & 1)
+          while (!ptx::mbar_try_wait(bar(c.full[i]), boxed_phase >> i & 1) && ptx::globaltimer() - t0 < kWaitLimitNs) {}
+      __syncwarp();
+    }
   } else {
     // ---------------------------------------------------------------- softmax: a thread a row
     if constexpr (kNQ == 2) grow_registers<176>();
@@ -966,8 +993,41 @@ __global__ void __launch_bounds__(Shape<DP>::kRows) k_join(const __grid_constant
 }
 
 // ------------------------------------------------------------------------------ host side
+// The tensor map of a cache [slot, head, page, dimension], its dimensions in the order of their strides.
+bool cache_map(const ChunkProblem& p, const void* cache, long long slot, long long head, long long page, int box_rows,
+               int* order, CUtensorMap* map) {
+  const uint64_t size[3] = {static_cast<uint64_t>(p.page_size), static_cast<uint64_t>(p.kv_heads), static_cast<uint64_t>(p.pages)};
+  uint64_t stride[3] = {static_cast<uint64_t>(slot) * 2, static_cast<uint64_t>(head) * 2, static_cast<uint64_t>(page) * 2};
+  const uint32_t rows[3] = {static_cast<uint32_t>(box_rows), 1, 1};
+  uint64_t longest = static_cast<uint64_t>(p.head_dim) * 2;
+  for (int i = 0; i < 3; ++i) {
+    if (size[i] > 1 && stride[i] == 0) return false;
+    if (stride[i] > longest) longest = stride[i];
+  }
+  for (int i = 0; i < 3; ++i) {
+    if (size[i] == 1) stride[i] = longest;                 // never stepped over
+    order[i] = i;
+  }
+  for (int i = 0; i < 2; ++i)
+    for (int j = 0; j < 2 - i; ++j)
+      if (stride[order[j]] > stride[order[j + 1]]) {
+        const int x = order[j];
+        order[j] = order[j + 1];
+        order[j + 1] = x;
+      }
+  uint64_t dims[4] = {static_cast<uint64_t>(p.head_dim)}, strides[3];
+  uint32_t box[4] = {64}, step[4] = {1, 1, 1, 1};
+  for (int i = 0; i < 3; ++i) {
+    dims[i + 1] = size[order[i]];
+    strides[i] = stride[order[i]];
+    box[i + 1] = rows[order[i]];
+  }
+  return encode_tensor_map_nd(map, p.dtype == 0 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                              const_cast<void*>(cache), dims, strides, box, step, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
 template <typename T, int DP>
-cudaError_t launch(const Args& a, cudaStream_t stream) {
+cudaError_t launch(const Args& args, cudaStream_t stream) {
   using S = Shape<DP>;
   constexpr size_t kSmem = S::kOffControl + sizeof(Control<DP>) + 1024;
   static_assert(kSmem <= 232448, "the layout must fit one CTA's shared memory (227 KB)");
@@ -990,7 +1050,20 @@ cudaError_t launch(const Args& a, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a);
+  Args a = args;
+  CUtensorMap map_k = {}, map_v = {};
+  // The cache as boxes of consecutive keys of one page and head, 64 dimensions wide: the most keys, a power of two from
+  // 8 (whole swizzle atoms) to a loader warp's share, that divide a page.  Other pages, and strides that a tensor map
+  // does not take, are copied by cp.async.
+  int box = a.p.page_size & -a.p.page_size;
+  if (box > S::kKeys / 4) box = S::kKeys / 4;
+  if (box >= 8 && cache_map(a.p, a.p.k_cache, a.p.k_slot, a.p.k_head, a.p.k_page, box, a.box_order, &map_k)) {
+    int order[3];
+    if (cache_map(a.p, a.p.v_cache, a.p.v_slot, a.p.v_head, a.p.v_page, box, order, &map_v) &&
+        order[0] == a.box_order[0] && order[1] == a.box_order[1] && order[2] == a.box_order[2])
+      a.box_rows = box;
+  }
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, map_k, map_v, a);
   if (e != cudaSuccess) return e;
   cfg.gridDim = dim3(grid, DP / kJoinCols);
   cfg.blockDim = dim3(S::kRows);
@@ -1014,7 +1087,7 @@ size_t chunk_attention_workspace_bytes(int, int, int head_dim) {
 }
 
 cudaError_t launch_chunk_attention(const ChunkProblem& p, cudaStream_t stream) {
-  chunk::Args a;
+  chunk::Args a = {};
   a.p = p;
   a.group = p.heads / p.kv_heads;
   a.negative = p.scale < 0.f;
