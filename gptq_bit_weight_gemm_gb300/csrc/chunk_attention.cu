@@ -113,6 +113,7 @@ struct Args {
   unsigned k_page16, k_slot16, k_head16, v_page16, v_slot16, v_head16;   // strides in 16-byte units
   int box_rows;            // keys of a TMA box: 0 where the cache is not read by TMA
   int box_order[3];        // which coordinate is the box's second, third and fourth: 0 slot, 1 head, 2 page
+  int q_boxes;             // queries come as boxes of 128 / group tokens with the heads of a group
   Record* records;
   float* partials;
 };
@@ -249,7 +250,8 @@ __device__ __forceinline__ long long head_units(const Args& a, const Sequence& s
 
 // ------------------------------------------------------------------------------ the kernel
 template <typename T, int DP>
-__global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                                                              const __grid_constant__ CUtensorMap map_q, const __grid_constant__ Args a) {
   using S = Shape<DP>;
   using C = Control<DP>;
   using Tr = F16Traits<T>;
@@ -643,7 +645,7 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
       if (open > S::kAhead) oldest();
     };
     const int blocks = (p.head_dim + 63) / 64;
-    uint32_t boxed = 0, boxed_phase = 0;   // stages that boxes were sent to, and in which phase
+    uint32_t boxed = 0, boxed_phase = 0, q_sent = 0;   // stages that boxes were sent to, and in which phase; queries too
     const bool boxes = a.box_rows > 0 && lane < kWarpKeys && lane % max(a.box_rows, 1) == 0;   // this lane's key begins a box
     while (ok) {
       const int slot = items & 1;
@@ -667,9 +669,23 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
         page = want ? __ldg(table + entry) : -1;
       };
       fetch(it.t0);
-      if (!wait_open(c.qempty, (queries & 1) ^ 1)) { ok = false; break; }
-      ++queries;
-      {                                    // queries: row r of the item is token r / group, head r % group
+      auto queries_of = [&]() {            // row r of the item is token r / group, head r % group
+        if (!wait_open(c.qempty, (queries & 1) ^ 1)) return false;
+        ++queries;
+        if (a.q_boxes) {
+          const bool mine = lw == 0 ? it.lo[0] < it.hi[0] : lw < kNQ && it.lo[1] < it.hi[1];
+          if (mine && lane == 0) {
+            const uint32_t at = sbase + lw * S::kQBytes;
+            q_sent |= 1;
+            ptx::mbar_arrive_expect_tx(bar(c.qfull), 128 * 128 * blocks);
+            for (int h = 0; h < blocks; ++h)
+              ptx::tma_load_4d(at + h * 128 * 128, &map_q, 64 * h, 0, it.kv_head, it.first + (it.row0 + lw * 128) / a.group, bar(c.qfull));
+          } else if (lane == 0) {
+            ptx::mbar_arrive(bar(c.qfull));
+          }
+          __syncwarp();
+          return true;
+        }
         const T* q = static_cast<const T*>(p.q);
 #pragma unroll
         for (int s = 0; s < kNQ; ++s) {
@@ -689,7 +705,8 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
           }
         }
         close(kQueries);
-      }
+        return true;
+      };
       for (int t = it.t0; ok && t < it.t1; ++t, ++tiles) {
         const bool good = want && page >= 0 && page < p.pages;
         if (want && !good) atomicOr(p.status, kStatusPageRange);
@@ -742,6 +759,8 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
           if (!(a.box_rows && all && !look)) close((look ? kLook : 0u) | (slot ? kSlot : 0u) | static_cast<unsigned>(stage) << 3);
           if (++stage == S::kStages) stage = 0, phase ^= 1;
         }
+        // the queries' place is free once the item before has its last scores: the first tile need not wait for that
+        if (ok && t == it.t0) ok = queries_of();
       }
     }
     if (!ok) {
@@ -751,6 +770,8 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
       for (int i = 0; i < S::kStages; ++i)
         if (boxed >> i & 1)
           while (!ptx::mbar_try_wait(bar(c.full[i]), boxed_phase >> i & 1) && ptx::globaltimer() - t0 < kWaitLimitNs) {}
+      if (q_sent)
+        while (!ptx::mbar_try_wait(bar(c.qfull), (queries & 1) ^ 1) && ptx::globaltimer() - t0 < kWaitLimitNs) {}
       __syncwarp();
     }
   } else {
@@ -1051,7 +1072,7 @@ cudaError_t launch(const Args& args, cudaStream_t stream) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   Args a = args;
-  CUtensorMap map_k = {}, map_v = {};
+  CUtensorMap map_k = {}, map_v = {}, map_q = {};
   // The cache as boxes of consecutive keys of one page and head, 64 dimensions wide: the most keys, a power of two from
   // 8 (whole swizzle atoms) to a loader warp's share, that divide a page.  Other pages, and strides that a tensor map
   // does not take, are copied by cp.async.
@@ -1063,7 +1084,20 @@ cudaError_t launch(const Args& args, cudaStream_t stream) {
         order[0] == a.box_order[0] && order[1] == a.box_order[1] && order[2] == a.box_order[2])
       a.box_rows = box;
   }
-  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, map_k, map_v, a);
+  // A block's 128 packed rows are whole tokens where the group divides it.  (The tail of a sequence's last block reads the
+  // next sequence's rows, or zeros: rows that nobody looks at.)
+  if (128 % a.group == 0) {
+    const uint64_t dims[4] = {static_cast<uint64_t>(a.p.head_dim), static_cast<uint64_t>(a.group),
+                              static_cast<uint64_t>(a.p.kv_heads), static_cast<uint64_t>(a.p.tokens)};
+    const uint64_t row = static_cast<uint64_t>(a.p.head_dim) * 2;
+    const uint64_t strides[3] = {row, row * a.group,
+                                 a.p.tokens > 1 ? static_cast<uint64_t>(a.p.q_token) * 2 : row * a.p.heads};
+    const uint32_t boxes[4] = {64, static_cast<uint32_t>(a.group), 1, static_cast<uint32_t>(128 / a.group)}, step[4] = {1, 1, 1, 1};
+    a.q_boxes = strides[2] > 0 &&
+                encode_tensor_map_nd(&map_q, a.p.dtype == 0 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                                     const_cast<void*>(a.p.q), dims, strides, boxes, step, CU_TENSOR_MAP_SWIZZLE_128B);
+  }
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, map_k, map_v, map_q, a);
   if (e != cudaSuccess) return e;
   cfg.gridDim = dim3(grid, DP / kJoinCols);
   cfg.blockDim = dim3(S::kRows);
