@@ -66,7 +66,7 @@ struct Shape {
   static constexpr int kStages = DP == 64 ? 8 : 5;         // tiles of keys or values in flight
   static constexpr int kAhead = kStages - 2;               // loads left open behind the last one issued (6 at most)
   static constexpr int kThreads = (kNQ + 2) * 128;
-  static constexpr int kLoadWarp0 = kNQ * 4, kMmaWarp = kLoadWarp0 + 4, kWalkWarp = kMmaWarp + 1;
+  static constexpr int kLoadWarp0 = kNQ * 4, kMmaWarp = kLoadWarp0 + 4, kWalkWarp = kMmaWarp + 1, kLookWarp0 = kMmaWarp + 2;
   static constexpr uint32_t kQBytes = 128 * DP * 2;        // queries of one accumulator
   static constexpr uint32_t kTileBytes = kKeys * DP * 2;
   static constexpr uint32_t kOffKV = kNQ * kQBytes;
@@ -89,7 +89,7 @@ struct Item {
 
 template <int DP>
 struct Control {
-  unsigned long long full[Shape<DP>::kStages], empty[Shape<DP>::kStages];
+  unsigned long long full[Shape<DP>::kStages], empty[Shape<DP>::kStages], raw[Shape<DP>::kStages];
   unsigned long long qfull, qempty, sfull[2], pready[2][2], ofull[2], ifull[2], iempty[2], drain;
   uint32_t valid[16][4];   // per tile: keys whose page could be read
   Item item[2];
@@ -138,6 +138,11 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {   // (of a NaN and numbers, the numbers)
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 // x * s + c of two values at a time
 __device__ __forceinline__ void fma2(float& a, float& b, float s, float c) {
@@ -323,7 +328,7 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
   // ---- set up
   if (threadIdx.x == 0) {
     auto init = [&](unsigned long long& bar, int count) { ptx::mbar_init(ptx::smem_addr(&bar), count); };
-    for (int i = 0; i < S::kStages; ++i) init(c.full[i], 4), init(c.empty[i], 1);
+    for (int i = 0; i < S::kStages; ++i) init(c.full[i], 4), init(c.empty[i], 1), init(c.raw[i], 4);
     init(c.qfull, 4);
     init(c.qempty, 1);
     for (int i = 0; i < 2; ++i) {
@@ -332,7 +337,7 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
       init(c.pready[i][1], 4);
       init(c.ofull[i], 1);
       init(c.ifull[i], 1);
-      init(c.iempty[i], 4 * kNQ + 5);      // softmax and loader warps, the MMA thread
+      init(c.iempty[i], 4 * kNQ + 7);      // softmax, loader and look warps, the MMA warp
     }
     init(c.drain, 1);
     c.abort = 0;
@@ -469,7 +474,8 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
       // -------------------------------------------------------------- MMAs
       const int kd = (p.head_dim + 15) / 16;
       constexpr uint32_t type = std::is_same<T, __half>::value ? 0u : 1u;
-      constexpr uint32_t idesc_s = ptx::umma_idesc_f16(type, 128u, kKeys);
+      // a negative scale is that of -q
+      const uint32_t idesc_s = ptx::umma_idesc_f16(type, 128u, kKeys) | (a.negative ? ptx::kUmmaNegateA : 0u);
       const uint32_t idesc_o = ptx::umma_idesc_f16(type, 128u, kd * 16u) | ptx::kUmmaBMajorMN;
       const uint32_t leader = ptx::elect_one();
       auto commit = [&](unsigned long long& b) { ptx::umma_commit_by(leader, bar(b)); };
@@ -569,6 +575,64 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
         while (!ptx::mbar_try_wait(bar(c.drain), 0) && ptx::globaltimer() - t0 < kWaitLimitNs) {}
         __syncwarp();
       }
+    } else if (warp >= S::kLookWarp0) {
+      // -------------------------------------------------------------- values that not every row sees
+      // Those of a key that no row sees leave, and so does what is not finite; then the tile is the MMA's.
+      int stage = 0;
+      uint32_t items = 0, raw_phase = 0;
+      bool ok = true;
+      while (ok) {
+        const int slot = items & 1;
+        if (!wait(c.ifull[slot], (items >> 1) & 1)) break;
+        ++items;
+        const Item& from = c.item[slot];
+        const struct { int b, key_lo, key_hi, t0, t1, full_lo, full_hi; } it = {from.b, from.key_lo, from.key_hi, from.t0, from.t1,
+                                                                               from.full_lo, from.full_hi};
+        if (it.b < 0) break;
+        for (int t = it.t0; ok && t < it.t1; ++t) {
+          if (++stage == S::kStages) stage = 0;            // past the keys
+          const bool full = t * kKeys >= it.full_lo && (t + 1) * kKeys <= it.full_hi;
+          if (a.box_rows && !full) {
+            if (!wait(c.raw[stage], raw_phase >> stage & 1)) { ok = false; break; }
+            raw_phase ^= 1u << stage;
+            unsigned bad = 0;
+            // 16 bytes a lane, as they lie: a row's pieces are swizzled within its 128 bytes
+            const int pieces = kKeys * ((p.head_dim + 63) / 64) / 8;
+            unsigned char* tile = smem + S::kOffKV + stage * S::kTileBytes;
+#pragma unroll 4
+            for (int i = 0; i < pieces; ++i) {
+              const int at = (i * 64 + (warp - S::kLookWarp0) * 32 + lane) * 16;
+              const int key = t * kKeys + at / 128 % kKeys;
+              uint4* v = reinterpret_cast<uint4*>(tile + at);
+              uint4 x = *v;
+              constexpr uint32_t kExp = std::is_same<T, __half>::value ? 0x7C007C00u : 0x7F807F80u;
+              unsigned here = 0;
+#pragma unroll
+              for (int w = 0; w < 4; ++w) {
+                const uint32_t hit = __vcmpeq2((&x.x)[w] & kExp, kExp);
+                (&x.x)[w] &= ~hit;
+                here |= hit;
+              }
+              if (key < it.key_lo || key >= it.key_hi) {
+                *v = make_uint4(0u, 0u, 0u, 0u);
+              } else if (here) {
+                *v = x;
+                bad = 1;
+              }
+            }
+            if (bad) *const_cast<volatile int*>(&c.item[slot].bad) = 1;
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              ptx::mbar_arrive(bar(c.full[stage]));
+              ptx::mbar_arrive(bar(c.full[stage]));
+            }
+          }
+          if (++stage == S::kStages) stage = 0;
+        }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(c.iempty[slot]));
+      }
     }
   } else if (warp >= S::kLoadWarp0) {
     // ---------------------------------------------------------------- loads
@@ -645,7 +709,7 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
       if (open > S::kAhead) oldest();
     };
     const int blocks = (p.head_dim + 63) / 64;
-    uint32_t boxed = 0, boxed_phase = 0, q_sent = 0;   // stages that boxes were sent to, and in which phase; queries too
+    uint32_t boxed = 0, boxed_phase = 0, looked = 0, raw_phase = ~0u, q_sent = 0;   // stages that boxes were sent to, in which phase, to whom; queries too
     const bool boxes = a.box_rows > 0 && lane < kWarpKeys && lane % max(a.box_rows, 1) == 0;   // this lane's key begins a box
     while (ok) {
       const int slot = items & 1;
@@ -715,6 +779,11 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
         const int place_in = key - entry * p.page_size, now = page;
         const unsigned off_k = good ? page * a.k_page16 + place_in * a.k_slot16 + it.kv_head * a.k_head16 : 0u;
         const unsigned off_v = good ? page * a.v_page16 + place_in * a.v_slot16 + it.kv_head * a.v_head16 : 0u;
+        // the page of the box that begins at this lane's key: that of any of its keys.  One without a page, or without a key
+        // that some row sees, is zeros: a coordinate past the cache
+        const unsigned in_box = rows >> lane & ((2u << (a.box_rows - 1 & 31)) - 1u);
+        const int some_page = __shfl_sync(0xFFFFFFFFu, now, in_box ? lane + __ffs(in_box) - 1 : lane);
+        const int box_page = in_box ? some_page : p.pages;
         if (t + 1 < it.t1) fetch(t + 1);
         const bool full = t * kKeys >= it.full_lo && (t + 1) * kKeys <= it.full_hi;
 #pragma unroll
@@ -724,18 +793,21 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
           const uint32_t at = kv_at + stage * S::kTileBytes;
           const unsigned off = kv ? off_v : off_k;
           const bool all = rows == static_cast<unsigned>((1ull << kWarpKeys) - 1), look = kv && !full;
-          if (a.box_rows && all && !look) {
-            if (lane == 0) ptx::mbar_arrive_expect_tx(bar(c.full[stage]), kWarpKeys * 128 * blocks);
+          if (a.box_rows) {
+            // values that not every row sees pass the look warps before the MMA
+            const uint32_t to = look ? bar(c.raw[stage]) : bar(c.full[stage]);
+            if (lane == 0) ptx::mbar_arrive_expect_tx(to, kWarpKeys * 128 * blocks);
             boxed |= 1u << stage;
             boxed_phase = (boxed_phase & ~(1u << stage)) | phase << stage;
+            looked = (looked & ~(1u << stage)) | (look ? 1u << stage : 0u);
+            if (look) raw_phase ^= 1u << stage;
             __syncwarp();
             if (boxes) {
-              auto coordinate = [&](int which) { return which == 0 ? place_in : (which == 1 ? it.kv_head : now); };
+              auto coordinate = [&](int which) { return which == 0 ? place_in : (which == 1 ? it.kv_head : box_page); };
               const int y = coordinate(a.box_order[0]), z = coordinate(a.box_order[1]), w = coordinate(a.box_order[2]);
 #pragma unroll
               for (int h = 0; h < kHalves; ++h)
-                if (h < blocks)
-                  ptx::tma_load_4d(at + lane * 128 + h * kKeys * 128, kv ? &map_v : &map_k, 64 * h, y, z, w, bar(c.full[stage]));
+                if (h < blocks) ptx::tma_load_4d(at + lane * 128 + h * kKeys * 128, kv ? &map_v : &map_k, 64 * h, y, z, w, to);
             }
           } else if (all) {
             const uint4* from = base + piece;
@@ -756,7 +828,7 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
                 if (h < halves) cp_async16(place(at, kKeys, i, h), row + (on ? piece + 8 * h : 0), on ? 16u : 0u);
             }
           }
-          if (!(a.box_rows && all && !look)) close((look ? kLook : 0u) | (slot ? kSlot : 0u) | static_cast<unsigned>(stage) << 3);
+          if (!a.box_rows) close((look ? kLook : 0u) | (slot ? kSlot : 0u) | static_cast<unsigned>(stage) << 3);
           if (++stage == S::kStages) stage = 0, phase ^= 1;
         }
         // the queries' place is free once the item before has its last scores: the first tile need not wait for that
@@ -769,7 +841,9 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
       const uint64_t t0 = ptx::globaltimer();
       for (int i = 0; i < S::kStages; ++i)
         if (boxed >> i & 1)
-          while (!ptx::mbar_try_wait(bar(c.full[i]), boxed_phase >> i & 1) && ptx::globaltimer() - t0 < kWaitLimitNs) {}
+          while (!ptx::mbar_try_wait(looked >> i & 1 ? bar(c.raw[i]) : bar(c.full[i]),
+                                     looked >> i & 1 ? raw_phase >> i & 1 : boxed_phase >> i & 1) &&
+                 ptx::globaltimer() - t0 < kWaitLimitNs) {}
       if (q_sent)
         while (!ptx::mbar_try_wait(bar(c.qfull), (queries & 1) ^ 1) && ptx::globaltimer() - t0 < kWaitLimitNs) {}
       __syncwarp();
@@ -805,10 +879,6 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
 #pragma unroll
           for (int i = 0; i < kKeys / 32; ++i) ptx::tmem_ld_32x32b_x32(sc + 32 * i, *reinterpret_cast<uint32_t(*)[32]>(x + 32 * i));
           ptx::tmem_ld_wait();
-          if (a.negative) {
-#pragma unroll
-            for (int i = 0; i < kKeys; ++i) x[i] = -x[i];
-          }
           // keys that the row does not see
           const int key0 = t * kKeys;
           if (__any_sync(0xFFFFFFFFu, key0 < row_lo || key0 + kKeys > row_hi)) {
@@ -828,7 +898,7 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
 #pragma unroll
           for (int i = 4; i + 8 <= kKeys; i += 8)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) top[j] = fmaxf(fmaxf(top[j], x[i + 2 * j]), x[i + 2 * j + 1]);
+            for (int j = 0; j < 4; ++j) top[j] = max3(top[j], x[i + 2 * j], x[i + 2 * j + 1]);
 #pragma unroll
           for (int j = 0; j < 4; ++j) top[j] = fmaxf(top[j], x[kKeys - 4 + j]);
           const float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;

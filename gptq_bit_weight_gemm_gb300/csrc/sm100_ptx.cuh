@@ -297,7 +297,8 @@ __device__ __forceinline__ uint64_t umma_desc_sw128_mnmajor(uint32_t smem_byte_a
   d |= static_cast<uint64_t>(2u) << 61;
   return d;
 }
-constexpr uint32_t kUmmaBMajorMN = 1u << 16;   // in the instruction descriptor
+// In the instruction descriptor: B is MN-major; A is taken negative.
+constexpr uint32_t kUmmaBMajorMN = 1u << 16, kUmmaNegateA = 1u << 13;
 
 // Instruction descriptor, kind::f16: fp32 accumulator, A and B of the same 16-bit type
 // (0 = f16, 1 = bf16), both K-major, shape M x N.  Fields: [4,6) D format (1 = f32),
