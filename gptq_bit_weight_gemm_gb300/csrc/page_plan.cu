@@ -5,6 +5,10 @@
 // saturate there: sums of numbers cut to a limit do not depend on the order either.
 //
 // Bound: latency.  The data are a few bytes a token; the chain is launch - lengths - sums - free list - table.
+//
+// One cluster of CTAs: each makes the same sums for itself and takes a share of the pages and rows, found back by
+// bisection in the sums.  Two cluster barriers order the steps: pages given back before pages taken (the same
+// places of the list), and all reading of the inputs before what may be written over them.
 #include <limits.h>
 
 #include <atomic>
@@ -16,9 +20,18 @@
 namespace gptq {
 namespace plan {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kThreads = 512, kWarps = kThreads / 32, kCtas = 8, kAll = kThreads * kCtas;
 
 __device__ __forceinline__ unsigned add_sat(unsigned a, unsigned b) { return min(a + b, static_cast<unsigned>(INT_MAX)); }
+__device__ __forceinline__ unsigned cluster_rank() {
+  unsigned r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// with release and acquire: global memory written before it is seen after it
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 
 // What becomes of a sequence: tokens before and after (after = -1: it would be longer than the table), new rows.
 struct Change {
@@ -36,7 +49,7 @@ __device__ __forceinline__ Change change_of(int cached, int added, int most, boo
   return c;
 }
 
-__global__ void __launch_bounds__(kThreads) k_plan(const PlanProblem p) {
+__global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads) k_plan(const PlanProblem p) {
   extern __shared__ int sm[];
   int* const before = sm;                       // per sequence: Change, then rows, pages given and taken before it
   int* const after = before + p.batch;
@@ -46,20 +59,23 @@ __global__ void __launch_bounds__(kThreads) k_plan(const PlanProblem p) {
   __shared__ unsigned warp_sum[3][kWarps];
   __shared__ int granted;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = cluster_rank(), all = rank * kThreads + tid;   // this thread among the cluster's
   decode::pdl_launch_dependents();
   decode::pdl_wait();
   const int most = p.table_width * p.page_size;
   auto pages_of = [&](int n) { return static_cast<int>((static_cast<unsigned>(n) + p.page_size - 1) / p.page_size); };
 
   // ---- the sums
+  const int count_in = *p.free_count, count = min(max(count_in, 0), p.free_capacity);
   unsigned total[3] = {0, 0, 0};
+  if (tid == 0) granted = 0;
   for (int b0 = 0; b0 < p.batch; b0 += kThreads) {
     const int b = b0 + tid;
     unsigned own[3] = {0, 0, 0}, sum[3];
     if (b < p.batch) {
       bool cut;
       const Change c = change_of(p.cached[b], p.added[b], most, &cut);
-      if (cut) atomicOr(p.status, kStatusSeqLen);
+      if (cut && rank == 0) atomicOr(p.status, kStatusSeqLen);
       before[b] = c.before;
       after[b] = c.after;
       const int have = pages_of(c.before), need = c.after < 0 ? have : pages_of(c.after);
@@ -83,12 +99,15 @@ __global__ void __launch_bounds__(kThreads) k_plan(const PlanProblem p) {
     __syncthreads();
 #pragma unroll
     for (int x = 0; x < 3; ++x) {
-      unsigned base = total[x];
-      for (int w = 0; w < kWarps; ++w) {
-        if (w == warp) sum[x] = add_sat(sum[x], base);
-        base = add_sat(base, warp_sum[x][w]);
+      unsigned v = lane < kWarps ? warp_sum[x][lane] : 0;
+#pragma unroll
+      for (int o = 1; o < kWarps; o <<= 1) {
+        const unsigned u = __shfl_up_sync(0xFFFFFFFFu, v, o);
+        if (lane >= o) v = add_sat(v, u);
       }
-      total[x] = base;
+      const unsigned base = __shfl_sync(0xFFFFFFFFu, v, max(warp - 1, 0));
+      sum[x] = add_sat(sum[x], add_sat(total[x], warp ? base : 0));
+      total[x] = add_sat(total[x], __shfl_sync(0xFFFFFFFFu, v, kWarps - 1));
     }
     if (b < p.batch) {
       row0[b] = sum[0];
@@ -98,11 +117,25 @@ __global__ void __launch_bounds__(kThreads) k_plan(const PlanProblem p) {
     __syncthreads();
   }
   const int rows = min(static_cast<int>(total[0]), p.max_tokens);
-  if (tid == 0 && static_cast<int>(total[0]) > p.max_tokens) atomicOr(p.status, kStatusTokenRows);
-  const int count_in = *p.free_count, count = min(max(count_in, 0), p.free_capacity);
   const int given = min(static_cast<int>(total[1]), p.free_capacity - count), avail = count + given;
-  if (tid == 0 && (count != count_in || given != static_cast<int>(total[1]))) atomicOr(p.status, kStatusNoPage);
-  // the last sequence whose index among items that start at first[] is not after x
+  if (all == 0) {
+    if (static_cast<int>(total[0]) > p.max_tokens) atomicOr(p.status, kStatusTokenRows);
+    if (count != count_in || given != static_cast<int>(total[1])) atomicOr(p.status, kStatusNoPage);
+  }
+  // ---- which sequences get their pages: all of them or none, while the list lasts
+  for (int b = tid; b < p.batch; b += kThreads) {
+    const int take = after[b] < 0 ? 0 : max(pages_of(after[b]) - pages_of(before[b]), 0);
+    if (take > 0) {
+      if (take > avail - take0[b]) {
+        if (rank == 0) atomicOr(p.status, kStatusNoPage);
+        after[b] = -1;
+      } else {
+        atomicMax(&granted, take0[b] + take);
+      }
+    }
+  }
+  __syncthreads();
+  // the last sequence whose items begin at or before x
   auto owner = [&](const int* first, int x) {
     int lo = 0, hi = p.batch - 1;
     while (lo < hi) {
@@ -113,41 +146,38 @@ __global__ void __launch_bounds__(kThreads) k_plan(const PlanProblem p) {
     return lo;
   };
   auto entry = [&](int b, int e) { return p.table + static_cast<long long>(b) * p.table_width + e; };
-  if (tid == 0) granted = 0;
-  __syncthreads();
   // ---- pages back to the list
-  for (int g = tid; g < given; g += kThreads) {
+  for (int g = all; g < given; g += kAll) {
     const int b = owner(give0, g);
     p.free_pages[count + g] = *entry(b, pages_of(after[b]) + g - give0[b]);
   }
-  __syncthreads();
-  // ---- pages from it: a sequence gets all of its pages or none
-  for (int b = tid; b < p.batch; b += kThreads) {
-    const int have = pages_of(before[b]), take = after[b] < 0 ? 0 : max(pages_of(after[b]) - have, 0);
-    const bool refused = take > avail - take0[b];
-    if (refused && take > 0) {
-      atomicOr(p.status, kStatusNoPage);
-      after[b] = -1;
-    } else if (take > 0) {
-      for (int i = 0; i < take; ++i) *entry(b, have + i) = p.free_pages[avail - 1 - take0[b] - i];
-      atomicMax(&granted, take0[b] + take);
-    }
+  // every CTA has read the inputs, and the pages are on the list
+  cluster_barrier();
+  // ---- pages from it
+  for (int x = all; x < granted; x += kAll) {
+    const int b = owner(take0, x);
+    *entry(b, pages_of(before[b]) + x - take0[b]) = p.free_pages[avail - 1 - x];
+  }
+  for (int b = all; b < p.batch; b += kAll) {
     p.seq_lens[b] = after[b] < 0 ? before[b] : after[b];
     p.cu_tokens[b] = min(row0[b], rows);
   }
-  __syncthreads();
-  if (tid == 0) {
+  if (all == 0) {
     p.cu_tokens[p.batch] = rows;
     *p.free_count_out = avail - granted;
   }
-  // ---- rows
-  for (int t = tid; t < p.max_tokens; t += kThreads) {
+  // ---- rows: a page that this step takes is read from the list, not from the table
+  for (int t = all; t < p.max_tokens; t += kAll) {
     int at = 0;
     long long slot = -1;
     if (t < rows) {
       const int b = owner(row0, t);
       at = before[b] + t - row0[b];
-      if (after[b] >= 0) slot = static_cast<long long>(*entry(b, at / p.page_size)) * p.page_size + at % p.page_size;
+      if (after[b] >= 0) {
+        const int e = at / p.page_size, have = pages_of(before[b]);
+        const int page = e < have ? *entry(b, e) : p.free_pages[avail - 1 - take0[b] - (e - have)];
+        slot = static_cast<long long>(page) * p.page_size + (at - e * p.page_size);
+      }
     }
     p.positions[t] = at;
     p.slots[t] = slot;
@@ -166,7 +196,7 @@ cudaError_t launch_page_plan(const PlanProblem& p, cudaStream_t stream) {
     if (device < 64) opted_in.fetch_or(1ull << device, std::memory_order_relaxed);
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(1);
+  cfg.gridDim = dim3(plan::kCtas);
   cfg.blockDim = dim3(plan::kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
