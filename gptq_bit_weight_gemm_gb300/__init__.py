@@ -527,7 +527,7 @@ class _Runtime:
         torch = _torch()
         self.int32, self.float32, self.float16, self.int64 = torch.int32, torch.float32, torch.float16, torch.int64
         self.codes = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32}
-        self.lib = lib()
+        self.lib, self.empty = lib(), torch.empty
         raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
         if raw is None or device is None:
             self.stream = lambda: torch.cuda.current_stream().cuda_stream
@@ -819,6 +819,11 @@ def _cache_strides(t, dtype, shape, name, device):
     return stride
 
 
+def _fresh(rt, stream, like, shape, dtype):
+    """As _new, at half of its price where no stream is given."""
+    return rt.empty(shape, dtype=dtype, device=like.device) if stream is None else _new(stream, like, shape, dtype)
+
+
 def _raw_stream(rt, stream, device):
     if stream is None:
         return rt.stream()
@@ -852,12 +857,12 @@ def page_plan(cached, added, block_table, free_pages, free_count, *, page_size, 
     n_out = n_ptr if free_count_out is None else _here(free_count_out, i32, (1,), "free_count_out", device)
     raw = _raw_stream(rt, stream, device)
     if seq_lens is None:
-        seq_lens = _new(stream, cached, (batch,))
+        seq_lens = _fresh(rt, stream, cached, (batch,), i32)
         l_ptr = seq_lens.data_ptr()
     else:
         l_ptr = _here(seq_lens, i32, (batch,), "seq_lens", device)
-    cu, positions = _new(stream, cached, (batch + 1,)), _new(stream, cached, (max_tokens,))
-    slots = _new(stream, cached, (max_tokens,), rt.int64)
+    cu, positions = _fresh(rt, stream, cached, (batch + 1,), i32), _fresh(rt, stream, cached, (max_tokens,), i32)
+    slots = _fresh(rt, stream, cached, (max_tokens,), rt.int64)
     rc = rt.lib.gptq_page_plan(c_ptr, a_ptr, batch, page_size, t_ptr, table_shape[1], f_ptr, list_shape[0], n_ptr, n_out, l_ptr,
                                cu.data_ptr(), positions.data_ptr(), slots.data_ptr(), max_tokens, raw)
     if rc:
@@ -915,7 +920,7 @@ def rms_norm(x, weight=None, *, residual=None, residual_out=None, eps=1e-6, dtyp
         raise TypeError("the result must be float16, bfloat16 or float32, got %s" % dtype)
     raw = _raw_stream(rt, stream, device)
     if out is None:
-        out = x.new_empty(shape, dtype=dtype) if stream is None else _new(stream, x, shape, dtype)
+        out = _fresh(rt, stream, x, shape, dtype)
     os_ = out.stride()
     if not (out.get_device() == device and out.dtype == dtype and out.shape == shape and (os_[1] == 1 or hidden == 1)):
         _look_matrix(out, dtype, shape, "out", device)
@@ -978,11 +983,14 @@ def rotary(q, k, positions, turns, *, amplitude=1.0, interleaved=False, v=None, 
         raise ValueError("v, v_cache and slots go with k_cache")
     raw = _raw_stream(rt, stream, device)
     if q_out is None:
-        q_out = _new(stream, q, shape)
-    if k_out is None and k_cache is None:
-        k_out = _new(stream, k, k_shape)
-    qo = _row_stride(q_out, dtype, shape, "q_out", device)
-    ko = 0 if k_out is None else _row_stride(k_out, dtype, k_shape, "k_out", device)
+        q_out, qo = _fresh(rt, stream, q, shape, dtype), heads * dim
+    else:
+        qo = _row_stride(q_out, dtype, shape, "q_out", device)
+    ko = 0
+    if k_out is not None:
+        ko = _row_stride(k_out, dtype, k_shape, "k_out", device)
+    elif k_cache is None:
+        k_out, ko = _fresh(rt, stream, k, k_shape, dtype), kv_heads * dim
     strides = _RotaryStrides(qs, ks, vs, qo, ko, kc[0], kc[1], kc[2], vc[0], vc[1], vc[2])
     rc = rt.lib.gptq_rotary(q.data_ptr(), k.data_ptr(), v_ptr, tokens, heads, kv_heads, dim, 2 * turns.numel(),
                             1 if interleaved else 0, code, strides, p_ptr, t_ptr, amplitude, q_out.data_ptr(),
@@ -1033,7 +1041,7 @@ def chunk_attention(q, k_cache, v_cache, block_table, seq_lens, cu_tokens, *, sc
     lse_ptr = None if lse is None else _here(lse, rt.float32, (tokens, heads), "lse", device)
     raw = _raw_stream(rt, stream, device)
     if out is None:
-        out = q.new_empty(shape) if stream is None else _new(stream, q, shape)
+        out = _fresh(rt, stream, q, shape, dtype)
         o_ptr = out.data_ptr()
     else:
         o_ptr = _here(out, dtype, shape, "out", device)

@@ -43,7 +43,8 @@ extern "C" int gptq_page_plan(const int32_t* cached, const int32_t* added, int b
                               int32_t* free_count_out, int32_t* seq_lens, int32_t* cu_tokens, int32_t* positions,
                               long long* slots, int max_tokens, void* stream) {
   using gptq::aligned_to;
-  if (batch < 0 || batch > gptq::kMaxPlanBatch || page_size <= 0 || table_width <= 0 || free_capacity < 0 || max_tokens < 0)
+  if (batch < 0 || batch > gptq::kMaxPlanBatch || page_size <= 0 || table_width <= 0 || free_capacity < 0 ||
+      free_capacity > (1 << 30) || max_tokens < 0 || max_tokens > (1 << 30))
     return GPTQ_ERR_SHAPE;
   if (static_cast<long long>(table_width) * page_size > (1ll << 30)) return GPTQ_ERR_SHAPE;
   if (!free_count || !free_count_out || !cu_tokens) return GPTQ_ERR_ARG;

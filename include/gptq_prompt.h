@@ -51,7 +51,8 @@ extern "C" {
  * has too few pages (GPTQ_DEV_NO_PAGE), keeps its length and pages; its rows stay, with slots -1.  cached
  * outside [0, table] and added below -cached are cut (GPTQ_DEV_SEQ_LEN); a page given back to a full list
  * is lost (GPTQ_DEV_NO_PAGE); rows past max_tokens are left out and cu_tokens is cut
- * (GPTQ_DEV_TOKEN_ROWS).  batch up to 8192, table_width * page_size up to 2^30; otherwise GPTQ_ERR_SHAPE.
+ * (GPTQ_DEV_TOKEN_ROWS).  batch up to 8192, table_width * page_size, free_capacity and max_tokens up to 2^30;
+ * otherwise GPTQ_ERR_SHAPE.
  * All 4-byte aligned, slots 8-byte.  batch == 0 writes cu_tokens[0] and the padding.
  */
 int gptq_page_plan(const int32_t* cached, const int32_t* added, int batch, int page_size, int32_t* block_table,
