@@ -87,6 +87,10 @@ struct Item {
   int bad;                 // an infinite or NaN value was replaced by 0 in a tile not seen by every row
 };
 
+struct Sequence {
+  int first, tokens, n, blocks;    // its rows, keys, blocks of packed rows
+};
+
 template <int DP>
 struct Control {
   unsigned long long full[Shape<DP>::kStages], empty[Shape<DP>::kStages], raw[Shape<DP>::kStages];
@@ -95,8 +99,10 @@ struct Control {
   Item item[2];
   uint32_t tmem;
   int abort;
-  int sequence;
-  long long sum[Shape<DP>::kThreads / 32], at, total;
+  int sequence;            // that the run begins in, what it is, units before it and of each of its kv heads
+  Sequence found;
+  long long at, total;
+  long long sum[Shape<DP>::kThreads / 32];
 };
 
 // What is left of a cut item for the joining kernel, by the run that holds the item's first tile.
@@ -191,10 +197,6 @@ __device__ __forceinline__ long long divide(long long x, long long y) {
 }
 
 // ------------------------------------------------------------------------------ the line
-struct Sequence {
-  int first, tokens, n, blocks;    // its rows, keys, blocks of packed rows
-};
-
 template <int DP>
 __device__ __forceinline__ Sequence sequence_of(const Args& a, int b, bool report) {
   const ChunkProblem& p = a.p;
@@ -270,14 +272,20 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31, run = blockIdx.x;
 
   decode::pdl_launch_dependents();
+  if (warp == S::kLoadWarp0 && lane == 0) {
+    ptx::prefetch_tmap(&map_k);
+    ptx::prefetch_tmap(&map_v);
+    ptx::prefetch_tmap(&map_q);
+  }
   decode::pdl_wait();
 
   // ---- this CTA's run of the line: a scan over the sequences gives its length, and the sequence that the run
   // begins in
   long long before = 0, upto = 0, units = 0;
+  Sequence s = {0, 0, 0, 0};
   auto scan_chunk = [&](int b0, long long base) {
     const int b = b0 + static_cast<int>(threadIdx.x);
-    Sequence s = {0, 0, 0, 0};
+    s = {0, 0, 0, 0};
     if (b < p.batch) s = sequence_of<DP>(a, b, run == 0);
     units = head_units<DP>(a, s, lane);
     const long long w = units * p.kv_heads;
@@ -313,6 +321,7 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
       if (p.batch > S::kThreads) at = scan_chunk(b0, at);
       if (before <= begin && begin < upto) {
         c.sequence = b0 + static_cast<int>(threadIdx.x);
+        c.found = s;
         c.at = before;
         c.total = units;
       }
@@ -367,7 +376,7 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
     if (warp == S::kWalkWarp) {
       // -------------------------------------------------------------- the line's items, one after the other
       int b = c.sequence, h, block = 0;
-      Sequence s = sequence_of<DP>(a, b, false);
+      Sequence s = c.found;
       long long start;                     // the item's first unit
       {
         const long long rel = begin - c.at;
@@ -832,7 +841,10 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
           if (++stage == S::kStages) stage = 0, phase ^= 1;
         }
         // the queries' place is free once the item before has its last scores: the first tile need not wait for that
-        if (ok && t == it.t0) ok = queries_of();
+        if (ok && t == it.t0) {
+          ok = queries_of();
+          while (open) oldest();           // (copied: it is waited for before more is asked for)
+        }
       }
     }
     if (!ok) {
@@ -959,6 +971,7 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
       if (live_warp) {
         const int packed = it.row0 + r, token = packed / a.group, head = packed - token * a.group;
         const long long at = static_cast<long long>(it.first + token) * p.heads + it.kv_head * a.group + head;
+        const unsigned live_rows = __ballot_sync(0xFFFFFFFFu, live_row);
         const bool bad = *const_cast<const volatile int*>(&it.bad) != 0;
         const float inv = it.slot >= 0 ? 1.f : (l > 0.f || isnan(l) ? 1.f / l : 0.f);
         float* part = a.partials + static_cast<size_t>(max(it.slot, 0)) * partial_floats<DP>();
@@ -973,16 +986,34 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
             for (int j = 0; j < 32; ++j) o[j] = 0;
           }
           if (it.slot < 0) {
-            if (live_row) {
-              uint4* to = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + at * p.head_dim + i);
+            // the 4 lanes of a group exchange 16-byte pieces: lane x then holds piece x of each of their 4 rows, and an
+            // instruction writes 64 bytes of 8 rows (16 bytes of 32 took 4 times as long)
+            uint32_t w[4][4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+              for (int y = 0; y < 4; ++y)
+                w[j][y] = pack2(__uint_as_float(o[8 * j + 2 * y]) * inv, __uint_as_float(o[8 * j + 2 * y + 1]) * inv, T());
+#pragma unroll
+            for (int x = 1; x <= 2; x <<= 1)
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
-                uint4 w;
+                if (j & x) continue;
 #pragma unroll
-                for (int y = 0; y < 4; ++y)
-                  (&w.x)[y] = pack2(__uint_as_float(o[8 * j + 2 * y]) * inv, __uint_as_float(o[8 * j + 2 * y + 1]) * inv, T());
-                if (i + 8 * j < p.head_dim) to[j] = w;
+                for (int y = 0; y < 4; ++y) {
+                  const bool up = lane & x;
+                  const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, up ? w[j][y] : w[j | x][y], x);
+                  if (up) w[j][y] = got;
+                  else w[j | x][y] = got;
+                }
               }
+            const int d = i + 8 * (lane & 3);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int from = (lane & ~3) + j;
+              const long long row_at = __shfl_sync(0xFFFFFFFFu, at, from);
+              if ((live_rows >> from & 1) && d < p.head_dim)
+                *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + row_at * p.head_dim + d) = make_uint4(w[j][0], w[j][1], w[j][2], w[j][3]);
             }
           } else if (any) {
 #pragma unroll
@@ -995,6 +1026,7 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
         } else {
           __stcg(reinterpret_cast<float2*>(part + static_cast<size_t>(S::kRows) * DP) + r, make_float2(any ? m : -CUDART_INF_F, l));
         }
+        __syncwarp();
         if (bad && live_row) {
           // values that are not finite, of the keys that this row sees in the tiles not seen by all
 #pragma unroll 1
