@@ -32,6 +32,7 @@
 // in the tiles at the diagonal the loader replaces infinite and NaN values by 0, and the rows that do see
 // them get them added at the end.
 #include <cuda.h>
+#include <limits.h>
 #include <math_constants.h>
 
 #include <atomic>
@@ -315,7 +316,23 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
   // runs of `share` units, the first `extra` of them one longer
   const long long share = divide(total, runs), extra = total - share * runs;
   const long long begin = share * run + (run < extra ? run : extra), end = begin + share + (run < extra ? 1 : 0);
-  if (run < runs && total > 0) {
+  // Or no item is cut: they are dealt out whole, in turns that go to and fro through the CTAs, those of a sequence with the most
+  // keys first and its kv heads side by side.  All CTAs then read the same sequence at about the same time and place, so its
+  // keys come from DRAM once, in whole rows (of runs each reads a head and a sequence of its own: four prompts of 1300 to
+  // 4096 tokens and 32 kv heads took 331 us so, 232 dealt).  That asks for enough items, of which the last ones are small:
+  // each sequence's largest at most 1.25 times what each CTA has left from it on, and the last sequence's smallest at
+  // most 0.06 of a CTA's work (either with 0.06 of slack).
+  bool deal = false;
+  if (p.batch <= S::kThreads) {
+    bool good = true;
+    if (s.blocks > 0) {
+      const long long ctas = gridDim.x, rest = total - before;
+      good = units_of<DP>(a, s, s.blocks - 1) * ctas * 100 <= rest * 125 + total * 6 &&
+             (upto < total || units_of<DP>(a, s, 0) * ctas * 100 <= total * 6);
+    }
+    deal = __syncthreads_and(good) && total > 0;
+  }
+  if (!deal && run < runs && total > 0) {
     long long at = 0;
     for (int b0 = 0; b0 < p.batch; b0 += S::kThreads) {
       if (p.batch > S::kThreads) at = scan_chunk(b0, at);
@@ -329,7 +346,7 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
       if (c.sequence >= 0) break;
     }
   }
-  if (run >= runs || total == 0 || c.sequence < 0) {       // (the last: lengths written while this ran)
+  if (!deal && (run >= runs || total == 0 || c.sequence < 0)) {   // (the last: lengths written while this ran)
     if (threadIdx.x == 0) a.records[run].valid = 0;
     return;
   }
@@ -375,10 +392,13 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
     if constexpr (kNQ == 2) shrink_registers<80>();
     if (warp == S::kWalkWarp) {
       // -------------------------------------------------------------- the line's items, one after the other
-      int b = c.sequence, h, block = 0;
+      int b = c.sequence, h = 0, block = 0;
       Sequence s = c.found;
-      long long start;                     // the item's first unit
-      {
+      long long start = 0, first_unit = begin, end_unit = end;   // the item's first unit; those of the run
+      if (deal) {
+        first_unit = 0;
+        end_unit = LLONG_MAX;
+      } else {
         const long long rel = begin - c.at;
         h = static_cast<int>(divide(rel, c.total));
         long long left = rel - h * c.total;                // units of the head's items before the run
@@ -402,6 +422,39 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
         }
         start = begin - left;
       }
+      // dealt items: 32 sequences at a time, a lane each, with the items before them
+      Sequence mine = {0, 0, 0, 0};
+      int turn = 0, chunk0 = -32, chunk_items = 0, upto_items = 0;
+      long long base = 0;
+      auto deal_next = [&]() {             // the item of this CTA's next turn; false: there is none
+        const long long index = static_cast<long long>(turn) * gridDim.x + (turn & 1 ? gridDim.x - 1 - run : run);
+        ++turn;
+        while (index - base >= chunk_items) {
+          base += chunk_items;
+          chunk0 += 32;
+          if (chunk0 >= p.batch) return false;
+          mine = {0, 0, 0, 0};
+          if (chunk0 + lane < p.batch) mine = sequence_of<DP>(a, chunk0 + lane, false);
+          upto_items = mine.blocks * p.kv_heads;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xFFFFFFFFu, upto_items, o);
+            if (lane >= o) upto_items += v;
+          }
+          chunk_items = __shfl_sync(0xFFFFFFFFu, upto_items, 31);
+        }
+        const int within = static_cast<int>(index - base);
+        const int from = __ffs(__ballot_sync(0xFFFFFFFFu, upto_items > within)) - 1;
+        b = chunk0 + from;
+        s.first = __shfl_sync(0xFFFFFFFFu, mine.first, from);
+        s.tokens = __shfl_sync(0xFFFFFFFFu, mine.tokens, from);
+        s.n = __shfl_sync(0xFFFFFFFFu, mine.n, from);
+        s.blocks = __shfl_sync(0xFFFFFFFFu, mine.blocks, from);
+        const int item = within - (__shfl_sync(0xFFFFFFFFu, upto_items, from) - s.blocks * p.kv_heads);
+        block = s.blocks - 1 - item / p.kv_heads;
+        h = item % p.kv_heads;
+        return true;
+      };
       auto run_of = [&](long long unit) {
         const long long cut = extra * (share + 1);
         return static_cast<int>(unit < cut ? divide(unit, share + 1) : extra + divide(unit - cut, share));
@@ -410,9 +463,10 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
       bool ok = true;
       uint32_t n = 0;                      // items handed out
       while (true) {
-        const int u = units_of<DP>(a, s, block);
+        const bool out = deal && !deal_next();
+        const int u = out ? 0 : units_of<DP>(a, s, block);
         const long long tile0 = start + kItemUnits, stop = start + u;
-        const bool done = tile0 >= end;
+        const bool done = out || tile0 >= end_unit;
         const int slot = n & 1;
         if (!wait(c.iempty[slot], ((n >> 1) & 1) ^ 1)) {
           ok = false;
@@ -433,7 +487,7 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
           keys_of(a, s, r1, r1, &it.full_lo, &y);
           const bool any = it.key_hi > it.key_lo;
           const int t_lo = it.key_lo / kKeys;
-          const long long from = tile0 > begin ? 0 : begin - tile0, to = (stop < end ? stop : end) - tile0;
+          const long long from = tile0 > first_unit ? 0 : first_unit - tile0, to = (stop < end_unit ? stop : end_unit) - tile0;
           it.t0 = any ? t_lo + static_cast<int>(from) : 0;
           it.t1 = any ? t_lo + static_cast<int>(to) : 0;
 #pragma unroll
@@ -447,7 +501,7 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
               }
             }
           }
-          const bool whole = tile0 >= begin && stop <= end;
+          const bool whole = tile0 >= first_unit && stop <= end_unit;
           const int first_run = whole ? run : run_of(tile0);
           it.slot = whole ? -1 : 2 * run + (first_run == run ? 1 : 0);
           it.bad = 0;
@@ -461,6 +515,7 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
         __syncwarp();
         if (done) break;
         ++n;
+        if (deal) continue;
         start = stop;
         if (++block >= s.blocks) {
           block = 0;
@@ -472,7 +527,7 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
             } while (s.blocks == 0);
             if (b >= p.batch) {            // the line's end: nothing follows
               b = p.batch - 1;
-              start = end;
+              start = end_unit;
             }
           }
         }

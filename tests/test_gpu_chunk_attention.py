@@ -69,12 +69,26 @@ class Case:
         return dict(q=q, k_cache=self.k.to(DEV), v_cache=self.v.to(DEV), block_table=self.table.to(DEV),
                     seq_lens=torch.tensor(self.lens, dtype=torch.int32, device=DEV), cu_tokens=self.cu.to(DEV))
 
+    def one_head(self, b, row, h):
+        """The same problem of sequence b and kv head h alone (without a cache)."""
+        c, g_ = object.__new__(Case), self.heads // self.kv
+        c.new, c.lens, c.heads, c.kv, c.dim, c.dtype = [self.new[b]], [self.lens[b]], g_, 1, self.dim, self.dtype
+        c.q = self.q[row:row + self.new[b], h * g_:(h + 1) * g_]
+        c.keys, c.values = [self.keys[b][:, h:h + 1]], [self.values[b][:, h:h + 1]]
+        return c
+
     def ref(self, scale, window):
         """(out, tolerance, lse, lse tolerance) of the sequences' rows, in 64 bits."""
         u = 2.0 ** (-11 if self.dtype == torch.float16 else -8)
         out, tol, lse, lse_tol, row = [], [], [], [], 0
         for b, (m, n) in enumerate(zip(self.new, self.lens)):
             if m == 0:
+                continue
+            if m * n * self.heads > 1 << 28:
+                parts = [self.one_head(b, row, h).ref(scale, window) for h in range(self.kv)]
+                for into, x in zip((out, tol, lse, lse_tol), zip(*parts)):
+                    into.append(torch.cat(x, 1))
+                row += m
                 continue
             q = self.q[row:row + m].double().to(DEV).reshape(m, self.kv, self.heads // self.kv, self.dim)
             row += m
@@ -144,6 +158,17 @@ def test_sliding_window(window, dim):
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
 def test_long(new, length, dtype):
     check(Case([new, 1], [length, length // 7], 8, 2, 128, 64, dtype, seed=length))
+
+
+@pytest.mark.parametrize("new,lens,heads,kv,dim,window,dtype", [
+    # many items, the last of them small: dealt out whole (a CTA's share is some 90 key tiles and more, the smallest item 2)
+    ([2600, 0, 2300, 40], [2600, 50, 2300, 40], 64, 64, 64, 0, torch.float16),
+    ([1, 3000, 700], [9, 3100, 700], 96, 32, 128, 0, torch.bfloat16),
+    ([2900, 2500], [2900, 2700], 64, 64, 64, 1700, torch.bfloat16),
+    # as many, the last of them large: cut into runs
+    ([2300, 40, 2600], [2300, 40, 4000], 32, 32, 64, 0, torch.float16)])
+def test_prompts_of_many_items(new, lens, heads, kv, dim, window, dtype):
+    check(Case(new, lens, heads, kv, dim, 32, dtype, seed=len(new), pad=3), window=window)
 
 
 def test_long_without_grouped_heads_dim_256():
