@@ -18,10 +18,14 @@ cudaError_t launch_chunk_attention(const ChunkProblem& p, cudaStream_t stream) {
   // hidden scores are -inf, which times 0 is no number
   if (a.scale_log2 == 0.f) a.scale_log2 = 1.17549435e-38f;
   // m = ceil(2^(30 + L) / d) with 2^L >= d: n m / 2^(30 + L) is off by less than 1 / d for n < 2^30
-  unsigned log = 0;
-  while ((1ull << log) < static_cast<unsigned>(p.page_size)) ++log;
-  a.page_shift = 30 + log;
-  a.page_mul = static_cast<unsigned>(((1ull << a.page_shift) + p.page_size - 1) / p.page_size);
+  auto divisor = [](unsigned d, unsigned* mul, unsigned* shift) {
+    unsigned log = 0;
+    while ((1ull << log) < d) ++log;
+    *shift = 30 + log;
+    *mul = static_cast<unsigned>(((1ull << *shift) + d - 1) / d);
+  };
+  divisor(static_cast<unsigned>(p.page_size), &a.page_mul, &a.page_shift);
+  divisor(static_cast<unsigned>(a.group), &a.group_mul, &a.group_shift);
   a.k_page16 = static_cast<unsigned>(p.k_page / 8);
   a.k_slot16 = static_cast<unsigned>(p.k_slot / 8);
   a.k_head16 = static_cast<unsigned>(p.k_head / 8);

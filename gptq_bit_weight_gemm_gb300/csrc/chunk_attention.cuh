@@ -119,6 +119,7 @@ struct Args {
   float scale_log2;        // |scale| * log2(e)
   int negative;            // scale < 0
   unsigned page_mul, page_shift;   // key / page_size = key * page_mul >> page_shift for keys below 2^30
+  unsigned group_mul, group_shift; // and packed rows by the group's heads
   unsigned k_page16, k_slot16, k_head16, v_page16, v_slot16, v_head16;   // strides in 16-byte units
   int box_rows;            // keys of a TMA box: 0 where the cache is not read by TMA
   int box_order[3];        // which coordinate is the box's second, third and fourth: 0 slot, 1 head, 2 page
@@ -199,6 +200,11 @@ __device__ __forceinline__ long long divide(long long x, long long y) {
   return x / y;
 }
 
+// The token of a packed row (a division costs some 200 cycles, and an item takes a dozen).
+__device__ __forceinline__ int token_of(const Args& a, int row) {
+  return static_cast<int>(static_cast<unsigned long long>(static_cast<unsigned>(max(row, 0))) * a.group_mul >> a.group_shift);
+}
+
 // ------------------------------------------------------------------------------ the line
 template <int DP>
 __device__ __forceinline__ Sequence sequence_of(const Args& a, int b, bool report) {
@@ -220,8 +226,8 @@ __device__ __forceinline__ Sequence sequence_of(const Args& a, int b, bool repor
 // Keys [lo, hi) that the packed rows r0 .. r1 of a sequence see.
 __device__ __forceinline__ void keys_of(const Args& a, const Sequence& s, int r0, int r1, int* lo, int* hi) {
   const int position0 = s.n - s.tokens;
-  *hi = max(0, position0 + r1 / a.group + 1);
-  *lo = a.p.window > 0 ? max(0, position0 + r0 / a.group - a.p.window + 1) : 0;
+  *hi = max(0, position0 + token_of(a, r1) + 1);
+  *lo = a.p.window > 0 ? max(0, position0 + token_of(a, r0) - a.p.window + 1) : 0;
 }
 
 template <int DP>
@@ -809,7 +815,7 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
             q_sent |= 1;
             ptx::mbar_arrive_expect_tx(bar(c.qfull), 128 * 128 * blocks);
             for (int h = 0; h < blocks; ++h)
-              ptx::tma_load_4d(at + h * 128 * 128, &map_q, 64 * h, 0, it.kv_head, it.first + (it.row0 + lw * 128) / a.group, bar(c.qfull));
+              ptx::tma_load_4d(at + h * 128 * 128, &map_q, 64 * h, 0, it.kv_head, it.first + token_of(a, it.row0 + lw * 128), bar(c.qfull));
           } else if (lane == 0) {
             ptx::mbar_arrive(bar(c.qfull));
           }
@@ -821,7 +827,7 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
         for (int s = 0; s < kNQ; ++s) {
           if (it.lo[s] >= it.hi[s]) continue;
           const int r = s * 128 + lw * 32 + lane;
-          const int packed = it.row0 + r, token = packed / a.group, head = packed - token * a.group;
+          const int packed = it.row0 + r, token = token_of(a, packed), head = packed - token * a.group;
           const long long off = (it.first + token) * p.q_token + static_cast<long long>(it.kv_head * a.group + head) * p.head_dim;
           const unsigned rows = __ballot_sync(0xFFFFFFFFu, r < it.rows);
           const uint32_t at = sbase + s * S::kQBytes + lw * 32 * 128;
@@ -837,6 +843,9 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
         close(kQueries);
         return true;
       };
+      // the queries' place is free once the item before has its last scores: the first tile need not wait for that
+      const bool at_once = queries == 0;
+      if (at_once) ok = queries_of();
       for (int t = it.t0; ok && t < it.t1; ++t, ++tiles) {
         const bool good = want && page >= 0 && page < p.pages;
         if (want && !good) atomicOr(p.status, kStatusPageRange);
@@ -897,9 +906,8 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
           if (!a.box_rows) close((look ? kLook : 0u) | (slot ? kSlot : 0u) | static_cast<unsigned>(stage) << 3);
           if (++stage == S::kStages) stage = 0, phase ^= 1;
         }
-        // the queries' place is free once the item before has its last scores: the first tile need not wait for that
         if (ok && t == it.t0) {
-          ok = queries_of();
+          if (!at_once) ok = queries_of();
           while (open) oldest();           // (copied: it is waited for before more is asked for)
         }
       }
@@ -933,7 +941,7 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
       if (it.b < 0) break;
       const int r = s * 128 + row;
       const bool live_row = r < it.rows, live_warp = s * 128 + (warp & 3) * 32 < it.rows;
-      const int row_hi = it.position0 + (it.row0 + r) / a.group + 1;
+      const int row_hi = it.position0 + token_of(a, it.row0 + r) + 1;
       const int row_lo = p.window > 0 ? max(0, row_hi - p.window) : 0;
       float m = -CUDART_INF_F, l = 0.f;
       bool ok = true;
@@ -1026,7 +1034,7 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
         ptx::tc_fence_after();
       }
       if (live_warp) {
-        const int packed = it.row0 + r, token = packed / a.group, head = packed - token * a.group;
+        const int packed = it.row0 + r, token = token_of(a, packed), head = packed - token * a.group;
         const long long at = static_cast<long long>(it.first + token) * p.heads + it.kv_head * a.group + head;
         const unsigned live_rows = __ballot_sync(0xFFFFFFFFu, live_row);
         const bool bad = *const_cast<const volatile int*>(&it.bad) != 0;
@@ -1158,7 +1166,7 @@ __global__ void __launch_bounds__(Shape<DP>::kRows) k_join(const __grid_constant
       o[4 * i + 3] += v.w * f;
     }
   }
-  const int packed = rec.row0 + row, token = packed / a.group, head = packed - token * a.group;
+  const int packed = rec.row0 + row, token = token_of(a, packed), head = packed - token * a.group;
   const long long at = static_cast<long long>(rec.first + token) * p.heads + rec.kv_head * a.group + head;
   const float inv = l > 0.f || isnan(l) ? 1.f / l : 0.f;
   uint4* to = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + at * p.head_dim + col);
