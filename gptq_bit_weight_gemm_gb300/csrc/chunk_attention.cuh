@@ -49,7 +49,7 @@
 namespace gptq {
 namespace chunk {
 
-constexpr int kMaxRuns = 512;
+constexpr int kMaxRuns = 160;            // CTAs, at most: one on each of the 152 SMs
 constexpr size_t kRecordBytes = kMaxRuns * 32;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr float kGrow = 8.f;             // log2 of what a row's maximum may grow by before o is rescaled
@@ -1141,29 +1141,48 @@ __global__ void __launch_bounds__(Shape<DP>::kRows) k_join(const __grid_constant
   const ChunkProblem& p = a.p;
   decode::pdl_launch_dependents();
   decode::pdl_wait();
-  const Record rec = a.records[blockIdx.x];
+  Record rec = a.records[blockIdx.x];
+  rec.last_run = min(rec.last_run, static_cast<int>(gridDim.x) - 1);   // (past it only where lengths were written meanwhile)
   const int row = threadIdx.x, col = blockIdx.y * kJoinCols;
   if (!rec.valid || row >= rec.rows || col >= p.head_dim) return;
   auto part_of = [&](int run) {
     return a.partials + static_cast<size_t>(2 * run + (run == rec.first_run ? 1 : 0)) * partial_floats<DP>();
   };
-  auto ml_of = [&](int run) { return __ldcg(reinterpret_cast<const float2*>(part_of(run) + static_cast<size_t>(S::kRows) * DP) + row); };
-  float top = -CUDART_INF_F;
-  for (int run = rec.first_run; run <= rec.last_run; ++run) top = fmaxf(top, ml_of(run).x);
-  float l = 0.f, o[kJoinCols] = {};
-  for (int run = rec.first_run; run <= rec.last_run; ++run) {
-    const float2 ml = ml_of(run);
-    if (ml.x == -CUDART_INF_F && !isnan(ml.y)) continue;   // the run had no key of the row: its o says nothing
-    const float f = ex2(ml.x - (top == -CUDART_INF_F ? 0.f : top));
-    l += ml.y * f;
-    const float4* from = reinterpret_cast<const float4*>(part_of(run)) + static_cast<size_t>(col / 4) * S::kRows + row;
+  // kBatch parts in flight at a time (64 tokens on 4000 keys: 28.5 us with one after the other, 25.1 so)
+  constexpr int kBatch = 4;
+  float top = -CUDART_INF_F, l = 0.f, o[kJoinCols] = {};
+  for (int run0 = rec.first_run; run0 <= rec.last_run; run0 += kBatch) {
+    float2 ml[kBatch];
+    float4 v[kBatch][kJoinCols / 4];
 #pragma unroll
-    for (int i = 0; i < kJoinCols / 4; ++i) {
-      const float4 v = __ldcg(from + static_cast<size_t>(i) * S::kRows);
-      o[4 * i] += v.x * f;
-      o[4 * i + 1] += v.y * f;
-      o[4 * i + 2] += v.z * f;
-      o[4 * i + 3] += v.w * f;
+    for (int j = 0; j < kBatch; ++j) {
+      const float* part = part_of(min(run0 + j, rec.last_run));
+      ml[j] = __ldcg(reinterpret_cast<const float2*>(part + static_cast<size_t>(S::kRows) * DP) + row);
+#pragma unroll
+      for (int i = 0; i < kJoinCols / 4; ++i)
+        v[j][i] = __ldcg(reinterpret_cast<const float4*>(part) + static_cast<size_t>(col / 4 + i) * S::kRows + row);
+    }
+    float mn = top;
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) mn = fmaxf(mn, ml[j].x);   // (a repeated last part changes nothing)
+    const float base = mn == -CUDART_INF_F ? 0.f : mn, keep = ex2(top - base);
+    top = mn;
+    l *= keep;
+#pragma unroll
+    for (int i = 0; i < kJoinCols; ++i) o[i] *= keep;
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      // of a run that had no key of the row o says nothing
+      if (run0 + j > rec.last_run || (ml[j].x == -CUDART_INF_F && !isnan(ml[j].y))) continue;
+      const float f = ex2(ml[j].x - base);
+      l += ml[j].y * f;
+#pragma unroll
+      for (int i = 0; i < kJoinCols / 4; ++i) {
+        o[4 * i] += v[j][i].x * f;
+        o[4 * i + 1] += v[j][i].y * f;
+        o[4 * i + 2] += v[j][i].z * f;
+        o[4 * i + 3] += v[j][i].w * f;
+      }
     }
   }
   const int packed = rec.row0 + row, token = token_of(a, packed), head = packed - token * a.group;
