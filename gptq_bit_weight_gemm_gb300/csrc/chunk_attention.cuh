@@ -16,21 +16,39 @@
 // Split: items cost what their visible key tiles cost, from 1 to thousands.  All of them, one after the
 // other, are a line of key tiles that is cut into as many equal runs as there are SMs, on the device, from the
 // lengths; an item cut by a run's end leaves partial results (m, l, o) in the workspace, two a run at most, and a
-// second kernel joins them, all SMs at work on the rows.
+// second kernel joins them, all SMs at work on the rows.  Where there are many items and the last ones are small they
+// are dealt out whole instead.
 //
 // A CTA: softmax warps 0-3 and 4-7 (one accumulator each, a thread a row), loader warps 8-11, and in the last
-// four one that issues the MMAs and one that walks the line.  S = q k^T goes to tensor memory; a softmax
-// thread reads its row, writes the probabilities back over it as 16-bit values, and these are the A operand
-// of p v straight from tensor memory.  While one accumulator's softmax runs, the tensor cores work for the
-// other.  The accumulator o is rescaled by the softmax threads themselves, only where a row's maximum has
-// grown by more than 2^8 since the last time: until then probabilities are simply larger than 1 (the
-// scores' MMA completes after the p v before it, so o is at rest then).  fp16 probabilities are taken 2^7
-// times as large, so that a long flat tail behind one large score is not lost in fp16's range.
+// four one that issues the MMAs, one that walks the line and two that look over values.  S = q k^T goes to
+// tensor memory; a softmax thread reads its row, writes the probabilities back over it as 16-bit values, and
+// these are the A operand of p v straight from tensor memory, in two halves of the keys so that the product
+// of the first begins while the second is made.  While one accumulator's softmax runs, the tensor cores work
+// for the other.  The accumulator o is rescaled by the softmax threads themselves, only where a row's
+// maximum has grown by more than 2^8 since the last time: until then probabilities are simply larger than
+// 1 (the scores' MMA completes after the p v before it, so o is at rest then).
 //
-// Keys and values come through cp.async, 16 bytes a lane, whole rows: pages of any size, anywhere.
+// Rounding: a probability enters the product as one value of the cache's type (11 significant bits in fp16, 8 in bf16),
+// once; together with the rounding of the result the error against 64 bits is 1.4 times that of the rounding alone
+// (bf16 2.3e-3 against 1.7e-3, fp16 2.6e-4 against 2.0e-4).  As a sum of two values it would be the rounding alone, for
+// half as many MMAs again and more softmax instructions: 4096 tokens on 32768 keys took 2.8 ms so, against 1.34.
+// fp16 probabilities are taken 2^7 times as large, so that a long flat tail behind one large score is not lost
+// in fp16's range.
+//
+// Keys, values and queries come as TMA boxes of 64 dimensions by the keys that divide a page (8 to 32).  Pages that 8
+// does not divide, and caches whose strides a tensor map does not take, are copied by cp.async, 16 bytes a lane.  cp.async
+// alone reached 870 TFLOP/s on the case above, at 64 KB a tile its issue and the lanes' waiting for it was the bound.
+//
 // Values that some row of the item must not see (later tokens', outside the window) could reach it as 0 x NaN:
-// in the tiles at the diagonal the loader replaces infinite and NaN values by 0, and the rows that do see
-// them get them added at the end.
+// in the tiles that not every row sees, infinite and NaN values are replaced by 0 (and those of keys that no row sees,
+// which may never have been written), and the rows that do see them get them added at the end.
+//
+// What the steps brought, us for 4096 tokens on 32768 keys (32 query and 8 kv heads of 128, bf16) / four prompts of 1300 to
+// 4096 tokens (32 kv heads, fp16) / a mixed batch of 16: a warp a row 619708 / 59324 / 21621; tcgen05 3019 / 465 / 179;
+// no spills 2334 / 394 / 148; copies handed on as they land, P in halves, 128-byte blocks 2000 / 396 / 152; MMAs issued by
+// a converged warp (a lone thread's descriptors go through vector registers: 125 cycles an MMA, against 64 of the
+// tensor cores) 1648 / 335 / 135; TMA boxes, tiles at the diagonal looked over by two warps 1391 / 330 / 117; results in
+// 64-byte pieces 1330 / 331 / 111; items dealt out whole 1330 / 228 / 112.
 #pragma once
 
 #include <cuda.h>
@@ -40,11 +58,11 @@
 #include <atomic>
 #include <type_traits>
 
+#include "chunk_ptx.cuh"
 #include "decode.cuh"
 #include "gptq_device.cuh"
 #include "gptq_internal.h"
 #include "prompt_internal.h"
-#include "sm100_ptx.cuh"
 
 namespace gptq {
 namespace chunk {

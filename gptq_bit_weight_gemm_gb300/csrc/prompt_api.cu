@@ -232,6 +232,8 @@ extern "C" int gptq_chunk_attention(const void* q, int tokens, int heads, int dt
   p.k_page = ks[0]; p.k_slot = ks[1]; p.k_head = ks[2];
   p.v_page = vs[0]; p.v_slot = vs[1]; p.v_head = vs[2];
   p.table = block_table; p.table_width = table_width; p.lens = seq_lens; p.cu = cu_tokens; p.batch = batch;
-  p.scale = scale; p.window = window; p.out = out; p.lse = lse; p.workspace = workspace;
+  // (positions are below 2^30: a wider window hides nothing, and differences with it stay in 32 bits)
+  p.scale = scale; p.window = window < (1 << 30) ? window : 1 << 30;
+  p.out = out; p.lse = lse; p.workspace = workspace;
   return gptq::to_status(gptq::launch_chunk_attention(p, static_cast<cudaStream_t>(stream)));
 }

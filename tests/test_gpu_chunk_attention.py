@@ -184,7 +184,8 @@ def test_many_sequences_and_one_long_one():
 
 def test_rows_before_the_first_key_are_zero():
     # fewer keys than new tokens: the first rows stand before the sequence
-    check(Case([40, 9, 300], [33, 0, 170], 8, 2, 64, 16, torch.float16, seed=2, pad=1))
+    for window in (0, 50, 2 ** 31 - 1):
+        check(Case([40, 9, 300], [33, 0, 170], 8, 2, 64, 16, torch.float16, seed=2, pad=1), window=window)
 
 
 @pytest.mark.parametrize("scale", [1.0, -0.7, 0.0])
