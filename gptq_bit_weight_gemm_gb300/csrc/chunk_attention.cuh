@@ -127,7 +127,7 @@ struct Control {
 };
 
 // What is left of a cut item for the joining kernel, by the run that holds the item's first tile.
-struct Record {
+struct alignas(16) Record {
   int valid, first_run, last_run, kv_head, first, row0, rows, pad;
 };
 
@@ -820,7 +820,7 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
         key = t * kKeys + lw * kWarpKeys + lane;
         want = lane < kWarpKeys && key >= it.key_lo && key < it.key_hi;
         entry = static_cast<int>(static_cast<unsigned long long>(static_cast<unsigned>(key)) * a.page_mul >> a.page_shift);
-        page = want ? __ldg(table + entry) : -1;
+        page = want ? __ldcg(table + entry) : -1;          // (an earlier kernel that overlaps with this one may have written it)
       };
       fetch(it.t0);
       auto queries_of = [&]() {            // row r of the item is token r / group, head r % group
@@ -1159,15 +1159,18 @@ __global__ void __launch_bounds__(Shape<DP>::kRows) k_join(const __grid_constant
   const ChunkProblem& p = a.p;
   decode::pdl_launch_dependents();
   decode::pdl_wait();
-  Record rec = a.records[blockIdx.x];
+  Record rec;
+  reinterpret_cast<int4*>(&rec)[0] = __ldcg(reinterpret_cast<const int4*>(a.records + blockIdx.x));
+  reinterpret_cast<int4*>(&rec)[1] = __ldcg(reinterpret_cast<const int4*>(a.records + blockIdx.x) + 1);
   rec.last_run = min(rec.last_run, static_cast<int>(gridDim.x) - 1);   // (past it only where lengths were written meanwhile)
   const int row = threadIdx.x, col = blockIdx.y * kJoinCols;
   if (!rec.valid || row >= rec.rows || col >= p.head_dim) return;
   auto part_of = [&](int run) {
     return a.partials + static_cast<size_t>(2 * run + (run == rec.first_run ? 1 : 0)) * partial_floats<DP>();
   };
-  // kBatch parts in flight at a time (64 tokens on 4000 keys: 28.5 us with one after the other, 25.1 so)
-  constexpr int kBatch = 4;
+  // kBatch parts in flight at a time (64 tokens on 4000 keys / the mixed batch of 16: 28.5 / 111 us with one after the
+  // other, 24.7 / 108 so, 25.3 / 113 with four, which leave fewer CTAs an SM)
+  constexpr int kBatch = 2;
   float top = -CUDART_INF_F, l = 0.f, o[kJoinCols] = {};
   for (int run0 = rec.first_run; run0 <= rec.last_run; run0 += kBatch) {
     float2 ml[kBatch];

@@ -297,6 +297,70 @@ def test_captured_and_replayed_with_other_contents():
             assert bool((out[ref.shape[0]:] == MARK).all())
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_keys_and_values_in_different_layouts_and_shared_heads(dim):
+    c = Case(NEW, LENS, 8, 4, dim, 16, torch.float16, seed=8)
+    a = c.gpu()
+    want = check(c, a=a)
+    # values in another order than keys, then with padding between rows
+    a["v_cache"] = a["v_cache"].permute(0, 2, 1, 3).contiguous().permute(0, 2, 1, 3)
+    assert torch.equal(check(c, a=a), want)
+    wide = torch.full(a["v_cache"].shape[:3] + (dim + 24,), float("nan"), dtype=torch.float16, device=DEV)
+    wide[..., :dim] = a["v_cache"]
+    a["v_cache"] = wide[..., :dim]
+    assert torch.equal(check(c, a=a), want)
+    # one head's keys and values for all: strides of zero
+    c = Case(NEW, LENS, 8, 1, dim, 16, torch.float16, seed=9)
+    want = check(c)
+    a = c.gpu()
+    for name in ("k_cache", "v_cache"):
+        a[name] = a[name].expand(-1, -1, 4, -1)
+    out = torch.full((c.tokens, 8, dim), MARK, dtype=torch.float16, device=DEV)
+    g.chunk_attention(**a, out=out)
+    # (the rows of an item are others, and with them what is joined: the tolerance, not the bits)
+    ref, tol, _, _ = c.ref(dim ** -0.5, 0)
+    assert bool(((out.double() - ref).abs() <= tol).all()) and bool(torch.isfinite(want).all())
+
+
+def test_two_calls_at_once():
+    cases = [Case([500, 1, 60], [3000, 2000, 60], 16, 4, 128, 16, torch.bfloat16, seed=i) for i in (20, 21)]
+    args = [c.gpu() for c in cases]
+    want = [check(c, a=a) for c, a in zip(cases, args)]
+    streams = [torch.cuda.Stream() for _ in cases]
+    spaces = [g.chunk_attention_workspace(16, 4, 128) for _ in cases]
+    torch.cuda.synchronize()
+    got = []
+    for turn in range(10):
+        for a, s, w in zip(args, streams, spaces):
+            got.append(g.chunk_attention(**a, workspace=w, stream=s))
+    torch.cuda.synchronize()
+    for i, out in enumerate(got):
+        assert torch.equal(out, want[i % 2])
+
+
+def test_infinite_values_of_keys_that_every_row_sees():
+    # far behind the chunk, in tiles that all rows see: infinite where it is, not a number elsewhere never
+    c = Case([40], [900], 8, 2, 64, 16, torch.bfloat16, seed=10)
+    a = c.gpu()
+    clean = check(c, a=a)
+    at = c.pages[0][0][300], c.pages[0][1][300]
+    a["v_cache"][at][:, 5] = float("inf")
+    out = g.chunk_attention(**a)
+    assert bool((out[..., 5] == float("inf")).all())
+    rest = torch.arange(64, device=DEV) != 5
+    assert torch.equal(out[..., rest], clean[..., rest])
+    # a score of minus infinity is a key that does not count
+    a = c.gpu()
+    a["q"][:, :, 0] = 1.0
+    c.q[:, :, 0] = 1.0
+    a["k_cache"][at][:, 0] = float("-inf")
+    out = g.chunk_attention(**a)
+    keep = torch.arange(900) != 300
+    c.keys[0], c.values[0], c.lens, c.new = c.keys[0][keep], c.values[0][keep], [899], [40]
+    ref, tol, _, _ = c.ref(64 ** -0.5, 0)
+    assert bool(((out.double() - ref).abs() <= tol).all())
+
+
 def test_side_stream_and_current_stream_is_another():
     c = Case([100, 1, 30], [140, 900, 30], 8, 2, 64, 16, torch.float16, seed=5)
     a = c.gpu()

@@ -161,7 +161,7 @@ def test_generate_from_prompts(example):
     assert g.device_status() == 0
 
 
-def test_chain_captured_and_replayed():
+def test_chain_captured_replayed_and_without_waits():
     # plan, norm, rotary with the append and attention in one graph, its lengths changing from replay to replay
     B, T, heads, kv, dim, page, width = 5, 64, 8, 2, 64, 16, 20
     gen = torch.Generator(device=DEV).manual_seed(4)
@@ -207,4 +207,31 @@ def test_chain_captured_and_replayed():
         assert torch.equal(h, h_held) and torch.equal(eager["out"][:rows], held["out"][:rows])
         assert torch.equal(eager["cache"].view(torch.int16), held["cache"].view(torch.int16))
         assert bool(torch.isfinite(held["out"][:rows]).all())
+    assert g.device_status() == 0
+    # the same steps issued one after the other with nothing waited for between them
+    steps = [[3, 20, 1, 0, 40], [1, 1, 1, 1, 1], [0, -15, 30, 5, -41], [60, 0, 0, 0, 4], [-64, -6, 9, 16, 16]] * 4
+    alone = []
+    for waits in (True, False):
+        s = state()
+        gen.manual_seed(99)
+        s["x"].normal_(generator=gen), s["qkv"].normal_(generator=gen)
+        ahead = torch.tensor(steps, dtype=torch.int32, device=DEV)
+        torch.cuda.synchronize()
+        outs = []
+        for i in range(len(steps)):
+            if i % 5 == 0 and i:
+                s["added"].copy_(-s["lens"])           # everything ends, and the pages come back in another order
+                chain(s)
+            s["added"].copy_(ahead[i])
+            chain(s)
+            outs.append(s["out"].clone())
+            if waits:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        alone.append((outs, s))
+    for a, b, added in zip(alone[0][0], alone[1][0], steps):
+        rows = sum(max(0, x) for x in added)
+        assert torch.equal(a[:rows], b[:rows])
+    for name in ("lens", "table", "free", "count", "res"):
+        assert torch.equal(alone[0][1][name], alone[1][1][name]), name
     assert g.device_status() == 0
