@@ -48,7 +48,8 @@
 // no spills 2334 / 394 / 148; copies handed on as they land, P in halves, 128-byte blocks 2000 / 396 / 152; MMAs issued by
 // a converged warp (a lone thread's descriptors go through vector registers: 125 cycles an MMA, against 64 of the
 // tensor cores) 1648 / 335 / 135; TMA boxes, tiles at the diagonal looked over by two warps 1391 / 330 / 117; results in
-// 64-byte pieces 1330 / 331 / 111; items dealt out whole 1330 / 228 / 112.
+// 64-byte pieces 1330 / 331 / 111; items dealt out whole 1330 / 228 / 112; joins two parts at a time, the table past the
+// first-level cache 1345 / 227 / 109; the scores' MMAs unrolled for more head_dims 1315 / 225 / 106.
 #pragma once
 
 #include <cuda.h>
