@@ -136,7 +136,8 @@ int gptq_rotary(const void* q, const void* k, const void* v, int tokens, int hea
  * fp32, the probabilities enter the product with v in dtype, out is rounded once.  A row whose position
  * is negative (seq_lens[b] < m) gives zeros.  Rows outside every sequence are left as they were.  What a row does
  * not see is not used for it, whatever it holds: cache slots, block-table entries past a sequence's
- * length, infinite or NaN values of later tokens.
+ * length, infinite or NaN values of later tokens.  An infinite or NaN value that a row sees reaches it, however
+ * small its probability.
  *   q            [tokens, heads, head_dim]: heads of a token contiguous, tokens strides[0] apart
  *   k/v_cache    [pages, page_size, kv_heads, head_dim] in any order of the first three
  *   strides      HOST array of 7 strides in elements, multiples of 8 (anything where the dimension is
