@@ -169,6 +169,10 @@ extern "C" int gptq_rotary(const void* q, const void* k, const void* v, int toke
     int rc = gptq::cache_strides(strides + 5, pages, page_size, kv_heads, head_dim, ks);
     if (rc == GPTQ_OK) rc = gptq::cache_strides(strides + 8, pages, page_size, kv_heads, head_dim, vs);
     if (rc) return rc;
+    // rows of a cache that overlap would be written by several heads or tokens
+    const int steps[3] = {pages, page_size, kv_heads};
+    for (int i = 0; i < 3; ++i)
+      if (steps[i] > 1 && (ks[i] < head_dim || vs[i] < head_dim)) return GPTQ_ERR_SHAPE;
     p.k_page = ks[0]; p.k_slot = ks[1]; p.k_head = ks[2];
     p.v_page = vs[0]; p.v_slot = vs[1]; p.v_head = vs[2];
   }

@@ -114,7 +114,8 @@ int gptq_rotary_table(int rot_dim, double theta, int scaling, double factor, dou
  *   k/v_cache    nullable (both or neither, with v and slots): [pages, page_size, kv_heads, head_dim] in
  *                any order of the first three, strides[5..10] = k page, k slot, k head, v page, v slot,
  *                v head; row t's rotated key and its value go to slot slots[t] (int64: page * page_size +
- *                place), nowhere where that is negative; no two rows may have the same slot
+ *                place), nowhere where that is negative; no two rows may have the same slot.  A cache whose
+ *                rows overlap (a stride below head_dim) is refused with GPTQ_ERR_SHAPE
  *   positions    [tokens] int32          turns [rot_dim / 2], from gptq_rotary_table
  *   strides      HOST array of 11, in elements, multiples of 8 (anything where the dimension is one, or
  *                the tensor absent)
