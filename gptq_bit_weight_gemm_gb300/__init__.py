@@ -824,6 +824,18 @@ def _fresh(rt, stream, like, shape, dtype):
     return rt.empty(shape, dtype=dtype, device=like.device) if stream is None else _new(stream, like, shape, dtype)
 
 
+def _int32(value, name):
+    """A whole number that a C int holds (ctypes would drop the bits above)."""
+    if not -2 ** 31 <= value < 2 ** 31:
+        raise ValueError("%s does not fit 32 bits: %d" % (name, value))
+    return value
+
+
+def _window(window):
+    """A window as a C int: positions are below 2^30, so that one past 32 bits hides nothing."""
+    return window if 0 <= window < 2 ** 31 else (2 ** 31 - 1 if window > 0 else -1)
+
+
 def _raw_stream(rt, stream, device):
     if stream is None:
         return rt.stream()
@@ -841,6 +853,8 @@ def page_plan(cached, added, block_table, free_pages, free_count, *, page_size, 
     positions [max_tokens], slots [max_tokens] int64): sequence b's new tokens are rows cu_tokens[b] ..
     cu_tokens[b + 1]; rows behind the last have position 0 and slot -1.  seq_lens, when given, is written
     there (it may be `cached`); the new count goes to free_count_out, where given, and to free_count itself."""
+    _int32(page_size, "page_size")
+    _int32(max_tokens, "max_tokens")
     rt = _rt or _runtime()
     device, i32 = rt.device(), rt.int32
     (batch,) = cached.shape
@@ -940,7 +954,7 @@ def rotary_table(rot_dim, *, theta=10000.0, scaling="none", factor=1.0, original
     ln(factor) + 1) or in the turns ("bands")."""
     if scaling not in ROTARY_SCALINGS:
         raise ValueError("scaling must be one of %s, got %r" % (", ".join(ROTARY_SCALINGS), scaling))
-    turns = np.empty(max(0, rot_dim // 2), dtype=np.int64)
+    turns = np.empty(max(0, _int32(rot_dim, "rot_dim") // 2), dtype=np.int64)
     amplitude = _D(1.0)
     _check(lib().gptq_rotary_table(rot_dim, theta, ROTARY_SCALINGS[scaling], factor, original, low, high,
                                    turns.ctypes.data_as(ctypes.POINTER(_ULL)), ctypes.byref(amplitude)), "gptq_rotary_table")
@@ -1054,7 +1068,7 @@ def chunk_attention(q, k_cache, v_cache, block_table, seq_lens, cu_tokens, *, sc
     strides = _ChunkStrides(qs, ks[0], ks[1], ks[2], vs[0], vs[1], vs[2])
     rc = rt.lib.gptq_chunk_attention(q.data_ptr(), tokens, heads, code, k_cache.data_ptr(), v_cache.data_ptr(), pages, page_size,
                                      kv_heads, dim, strides, t_ptr, width, l_ptr, c_ptr, batch,
-                                     dim ** -0.5 if scale is None else scale, window, o_ptr, lse_ptr, ws, ws_bytes, raw)
+                                     dim ** -0.5 if scale is None else scale, _window(window), o_ptr, lse_ptr, ws, ws_bytes, raw)
     if rc:
         _check(rc, "gptq_chunk_attention")
     return out

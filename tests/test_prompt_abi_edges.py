@@ -2,6 +2,7 @@
 anything is launched, so none of this needs a GPU."""
 import pytest
 
+import gptq_bit_weight_gemm_gb300 as g
 from test_prompt_abi import APPEND, lib, rotary  # noqa: F401
 
 
@@ -19,3 +20,26 @@ def test_rotary_does_not_look_at_strides_of_dimensions_of_one(lib):  # noqa: F81
     from test_prompt_abi import P
     strides = (512, 128, 128, 512, 128, 0, 0, 0, 0, 0, 0)
     assert rotary(lib, **dict(APPEND, pages=1, page=1, kv=1, strides=strides, positions=P(0x10002))) == -3
+
+
+# ------------------------------------------------------------------------------ whole numbers past 32 bits, from Python
+@pytest.mark.parametrize("name", ["page_size", "max_tokens"])
+@pytest.mark.parametrize("value", [2 ** 32 + 16, 2 ** 31, -2 ** 32 + 16])
+def test_page_plan_refuses_numbers_past_32_bits(name, value):
+    with pytest.raises(ValueError, match=name):
+        g.page_plan(None, None, None, None, None, **dict(dict(page_size=16, max_tokens=16), **{name: value}))
+
+
+@pytest.mark.parametrize("rot", [2 ** 32 + 64, 2 ** 31, -2 ** 32 + 64])
+def test_rotary_table_refuses_numbers_past_32_bits(rot):
+    with pytest.raises((ValueError, g.GPTQError)):
+        g.rotary_table(rot, device="cpu")
+
+
+@pytest.mark.parametrize("window,used", [(0, 0), (5, 5), (2 ** 31 - 1, 2 ** 31 - 1), (2 ** 31, 2 ** 31 - 1), (2 ** 32 + 5, 2 ** 31 - 1)])
+def test_a_window_past_32_bits_hides_nothing(window, used):
+    assert g._window(window) == used
+
+
+def test_a_negative_window_stays_negative():
+    assert g._window(-1) == -1 and -2 ** 31 <= g._window(-2 ** 32 + 5) < 0
