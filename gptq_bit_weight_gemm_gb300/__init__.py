@@ -851,8 +851,9 @@ def page_plan(cached, added, block_table, free_pages, free_count, *, page_size, 
     [capacity] (its first free_count [1] entries), pages needed are taken from its end and entered into
     block_table [batch, width], both updated in place.  Returns (seq_lens [batch], cu_tokens [batch + 1],
     positions [max_tokens], slots [max_tokens] int64): sequence b's new tokens are rows cu_tokens[b] ..
-    cu_tokens[b + 1]; rows behind the last have position 0 and slot -1.  seq_lens, when given, is written
-    there (it may be `cached`); the new count goes to free_count_out, where given, and to free_count itself."""
+    cu_tokens[b + 1]; rows behind the last have position 0 and slot -1.  A sequence for which no pages are left (or
+    no room in the table; device_status() says so) keeps its length, and what chunk_attention gives its rows
+    means nothing.  seq_lens, when given, is written there (it may be `cached`); the new count goes to free_count_out, where given, and to free_count itself."""
     _int32(page_size, "page_size")
     _int32(max_tokens, "max_tokens")
     rt = _rt or _runtime()

@@ -48,7 +48,9 @@ extern "C" {
  *                sequence get position 0 and slot -1, so that a padded step writes nothing for them
  * seq_lens may be cached itself, and free_count_out free_count; other buffers must not overlap.
  * A sequence that would be longer than the block table (GPTQ_DEV_SEQ_LEN), or one from which on the list
- * has too few pages (GPTQ_DEV_NO_PAGE), keeps its length and pages; its rows stay, with slots -1.  cached
+ * has too few pages (GPTQ_DEV_NO_PAGE), keeps its length and pages; its rows stay, with slots -1: gptq_rotary
+ * appends nothing for them, and what gptq_chunk_attention, which counts positions back from seq_lens, gives them
+ * means nothing and is to be left out; the other sequences' rows are not touched by it.  cached
  * outside [0, table] and added below -cached are cut (GPTQ_DEV_SEQ_LEN); a page given back to a full list
  * is lost (GPTQ_DEV_NO_PAGE); rows past max_tokens are left out and cu_tokens is cut
  * (GPTQ_DEV_TOKEN_ROWS).  batch up to 8192, table_width * page_size, free_capacity and max_tokens up to 2^30;
@@ -135,7 +137,8 @@ int gptq_rotary(const void* q, const void* k, const void* v, int tokens, int hea
  * the keys j in [max(0, t - window + 1), t] (window 0: [0, t]), k and v of head h / (heads / kv_heads).  Key j
  * is slot j % page_size of page block_table[b, j / page_size].  Sums, maxima and accumulators are
  * fp32, the probabilities enter the product with v in dtype, out is rounded once.  A row whose position
- * is negative (seq_lens[b] < m) gives zeros.  Rows outside every sequence are left as they were.  What a row does
+ * is negative (seq_lens[b] < m) gives zeros.  Rows outside every sequence are left as they were; a row that
+ * cu_tokens gives to two sequences (GPTQ_DEV_TOKEN_ROWS) gets the result of either.  What a row does
  * not see is not used for it, whatever it holds: cache slots, block-table entries past a sequence's
  * length, infinite or NaN values of later tokens.  An infinite or NaN value that a row sees reaches it, however
  * small its probability.
