@@ -1,6 +1,6 @@
 """gptq_chunk_attention at edges that the sizes and masks do not reach: infinite values under probabilities that are
-nothing in 16 bits.  A probability is above 0 in the definition, however small: an infinite value of a key that a row
-sees is infinite in the row, wherever the key lies."""
+nothing in 16 bits, and lengths and rows that do not fit.  A probability is above 0 in the definition, however
+small: an infinite value of a key that a row sees is infinite in the row, wherever the key lies."""
 import pytest
 import torch
 
@@ -72,3 +72,44 @@ def test_rows_of_a_nan_score_and_finite_sums_beside_infinite_ones():
     assert bool((out[live][:, 3] == float("inf")).all())
     rest = torch.arange(64, device=DEV) != 3
     assert bool(torch.isfinite(out[live][:, rest]).all())
+
+
+def test_a_length_past_the_table_is_cut_to_it():
+    c = Case([40, 33], [48, 33], 8, 2, 64, 16, torch.float16, seed=21, pad=2)
+    a = c.gpu()
+    a["block_table"] = a["block_table"][:, :3].contiguous()          # 48 keys
+    clean = check(c, a=a)
+    for length in (49, 1000, 2 ** 31 - 1):
+        a["seq_lens"][0] = length
+        assert torch.equal(check(c, a=a), clean)
+        assert g.device_status() == g.DEV_SEQ_LEN
+
+
+def test_rows_that_decrease_or_lie_outside():
+    c = Case([40, 50, 33], [40, 60, 33], 8, 2, 64, 16, torch.float16, seed=6, pad=5)
+    a = c.gpu()
+    check(c, a=a)
+    ref, tol, _, _ = c.ref(c.dim ** -0.5, 0)
+
+    def rows(cu):
+        a["cu_tokens"].copy_(torch.tensor(cu))
+        out = torch.full((c.tokens, 8, 64), MARK, dtype=torch.float16, device=DEV)
+        g.chunk_attention(**a, out=out)
+        return out, lambda x, y: bool(((out[x:y].double() - ref[x:y]).abs() <= tol[x:y]).all())
+    # the first sequence is cut to its rows from 0 on, the second has none, the third gets 103 rows for 33 keys: 20 .. 39 are
+    # the first's too, 40 .. 89 stand before its first key
+    out, right = rows([-7, 40, 20, 123])
+    assert g.device_status() == g.DEV_TOKEN_ROWS
+    assert right(0, 20) and right(90, 123)
+    twice = (out[20:40].double() - ref[20:40]).abs() <= tol[20:40]
+    assert bool((twice | (out[20:40] == 0)).all())
+    assert bool((out[40:90] == 0).all()) and bool((out[123:] == MARK).all())
+    # no rows but the middle sequence's
+    out, right = rows([40, 40, 90, 90])
+    assert g.device_status() == 0
+    assert right(40, 90) and bool((out[:40] == MARK).all()) and bool((out[90:] == MARK).all())
+    # all of them outside
+    for cu in ([-9, -8, -2, -1], [500, 600, 700, 800]):
+        out, _ = rows(cu)
+        assert g.device_status() == g.DEV_TOKEN_ROWS
+        assert bool((out == MARK).all())
