@@ -73,8 +73,9 @@ int gptq_page_plan(const int32_t* cached, const int32_t* added, int batch, int p
  *   weight       nullable [hidden] of weight_dtype: ones where absent
  *   out          [rows, hidden] of out_dtype, rows out_stride elements apart (may be x, with its type
  *                and stride)
- * hidden up to 2^20.  Pointers aligned to their elements; rows that start on 16 bytes are read
- * and written 16 bytes at a time.  rows == 0 is a no-op.
+ * hidden up to 2^20.  Pointers aligned to their elements; where the rows of x, out and the residuals all start
+ * on 16 bytes, or all as many elements behind such a place, they are read and written 16 bytes at a time, otherwise
+ * one element at a time.  Buffers other than those named must not overlap.  rows == 0 is a no-op.
  */
 int gptq_rms_norm(const void* x, int rows, int hidden, long long x_stride, int dtype, const void* residual,
                   long long residual_stride, int residual_dtype, void* residual_out,
