@@ -844,7 +844,9 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
         key = t * kKeys + lw * kWarpKeys + lane;
         want = lane < kWarpKeys && key >= it.key_lo && key < it.key_hi;
         entry = static_cast<int>(static_cast<unsigned long long>(static_cast<unsigned>(key)) * a.page_mul >> a.page_shift);
-        page = want ? __ldcg(table + entry) : -1;          // (an earlier kernel that overlaps with this one may have written it)
+        // (read once: past the first-level cache.  Not by the read-only path, which asks that nobody writes while this kernel
+        // lives: it may have been launched while the plan was still being written, and waits for that above)
+        page = want ? __ldcg(table + entry) : -1;
       };
       fetch(it.t0);
       auto queries_of = [&]() {            // row r of the item is token r / group, head r % group

@@ -7,7 +7,7 @@
 // Bound: latency.  The data are a few bytes a token; the chain is launch - lengths - sums - free list - table.
 //
 // One cluster of CTAs: each makes the same sums for itself and takes a share of the pages and rows, found back by
-// bisection in the sums.  Two cluster barriers order the steps: pages given back before pages taken (the same
+// bisection in the sums.  One cluster barrier orders the steps: pages given back before pages taken (the same
 // places of the list), and all reading of the inputs before what may be written over them.
 #include <limits.h>
 
