@@ -313,9 +313,11 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
 
   decode::pdl_launch_dependents();
   if (warp == S::kLoadWarp0 && lane == 0) {
-    ptx::prefetch_tmap(&map_k);
-    ptx::prefetch_tmap(&map_v);
-    ptx::prefetch_tmap(&map_q);
+    if (a.box_rows) {                      // (the others hold nothing)
+      ptx::prefetch_tmap(&map_k);
+      ptx::prefetch_tmap(&map_v);
+    }
+    if (a.q_boxes) ptx::prefetch_tmap(&map_q);
   }
   decode::pdl_wait();
 
@@ -499,7 +501,6 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
         return static_cast<int>(unit < cut ? divide(unit, share + 1) : extra + divide(unit - cut, share));
       };
       Record record = {};
-      bool ok = true;
       uint32_t n = 0;                      // items handed out
       while (true) {
         const bool out = deal && !deal_next();
@@ -507,10 +508,7 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
         const long long tile0 = start + kItemUnits, stop = start + u;
         const bool done = out || tile0 >= end_unit;
         const int slot = n & 1;
-        if (!wait(c.iempty[slot], ((n >> 1) & 1) ^ 1)) {
-          ok = false;
-          break;
-        }
+        if (!wait(c.iempty[slot], ((n >> 1) & 1) ^ 1)) break;
         Item it;
         it.b = done ? -1 : b;
         if (!done) {
@@ -572,7 +570,6 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
         }
       }
       if (lane == 0) a.records[run] = record;
-      (void)ok;
     } else if (warp == S::kMmaWarp) {
       // -------------------------------------------------------------- MMAs
       const int kd = (p.head_dim + 15) / 16;
