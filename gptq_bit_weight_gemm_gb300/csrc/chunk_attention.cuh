@@ -585,26 +585,15 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
       // Descriptors hold addresses in units of 16 bytes in their lowest bits: a step is an addition of a constant.
       const uint64_t q_desc = ptx::umma_desc_sw128_kmajor(sbase), k_desc = ptx::umma_desc_sw128_kmajor(sbase + S::kOffKV);
       const uint64_t v_desc = ptx::umma_desc_sw128_mnmajor(sbase + S::kOffKV, kKeys * 128);
-      auto scores = [&](int s, int at) {   // S[s] = q[s] k^T
+      auto scores = [&](int s, int at, auto steps) {       // S[s] = q[s] k^T
         const uint64_t qd = q_desc + s * (S::kQBytes >> 4), kt = k_desc + at * (S::kTileBytes >> 4);
         auto step = [&](int k) {
           ptx::umma_f16_by(leader, s_col(s), qd + ((k >> 2) * 128 * 128 + (k & 3) * 32) / 16,
                            kt + ((k >> 2) * kKeys * 128 + (k & 3) * 32) / 16, idesc_s, k != 0);
         };
-        auto steps = [&](auto n) {
+        if constexpr (steps.value > 0) {
 #pragma unroll
-          for (int k = 0; k < n.value; ++k) step(k);
-        };
-        // (Unrolled where head_dim fills DP, and at 80 and 96 in a DP of 128: a loop makes its
-        // descriptors anew for each MMA.  4096 tokens on 28672, 32 heads of 8 caches: at 96
-        // 1271 us against 1391 in the loop, at 80 1318 against 1330.  At a DP of 64 further
-        // unrolled forms cost 7 %, 1321 us against 1240; at 256 they change nothing.)
-        if (kd == DP / 16) {
-          steps(std::integral_constant<int, DP / 16>());
-        } else if (DP == 128 && kd == 6) {
-          steps(std::integral_constant<int, 6>());
-        } else if (DP == 128 && kd == 5) {
-          steps(std::integral_constant<int, 5>());
+          for (int k = 0; k < steps.value; ++k) step(k);
         } else {
 #pragma unroll 1
           for (int k = 0; k < kd; ++k) step(k);
@@ -621,63 +610,81 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
       auto next_stage = [&]() {
         if (++stage == S::kStages) stage = 0, phase ^= 1;
       };
-      while (ok) {
-        const int slot = items & 1;
-        if (!wait(c.ifull[slot], (items >> 1) & 1)) { ok = false; break; }
-        ++items;
-        const Item& from = c.item[slot];
-        if (from.b < 0) break;
-        struct { int t0, t1, lo[2], hi[2]; } it = {from.t0, from.t1, {from.lo[0], from.lo[1]}, {from.hi[0], from.hi[1]}};
-        __syncwarp();
-        if (leader) ptx::mbar_arrive(bar(c.iempty[slot]));
-        if (it.t0 >= it.t1) continue;
-        auto live = [&](int s, int t) { return s < kNQ && t >= it.lo[s] && t < it.hi[s]; };
-        if (!wait(c.qfull, queries & 1)) { ok = false; break; }
-        ++queries;
-        // the first tile's scores; from then on p v of a tile, then the scores of the next, accumulator by accumulator
-        if (!wait(c.full[stage], phase)) { ok = false; break; }
-        ptx::tc_fence_after();
-#pragma unroll
-        for (int s = 0; s < kNQ; ++s)
-          if (live(s, it.t0)) scores(s, stage);
-        commit(c.empty[stage]);
-        if (it.t0 + 1 == it.t1) commit(c.qempty);
-        next_stage();
-        for (int t = it.t0; t < it.t1; ++t) {
-          const int v_stage = stage;
+      // All items; a scores' product takes `steps` MMAs, as many as kd says where that is 0.  One sequence of MMAs stands in
+      // the loop over the tiles, chosen before it.
+      auto products = [&](auto steps) {
+        while (ok) {
+          const int slot = items & 1;
+          if (!wait(c.ifull[slot], (items >> 1) & 1)) { ok = false; break; }
+          ++items;
+          const Item& from = c.item[slot];
+          if (from.b < 0) break;
+          struct { int t0, t1, lo[2], hi[2]; } it = {from.t0, from.t1, {from.lo[0], from.lo[1]}, {from.hi[0], from.hi[1]}};
+          __syncwarp();
+          if (leader) ptx::mbar_arrive(bar(c.iempty[slot]));
+          if (it.t0 >= it.t1) continue;
+          auto live = [&](int s, int t) { return s < kNQ && t >= it.lo[s] && t < it.hi[s]; };
+          if (!wait(c.qfull, queries & 1)) { ok = false; break; }
+          ++queries;
+          // the first tile's scores; from then on p v of a tile, then the scores of the next, accumulator by accumulator
           if (!wait(c.full[stage], phase)) { ok = false; break; }
-          next_stage();
-          bool have_k = false;
+          ptx::tc_fence_after();
 #pragma unroll
-          for (int s = 0; s < kNQ; ++s) {
-            if (live(s, t)) {
-              if (!wait(c.pready[s][0], p_phase[s])) { ok = false; break; }
-              ptx::tc_fence_after();
-              values(s, v_stage, 0, t > it.lo[s]);
-              if (!wait(c.pready[s][1], p_phase[s])) { ok = false; break; }
-              p_phase[s] ^= 1;
-              ptx::tc_fence_after();
-              values(s, v_stage, 1, true);
-              if (t + 1 == it.hi[s]) commit(c.ofull[s]);
-            }
-            if (live(s, t + 1)) {
-              if (!have_k) {
-                if (!wait(c.full[stage], phase)) { ok = false; break; }
-                ptx::tc_fence_after();
-                have_k = true;
-              }
-              scores(s, stage);
-            }
-          }
-          if (!ok) break;
-          commit(c.empty[v_stage]);
-          if (t + 1 < it.t1) {
-            if (!have_k && !wait(c.full[stage], phase)) { ok = false; break; }
-            commit(c.empty[stage]);
-            if (t + 2 == it.t1) commit(c.qempty);
+          for (int s = 0; s < kNQ; ++s)
+            if (live(s, it.t0)) scores(s, stage, steps);
+          commit(c.empty[stage]);
+          if (it.t0 + 1 == it.t1) commit(c.qempty);
+          next_stage();
+          for (int t = it.t0; t < it.t1; ++t) {
+            const int v_stage = stage;
+            if (!wait(c.full[stage], phase)) { ok = false; break; }
             next_stage();
+            bool have_k = false;
+#pragma unroll
+            for (int s = 0; s < kNQ; ++s) {
+              if (live(s, t)) {
+                if (!wait(c.pready[s][0], p_phase[s])) { ok = false; break; }
+                ptx::tc_fence_after();
+                values(s, v_stage, 0, t > it.lo[s]);
+                if (!wait(c.pready[s][1], p_phase[s])) { ok = false; break; }
+                p_phase[s] ^= 1;
+                ptx::tc_fence_after();
+                values(s, v_stage, 1, true);
+                if (t + 1 == it.hi[s]) commit(c.ofull[s]);
+              }
+              if (live(s, t + 1)) {
+                if (!have_k) {
+                  if (!wait(c.full[stage], phase)) { ok = false; break; }
+                  ptx::tc_fence_after();
+                  have_k = true;
+                }
+                scores(s, stage, steps);
+              }
+            }
+            if (!ok) break;
+            commit(c.empty[v_stage]);
+            if (t + 1 < it.t1) {
+              if (!have_k && !wait(c.full[stage], phase)) { ok = false; break; }
+              commit(c.empty[stage]);
+              if (t + 2 == it.t1) commit(c.qempty);
+              next_stage();
+            }
           }
         }
+      };
+      // (Unrolled where head_dim fills DP, and in a DP of 128 always: a loop makes its descriptors anew for each MMA.
+      // 4096 tokens on 28672, 32 heads of 8 caches: at 112 1270-1390 us against 1470-1500 in the loop, at 104 1335
+      // against 1495, at 96 1271 against 1391.  At a DP of 64 unrolled forms for the smaller head_dims cost 7 %, at
+      // 256 they changed nothing.  Chosen here and not within the tiles' loop: at 128 1283 us against 1308, at 80
+      // 1225 against 1319, at 64 1224 against 1246, at 256 990 against 982, a mixed batch 103.5 against 108.)
+      if (kd == DP / 16) {
+        products(std::integral_constant<int, DP / 16>());
+      } else if constexpr (DP == 128) {
+        if (kd == 7) products(std::integral_constant<int, 7>());
+        else if (kd == 6) products(std::integral_constant<int, 6>());
+        else products(std::integral_constant<int, 5>());   // (head_dim is above 64)
+      } else {
+        products(std::integral_constant<int, 0>());
       }
       if (!ok) {
         // wait (bounded) for the MMAs already issued before tensor memory is released
