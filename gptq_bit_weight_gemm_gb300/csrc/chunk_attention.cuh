@@ -73,7 +73,7 @@ namespace chunk {
 
 constexpr int kMaxRuns = 160;            // CTAs, at most: one on each of the 152 SMs
 constexpr size_t kRecordBytes = kMaxRuns * 32;
-constexpr uint64_t kWaitLimitNs = 2000000000ull;
+constexpr uint64_t kDrainLimitNs = 2000000000ull;   // for what is in flight when a wait has given up
 constexpr float kGrow = 8.f;             // log2 of what a row's maximum may grow by before o is rescaled
 // An item counts as its tiles and kItemUnits more: opening and closing it.
 constexpr int kItemUnits = 3;
@@ -208,21 +208,21 @@ template <int N>
 __device__ __forceinline__ void shrink_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
 // Bounded wait on an mbarrier phase; false if the wait ran out or another role gave up.  All lanes agree.
-__device__ __forceinline__ bool wait_one(uint32_t bar, uint32_t parity, volatile int* abort, unsigned* status) {
+__device__ __forceinline__ bool wait_one(uint32_t bar, uint32_t parity, volatile int* abort, const ChunkProblem& p) {
   if (ptx::mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = ptx::globaltimer();
+  const uint32_t t0 = static_cast<uint32_t>(ptx::globaltimer());   // (limits are below 2^32 ns, and 64 bits cost registers)
   while (true) {
-    if (ptx::mbar_try_wait_hint(bar, parity, 200000u)) return true;
+    if (ptx::mbar_try_wait_hint(bar, parity, min(p.wait_ns, 200000u))) return true;
     if (*abort) return false;
-    if (ptx::globaltimer() - t0 > kWaitLimitNs) {
+    if (static_cast<uint32_t>(ptx::globaltimer()) - t0 > p.wait_ns) {
       *abort = 1;
-      atomicOr(status, kStatusTimeout);
+      atomicOr(p.status, kStatusTimeout);
       return false;
     }
   }
 }
-__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int* abort, unsigned* status) {
-  return __all_sync(0xFFFFFFFFu, wait_one(bar, parity, abort, status));
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int* abort, const ChunkProblem& p) {
+  return __all_sync(0xFFFFFFFFu, wait_one(bar, parity, abort, p));
 }
 
 // x / y of nonnegative numbers: mostly they fit 32 bits
@@ -425,7 +425,7 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, c.tmem, 0);
   volatile int* const abort = &c.abort;
   auto bar = [&](unsigned long long& b) { return ptx::smem_addr(&b); };
-  auto wait = [&](unsigned long long& b, uint32_t parity) { return wait_warp(bar(b), parity, abort, p.status); };
+  auto wait = [&](unsigned long long& b, uint32_t parity) { return wait_warp(bar(b), parity, abort, p); };
   auto s_col = [&](int s) { return tmem + s * 128; };
   auto o_col = [&](int s) { return tmem + 256 + s * DP; };
 
@@ -690,7 +690,7 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
         // wait (bounded) for the MMAs already issued before tensor memory is released
         commit(c.drain);
         const uint64_t t0 = ptx::globaltimer();
-        while (!ptx::mbar_try_wait(bar(c.drain), 0) && ptx::globaltimer() - t0 < kWaitLimitNs) {}
+        while (!ptx::mbar_try_wait(bar(c.drain), 0) && ptx::globaltimer() - t0 < kDrainLimitNs) {}
         __syncwarp();
       }
     } else if (warp >= S::kLookWarp0) {
@@ -968,9 +968,9 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) k_chunk(const __grid_c
         if (boxed >> i & 1)
           while (!ptx::mbar_try_wait(looked >> i & 1 ? bar(c.raw[i]) : bar(c.full[i]),
                                      looked >> i & 1 ? raw_phase >> i & 1 : boxed_phase >> i & 1) &&
-                 ptx::globaltimer() - t0 < kWaitLimitNs) {}
+                 ptx::globaltimer() - t0 < kDrainLimitNs) {}
       if (q_sent)
-        while (!ptx::mbar_try_wait(bar(c.qfull), (queries & 1) ^ 1) && ptx::globaltimer() - t0 < kWaitLimitNs) {}
+        while (!ptx::mbar_try_wait(bar(c.qfull), (queries & 1) ^ 1) && ptx::globaltimer() - t0 < kDrainLimitNs) {}
       __syncwarp();
     }
   } else {

@@ -194,6 +194,16 @@ extern "C" int gptq_rotary(const void* q, const void* k, const void* v, int toke
   return gptq::to_status(gptq::launch_rotary(p, static_cast<cudaStream_t>(stream)));
 }
 
+namespace {
+thread_local unsigned chunk_wait_ns = gptq::kChunkWaitNs;
+}
+
+extern "C" int gptq_selftest_chunk_attention_wait(unsigned limit_ns) {
+  if (limit_ns > 4000000000u) return GPTQ_ERR_ARG;
+  chunk_wait_ns = limit_ns ? limit_ns : gptq::kChunkWaitNs;
+  return GPTQ_OK;
+}
+
 extern "C" size_t gptq_chunk_attention_workspace_size(int heads, int kv_heads, int head_dim) {
   if (heads <= 0 || kv_heads <= 0 || heads % kv_heads || heads > (1 << 16) || !gptq::head_dim_ok(head_dim)) return 0;
   return gptq::chunk_attention_workspace_bytes(heads, kv_heads, head_dim);
@@ -238,6 +248,6 @@ extern "C" int gptq_chunk_attention(const void* q, int tokens, int heads, int dt
   p.table = block_table; p.table_width = table_width; p.lens = seq_lens; p.cu = cu_tokens; p.batch = batch;
   // (positions are below 2^30: a wider window hides nothing, and differences with it stay in 32 bits)
   p.scale = scale; p.window = window < (1 << 30) ? window : 1 << 30;
-  p.out = out; p.lse = lse; p.workspace = workspace;
+  p.out = out; p.lse = lse; p.workspace = workspace; p.wait_ns = chunk_wait_ns;
   return gptq::to_status(gptq::launch_chunk_attention(p, static_cast<cudaStream_t>(stream)));
 }

@@ -93,8 +93,15 @@ struct ChunkProblem {
   float* lse;
   void* workspace;
   unsigned* status;
+  unsigned wait_ns;                // after which a wait inside the kernel gives up
 };
+constexpr unsigned kChunkWaitNs = 2000000000u;
 size_t chunk_attention_workspace_bytes(int heads, int kv_heads, int head_dim);
 cudaError_t launch_chunk_attention(const ChunkProblem& p, cudaStream_t stream);
 
 }  // namespace gptq
+
+// The library's own test hook: gptq_chunk_attention calls of this thread give up their waits after limit_ns (1 ns to 4 s;
+// 0: as long as ever), so that a test can have a valid call run into its failure path: GPTQ_DEV_TIMEOUT, results
+// that mean nothing, everything in flight waited for, and a context that stays usable.
+extern "C" int gptq_selftest_chunk_attention_wait(unsigned limit_ns);

@@ -1,5 +1,7 @@
 """Refusals of a prompt step's operators at the edges of what their arguments can say.  Every check answers before
 anything is launched, so none of this needs a GPU."""
+import ctypes
+
 import pytest
 
 import gptq_bit_weight_gemm_gb300 as g
@@ -43,3 +45,9 @@ def test_a_window_past_32_bits_hides_nothing(window, used):
 
 def test_a_negative_window_stays_negative():
     assert g._window(-1) == -1 and -2 ** 31 <= g._window(-2 ** 32 + 5) < 0
+
+
+def test_chunk_wait_hook_refuses_more_than_four_seconds(lib):  # noqa: F811
+    hook = lib.gptq_selftest_chunk_attention_wait
+    hook.restype, hook.argtypes = ctypes.c_int, [ctypes.c_uint]
+    assert hook(4 * 10 ** 9 + 1) == -1 and hook(4 * 10 ** 9) == 0 and hook(1) == 0 and hook(0) == 0
