@@ -126,7 +126,7 @@ extern "C" int gptq_rotary_table(int rot_dim, double theta, int scaling, double 
     if (limits) {
       double keep;
       if (scaling == GPTQ_ROTARY_RAMP)
-        keep = 1.0 - (i - first) / fmax(last - first, 0.001);
+        keep = i >= last ? 0.0 : 1.0 - (i - first) / fmax(last - first, 0.001);   // (last may lie before the first pair)
       else
         keep = (original * f / two_pi - low) / (high - low);
       keep = fmin(fmax(keep, 0.0), 1.0);

@@ -51,3 +51,18 @@ def test_chunk_wait_hook_refuses_more_than_four_seconds(lib):  # noqa: F811
     hook = lib.gptq_selftest_chunk_attention_wait
     hook.restype, hook.argtypes = ctypes.c_int, [ctypes.c_uint]
     assert hook(4 * 10 ** 9 + 1) == -1 and hook(4 * 10 ** 9) == 0 and hook(1) == 0 and hook(0) == 0
+
+
+# ------------------------------------------------------------------------------ the ramp's ends
+@pytest.mark.parametrize("original,low", [(5.0, 1.0), (6.0, 1.0), (100.0, 20.0)])
+def test_a_ramp_over_fewer_positions_than_the_fastest_pair_needs(lib, original, low):  # noqa: F811
+    # pair 0 turns original / (2 pi) times, no more than `low`: every pair is divided by the factor
+    turns, _ = g.rotary_table(64, scaling="ramp", factor=4.0, original=original, low=low, high=32.0, device="cpu")
+    plain, _ = g.rotary_table(64, device="cpu")
+    want = plain.double() / 4
+    assert bool(((turns.double() - want).abs() <= 2.0 ** -48 * want + 1).all())
+
+
+def test_a_ramp_over_more_positions_than_the_slowest_pair_needs(lib):  # noqa: F811
+    turns, _ = g.rotary_table(64, scaling="ramp", factor=4.0, original=1e9, low=1.0, high=32.0, device="cpu")
+    assert turns.equal(g.rotary_table(64, device="cpu")[0])
