@@ -1033,8 +1033,9 @@ def chunk_attention(q, k_cache, v_cache, block_table, seq_lens, cu_tokens, *, sc
     [pages, page_size, kv_heads, dim] (views in any order of the first three), block_table [batch, width]
     int32 -> out [tokens, heads, dim].  window > 0: only the last `window` keys up to a token's own.  scale: dim
     ** -0.5 where not given.  lse [tokens, heads] fp32 takes the log of each row's exponential sum.  Rows outside
-    every sequence are left as they were.  A workspace (chunk_attention_workspace) is made here when none
-    is given."""
+    every sequence are left as they were.  Probabilities are rounded to q's type once, which paged_attention does not do
+    (an error of some 1.4 roundings of the result, for one).  A workspace (chunk_attention_workspace: 21 to
+    42 MB by head_dim, whatever the call's size) is made here when none is given."""
     rt = _rt or _runtime()
     device, i32 = rt.device(), rt.int32
     tokens, heads, dim = shape = q.shape

@@ -30,7 +30,8 @@
 //
 // Rounding: a probability enters the product as one value of the cache's type (11 significant bits in fp16, 8 in bf16),
 // once; together with the rounding of the result the error against 64 bits is 1.4 times that of the rounding alone
-// (bf16 2.3e-3 against 1.7e-3, fp16 2.6e-4 against 2.0e-4).  As a sum of two values it would be the rounding alone, for
+// (bf16 2.3e-3 against 1.7e-3, fp16 2.6e-4 against 2.0e-4; the attention of single tokens carries them in two values, whose
+// products it has to spare).  As a sum of two values it would be the rounding alone, for
 // half as many MMAs again and more softmax instructions: 4096 tokens on 32768 keys took 2.8 ms so, against 1.34.
 // fp16 probabilities are taken 2^7 times as large, so that a long flat tail behind one large score is not lost
 // in fp16's range.
@@ -52,7 +53,9 @@
 // a converged warp (a lone thread's descriptors go through vector registers: 125 cycles an MMA, against 64 of the
 // tensor cores) 1648 / 335 / 135; TMA boxes, tiles at the diagonal looked over by two warps 1391 / 330 / 117; results in
 // 64-byte pieces 1330 / 331 / 111; items dealt out whole 1330 / 228 / 112; joins two parts at a time, the table past the
-// first-level cache 1345 / 227 / 109; the scores' MMAs unrolled for more head_dims 1315 / 225 / 106.
+// first-level cache 1345 / 227 / 109; the scores' MMAs unrolled for more head_dims 1315 / 225 / 106; infinite values looked up again
+// 1340 / 229 / 109; the MMA sequence chosen before the loop over the tiles 1285 / 224 / 104 (1430 to 1480 us for the first where
+// calls follow one another for long: 1.37 kW, and clocks that go by it).
 #pragma once
 
 #include <cuda.h>

@@ -137,7 +137,9 @@ int gptq_rotary(const void* q, const void* k, const void* v, int tokens, int hea
  * for row r = cu_tokens[b] + i, i < m = cu_tokens[b + 1] - cu_tokens[b], at position t = seq_lens[b] - m + i, over
  * the keys j in [max(0, t - window + 1), t] (window 0: [0, t]), k and v of head h / (heads / kv_heads).  Key j
  * is slot j % page_size of page block_table[b, j / page_size].  Sums, maxima and accumulators are
- * fp32, the probabilities enter the product with v in dtype, out is rounded once.  A row whose position
+ * fp32, the probabilities enter the product with v in dtype, out is rounded once: its error is some 1.4 times that
+ * of the one rounding (gptq_paged_attention, for steps of one token a sequence, carries the probabilities in two
+ * parts and has the one rounding's).  A row whose position
  * is negative (seq_lens[b] < m) gives zeros.  Rows outside every sequence are left as they were; a row that
  * cu_tokens gives to two sequences (GPTQ_DEV_TOKEN_ROWS) gets the result of either.  What a row does
  * not see is not used for it, whatever it holds: cache slots, block-table entries past a sequence's
