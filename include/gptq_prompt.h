@@ -139,7 +139,7 @@ int gptq_rotary(const void* q, const void* k, const void* v, int tokens, int hea
  * is slot j % page_size of page block_table[b, j / page_size].  Sums, maxima and accumulators are
  * fp32, the probabilities enter the product with v in dtype, out is rounded once: its error is some 1.4 times that
  * of the one rounding (gptq_paged_attention, for steps of one token a sequence, carries the probabilities in two
- * parts and has the one rounding's).  A row whose position
+ * parts and has the one rounding's).  Values of up to 2^89 in magnitude cannot overflow the sums.  A row whose position
  * is negative (seq_lens[b] < m) gives zeros.  Rows outside every sequence are left as they were; a row that
  * cu_tokens gives to two sequences (GPTQ_DEV_TOKEN_ROWS) gets the result of either.  What a row does
  * not see is not used for it, whatever it holds: cache slots, block-table entries past a sequence's
